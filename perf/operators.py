@@ -153,7 +153,7 @@ def prepare(case, seed):
         if case["op"] == "join":
             st = DTYPES[case["stream"]]
             s["h_out"], s["xn"] = out((n, d), st), out((n, d), DTYPES[case["norm"]])
-            nbytes = rvq.moe_norm_join_workspace_bytes(n, d, train)
+            nbytes = rvq.moe_norm_join_workspace_bytes(n, d)
             if train:
                 s["rstd"] = out((2, n), torch.float32)
                 s["dh"], s["dy"] = torch.empty_like(s["h"]), torch.empty_like(s["y"])
@@ -312,7 +312,7 @@ def _own_linear(rvq, s, case):
 
 def _own_join(rvq, s, case):
     n, d = case["n"], case["d"]
-    rvq.moe_norm_join(s["y"], n, d, s["h_out"], s["xn"], s["ws"], h=s["h"], alpha=case["alpha"],
+    rvq.moe_norm_join(s["y"], n, d, s["h_out"], s["xn"], h=s["h"], alpha=case["alpha"],
                       gate=s["gate"], post_norm=case["post"], w_post=s["w_post"],
                       w_pre=s["w_pre"], eps=EPS, rstd=s.get("rstd"))
     out = {"h_out": s["h_out"], "xn": s["xn"]}
