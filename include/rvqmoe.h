@@ -67,7 +67,11 @@ typedef enum rvq_status {
     RVQ_ENOTIMPL = 8  /* configuration not supported by this build               */
 } rvq_status;
 
-typedef enum rvq_dtype { RVQ_F32 = 0, RVQ_BF16 = 1 } rvq_dtype;
+typedef enum rvq_dtype {
+    RVQ_F32 = 0,
+    RVQ_BF16 = 1,
+    RVQ_F16 = 2 /* the dense operators (moe_linear, moe_gated_linear, moe_norm_join) only */
+} rvq_dtype;
 
 /* Bits of the device status word (first 4 bytes of every workspace). */
 #define RVQ_DEV_ERR_INDEX 0x1u    /* expert index / offsets outside range      */
@@ -528,6 +532,143 @@ rvq_status moe_layer_forward_prenorm(const rvq_moe_bank *bank, const float *wr_d
  * aligned (EALIGN); eps >= 0; x may alias out only when both are fp32. */
 rvq_status moe_rms_norm(const void *x_dev, rvq_dtype xdt, int32_t n, int32_t d, float eps,
                         void *out_dev, rvq_dtype odt, rvq_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Dense operators beside the routed experts: the two halves of a shared
+ * (always active, unquantised) expert, and the norms, gate and residual that
+ * join one block to the next, each with its gradients.  The pages have no
+ * counterpart; the formulas are stated at each call.  A block with a shared
+ * expert runs them as
+ *     moe_norm_join -> moe_gated_linear -> moe_linear -> moe_layer_forward_ex
+ * with the shared expert's output as the layer's residual.
+ *
+ * Matrices are row-major with a row pitch `ld*` in elements: ld >= columns,
+ * ld % 8 == 0, base pointers 16-byte aligned (EALIGN).  n (tokens) is any
+ * number >= 1; rows and cols are multiples of 8 (EINVAL).  Element types are
+ * RVQ_BF16 or RVQ_F16 for the operands of a product (one type for x, w, bias
+ * and, in a gradient, dout and every output); products accumulate in fp32 on
+ * the tensor cores and each output is rounded once.
+ *
+ * `ws` (dev, 256-byte aligned) starts with the status block: rvq_ws_clear()
+ * once, then any number of calls on one stream.  A bounded device wait that
+ * expires sets RVQ_DEV_ERR_TIMEOUT; the outputs are then undefined.
+ * ------------------------------------------------------------------------ */
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,     /* max(v, 0); slope 0 at 0                            */
+    MOE_ACT_SILU = 2,     /* v / (1 + exp(-v))                                  */
+    MOE_ACT_GELU = 3,     /* v/2 (1 + erf(v / sqrt 2))                          */
+    MOE_ACT_GELU_TANH = 4 /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))      */
+} moe_act;
+
+/* Workspace of moe_linear (backward = 0) and moe_linear_backward (1); one of
+ * the larger size serves both.  0 for a shape the calls refuse. */
+size_t moe_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols, int32_t backward);
+
+/* out[t][r] = residual[t][r] + alpha * act(sum_c x[t][c] w[r][c] + bias[r])
+ *  - x [n][cols], w [rows][cols] of dt; bias [rows] of dt or NULL.
+ *  - residual [n][rows] of rdt, or NULL; out [n][rows] of odt; rdt and odt are
+ *    fp32 or 16-bit (any mix).  out may alias residual if type and pitch agree
+ *    (each element is read before it is written); no other overlap.
+ *  - pre: fp32 [n][rows] without padding, or NULL; receives x w^T + bias, which
+ *    moe_linear_backward needs for act != MOE_ACT_NONE. */
+rvq_status moe_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t ldw,
+                      const void *bias_dev, rvq_dtype dt, int32_t n, int32_t rows, int32_t cols,
+                      moe_act act, float alpha, const void *residual_dev, rvq_dtype rdt,
+                      int64_t ldr, void *out_dev, rvq_dtype odt, int64_t ldo, float *pre_dev,
+                      void *ws_dev, size_t ws_bytes, rvq_stream_t stream);
+
+/* Gradients of moe_linear, with dp = alpha * dout * act'(pre):
+ *   dx = dp w, dw = dp^T x, dbias[r] = sum_t dp[t][r]
+ * dout [n][rows]; dx [n][cols], dw [rows][cols], dbias [rows], all of dt, each
+ * NULL when not wanted (one at least is).  The gradient of the residual is dout
+ * itself.  pre: as written by the forward call (NULL for MOE_ACT_NONE).  With
+ * an activation dp is rounded to dt once as an operand of the products. */
+rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x_dev, int64_t ldx,
+                               const void *w_dev, int64_t ldw, const float *pre_dev, rvq_dtype dt,
+                               int32_t n, int32_t rows, int32_t cols, moe_act act, float alpha,
+                               void *dx_dev, int64_t lddx, void *dw_dev, int64_t lddw,
+                               void *dbias_dev, void *ws_dev, size_t ws_bytes,
+                               rvq_stream_t stream);
+
+/* Workspace of moe_gated_linear / moe_gated_linear_backward, as above. */
+size_t moe_gated_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols, int32_t backward);
+
+/* The first half of a gated feed-forward block in one kernel:
+ *   g = x wg^T + bg, u = x wu^T + bu, out = act(g) * u
+ *  - x [n][cols], wg and wu [rows][cols] (one pitch ldw), bg and bu [rows] or
+ *    NULL (each by itself), out [n][rows], all of dt.
+ *  - pre: fp32 [2][n][rows] or NULL; receives g and u for the gradients. */
+rvq_status moe_gated_linear(const void *x_dev, int64_t ldx, const void *wg_dev,
+                            const void *wu_dev, int64_t ldw, const void *bg_dev,
+                            const void *bu_dev, rvq_dtype dt, int32_t n, int32_t rows,
+                            int32_t cols, moe_act act, void *out_dev, int64_t ldo, float *pre_dev,
+                            void *ws_dev, size_t ws_bytes, rvq_stream_t stream);
+
+/* Gradients of moe_gated_linear, with dg = dout * u * act'(g) and
+ * du = dout * act(g) (each rounded to dt once as an operand of the products):
+ *   dx = dg wg + du wu, dwg = dg^T x, dwu = du^T x, dbg, dbu = sums over t
+ * Outputs are NULL when not wanted; dwg and dwu go together (one pitch lddw). */
+rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const void *x_dev,
+                                     int64_t ldx, const void *wg_dev, const void *wu_dev,
+                                     int64_t ldw, const float *pre_dev, rvq_dtype dt, int32_t n,
+                                     int32_t rows, int32_t cols, moe_act act, void *dx_dev,
+                                     int64_t lddx, void *dwg_dev, void *dwu_dev, int64_t lddw,
+                                     void *dbg_dev, void *dbu_dev, void *ws_dev, size_t ws_bytes,
+                                     rvq_stream_t stream);
+
+/* How the gate of moe_norm_join is broadcast over [n][d]. */
+typedef enum moe_gate {
+    MOE_GATE_NONE = 0,    /* no gate (1)              */
+    MOE_GATE_SCALAR = 1,  /* one value                */
+    MOE_GATE_TOKEN = 2,   /* [n], one per token       */
+    MOE_GATE_CHANNEL = 3, /* [d], one per channel     */
+    MOE_GATE_FULL = 4     /* [n][d]                   */
+} moe_gate;
+
+/* Joins a block's output y to the residual stream h and norms the result for
+ * the next block, in one pass (norm(v) = v / sqrt(mean_c v^2 + eps)):
+ *   z      = post_norm ? norm(y) * w_post : y
+ *   h_out  = alpha * h + gate * z
+ *   xn     = norm(h_out) * w_pre          (of h_out before its rounding)
+ *  - h, h_out: [n][d] of hdt; y: [n][d] of ydt; xn: [n][d] of xdt; gate of gdt;
+ *    w_post, w_pre: [d] of wdt, NULL = 1.  Types are fp32, bf16 or fp16.  Rows
+ *    are contiguous, as in moe_rms_norm; d % 8 == 0 and d <= 16384 (EINVAL).
+ *  - h may be NULL (no residual), h_out or xn may be NULL (not both).
+ *  - rstd: fp32 [2][n] or NULL; receives 1/rms of y (1 without a post norm) and
+ *    of h_out, for the gradients.
+ *  - h_out may alias h or y, and xn may alias y, if their types agree; xn must
+ *    not alias h_out.  Sums and statistics are fp32.  eps >= 0; a row of zeros
+ *    with eps = 0 gives NaN, as the formula does. */
+rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rvq_dtype ydt,
+                         int32_t n, int32_t d, float alpha, const void *gate_dev,
+                         moe_gate gate_kind, rvq_dtype gdt, int32_t post_norm,
+                         const void *w_post_dev, const void *w_pre_dev, rvq_dtype wdt, float eps,
+                         void *h_out_dev, void *xn_dev, rvq_dtype xdt, float *rstd_dev,
+                         rvq_stream_t stream);
+
+/* Workspace of moe_norm_join_backward (partial sums over tokens). */
+size_t moe_norm_join_workspace_bytes(int32_t n, int32_t d);
+
+/* Gradients of moe_norm_join from dh_out [n][d] of hdt and dxn [n][d] of xdt
+ * (each may be NULL: no gradient arrives there, not both), with the forward's
+ * inputs and rstd:
+ *   e      = dh_out + r2 (dxn w_pre) - h_out r2^3 mean(dxn w_pre h_out)
+ *   dh     = alpha e (hdt);  dgate = e z, summed over the gate's broadcast (gdt)
+ *   dz     = gate e;  dw_post = sum_t dz y r1;  dw_pre = sum_t dxn h_out r2 (wdt)
+ *   dy     = post_norm ? r1 (dz w_post) - y r1^3 mean(dz w_post y) : dz  (ydt)
+ * h_out is recomputed from h, y and rstd.  Outputs are NULL when not wanted.
+ * Sums over tokens run in a fixed order: results repeat bit for bit.  dh may
+ * alias dh_out, and dy may alias dxn, if their types agree. */
+rvq_status moe_norm_join_backward(const void *dh_out_dev, const void *dxn_dev, rvq_dtype xdt,
+                                  const void *h_dev, rvq_dtype hdt, const void *y_dev,
+                                  rvq_dtype ydt, int32_t n, int32_t d, float alpha,
+                                  const void *gate_dev, moe_gate gate_kind, rvq_dtype gdt,
+                                  int32_t post_norm, const void *w_post_dev,
+                                  const void *w_pre_dev, rvq_dtype wdt, const float *rstd_dev,
+                                  void *dh_dev, void *dy_dev, void *dgate_dev, void *dw_post_dev,
+                                  void *dw_pre_dev, void *ws_dev, size_t ws_bytes,
+                                  rvq_stream_t stream);
 
 /* Self-test of the failure path of the tensor-core kernel (no counterpart in
  * the pages): launches the prefill GEMM on one zero token routed to expert 0

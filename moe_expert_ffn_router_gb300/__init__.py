@@ -17,13 +17,17 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librvqmoe.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "rvqmoe.h")
 
-RVQ_F32, RVQ_BF16 = 0, 1
+RVQ_F32, RVQ_BF16, RVQ_F16 = 0, 1, 2
 RVQ_WS_STATUS_BYTES = 256
 RVQ_CODEBOOK_BYTES = 24576
 RVQ_BANK_MAGIC = 0x31515652
 RVQ_HDR_FLAG_CRC32 = 0x1
 MOE_LAYER_EVENTS = 8
 RVQMOE_PREFILL_MIN_TOKENS = 6
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
+MOE_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU,
+            "gelu": MOE_ACT_GELU, "gelu_tanh": MOE_ACT_GELU_TANH}
+(MOE_GATE_NONE, MOE_GATE_SCALAR, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL) = range(5)
 DEV_ERR_INDEX, DEV_ERR_NONFINITE, DEV_ERR_CORRUPT, DEV_ERR_TIMEOUT = 1, 2, 4, 8
 STATUS = {0: "RVQ_OK", 1: "RVQ_EINVAL", 2: "RVQ_EALIGN", 3: "RVQ_ENOMEM", 4: "RVQ_ECORRUPT",
           5: "RVQ_EDEVICE", 6: "RVQ_ETIMEOUT", 7: "RVQ_ECUDA", 8: "RVQ_ENOTIMPL"}
@@ -55,6 +59,7 @@ if not os.path.exists(LIB_PATH):
 
 _vp, _i32, _u32, _u64, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32,
                               ctypes.c_uint64, ctypes.c_size_t)
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
 _lib = ctypes.CDLL(LIB_PATH)
 _BANKP = ctypes.POINTER(RvqMoeBank)
 _SIGS = {
@@ -108,6 +113,23 @@ _SIGS = {
     "moe_layer_forward_prenorm": (_i32, [_BANKP, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float,
                                          _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp]),
     "moe_rms_norm": (_i32, [_vp, _i32, _i32, _i32, ctypes.c_float, _vp, _i32, _vp]),
+    "moe_linear_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_linear": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32,
+                          _i64, _vp, _i32, _i64, _vp, _vp, _sz, _vp]),
+    "moe_linear_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32,
+                                   _i32, _f32, _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "moe_gated_linear_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_gated_linear": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                _vp, _i64, _vp, _vp, _sz, _vp]),
+    "moe_gated_linear_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _i32,
+                                         _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                                         _vp, _sz, _vp]),
+    "moe_norm_join": (_i32, [_vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _i32, _i32, _i32, _vp,
+                             _vp, _i32, _f32, _vp, _vp, _i32, _vp, _vp]),
+    "moe_norm_join_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_norm_join_backward": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp,
+                                      _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _sz, _vp]),
     "rvq_selftest_prefill_timeout": (_i32, [_BANKP, _vp, _sz, _vp]),
     "rvq_ws_clear": (_i32, [_vp, _vp]),
     "rvq_ws_status": (_i32, [_vp, ctypes.POINTER(_u32), _vp]),
@@ -445,6 +467,196 @@ def rvq_selftest_prefill_timeout(bank, ws, stream=None):
 def moe_rms_norm(x, n, d, out, eps=1e-6, stream=None):
     _check("moe_rms_norm", _lib.moe_rms_norm(_p(x), _dt(x), n, d, float(eps), _p(out), _dt(out),
                                              _stream(stream)))
+
+
+# ------------------------------------------------------------------ dense operators
+
+_DTYPES = {torch.float32: RVQ_F32, torch.bfloat16: RVQ_BF16, torch.float16: RVQ_F16}
+
+
+def _dt_any(t) -> int:
+    """dtype code of a dense operator's tensor (None: fp32, unused)."""
+    if t is None:
+        return RVQ_F32
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype} (bf16, fp16 or fp32)") from None
+
+
+def _mat(t, rows, cols, what, dtype=None) -> int:
+    """Row pitch of a [rows][cols] matrix; columns must be contiguous."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    pitch, step = t.stride()
+    if step != 1:
+        raise ValueError(f"{what}: columns are not contiguous (strides {t.stride()})")
+    return pitch if rows > 1 else max(cols, pitch // 8 * 8)
+
+
+def _vec(t, numel, what, dtype=None):
+    """A contiguous tensor of numel elements (or None)."""
+    if t is None:
+        return
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{what}: {tuple(t.shape)} with strides {t.stride()}, expected {numel} "
+                         "contiguous elements")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+
+
+def moe_linear_workspace_bytes(n, rows, cols, backward=False) -> int:
+    return int(_lib.moe_linear_workspace_bytes(n, rows, cols, int(backward)))
+
+
+def moe_linear(x, w, n, rows, cols, out, ws, bias=None, act=MOE_ACT_NONE, alpha=1.0, residual=None,
+               pre=None, stream=None):
+    """out = residual + alpha * act(x w^T + bias); x [n][cols], w [rows][cols]
+    (bf16 or fp16, any row pitch), out and residual [n][rows].  pre (fp32
+    [n][rows]) keeps x w^T + bias for moe_linear_backward."""
+    ldx, ldw = _mat(x, n, cols, "x"), _mat(w, rows, cols, "w", x.dtype)
+    ldo, ldr = _mat(out, n, rows, "out"), _mat(residual, n, rows, "residual")
+    _vec(bias, rows, "bias", x.dtype)
+    _vec(pre, n * rows, "pre", torch.float32)
+    _check("moe_linear",
+           _lib.moe_linear(_p(x), ldx, _p(w), ldw, _p(bias), _dt_any(x), n, rows, cols, act, alpha,
+                           _p(residual), _dt_any(residual), ldr, _p(out), _dt_any(out), ldo,
+                           _p(pre), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_linear_backward(dout, x, w, n, rows, cols, ws, dx=None, dw=None, dbias=None, pre=None,
+                        act=MOE_ACT_NONE, alpha=1.0, stream=None):
+    """Gradients of moe_linear (those given a tensor): dx [n][cols], dw
+    [rows][cols], dbias [rows]; the residual's gradient is dout itself."""
+    dt = dout.dtype
+    ldd, ldx, ldw = (_mat(dout, n, rows, "dout"), _mat(x, n, cols, "x", dt),
+                     _mat(w, rows, cols, "w", dt))
+    lddx, lddw = _mat(dx, n, cols, "dx", dt), _mat(dw, rows, cols, "dw", dt)
+    _vec(dbias, rows, "dbias", dt)
+    _vec(pre, n * rows, "pre", torch.float32)
+    _check("moe_linear_backward",
+           _lib.moe_linear_backward(_p(dout), ldd, _p(x), ldx, _p(w), ldw, _p(pre), _dt_any(dout),
+                                    n, rows, cols, act, alpha, _p(dx), lddx, _p(dw), lddw,
+                                    _p(dbias), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_gated_linear_workspace_bytes(n, rows, cols, backward=False) -> int:
+    return int(_lib.moe_gated_linear_workspace_bytes(n, rows, cols, int(backward)))
+
+
+def moe_gated_linear(x, wg, wu, n, rows, cols, out, ws, bg=None, bu=None, act=MOE_ACT_SILU,
+                     pre=None, stream=None):
+    """out = act(x wg^T + bg) * (x wu^T + bu) in one kernel.  wg and wu share
+    their row pitch (two halves of one tensor do).  pre (fp32 [2][n][rows])
+    keeps both projections for moe_gated_linear_backward."""
+    dt = x.dtype
+    ldx, ldw = _mat(x, n, cols, "x"), _mat(wg, rows, cols, "wg", dt)
+    if _mat(wu, rows, cols, "wu", dt) != ldw:
+        raise ValueError("wg and wu have different row pitches")
+    ldo = _mat(out, n, rows, "out", dt)
+    _vec(bg, rows, "bg", dt)
+    _vec(bu, rows, "bu", dt)
+    _vec(pre, 2 * n * rows, "pre", torch.float32)
+    _check("moe_gated_linear",
+           _lib.moe_gated_linear(_p(x), ldx, _p(wg), _p(wu), ldw, _p(bg), _p(bu), _dt_any(x), n,
+                                 rows, cols, act, _p(out), ldo, _p(pre), _p(ws), _nbytes(ws),
+                                 _stream(stream)))
+
+
+def moe_gated_linear_backward(dout, x, wg, wu, pre, n, rows, cols, ws, dx=None, dwg=None, dwu=None,
+                              dbg=None, dbu=None, act=MOE_ACT_SILU, stream=None):
+    """Gradients of moe_gated_linear (those given a tensor) from the forward
+    call's inputs and `pre`."""
+    dt = dout.dtype
+    ldd, ldx, ldw = (_mat(dout, n, rows, "dout"), _mat(x, n, cols, "x", dt),
+                     _mat(wg, rows, cols, "wg", dt))
+    if _mat(wu, rows, cols, "wu", dt) != ldw:
+        raise ValueError("wg and wu have different row pitches")
+    lddx, lddw = _mat(dx, n, cols, "dx", dt), _mat(dwg, rows, cols, "dwg", dt)
+    if _mat(dwu, rows, cols, "dwu", dt) != lddw:
+        raise ValueError("dwg and dwu have different row pitches")
+    _vec(dbg, rows, "dbg", dt)
+    _vec(dbu, rows, "dbu", dt)
+    _vec(pre, 2 * n * rows, "pre", torch.float32)
+    _check("moe_gated_linear_backward",
+           _lib.moe_gated_linear_backward(_p(dout), ldd, _p(x), ldx, _p(wg), _p(wu), ldw, _p(pre),
+                                          _dt_any(dout), n, rows, cols, act, _p(dx), lddx, _p(dwg),
+                                          _p(dwu), lddw, _p(dbg), _p(dbu), _p(ws), _nbytes(ws),
+                                          _stream(stream)))
+
+
+def _gate_kind(gate, n, d) -> int:
+    """MOE_GATE_* of a contiguous gate tensor: one element, [n][1], [1][d] or
+    [d], or [n][d]."""
+    if gate is None:
+        return MOE_GATE_NONE
+    if not gate.is_contiguous():
+        raise ValueError(f"gate: not contiguous (strides {gate.stride()})")
+    shape = tuple(gate.shape)
+    if shape == (n, d):
+        return MOE_GATE_FULL
+    if shape in ((d,), (1, d)):
+        return MOE_GATE_CHANNEL
+    if shape == (n, 1):
+        return MOE_GATE_TOKEN
+    if gate.numel() == 1:
+        return MOE_GATE_SCALAR
+    raise ValueError(f"gate: shape {shape} does not broadcast over ({n}, {d})")
+
+
+def moe_norm_join(y, n, d, h_out, xn, h=None, alpha=1.0, gate=None, post_norm=True, w_post=None,
+                  w_pre=None, eps=1e-6, rstd=None, stream=None):
+    """h_out = alpha * h + gate * norm(y) * w_post (post_norm; else y itself),
+    xn = norm(h_out) * w_pre.  gate broadcasts over [n][d]; gains None are 1.
+    h_out or xn may be None.  rstd (fp32 [2][n]) is kept for the gradients."""
+    for t, what in ((y, "y"), (h, "h"), (h_out, "h_out"), (xn, "xn")):
+        _vec(t, n * d, what)
+    if h is not None and h_out is not None and h.dtype != h_out.dtype:
+        raise TypeError(f"h_out: dtype {h_out.dtype}, expected {h.dtype}")
+    _vec(w_post, d, "w_post")
+    _vec(w_pre, d, "w_pre", None if w_post is None else w_post.dtype)
+    _vec(rstd, 2 * n, "rstd", torch.float32)
+    _check("moe_norm_join",
+           _lib.moe_norm_join(_p(h), _dt_any(h if h is not None else h_out), _p(y), _dt_any(y), n,
+                              d, alpha, _p(gate), _gate_kind(gate, n, d), _dt_any(gate),
+                              int(post_norm), _p(w_post), _p(w_pre),
+                              _dt_any(w_post if w_post is not None else w_pre), eps, _p(h_out),
+                              _p(xn), _dt_any(xn), _p(rstd), _stream(stream)))
+
+
+def moe_norm_join_workspace_bytes(n, d) -> int:
+    return int(_lib.moe_norm_join_workspace_bytes(n, d))
+
+
+def moe_norm_join_backward(dh_out, dxn, y, n, d, rstd, ws, h=None, alpha=1.0, gate=None,
+                           post_norm=True, w_post=None, w_pre=None, dh=None, dy=None, dgate=None,
+                           dw_post=None, dw_pre=None, stream=None):
+    """Gradients of moe_norm_join (those given a tensor) from its inputs and
+    rstd.  dh_out or dxn may be None."""
+    for t, what in ((y, "y"), (h, "h"), (dh_out, "dh_out"), (dxn, "dxn")):
+        _vec(t, n * d, what)
+    hdt = next((t.dtype for t in (h, dh_out, dh) if t is not None), torch.float32)
+    _vec(dh_out, n * d, "dh_out", hdt)
+    _vec(dh, n * d, "dh", hdt)
+    _vec(dy, n * d, "dy", y.dtype)
+    wdt = next((t.dtype for t in (w_post, w_pre, dw_post, dw_pre) if t is not None), torch.float32)
+    for t, what in ((w_post, "w_post"), (w_pre, "w_pre"), (dw_post, "dw_post"),
+                    (dw_pre, "dw_pre")):
+        _vec(t, d, what, wdt)
+    _vec(rstd, 2 * n, "rstd", torch.float32)
+    if gate is not None:
+        _vec(dgate, gate.numel(), "dgate", gate.dtype)
+    _check("moe_norm_join_backward",
+           _lib.moe_norm_join_backward(_p(dh_out), _p(dxn), _dt_any(dxn), _p(h), _DTYPES[hdt],
+                                       _p(y), _dt_any(y), n, d, alpha, _p(gate),
+                                       _gate_kind(gate, n, d), _dt_any(gate), int(post_norm),
+                                       _p(w_post), _p(w_pre), _DTYPES[wdt], _p(rstd), _p(dh),
+                                       _p(dy), _p(dgate), _p(dw_post), _p(dw_pre), _p(ws),
+                                       _nbytes(ws), _stream(stream)))
 
 
 def rvq_ws_clear(ws, stream=None):

@@ -1,0 +1,189 @@
+// Internal declarations of the dense (unquantised) operators beside the routed
+// experts: moe_linear, moe_gated_linear and their gradients (dense_api.cu,
+// dense_gemm.cu, dense_bwd.cu) and moe_norm_join (norm_join.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.cuh"
+
+namespace rvq {
+
+// ---------------------------------------------------------------- elements
+// Scalars and groups of eight of the three element types, as fp32.
+__device__ __forceinline__ float ld_elem(const void *p, int dt, int64_t i) {
+    if (dt == RVQ_F32) return reinterpret_cast<const float *>(p)[i];
+    const uint16_t b = reinterpret_cast<const uint16_t *>(p)[i];
+    if (dt == RVQ_BF16) return __uint_as_float((uint32_t)b << 16);
+    return __half2float(__ushort_as_half(b));
+}
+
+__device__ __forceinline__ void st_elem(void *p, int dt, int64_t i, float v) {
+    if (dt == RVQ_F32)
+        reinterpret_cast<float *>(p)[i] = v;
+    else if (dt == RVQ_BF16)
+        reinterpret_cast<uint16_t *>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else
+        reinterpret_cast<uint16_t *>(p)[i] = __half_as_ushort(__float2half_rn(v));
+}
+
+__device__ __forceinline__ uint32_t pack16(int dt, float lo, float hi) {
+    if (dt == RVQ_BF16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void unpack16(int dt, uint32_t w, float &lo, float &hi) {
+    if (dt == RVQ_BF16) {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        lo = f.x;
+        hi = f.y;
+    }
+}
+
+// eight consecutive elements at a 16-byte aligned place
+__device__ __forceinline__ void ld8(const void *p, int dt, int64_t i, float (&v)[8]) {
+    if (dt == RVQ_F32) {
+        const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
+        const float4 a = q[0], b = q[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p) + i);
+        unpack16(dt, q.x, v[0], v[1]);
+        unpack16(dt, q.y, v[2], v[3]);
+        unpack16(dt, q.z, v[4], v[5]);
+        unpack16(dt, q.w, v[6], v[7]);
+    }
+}
+
+__device__ __forceinline__ void st8(void *p, int dt, int64_t i, const float (&v)[8]) {
+    if (dt == RVQ_F32) {
+        float4 *q = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i);
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p) + i) =
+            make_uint4(pack16(dt, v[0], v[1]), pack16(dt, v[2], v[3]), pack16(dt, v[4], v[5]),
+                       pack16(dt, v[6], v[7]));
+    }
+}
+
+// ------------------------------------------------------------- activations
+__device__ __forceinline__ float act_value(int act, float v) {
+    switch (act) {
+        case MOE_ACT_RELU: return v > 0.f ? v : 0.f;
+        case MOE_ACT_SILU: return v / (1.f + expf(-v));
+        case MOE_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+        case MOE_ACT_GELU_TANH:
+            return 0.5f * v *
+                   (1.f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
+        default: return v;
+    }
+}
+
+__device__ __forceinline__ float act_slope(int act, float v) {
+    switch (act) {
+        case MOE_ACT_RELU: return v > 0.f ? 1.f : 0.f;
+        case MOE_ACT_SILU: {
+            const float s = 1.f / (1.f + expf(-v));
+            return s * (1.f + v * (1.f - s));
+        }
+        case MOE_ACT_GELU:
+            return 0.5f * (1.f + erff(v * 0.70710678118654752f)) +
+                   v * 0.39894228040143268f * expf(-0.5f * v * v);
+        case MOE_ACT_GELU_TANH: {
+            // beyond |v| = 16 the slope is 0 or 1 to fp32, and v * v * v may overflow
+            if (v >= 16.f) return 1.f;
+            if (v <= -16.f) return 0.f;
+            const float c = 0.79788456080286536f;
+            const float t = tanhf(c * (v + 0.044715f * v * v * v));
+            return 0.5f * (1.f + t) +
+                   0.5f * v * (1.f - t * t) * c * (1.f + 3.f * 0.044715f * v * v);
+        }
+        default: return 1.f;
+    }
+}
+
+// --------------------------------------------------------------------- GEMM
+// One product, or two that share an operand or an output, for one launch:
+//   PLAIN   out0[m][n] = sum_k A0[m][k] B0[n][k]
+//   GATED   g = A0 B0^T, u = A0 B1^T; out0 = act(g + bias0) * (u + bias1)
+//   SUM_K   out0 = A0 B0^T + A1 B1^T
+//   PAIR_M  out0 = A0 B0^T, out1 = A1 B0^T
+// An operand is stored K-contiguous ([rows][K]) or, with *_t set, as its
+// transpose ([K][rows]).  out0 = residual + alpha * act(product + bias0) in the
+// other modes.  pre (fp32, contiguous [M][N]) receives product + bias.
+enum DgMode { DG_PLAIN = 0, DG_GATED = 1, DG_SUM_K = 2, DG_PAIR_M = 3 };
+struct DenseJob {
+    int mode;
+    int M, N, K;
+    int a_t, b_t;
+    const void *a[2];
+    int64_t lda;
+    const void *b[2];
+    int64_t ldb;
+    int dt;                 // of A, B and the biases: RVQ_BF16 or RVQ_F16
+    const void *bias[2];
+    int act;
+    float alpha;
+    const void *residual;
+    int rdt;
+    int64_t ldr;
+    void *out[2];
+    int odt;
+    int64_t ldo;
+    float *pre[2];
+    uint32_t *status;
+};
+rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream);
+
+// Gradient of the gated product (mats = 2) or of an activation (mats = 1):
+//   mats 2: dp0 = dout * pre1 * act'(pre0), dp1 = dout * act(pre0)
+//   mats 1: dp0 = alpha * dout * act'(pre0)      (pre0 NULL: act' = 1)
+// dp (16-bit [n][rows] each, NULL: not written) and, with dbias[i] set, the
+// sums over the n rows through fp32 partials ([chunks][mats][rows] in part).
+struct DenseBwdJob {
+    int mats, n, rows, act;
+    float alpha;
+    const void *dout;
+    int64_t ldd;
+    int dt;
+    const float *pre[2];
+    void *dp[2];
+    void *dbias[2];
+    float *part;
+};
+constexpr int kBwdChunkRows = 32;  // rows per partial of a bias gradient
+inline int dense_bwd_chunks(int n) { return (n + kBwdChunkRows - 1) / kBwdChunkRows; }
+rvq_status launch_dense_bwd(const DenseBwdJob &job, cudaStream_t stream);
+
+// ---------------------------------------------------------------- norm join
+struct JoinJob {
+    int n, d;
+    float eps, alpha;
+    const void *h, *y, *gate, *w_post, *w_pre;
+    int hdt, ydt, gdt, wdt;
+    int gate_kind, post_norm;
+    void *h_out, *xn;
+    int xdt;
+    float *rstd;            // [2][n]: of y (1 without a post norm), of h_out
+    // gradients
+    const void *dh_out, *dxn;
+    void *dh, *dy, *dgate, *dw_post, *dw_pre;
+    float *part;            // [slots][3][d] column sums, then [slots] scalar sums
+    int slots;
+};
+constexpr int kJoinMaxD = 16384;
+int join_bwd_slots(int n, int d);
+rvq_status launch_norm_join(const JoinJob &job, cudaStream_t stream);
+rvq_status launch_norm_join_bwd(const JoinJob &job, cudaStream_t stream);
+
+}  // namespace rvq

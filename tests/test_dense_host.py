@@ -1,0 +1,174 @@
+"""Host side of the dense operators (no GPU): workspace sizes and refusals
+before any launch, in the library and in the binding."""
+import ctypes
+
+import pytest
+import torch
+
+import moe_expert_ffn_router_gb300 as rvq
+
+lib = rvq._lib
+A = 0x10000000       # fake, aligned "device" addresses far apart (never dereferenced)
+B, C, D, E_, F = (A + i * 0x10000000 for i in range(1, 6))
+OK, EINVAL, EALIGN, ENOMEM = 0, 1, 2, 3
+F32, BF16, F16 = 0, 1, 2
+
+
+def up256(v):
+    return (v + 255) // 256 * 256
+
+
+def test_workspace_sizes():
+    for n, r, c in ((1, 8, 8), (7, 256, 512), (4096, 2048, 7168)):
+        assert rvq.moe_linear_workspace_bytes(n, r, c) >= 256
+        assert rvq.moe_gated_linear_workspace_bytes(n, r, c) >= 256
+        # dp (16 bits) of each matrix and one bias partial per 32 tokens
+        for f, m in ((rvq.moe_linear_workspace_bytes, 1), (rvq.moe_gated_linear_workspace_bytes, 2)):
+            assert f(n, r, c, True) >= 256 + m * n * r * 2 + (n + 31) // 32 * m * r * 4
+        assert rvq.moe_norm_join_workspace_bytes(n, c) >= 256 + 4 * 3 * c
+    for n, r, c in ((0, 8, 8), (1, 12, 8), (1, 8, 12), (1, 0, 8), (-1, 8, 8)):
+        assert rvq.moe_linear_workspace_bytes(n, r, c) == 0
+        assert rvq.moe_gated_linear_workspace_bytes(n, r, c, True) == 0
+    assert rvq.moe_norm_join_workspace_bytes(0, 8) == 0
+    assert rvq.moe_norm_join_workspace_bytes(1, 12) == 0
+    assert rvq.moe_norm_join_workspace_bytes(1, 16384 + 8) == 0
+
+
+LIN = dict(x=A, ldx=64, w=B, ldw=64, bias=None, dt=BF16, n=4, rows=32, cols=64, act=0, alpha=1.0,
+           res=None, rdt=F32, ldr=0, out=C, odt=BF16, ldo=32, pre=None, ws=D, wsb=1 << 20, st=None)
+
+
+def lin(**kw):
+    return lib.moe_linear(*{**LIN, **kw}.values())
+
+
+def test_linear_refusals():
+    for bad in (dict(n=0), dict(rows=12), dict(cols=60), dict(rows=0), dict(dt=F32), dict(dt=3),
+                dict(act=5), dict(act=-1), dict(x=None), dict(w=None), dict(out=None),
+                dict(ldx=56), dict(ldx=68), dict(ldw=0), dict(ldo=31), dict(odt=7),
+                dict(res=E_, rdt=5, ldr=32), dict(res=E_, ldr=24), dict(ws=None), dict(ws=D + 16),
+                dict(out=A), dict(out=B + 64), dict(out=A + 4 * 64 * 2 - 16),
+                dict(res=C, rdt=F32, ldr=32), dict(res=C + 16, rdt=BF16, ldr=32),
+                dict(res=C, rdt=BF16, ldr=40), dict(pre=C)):
+        assert lin(**bad) == EINVAL, bad
+    for bad in (dict(x=A + 2), dict(w=B + 8), dict(out=C + 4), dict(bias=E_ + 2), dict(pre=E_ + 4),
+                dict(res=E_ + 8, ldr=32)):
+        assert lin(**bad) == EALIGN, bad
+    assert lin(wsb=255) == ENOMEM
+    assert b"workspace" in lib.rvq_last_error()
+
+
+GAT = dict(x=A, ldx=64, wg=B, wu=B + 0x10000, ldw=64, bg=None, bu=None, dt=BF16, n=4, rows=32,
+           cols=64, act=2, out=C, ldo=32, pre=None, ws=D, wsb=1 << 20, st=None)
+
+
+def test_gated_refusals():
+    def gat(**kw):
+        return lib.moe_gated_linear(*{**GAT, **kw}.values())
+
+    for bad in (dict(n=0), dict(rows=4), dict(cols=4), dict(dt=F32), dict(act=9), dict(x=None),
+                dict(wg=None), dict(wu=None), dict(out=None), dict(ldw=60), dict(ldo=16),
+                dict(out=A), dict(out=B), dict(out=B + 0x10000), dict(pre=C), dict(ws=None)):
+        assert gat(**bad) == EINVAL, bad
+    for bad in (dict(x=A + 2), dict(wu=B + 8), dict(out=C + 8), dict(bg=E_ + 8), dict(bu=E_ + 8),
+                dict(pre=E_ + 8)):
+        assert gat(**bad) == EALIGN, bad
+    assert gat(wsb=0) == ENOMEM
+
+
+def test_backward_refusals():
+    base = dict(do=A, ldd=32, x=B, ldx=64, w=C, ldw=64, pre=D, dt=BF16, n=4, rows=32, cols=64,
+                act=2, alpha=1.0, dx=E_, lddx=64, dw=F, lddw=64, db=None, ws=F + 0x10000000,
+                wsb=1 << 20, st=None)
+
+    def back(**kw):
+        return lib.moe_linear_backward(*{**base, **kw}.values())
+
+    for bad in (dict(do=None), dict(pre=None), dict(dx=None, dw=None), dict(x=None), dict(w=None),
+                dict(lddx=32), dict(lddw=65), dict(dx=A), dict(dx=C), dict(dw=B), dict(dx=B),
+                dict(dw=A), dict(n=0), dict(dt=F32), dict(ws=None)):
+        assert back(**bad) == EINVAL, bad
+    for bad in (dict(do=A + 2), dict(dx=E_ + 8), dict(dw=F + 8), dict(db=A + 4), dict(pre=D + 4)):
+        assert back(**bad) == EALIGN, bad
+    assert back(wsb=rvq.moe_linear_workspace_bytes(4, 32, 64, True) - 1) == ENOMEM
+    gb = dict(do=A, ldd=32, x=B, ldx=64, wg=C, wu=C + 0x10000, ldw=64, pre=D, dt=BF16, n=4,
+              rows=32, cols=64, act=2, dx=E_, lddx=64, dwg=F, dwu=F + 0x10000, lddw=64, dbg=None,
+              dbu=None, ws=F + 0x10000000, wsb=1 << 20, st=None)
+
+    def gback(**kw):
+        return lib.moe_gated_linear_backward(*{**gb, **kw}.values())
+
+    for bad in (dict(do=None), dict(pre=None), dict(dwu=None), dict(dwg=None), dict(dwu=F),
+                dict(dx=None, dwg=None, dwu=None), dict(wu=None), dict(dx=C), dict(dwg=B),
+                dict(dx=B), dict(lddw=60)):
+        assert gback(**bad) == EINVAL, bad
+    assert gback(wsb=rvq.moe_gated_linear_workspace_bytes(4, 32, 64, True) - 1) == ENOMEM
+
+
+def test_join_refusals():
+    base = dict(h=A, hdt=F32, y=B, ydt=BF16, n=4, d=64, alpha=1.0, gate=None, kind=0, gdt=F32,
+                post=1, wpost=None, wpre=None, wdt=F32, eps=1e-6, ho=C, xn=D, xdt=BF16, rstd=None,
+                st=None)
+
+    def join(**kw):
+        return lib.moe_norm_join(*{**base, **kw}.values())
+
+    for bad in (dict(n=0), dict(d=60), dict(d=16392), dict(hdt=3), dict(ydt=-1), dict(gdt=4),
+                dict(wdt=9), dict(xdt=3), dict(y=None), dict(kind=2), dict(gate=E_, kind=0),
+                dict(gate=E_, kind=5), dict(post=0, wpost=E_), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(ho=None, xn=None), dict(ho=B), dict(xn=A),
+                dict(xn=C), dict(ho=A + 16), dict(xn=B + 32)):
+        assert join(**bad) == EINVAL, bad
+    for bad in (dict(h=A + 4), dict(y=B + 2), dict(gate=E_ + 2, kind=3), dict(wpost=E_ + 4),
+                dict(wpre=E_ + 4), dict(ho=C + 8), dict(xn=D + 8), dict(rstd=E_ + 4)):
+        assert join(**bad) == EALIGN, bad
+    bb = dict(dho=A, dxn=B, xdt=BF16, h=C, hdt=F32, y=D, ydt=BF16, n=4, d=64, alpha=1.0, gate=None,
+              kind=0, gdt=F32, post=1, wpost=None, wpre=None, wdt=F32, rstd=E_, dh=F, dy=None,
+              dgate=None, dwpost=None, dwpre=None, ws=F + 0x10000000, wsb=1 << 20, st=None)
+
+    def back(**kw):
+        return lib.moe_norm_join_backward(*{**bb, **kw}.values())
+
+    for bad in (dict(dho=None, dxn=None), dict(dh=None), dict(rstd=None), dict(dgate=F + 0x1000),
+                dict(h=None), dict(post=0, dwpost=F + 0x1000), dict(dxn=None, dwpre=F + 0x1000),
+                dict(dh=B), dict(dy=A), dict(dy=F), dict(ws=None), dict(n=0)):
+        assert back(**bad) == EINVAL, bad
+    assert back(dh=F + 4) == EALIGN and back(rstd=E_ + 4) == EALIGN
+    assert back(wsb=512) == ENOMEM
+
+
+def test_other_calls_still_refuse_fp16():
+    """RVQ_F16 is the dense operators' own type code."""
+    assert lib.rvq_lut_build(A, A, F16, 1, 16, B, None) == EINVAL
+    assert lib.moe_router_logits(A, None, A, F16, 1, 64, 512, B, None) == EINVAL
+    assert lib.moe_rms_norm(A, F16, 1, 64, ctypes.c_float(1e-6), B, F32, None) == EINVAL
+    assert lib.moe_combine(A, A, 2, 2, 8, A, F16, B, None) == EINVAL
+
+
+def test_binding_refusals():
+    """Shapes, types and layouts the binding can see are refused there."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = torch.zeros(32, 64, dtype=torch.bfloat16)
+    out = torch.zeros(4, 32, dtype=torch.bfloat16)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="shape"):
+        rvq.moe_linear(x, w, 5, 32, 64, out, ws)
+    with pytest.raises(ValueError, match="not contiguous"):
+        rvq.moe_linear(torch.zeros(64, 4, dtype=torch.bfloat16).t(), w, 4, 32, 64, out, ws)
+    with pytest.raises(TypeError, match="dtype"):
+        rvq.moe_linear(x, w.half(), 4, 32, 64, out, ws)
+    with pytest.raises(TypeError, match="unsupported"):
+        rvq.moe_linear(x, w, 4, 32, 64, out.double(), ws)
+    with pytest.raises(ValueError, match="bias"):
+        rvq.moe_linear(x, w, 4, 32, 64, out, ws, bias=torch.zeros(31, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="pitches"):
+        rvq.moe_gated_linear(x, w, torch.zeros(32, 128, dtype=torch.bfloat16)[:, :64], 4, 32, 64,
+                             out, ws)
+    y = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="broadcast"):
+        rvq.moe_norm_join(y, 4, 64, y.clone(), None, gate=torch.zeros(3, 1))
+    with pytest.raises(ValueError, match="gate"):
+        rvq.moe_norm_join(y, 4, 64, y.clone(), None, gate=torch.zeros(64, 4).t())
+    assert [rvq._gate_kind(g, 4, 64) for g in
+            (None, torch.zeros(1), torch.zeros(4, 1), torch.zeros(64), torch.zeros(1, 64),
+             torch.zeros(4, 64))] == [0, 1, 2, 3, 3, 4]
