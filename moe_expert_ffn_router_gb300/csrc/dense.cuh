@@ -77,38 +77,82 @@ __device__ __forceinline__ void st8(void *p, int dt, int64_t i, const float (&v)
 }
 
 // ------------------------------------------------------------- activations
-__device__ __forceinline__ float act_value(int act, float v) {
+// 1 / (1 + exp(-v)) from the hardware exponential and reciprocal: relative
+// error below 2^-22 + |v| 2^-23 (the argument's rounding), 0 and 1 at the ends.
+__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+// argument of the sigmoid that the tanh form of GELU multiplies v with:
+// (1 + tanh(t)) / 2 = sigmoid(2 t), t = sqrt(2/pi) (v + 0.044715 v^3)
+__device__ __forceinline__ float gelu_tanh_arg(float v) {
+    return 1.5957691216057308f * (v + 0.044715f * v * v * v);
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value_of(float v) {
+    if (ACT == MOE_ACT_RELU) return v > 0.f ? v : (v != v ? v : 0.f);
+    if (ACT == MOE_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
+    if (ACT == MOE_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    if (ACT == MOE_ACT_GELU_TANH) return __fdividef(v, 1.f + __expf(-gelu_tanh_arg(v)));
+    return v;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope_of(float v) {
+    if (ACT == MOE_ACT_RELU) return v > 0.f ? 1.f : 0.f;
+    if (ACT == MOE_ACT_SILU) {
+        const float s = sigmoid_f(v);
+        return s * (1.f + v * (1.f - s));
+    }
+    if (ACT == MOE_ACT_GELU)
+        return 0.5f * (1.f + erff(v * 0.70710678118654752f)) +
+               v * 0.39894228040143268f * __expf(-0.5f * v * v);
+    if (ACT == MOE_ACT_GELU_TANH) {
+        // beyond |v| = 16 the slope is 0 or 1 to fp32, and v * v * v may overflow
+        if (v >= 16.f) return 1.f;
+        if (v <= -16.f) return 0.f;
+        const float s = sigmoid_f(gelu_tanh_arg(v));
+        return s + v * s * (1.f - s) * 1.5957691216057308f * (1.f + 3.f * 0.044715f * v * v);
+    }
+    return 1.f;
+}
+
+// one branch per group of values, not per value
+template <int ACT, int N>
+__device__ __forceinline__ void act_values(float (&v)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = act_value_of<ACT>(v[e]);
+}
+
+template <int N>
+__device__ __forceinline__ void act_group(int act, float (&v)[N]) {
     switch (act) {
-        case MOE_ACT_RELU: return v > 0.f ? v : 0.f;
-        case MOE_ACT_SILU: return v / (1.f + expf(-v));
-        case MOE_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-        case MOE_ACT_GELU_TANH:
-            return 0.5f * v *
-                   (1.f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
-        default: return v;
+        case MOE_ACT_RELU: act_values<MOE_ACT_RELU>(v); break;
+        case MOE_ACT_SILU: act_values<MOE_ACT_SILU>(v); break;
+        case MOE_ACT_GELU: act_values<MOE_ACT_GELU>(v); break;
+        case MOE_ACT_GELU_TANH: act_values<MOE_ACT_GELU_TANH>(v); break;
+        default: break;
     }
 }
 
-__device__ __forceinline__ float act_slope(int act, float v) {
+// v -> (act(v), act'(v))
+template <int ACT, int N>
+__device__ __forceinline__ void act_both(const float (&v)[N], float (&a)[N], float (&s)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        a[e] = act_value_of<ACT>(v[e]);
+        s[e] = act_slope_of<ACT>(v[e]);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void act_group_both(int act, const float (&v)[N], float (&a)[N],
+                                               float (&s)[N]) {
     switch (act) {
-        case MOE_ACT_RELU: return v > 0.f ? 1.f : 0.f;
-        case MOE_ACT_SILU: {
-            const float s = 1.f / (1.f + expf(-v));
-            return s * (1.f + v * (1.f - s));
-        }
-        case MOE_ACT_GELU:
-            return 0.5f * (1.f + erff(v * 0.70710678118654752f)) +
-                   v * 0.39894228040143268f * expf(-0.5f * v * v);
-        case MOE_ACT_GELU_TANH: {
-            // beyond |v| = 16 the slope is 0 or 1 to fp32, and v * v * v may overflow
-            if (v >= 16.f) return 1.f;
-            if (v <= -16.f) return 0.f;
-            const float c = 0.79788456080286536f;
-            const float t = tanhf(c * (v + 0.044715f * v * v * v));
-            return 0.5f * (1.f + t) +
-                   0.5f * v * (1.f - t * t) * c * (1.f + 3.f * 0.044715f * v * v);
-        }
-        default: return 1.f;
+        case MOE_ACT_RELU: act_both<MOE_ACT_RELU>(v, a, s); break;
+        case MOE_ACT_SILU: act_both<MOE_ACT_SILU>(v, a, s); break;
+        case MOE_ACT_GELU: act_both<MOE_ACT_GELU>(v, a, s); break;
+        case MOE_ACT_GELU_TANH: act_both<MOE_ACT_GELU_TANH>(v, a, s); break;
+        default: act_both<MOE_ACT_NONE>(v, a, s); break;
     }
 }
 

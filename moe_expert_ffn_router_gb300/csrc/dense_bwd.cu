@@ -28,23 +28,25 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
             const int t = blockIdx.y * kBwdChunkRows + i * BW_LANES + lane;
             if (t >= j.n) break;
             const int64_t at = (int64_t)t * j.rows + c;
-            float g[8], d0[8], d1[8];
+            float g[8], a[8], sl[8], d0[8], d1[8];
             ld8(j.dout, j.dt, (int64_t)t * j.ldd + c, d0);
-            if (j.pre[0]) ld8(j.pre[0], RVQ_F32, at, g);
+            if (j.pre[0]) {
+                ld8(j.pre[0], RVQ_F32, at, g);
+                act_group_both(j.act, g, a, sl);
+            }
             if (j.mats == 2) {
                 float u[8];
                 ld8(j.pre[1], RVQ_F32, at, u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    d1[e] = d0[e] * act_value(j.act, g[e]);
-                    d0[e] = d0[e] * u[e] * act_slope(j.act, g[e]);
+                    d1[e] = d0[e] * a[e];
+                    d0[e] = d0[e] * u[e] * sl[e];
                     acc[1][e] += d1[e];
                 }
                 if (j.dp[1]) st8(j.dp[1], j.dt, at, d1);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    d0[e] *= j.pre[0] ? j.alpha * act_slope(j.act, g[e]) : j.alpha;
+                for (int e = 0; e < 8; ++e) d0[e] *= j.pre[0] ? j.alpha * sl[e] : j.alpha;
             }
             if (j.dp[0]) st8(j.dp[0], j.dt, at, d0);
 #pragma unroll

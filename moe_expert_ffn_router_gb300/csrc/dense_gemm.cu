@@ -49,6 +49,7 @@ struct GemmArgs {
     int mt, nt;          // output tiles (M tiles of both problems for PAIR_M)
     uint32_t idesc;
     int dt, act, rdt, odt;
+    int wide;            // rows of out (1) and pre (2) start on 32 bytes
     float alpha;
     const void *bias[2], *residual;
     int64_t ldr, ldo;
@@ -61,6 +62,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
     return r;
+}
+
+// One lane of a converged warp.  The instructions that feed the tensor cores
+// and TMA take their operands from uniform registers: behind elect.sync, in
+// code the whole warp runs, the compiler passes them directly; behind a test of
+// the lane number it loops over the lanes that might differ (measured: 126
+// cycles per MMA at any width, twice the work of a 128-column MMA).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -145,8 +157,32 @@ __device__ __forceinline__ void tile_at(const GemmArgs &g, int t, int &m, int &n
     n = r / rows;
 }
 
-// 16 (or the first 8) consecutive outputs
-__device__ __forceinline__ void store16(void *p, int dt, int64_t at, const float (&v)[16], int cols) {
+// 32 bytes of one lane: one whole sector per lane and instruction
+__device__ __forceinline__ void st32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 16 (or the first 8) consecutive outputs; `wide`: rows start on 32 bytes
+__device__ __forceinline__ void store16(void *p, int dt, int64_t at, const float (&v)[16], int cols,
+                                        bool wide) {
+    if (cols == 16 && wide) {
+        uint32_t w[8];
+        if (dt == RVQ_F32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[8 * h + e]);
+                st32(reinterpret_cast<float *>(p) + at + 8 * h, w);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pack16(dt, v[2 * e], v[2 * e + 1]);
+            st32(reinterpret_cast<uint16_t *>(p) + at, w);
+        }
+        return;
+    }
     float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -169,12 +205,6 @@ __device__ __forceinline__ void add_bias16(const void *bias, int dt, int c, int 
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[8 + e] += b[e];
     }
-}
-
-__device__ __forceinline__ void act16(int act, float (&v)[16]) {
-    if (act == MOE_ACT_NONE) return;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = act_value(act, v[e]);
 }
 
 template <bool GATED>
@@ -219,7 +249,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tslot;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // producer: this CTA's rows of A and of B for every slice
         const int bboxes = g.b_t ? (g.half + 63) / 64 : 1;
         const uint32_t bytes = DG_ABYTES + (g.b_t ? bboxes * 8192 : g.half * 128);
@@ -244,20 +274,25 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                 const CUtensorMap *tb = (GATED ? rank == 1 : k2) ? &mb1 : &mb0;
                 const uint32_t st = smem_u32(smem + s * DG_STAGE), sb = st + DG_ABYTES;
                 const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
-                if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
-                if (g.a_t) {
-                    tma_pair(st, ta, m0, kx, bar);
-                    tma_pair(st + 8192, ta, m0 + 64, kx, bar);
-                } else {
-                    tma_pair(st, ta, kx, m0, bar);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+                    if (g.a_t) {
+                        tma_pair(st, ta, m0, kx, bar);
+                        tma_pair(st + 8192, ta, m0 + 64, kx, bar);
+                    } else {
+                        tma_pair(st, ta, kx, m0, bar);
+                    }
+                    if (g.b_t) {
+                        tma_pair(sb, tb, n0, kx, bar);
+                        if (bboxes > 1) tma_pair(sb + 8192, tb, n0 + 64, kx, bar);
+                    } else {
+                        tma_pair(sb, tb, kx, n0, bar);
+                    }
                 }
-                if (g.b_t)
-                    for (int b = 0; b < bboxes; ++b) tma_pair(sb + b * 8192, tb, n0 + 64 * b, kx, bar);
-                else
-                    tma_pair(sb, tb, kx, n0, bar);
+                __syncwarp();
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // issuer: four 16-deep MMAs per slice
         const uint32_t da = g.a_t ? 2048u >> 4 : 2u, db = g.b_t ? 2048u >> 4 : 2u;
         int it = 0, done = 0;
@@ -279,12 +314,16 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                 const uint32_t st = smem_u32(smem + s * DG_STAGE);
                 const uint64_t a = operand_desc(st, g.a_t),
                                b = operand_desc(st + DG_ABYTES, g.b_t);
+                if (elect_one()) {
 #pragma unroll
-                for (int q = 0; q < DG_BK / 16; ++q)
-                    mma_pair(acc, a + q * da, b + q * db, g.idesc, (k > 0 || q > 0) ? 1u : 0u);
-                commit_pair(empty0 + 8 * s);
+                    for (int q = 0; q < DG_BK / 16; ++q)
+                        mma_pair(acc, a + q * da, b + q * db, g.idesc, (k > 0 || q > 0) ? 1u : 0u);
+                    commit_pair(empty0 + 8 * s);
+                }
+                __syncwarp();
             }
-            commit_pair(accfull0 + 8 * buf);
+            if (elect_one()) commit_pair(accfull0 + 8 * buf);
+            __syncwarp();
         }
     } else if (warp >= 4) {
         // epilogue: lanes 32 q .. 32 q + 31 of the accumulator, every other
@@ -315,14 +354,16 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r0[e]);
                     add_bias16(g.bias[0], g.dt, c, cols, v);
-                    if (g.pre[0]) store16(g.pre[0], RVQ_F32, (int64_t)row * g.N + c, v, cols);
-                    act16(g.act, v);
+                    if (g.pre[0]) store16(g.pre[0], RVQ_F32, (int64_t)row * g.N + c, v, cols,
+                                              g.wide & 2);
+                    act_group(g.act, v);
                     if (GATED) {
                         float w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(r1[e]);
                         add_bias16(g.bias[1], g.dt, c, cols, w);
-                        if (g.pre[1]) store16(g.pre[1], RVQ_F32, (int64_t)row * g.N + c, w, cols);
+                        if (g.pre[1]) store16(g.pre[1], RVQ_F32, (int64_t)row * g.N + c, w, cols,
+                                                  g.wide & 2);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] *= w[e];
                     } else {
@@ -333,7 +374,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                                               : nullptr,
                                    g.rdt, c, cols, v);
                     }
-                    store16(out, g.odt, (int64_t)row * g.ldo + c, v, cols);
+                    store16(out, g.odt, (int64_t)row * g.ldo + c, v, cols, g.wide & 1);
                 }
                 __syncwarp();
             }
@@ -455,6 +496,11 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
         g.pre[i] = job.pre[i];
     }
     g.status = job.status;
+    const int64_t oe = job.odt == RVQ_F32 ? 4 : 2;
+    const uintptr_t outs = (uintptr_t)job.out[0] | (uintptr_t)job.out[1] |
+                           (uintptr_t)(job.ldo * oe) | (uintptr_t)(per * oe);
+    const uintptr_t pres = (uintptr_t)job.pre[0] | (uintptr_t)job.pre[1] | (uintptr_t)(per * 4);
+    g.wide = ((outs & 31) == 0 ? 1 : 0) | ((pres & 31) == 0 ? 2 : 0);
     CUtensorMap ma[2], mb[2];
     for (int i = 0; i < 2; ++i) {
         if (i == 1 && job.a[1] == nullptr)
