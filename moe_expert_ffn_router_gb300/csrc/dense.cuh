@@ -188,6 +188,11 @@ struct DenseJob {
     uint32_t *status;
 };
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream);
+// the same for few tokens (PLAIN and GATED, nothing transposed): the weights
+// streamed past the batch (dense_stream.cu)
+constexpr int kStreamMaxTokens = 256;
+bool dense_stream_fits(const DenseJob &job);
+rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream);
 
 // Gradient of the gated product (mats = 2) or of an activation (mats = 1):
 //   mats 2: dp0 = dout * pre1 * act'(pre0), dp1 = dout * act(pre0)

@@ -20,12 +20,9 @@
 //    and act(g) * u is formed in registers.
 // Rows, columns and depth past the ends are zero-filled by TMA and not stored.
 // Each output is rounded once, from fp32.  Every wait is bounded (1 s).
-#include "dense.cuh"
-#include "tc_util.cuh"
+#include "dense_tc.cuh"
 
-#include <cuda.h>
 #include <cudaTypedefs.h>
-#include <string.h>
 
 namespace rvq {
 namespace {
@@ -58,35 +55,6 @@ struct GemmArgs {
     uint32_t *status;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// One lane of a converged warp.  The instructions that feed the tensor cores
-// and TMA take their operands from uniform registers: behind elect.sync, in
-// code the whole warp runs, the compiler passes them directly; behind a test of
-// the lane number it loops over the lanes that might differ (measured: 126
-// cycles per MMA at any width, twice the work of a 128-column MMA).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// address of the same shared variable in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t a, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    return r;
-}
-
 __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
                  : "memory");
@@ -118,33 +86,6 @@ __device__ __forceinline__ void commit_pair(uint32_t mbar) {
         " [%0], %1;" ::"r"(mbar),
         "h"((uint16_t)3)
         : "memory");
-}
-
-// Shared-memory descriptor, 128-byte swizzle.  K-major: 8-row groups 1024 bytes
-// apart.  MN-major: 64 rows x 8 deep per 1024 bytes; the next 8 deep follow at
-// 1024 bytes (stride offset), the next 64 rows at 8192 (leading offset).
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int t) {
-    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(t ? 8192u >> 4 : 1u) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
-}
-
-// 16 columns of this warp's 32 TMEM lanes; the values are there after tmem_wait()
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_wait() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // output tile t -> (m tile, n tile): groups of DG_GROUP M tiles, N inside
@@ -263,7 +204,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
             const int n0 = GATED ? n * g.half : n * g.tile_n + (int)rank * g.half;
             for (int k = 0; k < slices; ++k, ++it) {
                 const int s = it % DG_ST;
-                if (it >= DG_ST && !mbar_wait(empty0 + 8 * s, ((it / DG_ST) - 1) & 1, abort_flag,
+                if (it >= DG_ST && !warp_wait(empty0 + 8 * s, ((it / DG_ST) - 1) & 1, abort_flag,
                                               g.status)) {
                     ok = false;
                     break;
@@ -299,14 +240,14 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, ++done) {
             const int buf = done & 1;
-            if (done >= 2 && !mbar_wait_spin(accempty0 + 8 * buf, ((done >> 1) - 1) & 1, abort_flag,
+            if (done >= 2 && !warp_wait_spin(accempty0 + 8 * buf, ((done >> 1) - 1) & 1, abort_flag,
                                              g.status))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC);
             for (int k = 0; k < slices; ++k, ++it) {
                 const int s = it % DG_ST;
-                if (!mbar_wait_spin(full0 + 8 * s, (it / DG_ST) & 1, abort_flag, g.status)) {
+                if (!warp_wait_spin(full0 + 8 * s, (it / DG_ST) & 1, abort_flag, g.status)) {
                     ok = false;
                     break;
                 }
@@ -337,9 +278,8 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
             const bool second = m >= mt1;
             const int row = (second ? m - mt1 : m) * 2 * DG_BM + (int)rank * DG_BM + 32 * q + lane;
             const int buf = done & 1;
-            if (!mbar_wait(accfull0 + 8 * buf, (done >> 1) & 1, abort_flag, g.status)) break;
+            if (!warp_wait(accfull0 + 8 * buf, (done >> 1) & 1, abort_flag, g.status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (*abort_flag) break;
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC) + ((uint32_t)(32 * q) << 16);
             void *out = g.out[second ? 1 : 0];
             for (int u = par; u < units; u += 2) {
@@ -398,32 +338,6 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     }
 }
 
-// Tensor map of an operand's slices: K-major boxes of 64 deep x box_rows, or,
-// transposed, of 64 rows x 64 deep.
-rvq_status encode_operand(CUtensorMap *map, const void *p, int rows, int K, int64_t ld, int t, int dt,
-                          int box_rows) {
-    const PFN_cuTensorMapEncodeTiled_v12000 encode =
-        reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder_entry());
-    if (encode == nullptr) {
-        set_error("dense product: cuTensorMapEncodeTiled is not available");
-        return RVQ_ECUDA;
-    }
-    const cuuint64_t dims[2] = {(cuuint64_t)(t ? rows : K), (cuuint64_t)(t ? K : rows)};
-    const cuuint64_t pitch[1] = {(cuuint64_t)ld * 2u};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)(t ? 64 : box_rows)};
-    const cuuint32_t step[2] = {1u, 1u};
-    const CUresult r =
-        encode(map, dt == RVQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-               2, const_cast<void *>(p), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        set_error("dense product: cuTensorMapEncodeTiled failed (%d)", (int)r);
-        return RVQ_ECUDA;
-    }
-    return RVQ_OK;
-}
-
 // Columns of an accumulator: the width with the least (waves of CTA pairs) x
 // (time of a slice), where a slice costs its MMAs (2 tile_n cycles) or, for
 // narrow tiles, its operand fill ((128 + tile_n / 2) rows of 128 bytes at about
@@ -448,7 +362,32 @@ int choose_tile_n(const DenseJob &j, int mt, int pairs) {
 
 }  // namespace
 
+rvq_status encode_operand(CUtensorMap *map, const void *p, int rows, int K, int64_t ld, int t, int dt,
+                          int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode =
+        reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder_entry());
+    if (encode == nullptr) {
+        set_error("dense product: cuTensorMapEncodeTiled is not available");
+        return RVQ_ECUDA;
+    }
+    const cuuint64_t dims[2] = {(cuuint64_t)(t ? rows : K), (cuuint64_t)(t ? K : rows)};
+    const cuuint64_t pitch[1] = {(cuuint64_t)ld * 2u};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)(t ? 64 : box_rows)};
+    const cuuint32_t step[2] = {1u, 1u};
+    const CUresult r =
+        encode(map, dt == RVQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               2, const_cast<void *>(p), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("dense product: cuTensorMapEncodeTiled failed (%d)", (int)r);
+        return RVQ_ECUDA;
+    }
+    return RVQ_OK;
+}
+
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
+    if (dense_stream_fits(job)) return launch_dense_stream(job, stream);
     static std::atomic<int> attr_done[64];  // per device; setting twice is harmless
     int dev = 0;
     RVQ_CUDA(cudaGetDevice(&dev));
