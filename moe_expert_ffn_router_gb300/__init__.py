@@ -484,11 +484,22 @@ def _dt_any(t) -> int:
         raise TypeError(f"unsupported dtype {t.dtype} (bf16, fp16 or fp32)") from None
 
 
+# The dense calls take a few microseconds on the GPU at decode sizes, so their
+# host side asks torch for as little as it can: raw stream handles, plain
+# integers, one look at each tensor's shape, strides and type.
+def _raw_stream(stream) -> int:
+    """cudaStream_t of `stream`, or of the current device's current stream
+    (the caller's CUDA tensors have initialised torch's CUDA state)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
 def _mat(t, rows, cols, what, dtype=None) -> int:
     """Row pitch of a [rows][cols] matrix; columns must be contiguous."""
     if t is None:
         return 0
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
@@ -523,9 +534,10 @@ def moe_linear(x, w, n, rows, cols, out, ws, bias=None, act=MOE_ACT_NONE, alpha=
     _vec(bias, rows, "bias", x.dtype)
     _vec(pre, n * rows, "pre", torch.float32)
     _check("moe_linear",
-           _lib.moe_linear(_p(x), ldx, _p(w), ldw, _p(bias), _dt_any(x), n, rows, cols, act, alpha,
-                           _p(residual), _dt_any(residual), ldr, _p(out), _dt_any(out), ldo,
-                           _p(pre), _p(ws), _nbytes(ws), _stream(stream)))
+           _lib.moe_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, _p(bias), _dt_any(x), n, rows,
+                           cols, act, alpha, _p(residual), _dt_any(residual), ldr, out.data_ptr(),
+                           _dt_any(out), ldo, _p(pre), ws.data_ptr(), ws.nbytes,
+                           _raw_stream(stream)))
 
 
 def moe_linear_backward(dout, x, w, n, rows, cols, ws, dx=None, dw=None, dbias=None, pre=None,
@@ -539,9 +551,10 @@ def moe_linear_backward(dout, x, w, n, rows, cols, ws, dx=None, dw=None, dbias=N
     _vec(dbias, rows, "dbias", dt)
     _vec(pre, n * rows, "pre", torch.float32)
     _check("moe_linear_backward",
-           _lib.moe_linear_backward(_p(dout), ldd, _p(x), ldx, _p(w), ldw, _p(pre), _dt_any(dout),
-                                    n, rows, cols, act, alpha, _p(dx), lddx, _p(dw), lddw,
-                                    _p(dbias), _p(ws), _nbytes(ws), _stream(stream)))
+           _lib.moe_linear_backward(dout.data_ptr(), ldd, _p(x), ldx, _p(w), ldw, _p(pre),
+                                    _dt_any(dout), n, rows, cols, act, alpha, _p(dx), lddx,
+                                    _p(dw), lddw,
+                                    _p(dbias), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 def moe_gated_linear_workspace_bytes(n, rows, cols, backward=False) -> int:
@@ -562,9 +575,9 @@ def moe_gated_linear(x, wg, wu, n, rows, cols, out, ws, bg=None, bu=None, act=MO
     _vec(bu, rows, "bu", dt)
     _vec(pre, 2 * n * rows, "pre", torch.float32)
     _check("moe_gated_linear",
-           _lib.moe_gated_linear(_p(x), ldx, _p(wg), _p(wu), ldw, _p(bg), _p(bu), _dt_any(x), n,
-                                 rows, cols, act, _p(out), ldo, _p(pre), _p(ws), _nbytes(ws),
-                                 _stream(stream)))
+           _lib.moe_gated_linear(x.data_ptr(), ldx, wg.data_ptr(), wu.data_ptr(), ldw, _p(bg),
+                                 _p(bu), _dt_any(x), n, rows, cols, act, out.data_ptr(), ldo,
+                                 _p(pre), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 def moe_gated_linear_backward(dout, x, wg, wu, pre, n, rows, cols, ws, dx=None, dwg=None, dwu=None,
@@ -583,10 +596,10 @@ def moe_gated_linear_backward(dout, x, wg, wu, pre, n, rows, cols, ws, dx=None, 
     _vec(dbu, rows, "dbu", dt)
     _vec(pre, 2 * n * rows, "pre", torch.float32)
     _check("moe_gated_linear_backward",
-           _lib.moe_gated_linear_backward(_p(dout), ldd, _p(x), ldx, _p(wg), _p(wu), ldw, _p(pre),
-                                          _dt_any(dout), n, rows, cols, act, _p(dx), lddx, _p(dwg),
-                                          _p(dwu), lddw, _p(dbg), _p(dbu), _p(ws), _nbytes(ws),
-                                          _stream(stream)))
+           _lib.moe_gated_linear_backward(dout.data_ptr(), ldd, _p(x), ldx, _p(wg), _p(wu), ldw,
+                                          _p(pre), _dt_any(dout), n, rows, cols, act, _p(dx), lddx, _p(dwg),
+                                          _p(dwu), lddw, _p(dbg), _p(dbu), ws.data_ptr(), ws.nbytes,
+                                          _raw_stream(stream)))
 
 
 def _gate_kind(gate, n, d) -> int:
@@ -621,11 +634,11 @@ def moe_norm_join(y, n, d, h_out, xn, h=None, alpha=1.0, gate=None, post_norm=Tr
     _vec(w_pre, d, "w_pre", None if w_post is None else w_post.dtype)
     _vec(rstd, 2 * n, "rstd", torch.float32)
     _check("moe_norm_join",
-           _lib.moe_norm_join(_p(h), _dt_any(h if h is not None else h_out), _p(y), _dt_any(y), n,
-                              d, alpha, _p(gate), _gate_kind(gate, n, d), _dt_any(gate),
+           _lib.moe_norm_join(_p(h), _dt_any(h if h is not None else h_out), y.data_ptr(),
+                              _dt_any(y), n, d, alpha, _p(gate), _gate_kind(gate, n, d), _dt_any(gate),
                               int(post_norm), _p(w_post), _p(w_pre),
                               _dt_any(w_post if w_post is not None else w_pre), eps, _p(h_out),
-                              _p(xn), _dt_any(xn), _p(rstd), _stream(stream)))
+                              _p(xn), _dt_any(xn), _p(rstd), _raw_stream(stream)))
 
 
 def moe_norm_join_workspace_bytes(n, d) -> int:
@@ -652,11 +665,11 @@ def moe_norm_join_backward(dh_out, dxn, y, n, d, rstd, ws, h=None, alpha=1.0, ga
         _vec(dgate, gate.numel(), "dgate", gate.dtype)
     _check("moe_norm_join_backward",
            _lib.moe_norm_join_backward(_p(dh_out), _p(dxn), _dt_any(dxn), _p(h), _DTYPES[hdt],
-                                       _p(y), _dt_any(y), n, d, alpha, _p(gate),
+                                       y.data_ptr(), _dt_any(y), n, d, alpha, _p(gate),
                                        _gate_kind(gate, n, d), _dt_any(gate), int(post_norm),
                                        _p(w_post), _p(w_pre), _DTYPES[wdt], _p(rstd), _p(dh),
-                                       _p(dy), _p(dgate), _p(dw_post), _p(dw_pre), _p(ws),
-                                       _nbytes(ws), _stream(stream)))
+                                       _p(dy), _p(dgate), _p(dw_post), _p(dw_pre), ws.data_ptr(),
+                                       ws.nbytes, _raw_stream(stream)))
 
 
 def rvq_ws_clear(ws, stream=None):

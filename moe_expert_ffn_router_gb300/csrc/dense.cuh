@@ -76,6 +76,27 @@ __device__ __forceinline__ void st8(void *p, int dt, int64_t i, const float (&v)
     }
 }
 
+// four consecutive elements at a place that is a multiple of four
+__device__ __forceinline__ void ld4(const void *p, int dt, int64_t i, float (&v)[4]) {
+    if (dt == RVQ_F32) {
+        const float4 q = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i);
+        unpack16(dt, q.x, v[0], v[1]);
+        unpack16(dt, q.y, v[2], v[3]);
+    }
+}
+
+__device__ __forceinline__ void st4(void *p, int dt, int64_t i, const float (&v)[4]) {
+    if (dt == RVQ_F32)
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i) =
+            make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + i) =
+            make_uint2(pack16(dt, v[0], v[1]), pack16(dt, v[2], v[3]));
+}
+
 // ------------------------------------------------------------- activations
 // 1 / (1 + exp(-v)) from the hardware exponential and reciprocal: relative
 // error below 2^-22 + |v| 2^-23 (the argument's rounding), 0 and 1 at the ends.
@@ -209,6 +230,7 @@ struct DenseBwdJob {
     void *dp[2];
     void *dbias[2];
     float *part;
+    int wide;               // pre starts on 32 bytes (rows are multiples of eight)
 };
 constexpr int kBwdChunkRows = 32;  // rows per partial of a bias gradient
 inline int dense_bwd_chunks(int n) { return (n + kBwdChunkRows - 1) / kBwdChunkRows; }
@@ -228,10 +250,10 @@ struct JoinJob {
     const void *dh_out, *dxn;
     void *dh, *dy, *dgate, *dw_post, *dw_pre;
     float *part;            // [slots][3][d] column sums, then [slots] scalar sums
-    int slots;
+    int slots;              // blocks of the gradient kernel
 };
 constexpr int kJoinMaxD = 16384;
-int join_bwd_slots(int n, int d);
+int join_bwd_slots(int n);  // at most, for the workspace
 rvq_status launch_norm_join(const JoinJob &job, cudaStream_t stream);
 rvq_status launch_norm_join_bwd(const JoinJob &job, cudaStream_t stream);
 

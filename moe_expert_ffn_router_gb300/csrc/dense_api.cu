@@ -391,8 +391,9 @@ static rvq_status check_join(const char *who, const void *h, rvq_dtype hdt, cons
                              rvq_dtype ydt, int32_t n, int32_t d, const void *gate, int kind,
                              rvq_dtype gdt, int32_t post_norm, const void *w_post,
                              const void *w_pre, rvq_dtype wdt, rvq_dtype xdt) {
-    CHECK_ARG(n >= 1 && d >= 8 && d % 8 == 0 && d <= kJoinMaxD,
-              "%s: n %d, d %d (n >= 1; d a multiple of 8, at most %d)", who, n, d, kJoinMaxD);
+    CHECK_ARG(n >= 1 && n <= kMaxDim && d >= 8 && d % 8 == 0 && d <= kJoinMaxD,
+              "%s: n %d, d %d (n from 1 to 2^24; d a multiple of 8, at most %d)", who, n, d,
+              kJoinMaxD);
     CHECK_ARG(dtype_any(hdt) && dtype_any(ydt) && dtype_any(gdt) && dtype_any(wdt) &&
                   dtype_any(xdt),
               "%s: dtypes %d, %d, %d, %d, %d", who, (int)hdt, (int)ydt, (int)gdt, (int)wdt,
@@ -462,11 +463,11 @@ rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rv
 }
 
 static size_t join_part_bytes(int32_t n, int32_t d) {
-    return (size_t)join_bwd_slots(n, d) * ((size_t)3 * d + 1) * 4;
+    return (size_t)join_bwd_slots(n) * ((size_t)3 * d + 1) * 4;
 }
 
 size_t moe_norm_join_workspace_bytes(int32_t n, int32_t d) {
-    if (n < 1 || d < 8 || d % 8 != 0 || d > kJoinMaxD) return 0;
+    if (n < 1 || n > kMaxDim || d < 8 || d % 8 != 0 || d > kJoinMaxD) return 0;
     return up256(RVQ_WS_STATUS_BYTES + join_part_bytes(n, d));
 }
 
@@ -528,7 +529,7 @@ rvq_status moe_norm_join_backward(const void *dh_out_dev, const void *dxn_dev, r
     j.dw_post = dw_post_dev;
     j.dw_pre = dw_pre_dev;
     j.part = (float *)((uint8_t *)ws_dev + RVQ_WS_STATUS_BYTES);
-    j.slots = join_bwd_slots(n, d);
+    j.slots = join_bwd_slots(n);
     return launch_norm_join_bwd(j, (cudaStream_t)stream);
 }
 

@@ -15,6 +15,18 @@ namespace {
 constexpr int BW_LANES = 8;
 static_assert(kBwdChunkRows % BW_LANES == 0, "rows of a chunk per lane");
 
+// eight fp32 values; `wide`: at a multiple of 32 bytes, one load per lane
+__device__ __forceinline__ void ld32(const float *p, int wide, float (&v)[8]) {
+    if (wide) {
+        asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                       "=f"(v[6]), "=f"(v[7])
+                     : "l"(p));
+    } else {
+        ld8(p, RVQ_F32, 0, v);
+    }
+}
+
 __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
     __shared__ float red[BW_LANES][2][264];
     const int q = threadIdx.x & 31, lane = threadIdx.x >> 5;
@@ -23,32 +35,45 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
     const bool sums = j.dbias[0] || j.dbias[1];
     float acc[2][8] = {};
     if (on) {
+        // every load of the block's rows is issued before the first is used
+        constexpr int R = kBwdChunkRows / BW_LANES;
+        uint4 d_raw[R];
+        float g[R][8], u[R][8];
+        int64_t at[R];
+        bool ok[R];
 #pragma unroll
-        for (int i = 0; i < kBwdChunkRows / BW_LANES; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int t = blockIdx.y * kBwdChunkRows + i * BW_LANES + lane;
-            if (t >= j.n) break;
-            const int64_t at = (int64_t)t * j.rows + c;
-            float g[8], a[8], sl[8], d0[8], d1[8];
-            ld8(j.dout, j.dt, (int64_t)t * j.ldd + c, d0);
-            if (j.pre[0]) {
-                ld8(j.pre[0], RVQ_F32, at, g);
-                act_group_both(j.act, g, a, sl);
-            }
+            ok[i] = t < j.n;
+            at[i] = (int64_t)t * j.rows + c;
+            if (!ok[i]) continue;
+            d_raw[i] = __ldg(reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const uint16_t *>(j.dout) + (int64_t)t * j.ldd + c));
+            if (j.pre[0]) ld32(j.pre[0] + at[i], j.wide, g[i]);
+            if (j.mats == 2) ld32(j.pre[1] + at[i], j.wide, u[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (!ok[i]) continue;
+            float a[8], sl[8], d0[8], d1[8];
+            unpack16(j.dt, d_raw[i].x, d0[0], d0[1]);
+            unpack16(j.dt, d_raw[i].y, d0[2], d0[3]);
+            unpack16(j.dt, d_raw[i].z, d0[4], d0[5]);
+            unpack16(j.dt, d_raw[i].w, d0[6], d0[7]);
+            if (j.pre[0]) act_group_both(j.act, g[i], a, sl);
             if (j.mats == 2) {
-                float u[8];
-                ld8(j.pre[1], RVQ_F32, at, u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     d1[e] = d0[e] * a[e];
-                    d0[e] = d0[e] * u[e] * sl[e];
+                    d0[e] = d0[e] * u[i][e] * sl[e];
                     acc[1][e] += d1[e];
                 }
-                if (j.dp[1]) st8(j.dp[1], j.dt, at, d1);
+                if (j.dp[1]) st8(j.dp[1], j.dt, at[i], d1);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d0[e] *= j.pre[0] ? j.alpha * sl[e] : j.alpha;
             }
-            if (j.dp[0]) st8(j.dp[0], j.dt, at, d0);
+            if (j.dp[0]) st8(j.dp[0], j.dt, at[i], d0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[0][e] += d0[e];
         }
@@ -69,12 +94,23 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
     }
 }
 
-__global__ void __launch_bounds__(256) dense_bias_sum_kernel(const DenseBwdJob j, int chunks) {
-    const int col = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
-    if (col >= j.rows || j.dbias[m] == nullptr) return;
+// Adds the chunks' partials: 32 columns x 32 lanes, a lane's chunks in order,
+// then the lanes in order.
+__global__ void __launch_bounds__(1024) dense_bias_sum_kernel(const DenseBwdJob j, int chunks) {
+    __shared__ float red[32][33];
+    const int q = threadIdx.x & 31, lane = threadIdx.x >> 5, m = blockIdx.y;
+    const int col = blockIdx.x * 32 + q;
+    if (j.dbias[m] == nullptr) return;
     float s = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < chunks; ++k) s += j.part[((int64_t)k * j.mats + m) * j.rows + col];
+    if (col < j.rows)
+#pragma unroll 4
+        for (int k = lane; k < chunks; k += 32) s += j.part[((int64_t)k * j.mats + m) * j.rows + col];
+    red[lane][q] = s;
+    __syncthreads();
+    if (lane != 0 || col >= j.rows) return;
+    s = 0.f;
+#pragma unroll
+    for (int l = 0; l < 32; ++l) s += red[l][q];
     st_elem(j.dbias[m], j.dt, col, s);
 }
 
@@ -87,10 +123,12 @@ rvq_status launch_dense_bwd(const DenseBwdJob &job, cudaStream_t stream) {
         return RVQ_ENOTIMPL;
     }
     const dim3 grid((unsigned)((job.rows + 255) / 256), (unsigned)chunks);
-    dense_bwd_kernel<<<grid, 256, 0, stream>>>(job);
+    DenseBwdJob j = job;
+    j.wide = (((uintptr_t)job.pre[0] | (uintptr_t)job.pre[1]) & 31) == 0;
+    dense_bwd_kernel<<<grid, 256, 0, stream>>>(j);
     RVQ_LAUNCHED("dense_bwd");
     if (job.dbias[0] || job.dbias[1]) {
-        dense_bias_sum_kernel<<<dim3((unsigned)((job.rows + 255) / 256), (unsigned)job.mats), 256, 0,
+        dense_bias_sum_kernel<<<dim3((unsigned)((job.rows + 31) / 32), (unsigned)job.mats), 1024, 0,
                                 stream>>>(job, chunks);
         RVQ_LAUNCHED("dense_bias_sum");
     }

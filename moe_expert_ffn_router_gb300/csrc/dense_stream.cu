@@ -68,27 +68,6 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     return v;
 }
 
-// four consecutive elements at a place that is a multiple of four
-__device__ __forceinline__ void ld4(const void *p, int dt, int64_t i, float (&v)[4]) {
-    if (dt == RVQ_F32) {
-        const float4 q = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
-        const uint2 q = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i);
-        unpack16(dt, q.x, v[0], v[1]);
-        unpack16(dt, q.y, v[2], v[3]);
-    }
-}
-
-__device__ __forceinline__ void st4(void *p, int dt, int64_t i, const float (&v)[4]) {
-    if (dt == RVQ_F32)
-        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i) =
-            make_float4(v[0], v[1], v[2], v[3]);
-    else
-        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + i) =
-            make_uint2(pack16(dt, v[0], v[1]), pack16(dt, v[2], v[3]));
-}
-
 template <bool GATED>
 __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
     const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
