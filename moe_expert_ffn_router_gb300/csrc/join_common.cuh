@@ -68,72 +68,31 @@ __device__ __forceinline__ void widen4(uint2 r, int dt, float (&v)[4]) {
     unpack16(dt, r.y, v[2], v[3]);
 }
 
-// four values at element i of a row in shared memory (byte address `at`); zeros
-// when off
+// four values at element i of a row in shared memory (byte address `at`)
 template <int DT>
-__device__ __forceinline__ void lds4(uint32_t at, int i, bool on, int dt, float (&v)[4]) {
+__device__ __forceinline__ void lds4(uint32_t at, int i, int dt, float (&v)[4]) {
     const int t = type_of<DT>(dt);
     if (t == RVQ_F32) {
-        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\nmov.f32 %0, 0f00000000;\nmov.f32 %1, "
-            "0f00000000;\nmov.f32 %2, 0f00000000;\nmov.f32 %3, 0f00000000;\n@p ld.shared.v4.f32 "
-            "{%0, %1, %2, %3}, [%4];\n}\n"
-            : "=&f"(v[0]), "=&f"(v[1]), "=&f"(v[2]), "=&f"(v[3])
-            : "r"(at + i * 4), "r"((int)on)
-            : "memory");
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "r"(at + i * 4)
+                     : "memory");
     } else {
         uint2 r;
-        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %3, 0;\nmov.b32 %0, 0;\nmov.b32 %1, 0;\n@p "
-            "ld.shared.v2.b32 {%0, %1}, [%2];\n}\n"
-            : "=&r"(r.x), "=&r"(r.y)
-            : "r"(at + i * 2), "r"((int)on)
-            : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(r.x), "=r"(r.y)
+                     : "r"(at + i * 2)
+                     : "memory");
         widen4(r, t, v);
     }
 }
 
-// four values in global memory; zeros when off
+// four values in global memory; `none` when off
 template <int DT>
-__device__ __forceinline__ void ldg4(const void *p, int64_t i, bool on, int dt, float (&v)[4]) {
-    const int t = type_of<DT>(dt);
-    v[0] = v[1] = v[2] = v[3] = 0.f;
-    if (on) ld4(p, t, i, v);
-}
-
-// a gain: 1 without one
-struct Gain {
-    const void *p;
-    uint32_t at;   // shared memory
-    bool have, shared;
-};
-
-template <int DT>
-__device__ __forceinline__ void gain4(const Gain &g, int i, bool on, int dt, float (&v)[4]) {
-    const int t = type_of<DT>(dt);
-    if (t == RVQ_F32) {
-        float4 r = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (g.have && on && !g.shared)
-            r = __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(g.p) + i));
-        if (g.have && on && g.shared)
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
-                         : "r"(g.at + i * 4)
-                         : "memory");
-        v[0] = r.x;
-        v[1] = r.y;
-        v[2] = r.z;
-        v[3] = r.w;
-    } else {
-        const uint32_t one = t == RVQ_BF16 ? 0x3F803F80u : 0x3C003C00u;
-        uint2 r = make_uint2(one, one);
-        if (g.have && on && !g.shared)
-            r = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(g.p) + i));
-        if (g.have && on && g.shared)
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(r.x), "=r"(r.y)
-                         : "r"(g.at + i * 2)
-                         : "memory");
-        widen4(r, t, v);
-    }
+__device__ __forceinline__ void ldg4(const void *p, int64_t i, bool on, int dt, float none,
+                                     float (&v)[4]) {
+    v[0] = v[1] = v[2] = v[3] = none;
+    if (on) ld4(p, type_of<DT>(dt), i, v);
 }
 
 template <int DT>
@@ -143,13 +102,16 @@ __device__ __forceinline__ void put4(void *p, int64_t i, bool on, int dt, const 
 
 // ------------------------------------------------------------ the ring of rows
 
-// Where a walking block keeps things in shared memory (bytes; rows and vectors
-// are multiples of 16 bytes since d % 8 == 0).
+// Where a walking block keeps things in shared memory (bytes).  Every row and
+// vector is `pad` columns long, the block's threads times their columns; what
+// lies past d is zero, so inner loops need no test of the column.
 struct JoinSmem {
+    int pad;
     int y, h, dh, dx, gate, row;  // places in a ring slot; a slot's size
     int stages;                   // ring depth (0: rows are read from global memory)
-    int chan;                     // after the ring: a channel gate
-    int w_post, w_pre;            // gains; -1: read from global memory
+    int zero;                     // after the ring: a row of zeros for absent tensors
+    int chan;                     // a channel gate
+    int w_post, w_pre;            // gains (1 for absent ones); -1: read from global memory
     int total;
 };
 
@@ -176,44 +138,77 @@ __device__ __forceinline__ void wait_row(int stages) {
         cp_wait<1>();
 }
 
-// four values of a row: in the ring, or (kAny instances without a ring) global
+// four values of a row: in the ring (or the row of zeros), or, for kAny
+// instances without a ring, in global memory
 template <int DT>
-__device__ __forceinline__ void row4(int stages, uint32_t at, const void *p, int64_t row, int i,
-                                     bool on, int dt, float (&v)[4]) {
+__device__ __forceinline__ void row4(int stages, uint32_t at, const void *p, int64_t row, int i, int d,
+                                     int dt, float (&v)[4]) {
     if (DT == kAny && stages == 0)
-        ldg4<DT>(p, row + i, on, dt, v);
+        ldg4<DT>(p, row + i, p != nullptr && i < d, dt, 0.f, v);
     else
-        lds4<DT>(at, i, on, dt, v);
+        lds4<DT>(at, i, dt, v);
 }
 
-__device__ __forceinline__ Gain keep_gain(uint8_t *smem, int at, const void *src, int dt, int d) {
-    Gain g;
-    g.p = src;
-    g.at = 0;
-    g.have = src != nullptr;
-    g.shared = at >= 0;
-    if (g.have && g.shared) {
-        const int n16 = d * esize(dt) / 16;
+// four gains: in shared memory (SHARED 1), in global memory (0), or as `at` says
+template <int DT, int SHARED>
+__device__ __forceinline__ void gain4(int at, uint32_t base, const void *p, int i, int d, int dt,
+                                      float (&v)[4]) {
+    if (SHARED == 1 || (SHARED == kAny && at >= 0))
+        lds4<DT>(base + at, i, dt, v);
+    else
+        ldg4<DT>(p, i, p != nullptr && i < d, dt, 1.f, v);
+}
+
+// Zeros past the rows' ends (and the row of zeros), gains, a channel gate; none of
+// it is written by the copies of rows, which are in flight already.
+__device__ __forceinline__ void fill_smem(uint8_t *smem, const JoinJob &j, const JoinSmem &L,
+                                          bool bwd) {
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const auto pad = [&](int at, int dt) {
+        const int e = esize(dt), n16 = (L.pad - j.d) * e / 16;  // d and pad are multiples of 8
         for (int i = threadIdx.x; i < n16; i += blockDim.x)
-            reinterpret_cast<uint4 *>(smem + at)[i] = reinterpret_cast<const uint4 *>(src)[i];
-        g.at = (uint32_t)__cvta_generic_to_shared(smem + at);
+            reinterpret_cast<uint4 *>(smem + at + j.d * e)[i] = zero;
+    };
+    if (L.pad > j.d)
+        for (int s = 0; s < L.stages; ++s) {
+            const int slot = s * L.row;
+            pad(slot + L.y, j.ydt);
+            if (j.h) pad(slot + L.h, j.hdt);
+            if (bwd && j.dh_out) pad(slot + L.dh, j.hdt);
+            if (bwd && j.dxn) pad(slot + L.dx, j.xdt);
+            if (j.gate_kind == MOE_GATE_FULL) pad(slot + L.gate, j.gdt);
+        }
+    for (int i = threadIdx.x; i < (L.chan - L.zero) / 16; i += blockDim.x)
+        reinterpret_cast<uint4 *>(smem + L.zero)[i] = zero;
+    const uint32_t one = j.wdt == RVQ_F32 ? 0x3F800000u : j.wdt == RVQ_BF16 ? 0x3F803F80u : 0x3C003C00u;
+    const auto gain = [&](int at, const void *src) {
+        if (at < 0) return;
+        pad(at, j.wdt);
+        const int n16 = j.d * esize(j.wdt) / 16;
+        for (int i = threadIdx.x; i < n16; i += blockDim.x)
+            reinterpret_cast<uint4 *>(smem + at)[i] =
+                src ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(one, one, one, one);
+    };
+    gain(L.w_post, j.w_post);
+    gain(L.w_pre, j.w_pre);
+    if (j.gate_kind == MOE_GATE_CHANNEL) {
+        pad(L.chan, RVQ_F32);
+        for (int i = threadIdx.x * 4; i < j.d; i += blockDim.x * 4) {
+            float g[4];
+            ld4(j.gate, j.gdt, i, g);
+            *reinterpret_cast<float4 *>(smem + L.chan + i * 4) = make_float4(g[0], g[1], g[2], g[3]);
+        }
     }
-    return g;
-}
-
-// a channel gate: in shared memory as fp32
-__device__ __forceinline__ uint32_t keep_gate(uint8_t *smem, int at, const void *src, int dt,
-                                              int d) {
-    float *to = reinterpret_cast<float *>(smem + at);
-    for (int i = threadIdx.x; i < d; i += blockDim.x) to[i] = ld_elem(src, dt, i);
-    return (uint32_t)__cvta_generic_to_shared(to);
+    __syncthreads();
 }
 
 // Types of an instance: h (and h_out, dh, dh_out), y (and dy), xn (and dxn),
 // gains, and a full gate.  GATE 0: one value per row, 1: per channel, 2: full.
-template <int V_, int H_, int Y_, int X_, int W_, int G_, int GATE_>
+// SHARED: gains in shared memory (1), global (0), or as the layout says (kAny).
+template <int V_, int H_, int Y_, int X_, int W_, int G_, int GATE_, int SHARED_>
 struct JoinTypes {
-    static constexpr int V = V_, H = H_, Y = Y_, X = X_, W = W_, G = G_, GATE = GATE_;
+    static constexpr int V = V_, H = H_, Y = Y_, X = X_, W = W_, G = G_, GATE = GATE_,
+                         SHARED = SHARED_;
 };
 
 constexpr int kBwdBlocksPerSm = 4;   // the partial sums to add grow with the blocks
@@ -224,43 +219,47 @@ inline int join_threads(int d, int group, int v) {
     return (t + 31) / 32 * 32;
 }
 
-inline JoinSmem join_layout(const JoinJob &j, bool bwd, int st) {
-    const auto size = [&](const void *p, int dt) { return p ? j.d * (dt == RVQ_F32 ? 4 : 2) : 0; };
+inline JoinSmem join_layout(const JoinJob &j, bool bwd, int st, int v, bool gains) {
     JoinSmem L = {};
+    L.pad = join_threads(j.d, 4, v) * v * 4;
+    const auto row = [&](const void *p, int dt) { return p ? L.pad * (dt == RVQ_F32 ? 4 : 2) : 0; };
     int at = 0;
     L.y = at;
-    at += size(j.y, j.ydt);
+    at += row(j.y, j.ydt);
     L.h = at;
-    at += size(j.h, j.hdt);
+    at += row(j.h, j.hdt);
     L.dh = at;
-    at += bwd ? size(j.dh_out, j.hdt) : 0;
+    at += bwd ? row(j.dh_out, j.hdt) : 0;
     L.dx = at;
-    at += bwd ? size(j.dxn, j.xdt) : 0;
+    at += bwd ? row(j.dxn, j.xdt) : 0;
     L.gate = at;
-    at += j.gate_kind == MOE_GATE_FULL ? size(j.gate, j.gdt) : 0;
+    at += j.gate_kind == MOE_GATE_FULL ? row(j.gate, j.gdt) : 0;
     L.row = at;
     L.stages = st;
     at *= st;
+    L.zero = at;
+    if (st > 0 && (!j.h || (bwd && (!j.dh_out || !j.dxn)))) at += L.pad * 4;
     L.chan = at;
-    at += j.gate_kind == MOE_GATE_CHANNEL ? j.d * 4 : 0;
-    int *const place[2] = {&L.w_post, &L.w_pre};
-    const int bytes[2] = {size(j.w_post, j.wdt), size(j.w_pre, j.wdt)};
-    for (int i = 0; i < 2; ++i) {
-        *place[i] = at + bytes[i] <= kSmemMax ? at : -1;
-        if (*place[i] >= 0) at += bytes[i];
+    at += j.gate_kind == MOE_GATE_CHANNEL ? L.pad * 4 : 0;
+    L.w_post = L.w_pre = -1;
+    if (gains) {
+        L.w_post = at;
+        at += row(&L, j.wdt);
+        L.w_pre = at;
+        at += row(&L, j.wdt);
     }
     L.total = at;
     return L;
 }
 
-// Three rows, or two, or (rows too long for shared memory) none.  Gains are kept
-// in shared memory where that costs no row.
-inline JoinSmem join_ring(const JoinJob &j, bool bwd) {
-    for (int st = 3; st > 1; --st) {
-        const JoinSmem L = join_layout(j, bwd, st);
+// Three rows and the gains, two rows and the gains, two rows alone, or (rows too
+// long for shared memory) none.
+inline JoinSmem join_ring(const JoinJob &j, bool bwd, int v) {
+    for (int i = 0; i < 3; ++i) {
+        const JoinSmem L = join_layout(j, bwd, i == 0 ? 3 : 2, v, i < 2);
         if (L.total <= kSmemMax) return L;
     }
-    return join_layout(j, bwd, 0);
+    return join_layout(j, bwd, 0, v, false);
 }
 
 // Walking blocks of kernel K: as many as an SM holds at once, up to `most`.
@@ -284,31 +283,36 @@ template <auto K>
     return RVQ_OK;
 }
 
-// Calls f(JoinTypes<...>()) for the instance of a job's types with S16 as its
-// 16-bit type: rows of up to 8192 columns that fit the ring, a 16-bit xn, every
-// 16-bit tensor of one type, and a full gate of h's type.  Anything else takes
-// the instance that looks types up.
+// Whether a typed instance serves a job: rows of up to 8192 columns that fit the
+// ring, a 16-bit xn, every 16-bit tensor of its type, a full gate of h's type,
+// and, for gains left in global memory, fp32 h and gains (shorter types fit).
 inline bool join_typed(const JoinJob &j, const JoinSmem &L) {
     const int s16 = j.xdt;
-    const auto fits = [&](const void *p, int dt) { return !p || dt == RVQ_F32 || dt == s16; };
-    return s16 != RVQ_F32 && j.d <= 8192 && L.stages > 0 && fits(j.y, j.hdt) && fits(j.y, j.ydt) &&
-           (!(j.w_post || j.w_pre || j.dw_post || j.dw_pre) || fits(j.y, j.wdt)) &&
-           (j.gate_kind != MOE_GATE_FULL || j.gdt == j.hdt);
+    const auto fits = [&](int dt) { return dt == RVQ_F32 || dt == s16; };
+    return s16 != RVQ_F32 && j.d <= 8192 && L.stages > 0 && fits(j.hdt) && fits(j.ydt) &&
+           fits(j.wdt) && (j.gate_kind != MOE_GATE_FULL || j.gdt == j.hdt) &&
+           (L.w_pre >= 0 || (j.hdt == RVQ_F32 && j.wdt == RVQ_F32));
 }
 
+// Calls f(JoinTypes<...>()) for the typed instance of a job.
 template <int S16, class F>
-rvq_status with_types(const JoinJob &j, F &&f) {
+rvq_status with_types(const JoinJob &j, const JoinSmem &L, F &&f) {
     using C0 = std::integral_constant<int, S16>;
     using C1 = std::integral_constant<int, (int)RVQ_F32>;
-    const auto gate = [&](auto H, auto Y, auto W) {
+    const auto gate = [&](auto H, auto Y, auto W, auto G) {
         if (j.gate_kind == MOE_GATE_FULL)
-            return f(JoinTypes<4, H.value, Y.value, S16, W.value, H.value, 2>());
+            return f(JoinTypes<4, H.value, Y.value, S16, W.value, H.value, 2, G.value>());
         if (j.gate_kind == MOE_GATE_CHANNEL)
-            return f(JoinTypes<4, H.value, Y.value, S16, W.value, RVQ_F32, 1>());
-        return f(JoinTypes<4, H.value, Y.value, S16, W.value, RVQ_F32, 0>());
+            return f(JoinTypes<4, H.value, Y.value, S16, W.value, RVQ_F32, 1, G.value>());
+        return f(JoinTypes<4, H.value, Y.value, S16, W.value, RVQ_F32, 0, G.value>());
     };
+    using Shared = std::integral_constant<int, 1>;
+    using Global = std::integral_constant<int, 0>;
     const auto pick_w = [&](auto H, auto Y) {
-        return j.wdt == RVQ_F32 ? gate(H, Y, C1()) : gate(H, Y, C0());
+        if (j.wdt != RVQ_F32) return gate(H, Y, C0(), Shared());
+        if constexpr (H.value == (int)RVQ_F32)
+            if (L.w_pre < 0) return gate(H, Y, C1(), Global());
+        return gate(H, Y, C1(), Shared());
     };
     const auto pick_y = [&](auto H) {
         return j.ydt == RVQ_F32 ? pick_w(H, C1()) : pick_w(H, C0());
@@ -316,12 +320,15 @@ rvq_status with_types(const JoinJob &j, F &&f) {
     return j.hdt == RVQ_F32 ? pick_y(C1()) : pick_y(C0());
 }
 
+constexpr int kAnyV = 8;
+
 template <class F>
 rvq_status with_any_types(const JoinJob &j, F &&f) {
-    if (j.gate_kind == MOE_GATE_FULL) return f(JoinTypes<8, kAny, kAny, kAny, kAny, kAny, 2>());
+    if (j.gate_kind == MOE_GATE_FULL)
+        return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 2, kAny>());
     if (j.gate_kind == MOE_GATE_CHANNEL)
-        return f(JoinTypes<8, kAny, kAny, kAny, kAny, kAny, 1>());
-    return f(JoinTypes<8, kAny, kAny, kAny, kAny, kAny, 0>());
+        return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 1, kAny>());
+    return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 0, kAny>());
 }
 
 // the walking kernels by 16-bit type (one translation unit each)
@@ -330,8 +337,11 @@ rvq_status join_walk_f16(JoinJob &j, const JoinSmem &L, bool bwd, cudaStream_t s
 rvq_status join_walk_any(JoinJob &j, const JoinSmem &L, bool bwd, cudaStream_t stream);
 
 inline rvq_status join_walk(JoinJob &j, bool bwd, cudaStream_t stream) {
-    const JoinSmem L = join_ring(j, bwd);
-    if (!join_typed(j, L)) return join_walk_any(j, L, bwd, stream);
+    // types of absent tensors do not matter: take those of the others
+    if (!(j.w_post || j.w_pre || j.dw_post || j.dw_pre)) j.wdt = RVQ_F32;
+    if (!(bwd ? j.dxn : j.xn)) j.xdt = j.hdt != RVQ_F32 ? j.hdt : j.ydt != RVQ_F32 ? j.ydt : RVQ_BF16;
+    const JoinSmem L = join_ring(j, bwd, 4);
+    if (!join_typed(j, L)) return join_walk_any(j, join_ring(j, bwd, kAnyV), bwd, stream);
     return j.xdt == RVQ_BF16 ? join_walk_bf16(j, L, bwd, stream) : join_walk_f16(j, L, bwd, stream);
 }
 

@@ -12,10 +12,6 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
     constexpr int V = T::V;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[4][32];
-    const Gain w_post = keep_gain(smem, L.w_post, j.w_post, j.wdt, j.d);
-    const Gain w_pre = keep_gain(smem, L.w_pre, j.w_pre, j.wdt, j.d);
-    uint32_t chan = 0;
-    if (T::GATE == 1) chan = keep_gate(smem, L.chan, j.gate, j.gdt, j.d);
     const bool has_h = j.h != nullptr;
     const float inv_d = 1.f / (float)j.d, alpha = has_h ? j.alpha : 0.f;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
@@ -32,10 +28,10 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
     const int G = gridDim.x, S = L.stages;
     int t = blockIdx.x;
     for (int s = 0; s + 1 < S; ++s) fetch(t + s * G, s);
+    fill_smem(smem, j, L, false);
     float g_next = 1.f;
     if (j.gate_kind == MOE_GATE_SCALAR) g_next = ld_elem(j.gate, j.gdt, 0);
     if (j.gate_kind == MOE_GATE_TOKEN && t < j.n) g_next = ld_elem(j.gate, j.gdt, t);
-    __syncthreads();  // gains are in place
     int slot_i = 0, flip = 0;
     for (; t < j.n; t += G, flip ^= 2) {
         if (S) {
@@ -47,13 +43,14 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
         const uint32_t slot = ring + slot_i * L.row;
         slot_i = slot_i + 1 >= S ? 0 : slot_i + 1;
         const int64_t row = (int64_t)t * j.d;
+        const uint32_t at_h = has_h ? slot + L.h : ring + L.zero;
         float y[V][4], h[V][4];
         float s1[1] = {0.f}, s2[1] = {0.f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
-            row4<T::Y>(S, slot + L.y, j.y, row, c, c < j.d, j.ydt, y[v]);
-            row4<T::H>(S, slot + L.h, j.h, row, c, has_h && c < j.d, j.hdt, h[v]);
+            row4<T::Y>(S, slot + L.y, j.y, row, c, j.d, j.ydt, y[v]);
+            row4<T::H>(S, at_h, j.h, row, c, j.d, j.hdt, h[v]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s1[0] += y[v][e] * y[v][e];
         }
@@ -66,9 +63,9 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
             float g[4] = {gt, gt, gt, gt}, w[4];
-            if (T::GATE == 1) lds4<RVQ_F32>(chan, c, c < j.d, RVQ_F32, g);
-            if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, c < j.d, j.gdt, g);
-            gain4<T::W>(w_post, c, c < j.d, j.wdt, w);
+            if (T::GATE == 1) lds4<RVQ_F32>(ring + L.chan, c, RVQ_F32, g);
+            if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, j.d, j.gdt, g);
+            gain4<T::W, T::SHARED>(L.w_post, ring, j.w_post, c, j.d, j.wdt, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 h[v][e] = alpha * h[v][e] + g[e] * (y[v][e] * r1 * w[e]);
@@ -86,7 +83,7 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
             float w[4];
-            gain4<T::W>(w_pre, c, c < j.d, j.wdt, w);
+            gain4<T::W, T::SHARED>(L.w_pre, ring, j.w_pre, c, j.d, j.wdt, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] *= h[v][e] * r2;
             put4<T::X>(j.xn, row + c, j.xn != nullptr && c < j.d, j.xdt, w);
@@ -106,10 +103,6 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     constexpr int V = T::V;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][96];
-    const Gain w_post = keep_gain(smem, L.w_post, j.w_post, j.wdt, j.d);
-    const Gain w_pre = keep_gain(smem, L.w_pre, j.w_pre, j.wdt, j.d);
-    uint32_t chan = 0;
-    if (T::GATE == 1) chan = keep_gate(smem, L.chan, j.gate, j.gdt, j.d);
     const bool has_h = j.h != nullptr, has_dh = j.dh_out != nullptr, has_dx = j.dxn != nullptr;
     const float inv_d = 1.f / (float)j.d, alpha = has_h ? j.alpha : 0.f;
     float acc[3][V][4], gate_sum = 0.f;
@@ -135,6 +128,7 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     const int G = gridDim.x, S = L.stages;
     int t = blockIdx.x;
     for (int s = 0; s + 1 < S; ++s) fetch(t + s * G, s);
+    fill_smem(smem, j, L, true);
     float r1n = 1.f, r2n = 1.f, gn = 1.f;
     const auto scalars = [&](int u) {
         if (u >= j.n) return;
@@ -144,7 +138,6 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     };
     if (j.gate_kind == MOE_GATE_SCALAR) gn = ld_elem(j.gate, j.gdt, 0);
     scalars(t);
-    __syncthreads();  // gains are in place
     int slot_i = 0, flip = 0;
     for (; t < j.n; t += G, flip ^= 1) {
         if (S) {
@@ -156,20 +149,22 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
         const uint32_t slot = ring + slot_i * L.row;
         slot_i = slot_i + 1 >= S ? 0 : slot_i + 1;
         const int64_t row = (int64_t)t * j.d;
+        const uint32_t at_h = has_h ? slot + L.h : ring + L.zero;
+        const uint32_t at_dh = has_dh ? slot + L.dh : ring + L.zero;
+        const uint32_t at_dx = has_dx ? slot + L.dx : ring + L.zero;
         // a group's y, h_out, P, dxn, q, gate, z, w_post (zeros past the row)
         const auto group = [&](int c, float (&y)[4], float (&ho)[4], float (&P)[4], float (&dx)[4],
                                float (&q)[4], float (&g)[4], float (&z)[4], float (&w)[4]) {
-            const bool on = c < j.d;
             float wp[4];
-            row4<T::Y>(S, slot + L.y, j.y, row, c, on, j.ydt, y);
-            row4<T::H>(S, slot + L.h, j.h, row, c, has_h && on, j.hdt, ho);
-            row4<T::H>(S, slot + L.dh, j.dh_out, row, c, has_dh && on, j.hdt, P);
-            row4<T::X>(S, slot + L.dx, j.dxn, row, c, has_dx && on, j.xdt, dx);
+            row4<T::Y>(S, slot + L.y, j.y, row, c, j.d, j.ydt, y);
+            row4<T::H>(S, at_h, j.h, row, c, j.d, j.hdt, ho);
+            row4<T::H>(S, at_dh, j.dh_out, row, c, j.d, j.hdt, P);
+            row4<T::X>(S, at_dx, j.dxn, row, c, j.d, j.xdt, dx);
             g[0] = g[1] = g[2] = g[3] = gt;
-            if (T::GATE == 1) lds4<RVQ_F32>(chan, c, on, RVQ_F32, g);
-            if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, on, j.gdt, g);
-            gain4<T::W>(w_post, c, on, j.wdt, w);
-            gain4<T::W>(w_pre, c, on, j.wdt, wp);
+            if (T::GATE == 1) lds4<RVQ_F32>(ring + L.chan, c, RVQ_F32, g);
+            if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, j.d, j.gdt, g);
+            gain4<T::W, T::SHARED>(L.w_post, ring, j.w_post, c, j.d, j.wdt, w);
+            gain4<T::W, T::SHARED>(L.w_pre, ring, j.w_pre, c, j.d, j.wdt, wp);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 z[e] = y[e] * r1 * w[e];
