@@ -240,14 +240,14 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, ++done) {
             const int buf = done & 1;
-            if (done >= 2 && !warp_wait_spin(accempty0 + 8 * buf, ((done >> 1) - 1) & 1, abort_flag,
+            if (done >= 2 && !warp_wait(accempty0 + 8 * buf, ((done >> 1) - 1) & 1, abort_flag,
                                              g.status))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC);
             for (int k = 0; k < slices; ++k, ++it) {
                 const int s = it % DG_ST;
-                if (!warp_wait_spin(full0 + 8 * s, (it / DG_ST) & 1, abort_flag, g.status)) {
+                if (!warp_wait(full0 + 8 * s, (it / DG_ST) & 1, abort_flag, g.status)) {
                     ok = false;
                     break;
                 }

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
     } else if (warp == 1) {
         for (int k = k0, it = 0; k < k1; ++k, ++it) {
             const int s = it % g.stages;
-            if (!warp_wait_spin(full0 + 8 * s, (it / g.stages) & 1, abort_flag, g.status)) break;
+            if (!warp_wait(full0 + 8 * s, (it / g.stages) & 1, abort_flag, g.status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t st = smem_u32(smem + s * stage);
             const uint64_t a = operand_desc(st, 0), b = operand_desc(st + DS_ABYTES, 0);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
         __syncwarp();
     }
     // the partial tile, [token][row], over the ring (its last slice is consumed)
-    mbar_wait(accfull, 0, abort_flag, g.status);
+    warp_wait(accfull, 0, abort_flag, g.status);
     __syncthreads();
     const bool ok = !*abort_flag;  // no wait of this CTA is left that could raise it
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

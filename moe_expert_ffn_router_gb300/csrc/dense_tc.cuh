@@ -26,16 +26,26 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Bounded waits of a whole warp: every lane gets the same answer, so the warp
-// stays converged when a wait gives up.
+// Bounded wait of a whole warp on a barrier phase; every lane gets the same
+// answer, so the warp stays converged when a wait gives up.  False once another
+// role has aborted, or after kWaitLimitNs (then the abort flag is raised and the
+// timeout recorded).  The clock is looked at every 256th try only: a global timer
+// read between two tries cost the tensor pipe more than the wait itself.
 __device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volatile int *abort_flag,
                                           uint32_t *status) {
-    return __all_sync(0xffffffffu, mbar_wait(mbar, parity, abort_flag, status));
-}
-
-__device__ __forceinline__ bool warp_wait_spin(uint32_t mbar, uint32_t parity,
-                                               volatile int *abort_flag, uint32_t *status) {
-    return __all_sync(0xffffffffu, mbar_wait_spin(mbar, parity, abort_flag, status));
+    unsigned long long t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_now(mbar, parity))) return true;
+        if ((i & 255u) != 255u) continue;
+        const unsigned long long now = global_ns();
+        if (t0 == 0) t0 = now;
+        const bool late = now - t0 > kWaitLimitNs;
+        if (late) {
+            *abort_flag = 1;
+            set_dev_error(status, RVQ_DEV_ERR_TIMEOUT);
+        }
+        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return false;
+    }
 }
 
 __device__ __forceinline__ void cluster_sync() {
