@@ -561,8 +561,9 @@ typedef enum moe_act {
     MOE_ACT_GELU_TANH = 4 /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))      */
 } moe_act;
 
-/* Workspace of moe_linear (backward = 0) and moe_linear_backward (1); one of
- * the larger size serves both.  0 for a shape the calls refuse. */
+/* Workspace of moe_linear (backward = 0), or of moe_linear_backward and
+ * moe_linear (1).  It depends on the current device's SM count.  0 for a shape
+ * the calls refuse. */
 size_t moe_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols, int32_t backward);
 
 /* out[t][r] = residual[t][r] + alpha * act(sum_c x[t][c] w[r][c] + bias[r])

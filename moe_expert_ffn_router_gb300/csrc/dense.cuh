@@ -206,8 +206,10 @@ struct DenseJob {
     int odt;
     int64_t ldo;
     float *pre[2];
-    uint32_t *status;
+    uint32_t *status;       // the workspace's status block
+    float *partial;         // dense_gemm_partial_bytes of workspace
 };
+size_t dense_gemm_partial_bytes(const DenseJob &job);
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream);
 // the same for few tokens (PLAIN and GATED, nothing transposed): the weights
 // streamed past the batch (dense_stream.cu)

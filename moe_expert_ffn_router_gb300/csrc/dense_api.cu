@@ -80,21 +80,46 @@ bool disjoint(const void *a, int64_t lda, int32_t ra, int32_t ca, size_t ea, con
     return a1 <= b0 || b1 <= a0;
 }
 
-// Backward workspace: status | dp 16-bit [mats][n][rows] | bias partials.
-struct BwdPlan {
-    size_t off_dp, off_part, total;
+// Workspace: status | partial sums of split products | and for a gradient dp
+// 16-bit [mats][n][rows] | bias partials.  The calls' products run one after
+// another and share the partial sums' place.
+struct WsPlan {
+    size_t off_partial, off_dp, off_part, total;
 };
-BwdPlan plan_bwd(int mats, int32_t n, int32_t rows) {
-    BwdPlan P;
-    P.off_dp = RVQ_WS_STATUS_BYTES;
+
+size_t product_partial(int mode, int32_t M, int32_t N, int32_t K, int a_t, int b_t) {
+    DenseJob j = {};
+    j.mode = mode;
+    j.M = M;
+    j.N = N;
+    j.K = K;
+    j.a_t = a_t;
+    j.b_t = b_t;
+    return dense_gemm_partial_bytes(j);
+}
+
+WsPlan plan_ws(int mats, int32_t n, int32_t rows, int32_t cols, bool backward) {
+    WsPlan P = {};
+    P.off_partial = RVQ_WS_STATUS_BYTES;
+    if (!backward) {
+        P.total = up256(P.off_partial +
+                        product_partial(mats == 2 ? DG_GATED : DG_PLAIN, n, rows, cols, 0, 0));
+        return P;
+    }
+    const size_t dx = product_partial(mats == 2 ? DG_SUM_K : DG_PLAIN, n, cols, rows, 0, 1);
+    const size_t dw = product_partial(mats == 2 ? DG_PAIR_M : DG_PLAIN, rows, cols, n, 1, 1);
+    P.off_dp = up256(P.off_partial + (dx > dw ? dx : dw));
     P.off_part = up256(P.off_dp + (size_t)mats * n * rows * 2);
     P.total = up256(P.off_part + (size_t)dense_bwd_chunks(n) * mats * rows * 4);
     return P;
 }
 
+// a gradient's workspace serves the forward call too
 size_t ws_bytes_of(int mats, int32_t n, int32_t rows, int32_t cols, int32_t backward) {
     if (!dense_shape(n, rows, cols)) return 0;
-    return backward ? plan_bwd(mats, n, rows).total : RVQ_WS_STATUS_BYTES;
+    const size_t f = plan_ws(mats, n, rows, cols, false).total;
+    const size_t b = backward ? plan_ws(mats, n, rows, cols, true).total : 0;
+    return f > b ? f : b;
 }
 
 }  // namespace
@@ -156,6 +181,7 @@ rvq_status moe_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t
     j.ldo = ldo;
     j.pre[0] = pre_dev;
     j.status = (uint32_t *)ws_dev;
+    j.partial = (float *)((uint8_t *)ws_dev + RVQ_WS_STATUS_BYTES);
     return launch_dense_gemm(j, (cudaStream_t)stream);
 }
 
@@ -201,6 +227,7 @@ rvq_status moe_gated_linear(const void *x_dev, int64_t ldx, const void *wg_dev,
     j.pre[0] = pre_dev;
     j.pre[1] = pre_dev ? pre_dev + (size_t)n * rows : nullptr;
     j.status = (uint32_t *)ws_dev;
+    j.partial = (float *)((uint8_t *)ws_dev + RVQ_WS_STATUS_BYTES);
     return launch_dense_gemm(j, (cudaStream_t)stream);
 }
 
@@ -234,7 +261,7 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
                    (disjoint(dw_dev, lddw, rows, cols, 2, dout_dev, lddo, n, rows, 2) &&
                     disjoint(dw_dev, lddw, rows, cols, 2, x_dev, ldx, n, cols, 2))),
               "%s: a gradient overlaps an input", who);
-    const BwdPlan P = plan_bwd(1, n, rows);
+    const WsPlan P = plan_ws(1, n, rows, cols, true);
     uint8_t *ws = (uint8_t *)ws_dev;
     cudaStream_t st = (cudaStream_t)stream;
     // without an activation the products read dout itself (alpha goes into
@@ -264,6 +291,7 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
     j.a[0] = direct ? dout_dev : ws + P.off_dp;
     j.lda = direct ? lddo : rows;
     j.status = (uint32_t *)ws_dev;
+    j.partial = (float *)(ws + P.off_partial);
     j.b_t = 1;
     if (dx_dev) {  // [n][rows] x [rows][cols]
         j.M = n;
@@ -325,7 +353,7 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
                     disjoint(dwu_dev, lddw, rows, cols, 2, x_dev, ldx, n, cols, 2) &&
                     disjoint(dwu_dev, lddw, rows, cols, 2, dwg_dev, lddw, rows, cols, 2))),
               "%s: a gradient overlaps an input or the other gradient", who);
-    const BwdPlan P = plan_bwd(2, n, rows);
+    const WsPlan P = plan_ws(2, n, rows, cols, true);
     uint8_t *ws = (uint8_t *)ws_dev;
     cudaStream_t st = (cudaStream_t)stream;
     const size_t plane = (size_t)n * rows;
@@ -356,6 +384,7 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
     j.lda = rows;
     j.b_t = 1;
     j.status = (uint32_t *)ws_dev;
+    j.partial = (float *)(ws + P.off_partial);
     if (dx_dev) {
         j.mode = DG_SUM_K;
         j.M = n;

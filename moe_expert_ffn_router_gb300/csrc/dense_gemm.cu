@@ -8,7 +8,7 @@
 //    one thread issues cta_group::2 MMAs on both halves.  Pairing halves the
 //    shared memory and L2 traffic of B per operation.
 //  * Both operands arrive by TMA in 64-deep slices (one 128-byte swizzled row
-//    of 16-bit elements), seven 32 KB stages per CTA; the slices of both CTAs
+//    of 16-bit elements), seven 32 KB stages per CTA (more of a narrower tile); the slices of both CTAs
 //    complete on the leader's barrier.
 //  * A transposed operand (stored [K][rows]) is loaded as it lies, in boxes of
 //    64 rows x 64 deep, and read through MN-major descriptors, so the gradients
@@ -23,17 +23,20 @@
 #include "dense_tc.cuh"
 
 #include <cudaTypedefs.h>
+#include <math.h>
 
 namespace rvq {
 namespace {
 
 constexpr int DG_BM = 128;   // rows of A per CTA
 constexpr int DG_BK = 64;    // depth of a slice
-constexpr int DG_ST = 7;     // stages
 constexpr int DG_ABYTES = DG_BM * DG_BK * 2;
-constexpr int DG_STAGE = 2 * DG_ABYTES;     // A, and up to 128 rows of B
-constexpr int DG_SMEM = DG_ST * DG_STAGE + 256;
+constexpr int DG_MAX_ST = 9;  // stages: as many as fit
+constexpr int DG_RING = 192 << 10;
 constexpr int DG_EPI_WARPS = 8;
+constexpr int DG_TURN = 4096;  // staging of an epilogue warp: 32 rows x 32 fp32 columns
+constexpr int DG_BARS = DG_RING + DG_EPI_WARPS * DG_TURN;
+constexpr int DG_SMEM = DG_BARS + 256;
 constexpr int DG_THREADS = 32 * (4 + DG_EPI_WARPS);
 constexpr int DG_ACC = 256;  // TMEM columns per accumulator
 constexpr int DG_GROUP = 8;  // M tiles walked together (operand reuse in L2)
@@ -42,16 +45,19 @@ static_assert(DG_SMEM <= 232448, "shared memory of a CTA");
 struct GemmArgs {
     int mode, M, N, a_t, b_t;
     int kb;              // slices of one product
+    int slices;          // slices of a tile
     int tile_n, half;    // columns of an accumulator; rows of B per CTA
+    int stages, stage;   // ring depth; bytes of a stage (A, then B)
     int mt, nt;          // output tiles (M tiles of both problems for PAIR_M)
+    int parts;           // runs of slices that a tile is cut into (1: whole tiles)
     uint32_t idesc;
     int dt, act, rdt, odt;
-    int wide;            // rows of out (1) and pre (2) start on 32 bytes
     float alpha;
     const void *bias[2], *residual;
     int64_t ldr, ldo;
     void *out[2];
     float *pre[2];
+    float *partial;      // sums of the parts, [part][plane][M][N] (see plane_of)
     uint32_t *status;
 };
 
@@ -98,54 +104,142 @@ __device__ __forceinline__ void tile_at(const GemmArgs &g, int t, int &m, int &n
     n = r / rows;
 }
 
-// 32 bytes of one lane: one whole sector per lane and instruction
-__device__ __forceinline__ void st32(void *p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+// The work of a CTA pair, the same sequence in every role: units of one tile and
+// one run of its slices.
+struct Work {
+    int unit, pairs, units;
+    int m, n, part, k0, k1;
+
+    __device__ __forceinline__ Work(const GemmArgs &g, int pair, int pairs_)
+        : unit(pair), pairs(pairs_), units(g.mt * g.nt * g.parts) {}
+    __device__ __forceinline__ bool next(const GemmArgs &g) {
+        if (unit >= units) return false;
+        const int tiles = g.mt * g.nt;
+        part = unit / tiles;
+        tile_at(g, unit - part * tiles, m, n);
+        k0 = (int)((int64_t)g.slices * part / g.parts);
+        k1 = (int)((int64_t)g.slices * (part + 1) / g.parts);
+        unit += pairs;
+        return true;
+    }
+};
+
+// fp32 [M][N] of a part: the gate or the up half, or the first or second problem
+__device__ __forceinline__ float *plane_of(const GemmArgs &g, int part, int z) {
+    const int planes = g.mode == DG_GATED || g.mode == DG_PAIR_M ? 2 : 1;
+    return g.partial + ((int64_t)part * planes + z) * g.M * g.N;
+}
+
+// An epilogue warp's staging turns values held one row per lane into whole rows
+// in memory: 32 rows of eight 16-byte groups, group j of row r at r * 8 + (j ^
+// (r & 7)), conflict-free both ways.
+__device__ __forceinline__ void turn_in(uint32_t turn, int lane, const float (&v)[32]) {
+    __syncwarp();  // the rows before are read
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         turn + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                     "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                     : "memory");
+    __syncwarp();
+}
+
+__device__ __forceinline__ void turn_out(uint32_t turn, int r, int j, float (&v)[4]) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(turn + r * 128 + ((j ^ (r & 7)) << 4))
                  : "memory");
 }
 
-// 16 (or the first 8) consecutive outputs; `wide`: rows start on 32 bytes
-__device__ __forceinline__ void store16(void *p, int dt, int64_t at, const float (&v)[16], int cols,
-                                        bool wide) {
-    if (cols == 16 && wide) {
-        uint32_t w[8];
-        if (dt == RVQ_F32) {
+// The staged 32 x `width` values to fp32 rows at (row, col): 128 contiguous bytes
+// per row, four rows per instruction.
+__device__ __forceinline__ void rows_f32(uint32_t turn, int lane, float *p, int64_t ld, int row,
+                                         int rows, int col, int width, const void *res, int rdt,
+                                         int64_t ldr) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3), j = lane & 7;
+        float v[4];
+        turn_out(turn, r, j, v);
+        if (row + r >= rows || 4 * j >= width) continue;
+        if (res) {
+            float b[4];
+            ld4(res, rdt, (int64_t)(row + r) * ldr + col + 4 * j, b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[8 * h + e]);
-                st32(reinterpret_cast<float *>(p) + at + 8 * h, w);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = pack16(dt, v[2 * e], v[2 * e + 1]);
-            st32(reinterpret_cast<uint16_t *>(p) + at, w);
+            for (int e = 0; e < 4; ++e) v[e] += b[e];
         }
-        return;
+        st4(p, RVQ_F32, (int64_t)(row + r) * ld + col + 4 * j, v);
     }
-    float lo[8], hi[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        lo[e] = v[e];
-        hi[e] = v[8 + e];
-    }
-    st8(p, dt, at, lo);
-    if (cols == 16) st8(p, dt, at + 8, hi);
 }
 
-__device__ __forceinline__ void add_bias16(const void *bias, int dt, int c, int cols,
-                                           float (&v)[16]) {
-    if (bias == nullptr) return;
-    float b[8];
-    ld8(bias, dt, c, b);
+// The same to 16-bit rows: 64 contiguous bytes per row, eight rows per
+// instruction.
+__device__ __forceinline__ void rows_16(uint32_t turn, int lane, void *p, int dt, int64_t ld,
+                                        int row, int rows, int col, int width, const void *res,
+                                        int rdt, int64_t ldr) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += b[e];
-    if (cols == 16) {
-        ld8(bias, dt, c + 8, b);
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), j = lane & 3;
+        float lo[4], hi[4], v[8];
+        turn_out(turn, r, 2 * j, lo);
+        turn_out(turn, r, 2 * j + 1, hi);
+        if (row + r >= rows || 8 * j >= width) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 + e] += b[e];
+        for (int e = 0; e < 4; ++e) {
+            v[e] = lo[e];
+            v[4 + e] = hi[e];
+        }
+        if (res) {
+            float b[8];
+            ld8(res, rdt, (int64_t)(row + r) * ldr + col + 8 * j, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += b[e];
+        }
+        st8(p, dt, (int64_t)(row + r) * ld + col + 8 * j, v);
     }
+}
+
+__device__ __forceinline__ void add_bias32(const void *bias, int dt, int c, int width,
+                                           float (&v)[32]) {
+    if (bias == nullptr) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (8 * q < width) {
+            float b[8];
+            ld8(bias, dt, c + 8 * q, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
+        }
+}
+
+// 32 columns of a row per lane, finished and written: v (and w, the up half) are
+// the sums of columns c .. c + width - 1 of rows row .. row + 31.
+template <bool GATED>
+__device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lane, void *out, int row,
+                                       int c, int width, float (&v)[32], float (&w)[32]) {
+    add_bias32(g.bias[0], g.dt, c, width, v);
+    if (g.pre[0]) {
+        turn_in(turn, lane, v);
+        rows_f32(turn, lane, g.pre[0], g.N, row, g.M, c, width, nullptr, 0, 0);
+    }
+    act_group(g.act, v);
+    if (GATED) {
+        add_bias32(g.bias[1], g.dt, c, width, w);
+        if (g.pre[1]) {
+            turn_in(turn, lane, w);
+            rows_f32(turn, lane, g.pre[1], g.N, row, g.M, c, width, nullptr, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= w[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= g.alpha;
+    }
+    turn_in(turn, lane, v);
+    if (g.odt == RVQ_F32)
+        rows_f32(turn, lane, (float *)out, g.ldo, row, g.M, c, width, g.residual, g.rdt, g.ldr);
+    else
+        rows_16(turn, lane, out, g.odt, g.ldo, row, g.M, c, width, g.residual, g.rdt, g.ldr);
 }
 
 template <bool GATED>
@@ -156,17 +250,15 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int tiles = g.mt * g.nt;
+    Work work(g, blockIdx.x >> 1, gridDim.x >> 1);
     const int mt1 = g.mode == DG_PAIR_M ? g.mt / 2 : g.mt;  // M tiles of one problem
-    const int slices = g.mode == DG_SUM_K ? 2 * g.kb : g.kb;
-    uint8_t *bars = smem + DG_ST * DG_STAGE;
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * DG_ST,
-                   accfull0 = empty0 + 8 * DG_ST, accempty0 = accfull0 + 16;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 8 * (2 * DG_ST + 4));
+    uint8_t *bars = smem + DG_BARS;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * DG_MAX_ST,
+                   accfull0 = empty0 + 8 * DG_MAX_ST, accempty0 = accfull0 + 16;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 8 * (2 * DG_MAX_ST + 4));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < DG_ST; ++s) {
+        for (int s = 0; s < g.stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
@@ -178,7 +270,8 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        // one CTA per SM (shared memory), so the allocation never waits
+        // one CTA per SM (shared memory): the allocation waits for nothing but
+        // the end of a kernel before this one
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(tslot)),
                      "r"(512u));
@@ -189,23 +282,22 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     cluster_sync();  // the peer's barriers and TMEM are ready too
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tslot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
 
     if (warp == 0) {
         // producer: this CTA's rows of A and of B for every slice
         const int bboxes = g.b_t ? (g.half + 63) / 64 : 1;
         const uint32_t bytes = DG_ABYTES + (g.b_t ? bboxes * 8192 : g.half * 128);
-        int it = 0;
+        int s = 0;
+        uint32_t lap = 0;  // trips around the ring
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
-            int m, n;
-            tile_at(g, t, m, n);
-            const bool second = m >= mt1;
-            const int m0 = (second ? m - mt1 : m) * 2 * DG_BM + (int)rank * DG_BM;
-            const int n0 = GATED ? n * g.half : n * g.tile_n + (int)rank * g.half;
-            for (int k = 0; k < slices; ++k, ++it) {
-                const int s = it % DG_ST;
-                if (it >= DG_ST && !warp_wait(empty0 + 8 * s, ((it / DG_ST) - 1) & 1, abort_flag,
-                                              g.status)) {
+        while (ok && work.next(g)) {
+            const bool second = work.m >= mt1;
+            const int m0 = (second ? work.m - mt1 : work.m) * 2 * DG_BM + (int)rank * DG_BM;
+            const int n0 = GATED ? work.n * g.half : work.n * g.tile_n + (int)rank * g.half;
+            for (int k = work.k0; k < work.k1; ++k) {
+                if (lap > 0 && !warp_wait(empty0 + 8 * s, (lap - 1) & 1, abort_flag, g.status)) {
                     ok = false;
                     break;
                 }
@@ -213,7 +305,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                 const int kx = (k2 ? k - g.kb : k) * DG_BK;
                 const CUtensorMap *ta = (second || k2) ? &ma1 : &ma0;
                 const CUtensorMap *tb = (GATED ? rank == 1 : k2) ? &mb1 : &mb0;
-                const uint32_t st = smem_u32(smem + s * DG_STAGE), sb = st + DG_ABYTES;
+                const uint32_t st = smem_u32(smem + s * g.stage), sb = st + DG_ABYTES;
                 const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
@@ -231,92 +323,84 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                     }
                 }
                 __syncwarp();
+                if (++s == g.stages) {
+                    s = 0;
+                    ++lap;
+                }
             }
         }
     } else if (warp == 1 && rank == 0) {
         // issuer: four 16-deep MMAs per slice
         const uint32_t da = g.a_t ? 2048u >> 4 : 2u, db = g.b_t ? 2048u >> 4 : 2u;
-        int it = 0, done = 0;
+        int s = 0, done = 0;
+        uint32_t lap = 0;
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs, ++done) {
+        for (; ok && work.next(g); ++done) {
             const int buf = done & 1;
             if (done >= 2 && !warp_wait(accempty0 + 8 * buf, ((done >> 1) - 1) & 1, abort_flag,
-                                             g.status))
+                                        g.status))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC);
-            for (int k = 0; k < slices; ++k, ++it) {
-                const int s = it % DG_ST;
-                if (!warp_wait(full0 + 8 * s, (it / DG_ST) & 1, abort_flag, g.status)) {
+            for (int k = work.k0; k < work.k1; ++k) {
+                if (!warp_wait(full0 + 8 * s, lap & 1, abort_flag, g.status)) {
                     ok = false;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t st = smem_u32(smem + s * DG_STAGE);
+                const uint32_t st = smem_u32(smem + s * g.stage);
                 const uint64_t a = operand_desc(st, g.a_t),
                                b = operand_desc(st + DG_ABYTES, g.b_t);
                 if (elect_one()) {
 #pragma unroll
                     for (int q = 0; q < DG_BK / 16; ++q)
-                        mma_pair(acc, a + q * da, b + q * db, g.idesc, (k > 0 || q > 0) ? 1u : 0u);
+                        mma_pair(acc, a + q * da, b + q * db, g.idesc,
+                                 (k > work.k0 || q > 0) ? 1u : 0u);
                     commit_pair(empty0 + 8 * s);
                 }
                 __syncwarp();
+                if (++s == g.stages) {
+                    s = 0;
+                    ++lap;
+                }
             }
             if (elect_one()) commit_pair(accfull0 + 8 * buf);
             __syncwarp();
         }
     } else if (warp >= 4) {
         // epilogue: lanes 32 q .. 32 q + 31 of the accumulator, every other
-        // group of 16 columns
+        // group of 32 columns
         const int q = warp & 3, par = (warp - 4) >> 2;
-        const int units = (GATED ? g.half : g.tile_n) / 16;
-        int done = 0;
-        for (int t = pair; t < tiles; t += pairs, ++done) {
-            int m, n;
-            tile_at(g, t, m, n);
-            const bool second = m >= mt1;
-            const int row = (second ? m - mt1 : m) * 2 * DG_BM + (int)rank * DG_BM + 32 * q + lane;
+        const int per = GATED ? g.half : g.tile_n;  // outputs of a tile's row
+        const uint32_t turn = smem_u32(smem + DG_RING) + (uint32_t)(warp - 4) * DG_TURN;
+        for (int done = 0; work.next(g); ++done) {
+            const bool second = work.m >= mt1;
+            const int row =
+                (second ? work.m - mt1 : work.m) * 2 * DG_BM + (int)rank * DG_BM + 32 * q;
             const int buf = done & 1;
             if (!warp_wait(accfull0 + 8 * buf, (done >> 1) & 1, abort_flag, g.status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC) + ((uint32_t)(32 * q) << 16);
             void *out = g.out[second ? 1 : 0];
-            for (int u = par; u < units; u += 2) {
-                uint32_t r0[16], r1[16];
-                tmem_ld16(acc + 16 * u, r0);
-                if (GATED) tmem_ld16(acc + g.half + 16 * u, r1);
-                tmem_wait();
-                const int c = n * (GATED ? g.half : g.tile_n) + 16 * u;
-                const int cols = min(16, g.N - c);
-                if (row < g.M && cols > 0) {
-                    float v[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r0[e]);
-                    add_bias16(g.bias[0], g.dt, c, cols, v);
-                    if (g.pre[0]) store16(g.pre[0], RVQ_F32, (int64_t)row * g.N + c, v, cols,
-                                              g.wide & 2);
-                    act_group(g.act, v);
+            float v[32], w[32];
+            for (int c = par * 32; c < per; c += 64) {
+                tmem_ld32(acc + c, v);
+                if (GATED) tmem_ld32(acc + g.half + c, w);
+                const int col = work.n * per + c;
+                const int width = min(min(32, per - c), g.N - col);
+                if (row >= g.M || width <= 0) continue;
+                if (g.parts == 1) {
+                    finish<GATED>(g, turn, lane, out, row, col, width, v, w);
+                } else {
+                    turn_in(turn, lane, v);
+                    rows_f32(turn, lane, plane_of(g, work.part, second ? 1 : 0), g.N, row, g.M, col,
+                             width, nullptr, 0, 0);
                     if (GATED) {
-                        float w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(r1[e]);
-                        add_bias16(g.bias[1], g.dt, c, cols, w);
-                        if (g.pre[1]) store16(g.pre[1], RVQ_F32, (int64_t)row * g.N + c, w, cols,
-                                                  g.wide & 2);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] *= w[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] *= g.alpha;
-                        add_bias16(g.residual ? (const char *)g.residual +
-                                                    (int64_t)row * g.ldr * (g.rdt == RVQ_F32 ? 4 : 2)
-                                              : nullptr,
-                                   g.rdt, c, cols, v);
+                        turn_in(turn, lane, w);
+                        rows_f32(turn, lane, plane_of(g, work.part, 1), g.N, row, g.M, col, width,
+                                 nullptr, 0, 0);
                     }
-                    store16(out, g.odt, (int64_t)row * g.ldo + c, v, cols, g.wide & 1);
                 }
-                __syncwarp();
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
@@ -338,26 +422,109 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     }
 }
 
-// Columns of an accumulator: the width with the least (waves of CTA pairs) x
-// (time of a slice), where a slice costs its MMAs (2 tile_n cycles) or, for
-// narrow tiles, its operand fill ((128 + tile_n / 2) rows of 128 bytes at about
-// 72 bytes per cycle and SM).
-int choose_tile_n(const DenseJob &j, int mt, int pairs) {
-    int best = 0;
+// Adds a tile's parts in slice order and finishes the outputs: eight columns per
+// thread.  Memory-bound (the parts are in L2).
+template <bool GATED>
+__global__ void __launch_bounds__(256) dense_parts_kernel(const __grid_constant__ GemmArgs g) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int n8 = g.N / 8, z = blockIdx.y;  // second problem of PAIR_M
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)g.M * n8) return;
+    const int64_t row = i / n8;
+    const int c = (int)(i % n8) * 8;
+    const int64_t at = row * g.N + c;
+    float v[8] = {}, w[8] = {}, t[8];
+    for (int p = 0; p < g.parts; ++p) {
+        ld8(plane_of(g, p, z), RVQ_F32, at, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += t[e];
+        if (GATED) {
+            ld8(plane_of(g, p, 1), RVQ_F32, at, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] += t[e];
+        }
+    }
+    if (g.bias[0]) {
+        ld8(g.bias[0], g.dt, c, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+    if (g.pre[0]) st8(g.pre[0], RVQ_F32, at, v);
+    act_group(g.act, v);
+    if (GATED) {
+        if (g.bias[1]) {
+            ld8(g.bias[1], g.dt, c, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] += t[e];
+        }
+        if (g.pre[1]) st8(g.pre[1], RVQ_F32, at, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= w[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= g.alpha;
+        if (g.residual) {
+            ld8(g.residual, g.rdt, row * g.ldr + c, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += t[e];
+        }
+    }
+    st8(g.out[z], g.odt, row * g.ldo + c, v);
+}
+
+// How a product is cut: tile width, and the parts of a tile.
+struct GemmPlan {
+    int tile_n, mt, nt, slices, parts;
+};
+
+// Cycles of a 64-deep slice of a 256 x tile_n tile, as measured: the MMAs' 2 per
+// column, or, for narrower tiles, the issue and the operand fill.
+double slice_cycles(int tile_n) {
+    const double fill = 460.0 + 0.375 * tile_n;
+    return 2.0 * tile_n > fill ? 2.0 * tile_n : fill;
+}
+
+// The cheapest of the tile widths: (waves of pairs) x (slices of a tile).  Where
+// not even half the pairs would have a tile, the tiles' slices are cut into parts
+// for the others, which costs the parts' way through L2 and a second launch.
+GemmPlan plan_gemm(const DenseJob &j, int pairs) {
+    constexpr double kTile = 600.0, kParts = 6000.0;
+    GemmPlan best = {};
     double cost = 1e300;
+    const int mt = (j.M + 2 * DG_BM - 1) / (2 * DG_BM) * (j.mode == DG_PAIR_M ? 2 : 1);
+    const int kb = (j.K + DG_BK - 1) / DG_BK, slices = j.mode == DG_SUM_K ? 2 * kb : kb;
+    const double planes = j.mode == DG_GATED || j.mode == DG_PAIR_M ? 2.0 : 1.0;
     for (int tn = 256; tn >= 64; tn -= 32) {
         if (j.b_t && tn != 256 && tn != 128) continue;  // whole 64-row boxes per CTA
         const int per = j.mode == DG_GATED ? tn / 2 : tn;
-        const long long tiles = (long long)mt * ((j.N + per - 1) / per);
-        const double waves = (double)((tiles + pairs - 1) / pairs);
-        const double fill = (128.0 + tn / 2) * 128.0 / 72.0;
-        const double c = waves * (2.0 * tn > fill ? 2.0 * tn : fill);
-        if (c < cost * 0.999) {
-            cost = c;
-            best = tn;
+        const int nt = (j.N + per - 1) / per;
+        const double tiles = (double)mt * nt;
+        int parts = 1;
+        for (; parts <= 8 && tiles * parts <= pairs && slices >= 8 * parts; ++parts) {
+            const double waves = parts > 1 ? 1.0 : ceil(tiles / pairs);
+            // the parts' bytes, written and read at about 5 KB per cycle
+            const double join = parts > 1 ? kParts + parts * planes * j.M * j.N * 8.0 / 5000.0 : 0.0;
+            const double t = waves * (ceil((double)slices / parts) * slice_cycles(tn) + kTile) + join;
+            if (t < cost * 0.999) {
+                cost = t;
+                best = {tn, mt, nt, slices, parts};
+            }
+        }
+        if (parts == 1) {  // more tiles than pairs, or few slices
+            const double t = ceil(tiles / pairs) * (slices * slice_cycles(tn) + kTile);
+            if (t < cost * 0.999) {
+                cost = t;
+                best = {tn, mt, nt, slices, 1};
+            }
         }
     }
     return best;
+}
+
+size_t partial_bytes(const GemmPlan &p, const DenseJob &j) {
+    const size_t planes = j.mode == DG_GATED || j.mode == DG_PAIR_M ? 2 : 1;
+    return p.parts > 1 ? (size_t)p.parts * planes * j.M * j.N * 4 : 0;
 }
 
 }  // namespace
@@ -386,6 +553,11 @@ rvq_status encode_operand(CUtensorMap *map, const void *p, int rows, int K, int6
     return RVQ_OK;
 }
 
+size_t dense_gemm_partial_bytes(const DenseJob &job) {
+    if (dense_stream_fits(job)) return 0;
+    return partial_bytes(plan_gemm(job, num_sms() / 2), job);
+}
+
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     if (dense_stream_fits(job)) return launch_dense_stream(job, stream);
     static std::atomic<int> attr_done[64];  // per device; setting twice is harmless
@@ -400,6 +572,7 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     }
     const bool gated = job.mode == DG_GATED;
     const int pairs_max = num_sms() / 2;
+    const GemmPlan plan = plan_gemm(job, pairs_max);
     GemmArgs g = {};
     g.mode = job.mode;
     g.M = job.M;
@@ -407,11 +580,15 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     g.a_t = job.a_t;
     g.b_t = job.b_t;
     g.kb = (job.K + DG_BK - 1) / DG_BK;
-    g.mt = (job.M + 2 * DG_BM - 1) / (2 * DG_BM) * (job.mode == DG_PAIR_M ? 2 : 1);
-    g.tile_n = choose_tile_n(job, g.mt, pairs_max);
+    g.slices = plan.slices;
+    g.mt = plan.mt;
+    g.nt = plan.nt;
+    g.parts = plan.parts;
+    g.tile_n = plan.tile_n;
     g.half = g.tile_n / 2;
-    const int per = gated ? g.half : g.tile_n;
-    g.nt = (job.N + per - 1) / per;
+    // B's rows in whole swizzle atoms of 8 rows (1 KB), so every stage starts on one
+    g.stage = DG_ABYTES + g.half * 128;
+    g.stages = DG_RING / g.stage < DG_MAX_ST ? DG_RING / g.stage : DG_MAX_ST;
     const long long tiles = (long long)g.mt * g.nt;
     if (tiles > 0x7fffffffll / DG_GROUP) {
         set_error("dense product: %lld output tiles", tiles);
@@ -434,12 +611,8 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
         g.out[i] = job.out[i];
         g.pre[i] = job.pre[i];
     }
+    g.partial = job.partial;
     g.status = job.status;
-    const int64_t oe = job.odt == RVQ_F32 ? 4 : 2;
-    const uintptr_t outs = (uintptr_t)job.out[0] | (uintptr_t)job.out[1] |
-                           (uintptr_t)(job.ldo * oe) | (uintptr_t)(per * oe);
-    const uintptr_t pres = (uintptr_t)job.pre[0] | (uintptr_t)job.pre[1] | (uintptr_t)(per * 4);
-    g.wide = ((outs & 31) == 0 ? 1 : 0) | ((pres & 31) == 0 ? 2 : 0);
     CUtensorMap ma[2], mb[2];
     for (int i = 0; i < 2; ++i) {
         if (i == 1 && job.a[1] == nullptr)
@@ -451,23 +624,38 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
         else
             RVQ_TRY(encode_operand(&mb[i], job.b[i], job.N, job.K, job.ldb, job.b_t, job.dt, g.half));
     }
+    const long long units = tiles * g.parts, pairs = units < pairs_max ? units : pairs_max;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs_max ? tiles : pairs_max)));
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(DG_THREADS);
     cfg.dynamicSmemBytes = DG_SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (gated)
         RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_gemm_kernel<true>, ma[0], ma[1], mb[0], mb[1], g));
     else
         RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_gemm_kernel<false>, ma[0], ma[1], mb[0], mb[1], g));
     RVQ_LAUNCHED("dense_gemm");
+    if (g.parts == 1) return RVQ_OK;
+    const int64_t threads = (int64_t)job.M * (job.N / 8);
+    cfg.gridDim = dim3((unsigned)((threads + 255) / 256), job.mode == DG_PAIR_M ? 2u : 1u);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    if (gated)
+        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_parts_kernel<true>, g));
+    else
+        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_parts_kernel<false>, g));
+    RVQ_LAUNCHED("dense_parts");
     return RVQ_OK;
 }
 
