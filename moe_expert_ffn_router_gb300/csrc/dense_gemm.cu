@@ -152,51 +152,91 @@ __device__ __forceinline__ void turn_out(uint32_t turn, int r, int j, float (&v)
 }
 
 // The staged 32 x `width` values to fp32 rows at (row, col): 128 contiguous bytes
-// per row, four rows per instruction.
+// per row, four rows per instruction.  Everything is read before the first store:
+// a test per row between loads and stores exposed each load's latency.
 __device__ __forceinline__ void rows_f32(uint32_t turn, int lane, float *p, int64_t ld, int row,
                                          int rows, int col, int width, const void *res, int rdt,
                                          int64_t ldr) {
+    const int j = lane & 7, r0 = lane >> 3;
+    const bool on = 4 * j < width;
+    float v[8][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3), j = lane & 7;
-        float v[4];
-        turn_out(turn, r, j, v);
-        if (row + r >= rows || 4 * j >= width) continue;
-        if (res) {
-            float b[4];
-            ld4(res, rdt, (int64_t)(row + r) * ldr + col + 4 * j, b);
+    for (int i = 0; i < 8; ++i) turn_out(turn, 4 * i + r0, j, v[i]);
+    if (res) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += b[e];
+        for (int i = 0; i < 8; ++i) {
+            float b[4] = {};
+            if (on && row + 4 * i + r0 < rows)
+                ld4(res, rdt, (int64_t)(row + 4 * i + r0) * ldr + col + 4 * j, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] += b[e];
         }
-        st4(p, RVQ_F32, (int64_t)(row + r) * ld + col + 4 * j, v);
     }
+    float *q = p + (int64_t)(row + r0) * ld + col + 4 * j;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, q += 4 * ld)
+        if (on && row + 4 * i + r0 < rows)
+            *reinterpret_cast<float4 *>(q) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
 }
 
-// The same to 16-bit rows: 64 contiguous bytes per row, eight rows per
-// instruction.
+// The same to 16-bit rows with a residual: 64 contiguous bytes per row, eight
+// rows per instruction.
 __device__ __forceinline__ void rows_16(uint32_t turn, int lane, void *p, int dt, int64_t ld,
                                         int row, int rows, int col, int width, const void *res,
                                         int rdt, int64_t ldr) {
+    const int j = lane & 3, r0 = lane >> 2;
+    const bool on = 8 * j < width;
+    float v[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2), j = lane & 3;
-        float lo[4], hi[4], v[8];
-        turn_out(turn, r, 2 * j, lo);
-        turn_out(turn, r, 2 * j + 1, hi);
-        if (row + r >= rows || 8 * j >= width) continue;
+        float lo[4], hi[4], b[8] = {};
+        turn_out(turn, 8 * i + r0, 2 * j, lo);
+        turn_out(turn, 8 * i + r0, 2 * j + 1, hi);
+        if (on && row + 8 * i + r0 < rows)
+            ld8(res, rdt, (int64_t)(row + 8 * i + r0) * ldr + col + 8 * j, b);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            v[e] = lo[e];
-            v[4 + e] = hi[e];
+            v[i][e] = lo[e] + b[e];
+            v[i][4 + e] = hi[e] + b[4 + e];
         }
-        if (res) {
-            float b[8];
-            ld8(res, rdt, (int64_t)(row + r) * ldr + col + 8 * j, b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += b[e];
-        }
-        st8(p, dt, (int64_t)(row + r) * ld + col + 8 * j, v);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (on && row + 8 * i + r0 < rows)
+            st8(p, dt, (int64_t)(row + 8 * i + r0) * ld + col + 8 * j, v[i]);
+}
+
+// 32 values per lane, one row per lane, to 16-bit rows without a residual:
+// rounded first, so half as much goes through the staging (32 rows of four
+// 16-byte groups, group j of row r at r * 4 + (j ^ (r / 2 & 3))).
+__device__ __forceinline__ void rows_16_plain(uint32_t turn, int lane, void *p, int dt, int64_t ld,
+                                              int row, int rows, int col, int width,
+                                              const float (&v)[32]) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = pack16(dt, v[2 * e], v[2 * e + 1]);
+    __syncwarp();  // the rows before are read
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         turn + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
+                     "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                     : "memory");
+    __syncwarp();
+    const int j = lane & 3, r0 = lane >> 2;
+    uint4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + r0;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(o[i].x), "=r"(o[i].y), "=r"(o[i].z), "=r"(o[i].w)
+                     : "r"(turn + r * 64 + ((j ^ ((r >> 1) & 3)) << 4))
+                     : "memory");
+    }
+    uint16_t *q = reinterpret_cast<uint16_t *>(p) + (int64_t)(row + r0) * ld + col + 8 * j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, q += 8 * ld)
+        if (8 * j < width && row + 8 * i + r0 < rows) *reinterpret_cast<uint4 *>(q) = o[i];
 }
 
 __device__ __forceinline__ void add_bias32(const void *bias, int dt, int c, int width,
@@ -222,7 +262,7 @@ __device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lan
         turn_in(turn, lane, v);
         rows_f32(turn, lane, g.pre[0], g.N, row, g.M, c, width, nullptr, 0, 0);
     }
-    act_group(g.act, v);
+    if (g.act != MOE_ACT_NONE) act_group(g.act, v);
     if (GATED) {
         add_bias32(g.bias[1], g.dt, c, width, w);
         if (g.pre[1]) {
@@ -231,9 +271,13 @@ __device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lan
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] *= w[e];
-    } else {
+    } else if (g.alpha != 1.f) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] *= g.alpha;
+    }
+    if (g.odt != RVQ_F32 && g.residual == nullptr) {
+        rows_16_plain(turn, lane, out, g.odt, g.ldo, row, g.M, c, width, v);
+        return;
     }
     turn_in(turn, lane, v);
     if (g.odt == RVQ_F32)
