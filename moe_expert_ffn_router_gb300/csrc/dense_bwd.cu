@@ -27,11 +27,13 @@ __device__ __forceinline__ void ld32(const float *p, int wide, float (&v)[8]) {
     }
 }
 
+template <int MATS>
 __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
-    __shared__ float red[BW_LANES][2][264];
+    __shared__ float red[BW_LANES][MATS][264];
     const int q = threadIdx.x & 31, lane = threadIdx.x >> 5;
     const int c = (blockIdx.x * 32 + q) * 8;
     const bool on = c < j.rows;
+    dependency_wait();
     const bool sums = j.dbias[0] || j.dbias[1];
     float acc[2][8] = {};
     if (on) {
@@ -50,7 +52,7 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
             d_raw[i] = __ldg(reinterpret_cast<const uint4 *>(
                 reinterpret_cast<const uint16_t *>(j.dout) + (int64_t)t * j.ldd + c));
             if (j.pre[0]) ld32(j.pre[0] + at[i], j.wide, g[i]);
-            if (j.mats == 2) ld32(j.pre[1] + at[i], j.wide, u[i]);
+            if (MATS == 2) ld32(j.pre[1] + at[i], j.wide, u[i]);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -60,8 +62,8 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
             unpack16(j.dt, d_raw[i].y, d0[2], d0[3]);
             unpack16(j.dt, d_raw[i].z, d0[4], d0[5]);
             unpack16(j.dt, d_raw[i].w, d0[6], d0[7]);
-            if (j.pre[0]) act_group_both(j.act, g[i], a, sl);
-            if (j.mats == 2) {
+            if (j.pre[0]) act_group_both<MATS == 2>(j.act, g[i], a, sl);
+            if (MATS == 2) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     d1[e] = d0[e] * a[e];
@@ -80,17 +82,17 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
     }
     if (!sums) return;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < MATS; ++m)
 #pragma unroll
         for (int e = 0; e < 8; ++e) red[lane][m][q * 8 + e] = acc[m][e];
     __syncthreads();
     const int col = blockIdx.x * 256 + threadIdx.x;
     if (col >= j.rows) return;
-    for (int m = 0; m < j.mats; ++m) {
+    for (int m = 0; m < MATS; ++m) {
         float s = 0.f;
 #pragma unroll
         for (int l = 0; l < BW_LANES; ++l) s += red[l][m][threadIdx.x];
-        j.part[((int64_t)blockIdx.y * j.mats + m) * j.rows + col] = s;
+        j.part[((int64_t)blockIdx.y * MATS + m) * j.rows + col] = s;
     }
 }
 
@@ -100,6 +102,7 @@ __global__ void __launch_bounds__(1024) dense_bias_sum_kernel(const DenseBwdJob 
     __shared__ float red[32][33];
     const int q = threadIdx.x & 31, lane = threadIdx.x >> 5, m = blockIdx.y;
     const int col = blockIdx.x * 32 + q;
+    dependency_wait();
     if (j.dbias[m] == nullptr) return;
     float s = 0.f;
     if (col < j.rows)
@@ -125,12 +128,12 @@ rvq_status launch_dense_bwd(const DenseBwdJob &job, cudaStream_t stream) {
     const dim3 grid((unsigned)((job.rows + 255) / 256), (unsigned)chunks);
     DenseBwdJob j = job;
     j.wide = (((uintptr_t)job.pre[0] | (uintptr_t)job.pre[1]) & 31) == 0;
-    dense_bwd_kernel<<<grid, 256, 0, stream>>>(j);
-    RVQ_LAUNCHED("dense_bwd");
+    RVQ_CUDA(job.mats == 2 ? launch_after(dense_bwd_kernel<2>, grid, 256, 0, stream, j)
+                           : launch_after(dense_bwd_kernel<1>, grid, 256, 0, stream, j));
     if (job.dbias[0] || job.dbias[1]) {
-        dense_bias_sum_kernel<<<dim3((unsigned)((job.rows + 31) / 32), (unsigned)job.mats), 1024, 0,
-                                stream>>>(job, chunks);
-        RVQ_LAUNCHED("dense_bias_sum");
+        RVQ_CUDA(launch_after(dense_bias_sum_kernel,
+                              dim3((unsigned)((job.rows + 31) / 32), (unsigned)job.mats), 1024, 0,
+                              stream, job, chunks));
     }
     return RVQ_OK;
 }

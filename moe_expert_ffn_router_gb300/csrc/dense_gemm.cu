@@ -151,12 +151,38 @@ __device__ __forceinline__ void turn_out(uint32_t turn, int r, int j, float (&v)
                  : "memory");
 }
 
-// The staged 32 x `width` values to fp32 rows at (row, col): 128 contiguous bytes
-// per row, four rows per instruction.  Everything is read before the first store:
-// a test per row between loads and stores exposed each load's latency.
-__device__ __forceinline__ void rows_f32(uint32_t turn, int lane, float *p, int64_t ld, int row,
-                                         int rows, int col, int width, const void *res, int rdt,
-                                         int64_t ldr) {
+// The residual of a 32 x 32 group, as turn_rows() wants it: row 4 i + lane / 8,
+// columns 4 (lane % 8) ..; all loads in flight at once.
+struct Residual {
+    uint4 r[8];
+    __device__ __forceinline__ void load(const void *p, int dt, int64_t ld, int lane, int row, int rows,
+                                         int col, int width) {
+        const int j = lane & 7, r0 = lane >> 3;
+        const bool f32 = dt == RVQ_F32;
+        const char *q = reinterpret_cast<const char *>(p) +
+                        ((int64_t)(row + r0) * ld + col + 4 * j) * (f32 ? 4 : 2);
+        const int64_t step = 4 * ld * (f32 ? 4 : 2);
+        const bool on = p != nullptr && 4 * j < width;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, q += step) {
+            r[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && f32 && row + 4 * i + r0 < rows) r[i] = *reinterpret_cast<const uint4 *>(q);
+            if (on && !f32 && row + 4 * i + r0 < rows) {
+                const uint2 t = *reinterpret_cast<const uint2 *>(q);
+                r[i].x = t.x;
+                r[i].y = t.y;
+            }
+        }
+    }
+};
+
+// The staged 32 x `width` values (plus a residual) to rows at (row, col): 128 (fp32)
+// or 64 (16-bit) contiguous bytes per row, four rows per instruction.
+// Everything is read before the first store: a test per row between loads and
+// stores exposed each load's latency.
+__device__ __forceinline__ void turn_rows(uint32_t turn, int lane, void *p, int dt, int64_t ld,
+                                          int row, int rows, int col, int width,
+                                          const Residual *res, int rdt) {
     const int j = lane & 7, r0 = lane >> 3;
     const bool on = 4 * j < width;
     float v[8][4];
@@ -165,45 +191,35 @@ __device__ __forceinline__ void rows_f32(uint32_t turn, int lane, float *p, int6
     if (res) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float b[4] = {};
-            if (on && row + 4 * i + r0 < rows)
-                ld4(res, rdt, (int64_t)(row + 4 * i + r0) * ldr + col + 4 * j, b);
+            float b[4];
+            if (rdt == RVQ_F32) {
+                b[0] = __uint_as_float(res->r[i].x);
+                b[1] = __uint_as_float(res->r[i].y);
+                b[2] = __uint_as_float(res->r[i].z);
+                b[3] = __uint_as_float(res->r[i].w);
+            } else {
+                unpack16(rdt, res->r[i].x, b[0], b[1]);
+                unpack16(rdt, res->r[i].y, b[2], b[3]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[i][e] += b[e];
         }
     }
-    float *q = p + (int64_t)(row + r0) * ld + col + 4 * j;
+    const int64_t at = (int64_t)(row + r0) * ld + col + 4 * j;
+    if (dt == RVQ_F32) {
+        float *q = reinterpret_cast<float *>(p) + at;
 #pragma unroll
-    for (int i = 0; i < 8; ++i, q += 4 * ld)
-        if (on && row + 4 * i + r0 < rows)
-            *reinterpret_cast<float4 *>(q) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-}
-
-// The same to 16-bit rows with a residual: 64 contiguous bytes per row, eight
-// rows per instruction.
-__device__ __forceinline__ void rows_16(uint32_t turn, int lane, void *p, int dt, int64_t ld,
-                                        int row, int rows, int col, int width, const void *res,
-                                        int rdt, int64_t ldr) {
-    const int j = lane & 3, r0 = lane >> 2;
-    const bool on = 8 * j < width;
-    float v[4][8];
+        for (int i = 0; i < 8; ++i, q += 4 * ld)
+            if (on && row + 4 * i + r0 < rows)
+                *reinterpret_cast<float4 *>(q) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    } else {
+        uint16_t *q = reinterpret_cast<uint16_t *>(p) + at;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo[4], hi[4], b[8] = {};
-        turn_out(turn, 8 * i + r0, 2 * j, lo);
-        turn_out(turn, 8 * i + r0, 2 * j + 1, hi);
-        if (on && row + 8 * i + r0 < rows)
-            ld8(res, rdt, (int64_t)(row + 8 * i + r0) * ldr + col + 8 * j, b);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[i][e] = lo[e] + b[e];
-            v[i][4 + e] = hi[e] + b[4 + e];
-        }
+        for (int i = 0; i < 8; ++i, q += 4 * ld)
+            if (on && row + 4 * i + r0 < rows)
+                *reinterpret_cast<uint2 *>(q) =
+                    make_uint2(pack16(dt, v[i][0], v[i][1]), pack16(dt, v[i][2], v[i][3]));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (on && row + 8 * i + r0 < rows)
-            st8(p, dt, (int64_t)(row + 8 * i + r0) * ld + col + 8 * j, v[i]);
 }
 
 // 32 values per lane, one row per lane, to 16-bit rows without a residual:
@@ -256,18 +272,19 @@ __device__ __forceinline__ void add_bias32(const void *bias, int dt, int c, int 
 // the sums of columns c .. c + width - 1 of rows row .. row + 31.
 template <bool GATED>
 __device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lane, void *out, int row,
-                                       int c, int width, float (&v)[32], float (&w)[32]) {
+                                       int c, int width, float (&v)[32], float (&w)[32],
+                                       const Residual &res) {
     add_bias32(g.bias[0], g.dt, c, width, v);
     if (g.pre[0]) {
         turn_in(turn, lane, v);
-        rows_f32(turn, lane, g.pre[0], g.N, row, g.M, c, width, nullptr, 0, 0);
+        turn_rows(turn, lane, g.pre[0], RVQ_F32, g.N, row, g.M, c, width, nullptr, 0);
     }
     if (g.act != MOE_ACT_NONE) act_group(g.act, v);
     if (GATED) {
         add_bias32(g.bias[1], g.dt, c, width, w);
         if (g.pre[1]) {
             turn_in(turn, lane, w);
-            rows_f32(turn, lane, g.pre[1], g.N, row, g.M, c, width, nullptr, 0, 0);
+            turn_rows(turn, lane, g.pre[1], RVQ_F32, g.N, row, g.M, c, width, nullptr, 0);
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] *= w[e];
@@ -280,10 +297,7 @@ __device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lan
         return;
     }
     turn_in(turn, lane, v);
-    if (g.odt == RVQ_F32)
-        rows_f32(turn, lane, (float *)out, g.ldo, row, g.M, c, width, g.residual, g.rdt, g.ldr);
-    else
-        rows_16(turn, lane, out, g.odt, g.ldo, row, g.M, c, width, g.residual, g.rdt, g.ldr);
+    turn_rows(turn, lane, out, g.odt, g.ldo, row, g.M, c, width, g.residual ? &res : nullptr, g.rdt);
 }
 
 template <bool GATED>
@@ -326,8 +340,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     cluster_sync();  // the peer's barriers and TMEM are ready too
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tslot;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+    dependency_wait();
 
     if (warp == 0) {
         // producer: this CTA's rows of A and of B for every slice
@@ -422,27 +435,38 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
             const int row =
                 (second ? work.m - mt1 : work.m) * 2 * DG_BM + (int)rank * DG_BM + 32 * q;
             const int buf = done & 1;
+            if (!GATED && g.residual && g.parts == 1 && row + lane < g.M) {
+                // this warp's part of the residual into L2 while the tile is multiplied
+                const int e = g.rdt == RVQ_F32 ? 4 : 2;
+                for (int c = par * 32; c < per && work.n * per + c < g.N; c += 64)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        reinterpret_cast<const char *>(g.residual) +
+                        ((int64_t)(row + lane) * g.ldr + work.n * per + c) * e));
+            }
             if (!warp_wait(accfull0 + 8 * buf, (done >> 1) & 1, abort_flag, g.status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC) + ((uint32_t)(32 * q) << 16);
             void *out = g.out[second ? 1 : 0];
             float v[32], w[32];
             for (int c = par * 32; c < per; c += 64) {
-                tmem_ld32(acc + c, v);
-                if (GATED) tmem_ld32(acc + g.half + c, w);
                 const int col = work.n * per + c;
                 const int width = min(min(32, per - c), g.N - col);
                 if (row >= g.M || width <= 0) continue;
+                Residual res;
+                if (!GATED && g.residual && g.parts == 1)
+                    res.load(g.residual, g.rdt, g.ldr, lane, row, g.M, col, width);
+                tmem_ld32(acc + c, v);
+                if (GATED) tmem_ld32(acc + g.half + c, w);
                 if (g.parts == 1) {
-                    finish<GATED>(g, turn, lane, out, row, col, width, v, w);
+                    finish<GATED>(g, turn, lane, out, row, col, width, v, w, res);
                 } else {
                     turn_in(turn, lane, v);
-                    rows_f32(turn, lane, plane_of(g, work.part, second ? 1 : 0), g.N, row, g.M, col,
-                             width, nullptr, 0, 0);
+                    turn_rows(turn, lane, plane_of(g, work.part, second ? 1 : 0), RVQ_F32, g.N, row,
+                              g.M, col, width, nullptr, 0);
                     if (GATED) {
                         turn_in(turn, lane, w);
-                        rows_f32(turn, lane, plane_of(g, work.part, 1), g.N, row, g.M, col, width,
-                                 nullptr, 0, 0);
+                        turn_rows(turn, lane, plane_of(g, work.part, 1), RVQ_F32, g.N, row, g.M, col,
+                                  width, nullptr, 0);
                     }
                 }
             }
@@ -470,8 +494,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
 // thread.  Memory-bound (the parts are in L2).
 template <bool GATED>
 __global__ void __launch_bounds__(256) dense_parts_kernel(const __grid_constant__ GemmArgs g) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+    dependency_wait();
     const int n8 = g.N / 8, z = blockIdx.y;  // second problem of PAIR_M
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)g.M * n8) return;
@@ -690,16 +713,9 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     RVQ_LAUNCHED("dense_gemm");
     if (g.parts == 1) return RVQ_OK;
     const int64_t threads = (int64_t)job.M * (job.N / 8);
-    cfg.gridDim = dim3((unsigned)((threads + 255) / 256), job.mode == DG_PAIR_M ? 2u : 1u);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    cfg.attrs = attr + 1;
-    cfg.numAttrs = 1;
-    if (gated)
-        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_parts_kernel<true>, g));
-    else
-        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_parts_kernel<false>, g));
-    RVQ_LAUNCHED("dense_parts");
+    const dim3 grid((unsigned)((threads + 255) / 256), job.mode == DG_PAIR_M ? 2u : 1u);
+    RVQ_CUDA(gated ? launch_after(dense_parts_kernel<true>, grid, 256, 0, stream, g)
+                   : launch_after(dense_parts_kernel<false>, grid, 256, 0, stream, g));
     return RVQ_OK;
 }
 

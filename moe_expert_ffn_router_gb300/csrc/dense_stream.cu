@@ -10,8 +10,8 @@
 //    depth; a cluster of up to 8 CTAs splits the depth, so that even a matrix
 //    of few rows keeps the memory system busy.
 //  * Weights and tokens arrive by TMA in 64-deep slices through a ring of about
-//    96 KB per CTA, two CTAs per SM (one of about 190 KB from 80 tokens on);
-//    one thread issues the MMAs.
+//    190 KB per CTA, or 96 KB where there are enough CTAs for two per SM; one
+//    thread issues the MMAs.
 //  * The partial tiles (fp32) go to shared memory, and each CTA of the cluster
 //    adds its share of the rows over the cluster in rank order (distributed
 //    shared memory): no workspace, no atomics, results repeat bit for bit.
@@ -32,6 +32,7 @@ struct StreamArgs {
     int n, rows, kb;      // tokens, rows of one matrix, 64-deep slices
     int npad;             // tokens padded to a multiple of 16
     int stages, split;    // ring depth; CTAs of a cluster
+    int ahead;            // slices prefetched before the kernel may read
     uint32_t cols;        // TMEM columns
     uint32_t idesc;
     int dt, act, rdt, odt;
@@ -52,6 +53,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *tm, in
         : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *tm, int col, int row) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(col), "r"(row)
+                 : "memory");
+}
+
 __device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         uint32_t acc) {
     asm volatile(
@@ -60,12 +68,22 @@ __device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint
         "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr));
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
     return v;
+}
+
+// two consecutive elements at an even place
+__device__ __forceinline__ void ld2(const void *p, int dt, int64_t i, float (&v)[2]) {
+    if (dt == RVQ_F32) {
+        const float2 q = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(p) + i);
+        v[0] = q.x;
+        v[1] = q.y;
+    } else {
+        unpack16(dt, *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint16_t *>(p) + i),
+                 v[0], v[1]);
+    }
 }
 
 template <bool GATED>
@@ -107,6 +125,16 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tslot;
+    if (warp == 0 && elect_one()) {
+        // While the kernel before this one ends, bring the first weights into L2
+        // (whatever that kernel writes is read coherently after the wait).
+        for (int k = k0; k < k1 && k < k0 + g.ahead; ++k) {
+            tma_prefetch(&mw0, k * DS_BK, r0);
+            if (GATED) tma_prefetch(&mw1, k * DS_BK, r0);
+        }
+    }
+    dependency_wait();
+    dependents_may_start();
 
     if (warp == 0) {
         for (int k = k0, it = 0; k < k1; ++k, ++it) {
@@ -167,49 +195,71 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     cluster_sync();  // every partial tile of the cluster is in place
     if (ok) {
-        const int quads = TR / 4 / g.split;  // groups of four rows this CTA finishes
-        for (int i = threadIdx.x; i < g.n * quads; i += DS_THREADS) {
-            const int t = i / quads, qr = (rank * quads + i % quads) * 4;
+        // two rows per thread, every peer's values requested before the first is
+        // added (a loop of load and add cost a round trip per peer: 9000 cycles
+        // for 64 tokens)
+        const int duos = TR / 2 / g.split;  // groups of two rows this CTA finishes
+        for (int i = threadIdx.x; i < g.n * duos; i += DS_THREADS) {
+            const int t = i / duos, qr = (rank * duos + i % duos) * 2;
             const int r = r0 + qr;
-            if (r >= g.rows) continue;
             const uint32_t at = smem_u32(part + t * DS_PITCH + qr);
-            float v[4] = {}, u[4] = {};
-            for (int p = 0; p < g.split; ++p) {
+            float2 x[8], y[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                if (p >= g.split) continue;
                 const uint32_t a = cluster_addr(at, (uint32_t)p);
-                const float4 x = ld_cluster4(a);
-                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                x[p] = ld_cluster2(a);
+                if (GATED) y[p] = ld_cluster2(a + TR * 4);
+            }
+            float v[2] = {}, u[2] = {};
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                if (p >= g.split) continue;
+                v[0] += x[p].x;
+                v[1] += x[p].y;
                 if (GATED) {
-                    const float4 y = ld_cluster4(a + TR * 4);
-                    u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+                    u[0] += y[p].x;
+                    u[1] += y[p].y;
                 }
             }
-            float b[4];
+            if (r >= g.rows) continue;
+            float b[2];
             if (g.bias[0]) {
-                ld4(g.bias[0], g.dt, r, b);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += b[e];
+                ld2(g.bias[0], g.dt, r, b);
+                v[0] += b[0];
+                v[1] += b[1];
             }
-            if (g.pre[0]) st4(g.pre[0], RVQ_F32, (int64_t)t * g.rows + r, v);
+            if (g.pre[0])
+                *reinterpret_cast<float2 *>(g.pre[0] + (int64_t)t * g.rows + r) =
+                    make_float2(v[0], v[1]);
             act_group(g.act, v);
             if (GATED) {
                 if (g.bias[1]) {
-                    ld4(g.bias[1], g.dt, r, b);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) u[e] += b[e];
+                    ld2(g.bias[1], g.dt, r, b);
+                    u[0] += b[0];
+                    u[1] += b[1];
                 }
-                if (g.pre[1]) st4(g.pre[1], RVQ_F32, (int64_t)t * g.rows + r, u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] *= u[e];
+                if (g.pre[1])
+                    *reinterpret_cast<float2 *>(g.pre[1] + (int64_t)t * g.rows + r) =
+                        make_float2(u[0], u[1]);
+                v[0] *= u[0];
+                v[1] *= u[1];
             } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] *= g.alpha;
+                v[0] *= g.alpha;
+                v[1] *= g.alpha;
                 if (g.residual) {
-                    ld4(g.residual, g.rdt, (int64_t)t * g.ldr + r, b);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += b[e];
+                    ld2(g.residual, g.rdt, (int64_t)t * g.ldr + r, b);
+                    v[0] += b[0];
+                    v[1] += b[1];
                 }
             }
-            st4(g.out, g.odt, (int64_t)t * g.ldo + r, v);
+            const int64_t o = (int64_t)t * g.ldo + r;
+            if (g.odt == RVQ_F32)
+                *reinterpret_cast<float2 *>(reinterpret_cast<float *>(g.out) + o) =
+                    make_float2(v[0], v[1]);
+            else
+                *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(g.out) + o) =
+                    pack16(g.odt, v[0], v[1]);
         }
     }
     cluster_sync();  // the peers' tiles stay in place until read
@@ -220,13 +270,25 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
 }
 
 constexpr int kRingSmall = 96 << 10, kRingLarge = 190 << 10;
-constexpr int kSmallTokens = 80;  // up to here two CTAs share an SM
 
 }  // namespace
 
+int stream_tiles(const DenseJob &j) {
+    const int rows = j.mode == DG_GATED ? DS_ROWS / 2 : DS_ROWS;
+    return (j.N + rows - 1) / rows;
+}
+
+// Up to how many tokens the stream of weights beats the tiled product (measured,
+// us, stream / tiled: gated 7168 -> 2048, 192 tokens 20.5 / 21.8, 256 23.9 / 22.2;
+// gated 1736 -> 1000, 128 8.7 / 9.9, 192 10.7 / 10.4; plain 2048 -> 7168, 96 12.8 /
+// 13.6, 128 14.3 / 13.6; 1736 -> 4104, 128 11.4 / 12.1; 512 -> 2048, 48 4.9 / 5.0,
+// 64 5.4 / 5.0).
+// 64 tokens is the end for few rows, which are split eightfold up to there (7168 ->
+// 512: 64 9.0 / 9.7, 96 14.7 / 10.1).
 bool dense_stream_fits(const DenseJob &j) {
-    return (j.mode == DG_PLAIN || j.mode == DG_GATED) && !j.a_t && !j.b_t &&
-           j.M <= kStreamMaxTokens;
+    if (j.a_t || j.b_t || (j.mode != DG_GATED && j.mode != DG_PLAIN)) return false;
+    const int most = j.mode == DG_GATED ? kStreamMaxTokens : j.K >= 1024 ? 112 : 48;
+    return j.M <= (stream_tiles(j) * 8 <= num_sms() / 2 && most > 64 ? 64 : most);
 }
 
 rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream) {
@@ -247,15 +309,22 @@ rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream) {
     g.kb = (job.K + DS_BK - 1) / DS_BK;
     g.npad = (job.M + 15) / 16 * 16;
     const int tile_rows = gated ? DS_ROWS / 2 : DS_ROWS;
-    const int tiles = (job.N + tile_rows - 1) / tile_rows;
-    const bool small = g.npad <= kSmallTokens;
-    const int ring = small ? kRingSmall : kRingLarge;
+    const int tiles = stream_tiles(job);
+    // Depth split: as many CTAs as are resident at once (two per SM up to 128
+    // tokens), each with two slices or more.  Past 16 tokens at most four, since
+    // the joined tile grows (64 tokens, 7168 -> 2 x 2048: 15.7 us with 128 CTAs
+    // of large rings, 18.5 us with 256 of small ones), unless tiles are few (64
+    // tokens, 7168 -> 512).  Clusters of eight take small rings: with one CTA per
+    // SM a GPC's SMs do not divide by eight.
+    const int sms = num_sms(), slots = g.npad <= 128 ? 2 * sms : sms;
+    const int most = g.npad <= 16 || (g.npad <= 64 && tiles * 8 <= sms / 2) ? 8 : 4;
+    g.split = 1;
+    while (g.split < most && tiles * g.split * 2 <= slots && g.kb >= g.split * 4) g.split *= 2;
+    const bool two = g.npad <= 128 && (tiles * g.split > sms || g.split == 8);
+    const int ring = two ? kRingSmall : kRingLarge;
     const int stage = DS_ABYTES + g.npad * DS_BK * 2;
     g.stages = ring / stage < DS_MAX_ST ? ring / stage : DS_MAX_ST;
-    // depth split: as many CTAs as are resident at once, each with two slices
-    const int slots = num_sms() * (small ? 2 : 1);
-    g.split = 1;
-    while (g.split < 8 && tiles * g.split * 2 <= slots && g.kb >= g.split * 4) g.split *= 2;
+    g.ahead = g.stages;
     g.cols = 32;
     while ((int)g.cols < g.npad) g.cols *= 2;
     const uint32_t fmt = job.dt == RVQ_BF16 ? 1u : 0u;
@@ -289,13 +358,15 @@ rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream) {
     cfg.blockDim = dim3(DS_THREADS);
     cfg.dynamicSmemBytes = (size_t)dyn;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)g.split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (gated)
         RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_stream_kernel<true>, mw[0], mw[1], mx, g));
     else

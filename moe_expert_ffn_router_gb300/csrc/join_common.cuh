@@ -278,8 +278,7 @@ template <auto K>
     if (per < 1) per = 1;
     const int blocks = per * num_sms();
     j.slots = j.n < blocks ? j.n : blocks;
-    K<<<j.slots, threads, (size_t)L.total, stream>>>(j, L);
-    RVQ_LAUNCHED("norm_join");
+    RVQ_CUDA(launch_after(K, (unsigned)j.slots, (unsigned)threads, (size_t)L.total, stream, j, L));
     return RVQ_OK;
 }
 

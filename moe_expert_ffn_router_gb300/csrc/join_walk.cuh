@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
     };
     const int G = gridDim.x, S = L.stages;
     int t = blockIdx.x;
+    dependency_wait();
     for (int s = 0; s + 1 < S; ++s) fetch(t + s * G, s);
     fill_smem(smem, j, L, false);
     float g_next = 1.f;
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     };
     const int G = gridDim.x, S = L.stages;
     int t = blockIdx.x;
+    dependency_wait();
     for (int s = 0; s + 1 < S; ++s) fetch(t + s * G, s);
     fill_smem(smem, j, L, true);
     float r1n = 1.f, r2n = 1.f, gn = 1.f;

@@ -37,6 +37,8 @@ __global__ void __launch_bounds__(1024) join_row_kernel(const JoinJob j) {
     __shared__ float red[2][32];
     const int t = blockIdx.x;
     const int64_t row = (int64_t)t * j.d;
+    dependency_wait();
+    dependents_may_start();
     float y[V][8], h[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinJob j) {
     const int k = blockIdx.y, q = threadIdx.x & 31, lane = threadIdx.x >> 5;
     void *dst = k == 0 ? j.dw_post : k == 1 ? j.dw_pre
                 : j.gate_kind == MOE_GATE_CHANNEL ? j.dgate : nullptr;
+    dependency_wait();
     const bool scalar = k == 2 && j.gate_kind == MOE_GATE_SCALAR && j.dgate && blockIdx.x == 0;
     if (scalar) {
         if (threadIdx.x == 0) {
@@ -140,10 +143,9 @@ rvq_status launch_norm_join(const JoinJob &job, cudaStream_t stream) {
     if (job.n <= 2 * num_sms()) {
         const unsigned n = (unsigned)job.n;
         if (job.d <= 8192)
-            join_row_kernel<1><<<n, join_threads(job.d, 8, 1), 0, stream>>>(job);
+            RVQ_CUDA(launch_after(join_row_kernel<1>, n, join_threads(job.d, 8, 1), 0, stream, job));
         else
-            join_row_kernel<2><<<n, join_threads(job.d, 8, 2), 0, stream>>>(job);
-        RVQ_LAUNCHED("norm_join");
+            RVQ_CUDA(launch_after(join_row_kernel<2>, n, join_threads(job.d, 8, 2), 0, stream, job));
         return RVQ_OK;
     }
     JoinJob j = job;
@@ -156,8 +158,8 @@ rvq_status launch_norm_join_bwd(const JoinJob &job, cudaStream_t stream) {
     const bool gate = j.dgate && (j.gate_kind == MOE_GATE_CHANNEL || j.gate_kind == MOE_GATE_SCALAR);
     if (j.dw_post || j.dw_pre || gate) {
         // the blocks' sums over rows, in order (no atomics: results repeat)
-        join_sum_kernel<<<dim3((unsigned)((j.d + 31) / 32), 3), 1024, 0, stream>>>(j);
-        RVQ_LAUNCHED("norm_join_sum");
+        RVQ_CUDA(launch_after(join_sum_kernel, dim3((unsigned)((j.d + 31) / 32), 3), 1024, 0, stream,
+                              j));
     }
     return RVQ_OK;
 }
