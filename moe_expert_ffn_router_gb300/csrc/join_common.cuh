@@ -4,13 +4,11 @@
 //
 // A walking block's thread owns the same columns of every row: groups of four,
 // a block's width apart, so that a warp's accesses are contiguous for every
-// type.  It copies them ahead into the ring (cp.async, one or two rows in flight
-// while one is worked on) and reads only what it copied itself: the ring needs
-// no barrier.  Inner loops have no branches: a type is a template parameter
-// (16-bit formats differ by a select), an absent tensor or column is a
-// predicated load with a neutral value.  With a branch per load (types chosen at
-// run time) every load's latency was exposed: 65 us against 34 us for 2048 rows
-// of 7168 (fp32 h and y, bf16 xn).
+// type.  The next row is copied into a ring of two while one is worked on
+// (cp.async).  Inner loops have no branches: a type is a template parameter, an
+// absent tensor is a row of zeros.  With types looked up at run time every
+// load's latency was exposed: 56 us against 36 us for 2048 rows of 7168 (fp32 h
+// and y, bf16 xn).
 #pragma once
 
 #include <type_traits>
@@ -43,9 +41,6 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float *red) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -56,6 +51,24 @@ __device__ __forceinline__ void cp_wait() {
 // DT: an rvq_dtype, or kAny (the type is looked up in dt).
 constexpr int kAny = -1;
 
+// Four fp32 values as two pairs: the arithmetic runs on packed pairs (half the
+// instructions; the gradients' kernel issues more than it loads).
+struct Four {
+    float2 a, b;
+};
+__device__ __forceinline__ Four four(float x) {
+    return {make_float2(x, x), make_float2(x, x)};
+}
+__device__ __forceinline__ Four operator*(const Four &x, const Four &y) {
+    return {__fmul2_rn(x.a, y.a), __fmul2_rn(x.b, y.b)};
+}
+__device__ __forceinline__ Four fma4(const Four &x, const Four &y, const Four &z) {
+    return {__ffma2_rn(x.a, y.a, z.a), __ffma2_rn(x.b, y.b, z.b)};
+}
+__device__ __forceinline__ float sum4(const Four &x) {
+    return (x.a.x + x.a.y) + (x.b.x + x.b.y);
+}
+
 template <int DT>
 __device__ __forceinline__ int type_of(int dt) {
     return DT == kAny ? dt : DT;
@@ -63,18 +76,18 @@ __device__ __forceinline__ int type_of(int dt) {
 
 __device__ __forceinline__ int esize(int dt) { return dt == RVQ_F32 ? 4 : 2; }
 
-__device__ __forceinline__ void widen4(uint2 r, int dt, float (&v)[4]) {
-    unpack16(dt, r.x, v[0], v[1]);
-    unpack16(dt, r.y, v[2], v[3]);
+__device__ __forceinline__ void widen4(uint2 r, int dt, Four &v) {
+    unpack16(dt, r.x, v.a.x, v.a.y);
+    unpack16(dt, r.y, v.b.x, v.b.y);
 }
 
 // four values at element i of a row in shared memory (byte address `at`)
 template <int DT>
-__device__ __forceinline__ void lds4(uint32_t at, int i, int dt, float (&v)[4]) {
+__device__ __forceinline__ void lds4(uint32_t at, int i, int dt, Four &v) {
     const int t = type_of<DT>(dt);
     if (t == RVQ_F32) {
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "=f"(v.a.x), "=f"(v.a.y), "=f"(v.b.x), "=f"(v.b.y)
                      : "r"(at + i * 4)
                      : "memory");
     } else {
@@ -90,14 +103,16 @@ __device__ __forceinline__ void lds4(uint32_t at, int i, int dt, float (&v)[4]) 
 // four values in global memory; `none` when off
 template <int DT>
 __device__ __forceinline__ void ldg4(const void *p, int64_t i, bool on, int dt, float none,
-                                     float (&v)[4]) {
-    v[0] = v[1] = v[2] = v[3] = none;
-    if (on) ld4(p, type_of<DT>(dt), i, v);
+                                     Four &v) {
+    float t[4] = {none, none, none, none};
+    if (on) ld4(p, type_of<DT>(dt), i, t);
+    v = {make_float2(t[0], t[1]), make_float2(t[2], t[3])};
 }
 
 template <int DT>
-__device__ __forceinline__ void put4(void *p, int64_t i, bool on, int dt, const float (&v)[4]) {
-    if (on) st4(p, type_of<DT>(dt), i, v);
+__device__ __forceinline__ void put4(void *p, int64_t i, bool on, int dt, const Four &v) {
+    const float t[4] = {v.a.x, v.a.y, v.b.x, v.b.y};
+    if (on) st4(p, type_of<DT>(dt), i, t);
 }
 
 // ------------------------------------------------------------ the ring of rows
@@ -108,41 +123,33 @@ __device__ __forceinline__ void put4(void *p, int64_t i, bool on, int dt, const 
 struct JoinSmem {
     int pad;
     int y, h, dh, dx, gate, row;  // places in a ring slot; a slot's size
-    int stages;                   // ring depth (0: rows are read from global memory)
+    int stages;                   // ring depth: 2, or 0 (rows are read from global memory)
     int zero;                     // after the ring: a row of zeros for absent tensors
     int chan;                     // a channel gate
     int w_post, w_pre;            // gains (1 for absent ones); -1: read from global memory
     int total;
 };
 
+// A row of a tensor into its place in the ring: 16 bytes per thread and copy, so
+// what a thread reads later has been copied by others (half the copies of 8 bytes
+// each of its own columns; the copies' issue was what bounded the gradients).
 template <int V, int DT>
 __device__ __forceinline__ void fetch_row(uint32_t slot, const void *p, int dt, int64_t row, int d) {
-    const bool f32 = type_of<DT>(dt) == RVQ_F32;
+    const int t = type_of<DT>(dt);
+    const char *src = reinterpret_cast<const char *>(p) + row * esize(t);
+    const int n16 = d * esize(t) / 16;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = (v * blockDim.x + threadIdx.x) * 4;
-        if (c < d) {
-            if (f32)
-                cp_async16(slot + c * 4, reinterpret_cast<const float *>(p) + row + c);
-            else
-                cp_async8(slot + c * 2, reinterpret_cast<const uint16_t *>(p) + row + c);
-        }
+    for (int v = 0; v < (DT == kAny || DT == RVQ_F32 ? V : (V + 1) / 2); ++v) {
+        const int i = v * blockDim.x + threadIdx.x;
+        if (i < n16) cp_async16(slot + i * 16, src + i * 16);
     }
-}
-
-// the oldest row's copies are done, with a ring of `stages` rows
-__device__ __forceinline__ void wait_row(int stages) {
-    if (stages == 3)
-        cp_wait<2>();
-    else
-        cp_wait<1>();
 }
 
 // four values of a row: in the ring (or the row of zeros), or, for kAny
 // instances without a ring, in global memory
 template <int DT>
 __device__ __forceinline__ void row4(int stages, uint32_t at, const void *p, int64_t row, int i, int d,
-                                     int dt, float (&v)[4]) {
+                                     int dt, Four &v) {
     if (DT == kAny && stages == 0)
         ldg4<DT>(p, row + i, p != nullptr && i < d, dt, 0.f, v);
     else
@@ -152,7 +159,7 @@ __device__ __forceinline__ void row4(int stages, uint32_t at, const void *p, int
 // four gains: in shared memory (SHARED 1), in global memory (0), or as `at` says
 template <int DT, int SHARED>
 __device__ __forceinline__ void gain4(int at, uint32_t base, const void *p, int i, int d, int dt,
-                                      float (&v)[4]) {
+                                      Four &v) {
     if (SHARED == 1 || (SHARED == kAny && at >= 0))
         lds4<DT>(base + at, i, dt, v);
     else
@@ -252,11 +259,12 @@ inline JoinSmem join_layout(const JoinJob &j, bool bwd, int st, int v, bool gain
     return L;
 }
 
-// Three rows and the gains, two rows and the gains, two rows alone, or (rows too
-// long for shared memory) none.
+// Two rows and the gains, two rows alone, or (rows too long for shared memory)
+// none.  A third row cost more than it hid, in blocks per SM and in the wait for
+// the first rows (gradients of 2048 x 7168 68 us with three, 60 us with two).
 inline JoinSmem join_ring(const JoinJob &j, bool bwd, int v) {
-    for (int i = 0; i < 3; ++i) {
-        const JoinSmem L = join_layout(j, bwd, i == 0 ? 3 : 2, v, i < 2);
+    for (int i = 0; i < 2; ++i) {
+        const JoinSmem L = join_layout(j, bwd, 2, v, i == 0);
         if (L.total <= kSmemMax) return L;
     }
     return join_layout(j, bwd, 0, v, false);

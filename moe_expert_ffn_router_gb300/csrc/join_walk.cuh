@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
     const int G = gridDim.x, S = L.stages;
     int t = blockIdx.x;
     dependency_wait();
-    for (int s = 0; s + 1 < S; ++s) fetch(t + s * G, s);
+    if (S) fetch(t, 0);
     fill_smem(smem, j, L, false);
     float g_next = 1.f;
     if (j.gate_kind == MOE_GATE_SCALAR) g_next = ld_elem(j.gate, j.gdt, 0);
@@ -36,44 +36,46 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
     int slot_i = 0, flip = 0;
     for (; t < j.n; t += G, flip ^= 2) {
         if (S) {
-            fetch(t + (S - 1) * G, slot_i == 0 ? S - 1 : slot_i - 1);
-            wait_row(S);
+            // this row has arrived everywhere, and the row before is read
+            cp_wait<0>();
+            __syncthreads();
+            fetch(t + G, slot_i ^ 1);
         }
         const float gt = g_next;
         if (j.gate_kind == MOE_GATE_TOKEN && t + G < j.n) g_next = ld_elem(j.gate, j.gdt, t + G);
         const uint32_t slot = ring + slot_i * L.row;
-        slot_i = slot_i + 1 >= S ? 0 : slot_i + 1;
+        slot_i ^= 1;
         const int64_t row = (int64_t)t * j.d;
         const uint32_t at_h = has_h ? slot + L.h : ring + L.zero;
-        float y[V][4], h[V][4];
-        float s1[1] = {0.f}, s2[1] = {0.f};
+        Four y[V], h[V];
+        float s1[1], s2[1];
+        Four q = four(0.f);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
             row4<T::Y>(S, slot + L.y, j.y, row, c, j.d, j.ydt, y[v]);
             row4<T::H>(S, at_h, j.h, row, c, j.d, j.hdt, h[v]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s1[0] += y[v][e] * y[v][e];
+            q = fma4(y[v], y[v], q);
         }
         float r1 = 1.f;
         if (j.post_norm) {
+            s1[0] = sum4(q);
             block_sum(s1, red[flip]);
             r1 = 1.f / sqrtf(s1[0] * inv_d + j.eps);
         }
+        q = four(0.f);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
-            float g[4] = {gt, gt, gt, gt}, w[4];
+            Four g = four(gt), w;
             if (T::GATE == 1) lds4<RVQ_F32>(ring + L.chan, c, RVQ_F32, g);
             if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, j.d, j.gdt, g);
             gain4<T::W, T::SHARED>(L.w_post, ring, j.w_post, c, j.d, j.wdt, w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                h[v][e] = alpha * h[v][e] + g[e] * (y[v][e] * r1 * w[e]);
-                s2[0] += h[v][e] * h[v][e];
-            }
+            h[v] = fma4(g, y[v] * four(r1) * w, four(alpha) * h[v]);
+            q = fma4(h[v], h[v], q);
             put4<T::H>(j.h_out, row + c, j.h_out != nullptr && c < j.d, j.hdt, h[v]);
         }
+        s2[0] = sum4(q);
         block_sum(s2, red[flip + 1]);
         const float r2 = 1.f / sqrtf(s2[0] * inv_d + j.eps);
         if (j.rstd && threadIdx.x == 0) {
@@ -83,11 +85,9 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
-            float w[4];
+            Four w;
             gain4<T::W, T::SHARED>(L.w_pre, ring, j.w_pre, c, j.d, j.wdt, w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] *= h[v][e] * r2;
-            put4<T::X>(j.xn, row + c, j.xn != nullptr && c < j.d, j.xdt, w);
+            put4<T::X>(j.xn, row + c, j.xn != nullptr && c < j.d, j.xdt, h[v] * four(r2) * w);
         }
     }
     cp_wait<0>();
@@ -106,13 +106,13 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     __shared__ float red[2][96];
     const bool has_h = j.h != nullptr, has_dh = j.dh_out != nullptr, has_dx = j.dxn != nullptr;
     const float inv_d = 1.f / (float)j.d, alpha = has_h ? j.alpha : 0.f;
-    float acc[3][V][4], gate_sum = 0.f;
+    constexpr int SUMS = T::GATE == 1 ? 3 : 2;  // dw_post, dw_pre, dgate per channel
+    Four acc[SUMS][V];
+    float gate_sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < SUMS; ++k)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[k][v][e] = 0.f;
+        for (int v = 0; v < V; ++v) acc[k][v] = four(0.f);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
     const auto fetch = [&](int t, int s) {
         if (t < j.n) {
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     const int G = gridDim.x, S = L.stages;
     int t = blockIdx.x;
     dependency_wait();
-    for (int s = 0; s + 1 < S; ++s) fetch(t + s * G, s);
+    if (S) fetch(t, 0);
     fill_smem(smem, j, L, true);
     float r1n = 1.f, r2n = 1.f, gn = 1.f;
     const auto scalars = [&](int u) {
@@ -143,52 +143,53 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     int slot_i = 0, flip = 0;
     for (; t < j.n; t += G, flip ^= 1) {
         if (S) {
-            fetch(t + (S - 1) * G, slot_i == 0 ? S - 1 : slot_i - 1);
-            wait_row(S);
+            // this row has arrived everywhere, and the row before is read
+            cp_wait<0>();
+            __syncthreads();
+            fetch(t + G, slot_i ^ 1);
         }
         const float r1 = r1n, r2 = r2n, gt = gn;
         scalars(t + G);
         const uint32_t slot = ring + slot_i * L.row;
-        slot_i = slot_i + 1 >= S ? 0 : slot_i + 1;
+        slot_i ^= 1;
         const int64_t row = (int64_t)t * j.d;
         const uint32_t at_h = has_h ? slot + L.h : ring + L.zero;
         const uint32_t at_dh = has_dh ? slot + L.dh : ring + L.zero;
         const uint32_t at_dx = has_dx ? slot + L.dx : ring + L.zero;
-        // a group's y, h_out, P, dxn, q, gate, z, w_post (zeros past the row)
-        const auto group = [&](int c, float (&y)[4], float (&ho)[4], float (&P)[4], float (&dx)[4],
-                               float (&q)[4], float (&g)[4], float (&z)[4], float (&w)[4]) {
-            float wp[4];
-            row4<T::Y>(S, slot + L.y, j.y, row, c, j.d, j.ydt, y);
-            row4<T::H>(S, at_h, j.h, row, c, j.d, j.hdt, ho);
-            row4<T::H>(S, at_dh, j.dh_out, row, c, j.d, j.hdt, P);
-            row4<T::X>(S, at_dx, j.dxn, row, c, j.d, j.xdt, dx);
-            g[0] = g[1] = g[2] = g[3] = gt;
-            if (T::GATE == 1) lds4<RVQ_F32>(ring + L.chan, c, RVQ_F32, g);
-            if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, j.d, j.gdt, g);
-            gain4<T::W, T::SHARED>(L.w_post, ring, j.w_post, c, j.d, j.wdt, w);
-            gain4<T::W, T::SHARED>(L.w_pre, ring, j.w_pre, c, j.d, j.wdt, wp);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                z[e] = y[e] * r1 * w[e];
-                ho[e] = alpha * ho[e] + g[e] * z[e];
-                q[e] = dx[e] * wp[e];
-                P[e] += r2 * q[e];
-            }
+        const Four R1 = four(r1), R2 = four(r2), AL = four(alpha);
+        // a group's y r1, z, h_out, q, P, dxn, gate, w_post (zeros past the row)
+        struct Group {
+            Four yr, z, ho, q, P, dx, g, w;
         };
-        float s[3] = {0.f, 0.f, 0.f};
+        const auto group = [&](int c) {
+            Group u;
+            Four y, h, dh, wp;
+            row4<T::Y>(S, slot + L.y, j.y, row, c, j.d, j.ydt, y);
+            row4<T::H>(S, at_h, j.h, row, c, j.d, j.hdt, h);
+            row4<T::H>(S, at_dh, j.dh_out, row, c, j.d, j.hdt, dh);
+            row4<T::X>(S, at_dx, j.dxn, row, c, j.d, j.xdt, u.dx);
+            u.g = four(gt);
+            if (T::GATE == 1) lds4<RVQ_F32>(ring + L.chan, c, RVQ_F32, u.g);
+            if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, j.d, j.gdt, u.g);
+            gain4<T::W, T::SHARED>(L.w_post, ring, j.w_post, c, j.d, j.wdt, u.w);
+            gain4<T::W, T::SHARED>(L.w_pre, ring, j.w_pre, c, j.d, j.wdt, wp);
+            u.yr = y * R1;
+            u.z = u.yr * u.w;
+            u.ho = fma4(u.g, u.z, AL * h);
+            u.q = u.dx * wp;
+            u.P = fma4(R2, u.q, dh);
+            return u;
+        };
+        Four s0 = four(0.f), sA = four(0.f), sB = four(0.f);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (v * blockDim.x + threadIdx.x) * 4;
-            float y[4], ho[4], P[4], dx[4], q[4], g[4], z[4], w[4];
-            group(c, y, ho, P, dx, q, g, z, w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float gz = T::GATE == 0 ? z[e] : g[e] * z[e];
-                s[0] += q[e] * ho[e];
-                s[1] += P[e] * gz;
-                s[2] += ho[e] * gz;
-            }
+            const Group u = group((v * blockDim.x + threadIdx.x) * 4);
+            const Four gz = T::GATE == 0 ? u.z : u.g * u.z;
+            s0 = fma4(u.q, u.ho, s0);
+            sA = fma4(u.P, gz, sA);
+            sB = fma4(u.ho, gz, sB);
         }
+        float s[3] = {sum4(s0), sum4(sA), sum4(sB)};
         block_sum(s, red[flip]);
         const float cS = r2 * r2 * r2 * inv_d * s[0];
         const float ez = s[1] - cS * s[2];  // sum e z (one gate per row) or sum e gate z
@@ -198,29 +199,23 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
             else
                 gate_sum += ez;
         }
-        const float cy = j.post_norm ? r1 * r1 * inv_d * (T::GATE == 0 ? gt * ez : ez) : 0.f;
+        // dy = r1 (dz w_post - y r1 mean(...)): mean = (sum e gate z) / d
+        const float cy = j.post_norm ? inv_d * (T::GATE == 0 ? gt * ez : ez) : 0.f;
+        const Four NS = four(-cS), NY = four(-cy);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
-            float y[4], ho[4], P[4], dx[4], q[4], g[4], z[4], w[4], o[4];
-            group(c, y, ho, P, dx, q, g, z, w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                P[e] -= cS * ho[e];
-                o[e] = alpha * P[e];
-            }
-            put4<T::H>(j.dh, row + c, j.dh != nullptr && c < j.d, j.hdt, o);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float dz = g[e] * P[e], ze = P[e] * z[e];
-                o[e] = r1 * dz * w[e] - y[e] * cy;
-                acc[0][v][e] += dz * y[e] * r1;
-                acc[1][v][e] += dx[e] * ho[e] * r2;
-                acc[2][v][e] += ze;
-                P[e] = ze;
-            }
-            put4<T::Y>(j.dy, row + c, j.dy != nullptr && c < j.d, j.ydt, o);
-            if (T::GATE == 2) put4<T::G>(j.dgate, row + c, j.dgate != nullptr && c < j.d, j.gdt, P);
+            const Group u = group(c);
+            const Four e = fma4(NS, u.ho, u.P);
+            put4<T::H>(j.dh, row + c, j.dh != nullptr && c < j.d, j.hdt, AL * e);
+            const Four dz = u.g * e;
+            put4<T::Y>(j.dy, row + c, j.dy != nullptr && c < j.d, j.ydt,
+                       R1 * fma4(NY, u.yr, dz * u.w));
+            acc[0][v] = fma4(dz, u.yr, acc[0][v]);
+            acc[1][v] = fma4(u.dx, u.ho * R2, acc[1][v]);
+            if (T::GATE == 1) acc[SUMS - 1][v] = fma4(e, u.z, acc[SUMS - 1][v]);
+            if (T::GATE == 2)
+                put4<T::G>(j.dgate, row + c, j.dgate != nullptr && c < j.d, j.gdt, e * u.z);
         }
     }
     cp_wait<0>();
@@ -228,7 +223,7 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     const bool want[3] = {j.dw_post != nullptr, j.dw_pre != nullptr,
                           T::GATE == 1 && j.dgate != nullptr};
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < SUMS; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
