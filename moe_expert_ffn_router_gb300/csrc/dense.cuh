@@ -305,7 +305,7 @@ struct JoinJob {
     int slots;              // blocks of the gradient kernel
 };
 constexpr int kJoinMaxD = 16384;
-int join_bwd_slots(int n);  // at most, for the workspace
+int join_bwd_slots(int n, int d);  // at most, for the workspace
 rvq_status launch_norm_join(const JoinJob &job, cudaStream_t stream);
 rvq_status launch_norm_join_bwd(const JoinJob &job, cudaStream_t stream);
 

@@ -492,7 +492,7 @@ rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rv
 }
 
 static size_t join_part_bytes(int32_t n, int32_t d) {
-    return (size_t)join_bwd_slots(n) * ((size_t)3 * d + 1) * 4;
+    return (size_t)join_bwd_slots(n, d) * ((size_t)3 * d + 1) * 4;
 }
 
 size_t moe_norm_join_workspace_bytes(int32_t n, int32_t d) {
@@ -558,7 +558,7 @@ rvq_status moe_norm_join_backward(const void *dh_out_dev, const void *dxn_dev, r
     j.dw_post = dw_post_dev;
     j.dw_pre = dw_pre_dev;
     j.part = (float *)((uint8_t *)ws_dev + RVQ_WS_STATUS_BYTES);
-    j.slots = join_bwd_slots(n);
+    j.slots = join_bwd_slots(n, d);
     return launch_norm_join_bwd(j, (cudaStream_t)stream);
 }
 

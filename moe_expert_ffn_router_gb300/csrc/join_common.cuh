@@ -123,10 +123,10 @@ __device__ __forceinline__ void put4(void *p, int64_t i, bool on, int dt, const 
 struct JoinSmem {
     int pad;
     int y, h, dh, dx, gate, row;  // places in a ring slot; a slot's size
-    int stages;                   // ring depth: 2, or 0 (rows are read from global memory)
+    int stages;                   // ring depth: 2, 1, or 0 (rows are read from global memory)
     int zero;                     // after the ring: a row of zeros for absent tensors
     int chan;                     // a channel gate
-    int w_post, w_pre;            // gains (1 for absent ones); -1: read from global memory
+    int w_post, w_pre;            // gains (1 for absent ones), with a ring
     int total;
 };
 
@@ -156,14 +156,14 @@ __device__ __forceinline__ void row4(int stages, uint32_t at, const void *p, int
         lds4<DT>(at, i, dt, v);
 }
 
-// four gains: in shared memory (SHARED 1), in global memory (0), or as `at` says
-template <int DT, int SHARED>
-__device__ __forceinline__ void gain4(int at, uint32_t base, const void *p, int i, int d, int dt,
+// four gains: in shared memory, or (no ring) in global memory
+template <int DT>
+__device__ __forceinline__ void gain4(int stages, uint32_t at, const void *p, int i, int d, int dt,
                                       Four &v) {
-    if (SHARED == 1 || (SHARED == kAny && at >= 0))
-        lds4<DT>(base + at, i, dt, v);
-    else
+    if (DT == kAny && stages == 0)
         ldg4<DT>(p, i, p != nullptr && i < d, dt, 1.f, v);
+    else
+        lds4<DT>(at, i, dt, v);
 }
 
 // Zeros past the rows' ends (and the row of zeros), gains, a channel gate; none of
@@ -189,7 +189,7 @@ __device__ __forceinline__ void fill_smem(uint8_t *smem, const JoinJob &j, const
         reinterpret_cast<uint4 *>(smem + L.zero)[i] = zero;
     const uint32_t one = j.wdt == RVQ_F32 ? 0x3F800000u : j.wdt == RVQ_BF16 ? 0x3F803F80u : 0x3C003C00u;
     const auto gain = [&](int at, const void *src) {
-        if (at < 0) return;
+        if (L.stages == 0) return;
         pad(at, j.wdt);
         const int n16 = j.d * esize(j.wdt) / 16;
         for (int i = threadIdx.x; i < n16; i += blockDim.x)
@@ -211,14 +211,17 @@ __device__ __forceinline__ void fill_smem(uint8_t *smem, const JoinJob &j, const
 
 // Types of an instance: h (and h_out, dh, dh_out), y (and dy), xn (and dxn),
 // gains, and a full gate.  GATE 0: one value per row, 1: per channel, 2: full.
-// SHARED: gains in shared memory (1), global (0), or as the layout says (kAny).
-template <int V_, int H_, int Y_, int X_, int W_, int G_, int GATE_, int SHARED_>
+template <int V_, int H_, int Y_, int X_, int W_, int G_, int GATE_>
 struct JoinTypes {
-    static constexpr int V = V_, H = H_, Y = Y_, X = X_, W = W_, G = G_, GATE = GATE_,
-                         SHARED = SHARED_;
+    static constexpr int V = V_, H = H_, Y = Y_, X = X_, W = W_, G = G_, GATE = GATE_;
 };
 
-constexpr int kBwdBlocksPerSm = 4;   // the partial sums to add grow with the blocks
+// Blocks per SM of the gradients' kernel, at most: the partial sums to add grow
+// with the blocks, so only as many as give an SM 512 threads.
+inline int join_bwd_blocks(int d) {
+    const int b = 512 / (((d / 4 + 3) / 4 + 31) / 32 * 32);
+    return b < 4 ? 4 : b;
+}
 constexpr int kSmemMax = 225 << 10;  // of a block, beside its static part
 
 inline int join_threads(int d, int group, int v) {
@@ -226,7 +229,7 @@ inline int join_threads(int d, int group, int v) {
     return (t + 31) / 32 * 32;
 }
 
-inline JoinSmem join_layout(const JoinJob &j, bool bwd, int st, int v, bool gains) {
+inline JoinSmem join_layout(const JoinJob &j, bool bwd, int st, int v) {
     JoinSmem L = {};
     L.pad = join_threads(j.d, 4, v) * v * 4;
     const auto row = [&](const void *p, int dt) { return p ? L.pad * (dt == RVQ_F32 ? 4 : 2) : 0; };
@@ -248,8 +251,7 @@ inline JoinSmem join_layout(const JoinJob &j, bool bwd, int st, int v, bool gain
     if (st > 0 && (!j.h || (bwd && (!j.dh_out || !j.dxn)))) at += L.pad * 4;
     L.chan = at;
     at += j.gate_kind == MOE_GATE_CHANNEL ? L.pad * 4 : 0;
-    L.w_post = L.w_pre = -1;
-    if (gains) {
+    if (st > 0) {
         L.w_post = at;
         at += row(&L, j.wdt);
         L.w_pre = at;
@@ -259,15 +261,16 @@ inline JoinSmem join_layout(const JoinJob &j, bool bwd, int st, int v, bool gain
     return L;
 }
 
-// Two rows and the gains, two rows alone, or (rows too long for shared memory)
-// none.  A third row cost more than it hid, in blocks per SM and in the wait for
-// the first rows (gradients of 2048 x 7168 68 us with three, 60 us with two).
+// Two rows, one (then a block's copies and its work take turns), or (rows of more
+// than 8192 fp32 columns) none.  A third row cost more than it hid, in blocks per
+// SM and in the wait for the first rows (gradients of 2048 x 7168 68 us with
+// three, 60 us with two).
 inline JoinSmem join_ring(const JoinJob &j, bool bwd, int v) {
-    for (int i = 0; i < 2; ++i) {
-        const JoinSmem L = join_layout(j, bwd, 2, v, i == 0);
+    for (int st = 2; st > 0; --st) {
+        const JoinSmem L = join_layout(j, bwd, st, v);
         if (L.total <= kSmemMax) return L;
     }
-    return join_layout(j, bwd, 0, v, false);
+    return join_layout(j, bwd, 0, v);
 }
 
 // Walking blocks of kernel K: as many as an SM holds at once, up to `most`.
@@ -290,39 +293,38 @@ template <auto K>
     return RVQ_OK;
 }
 
-// Whether a typed instance serves a job: rows of up to 8192 columns that fit the
-// ring, a 16-bit xn, every 16-bit tensor of its type, a full gate of h's type,
-// and, for gains left in global memory, fp32 h and gains (shorter types fit).
-inline bool join_typed(const JoinJob &j, const JoinSmem &L) {
-    const int s16 = j.xdt;
+// Whether a typed instance serves a job: rows of up to 8192 columns (they fit the
+// ring), every 16-bit tensor of type s16, an fp32 xn beside an fp32 h only, and a
+// full gate of h's type.
+inline bool join_typed(const JoinJob &j, const JoinSmem &L, int s16) {
     const auto fits = [&](int dt) { return dt == RVQ_F32 || dt == s16; };
-    return s16 != RVQ_F32 && j.d <= 8192 && L.stages > 0 && fits(j.hdt) && fits(j.ydt) &&
-           fits(j.wdt) && (j.gate_kind != MOE_GATE_FULL || j.gdt == j.hdt) &&
-           (L.w_pre >= 0 || (j.hdt == RVQ_F32 && j.wdt == RVQ_F32));
+    return j.d <= 8192 && L.stages > 0 && fits(j.hdt) && fits(j.ydt) && fits(j.xdt) &&
+           fits(j.wdt) && (j.xdt != RVQ_F32 || j.hdt == RVQ_F32) &&
+           (j.gate_kind != MOE_GATE_FULL || j.gdt == j.hdt);
 }
 
 // Calls f(JoinTypes<...>()) for the typed instance of a job.
 template <int S16, class F>
-rvq_status with_types(const JoinJob &j, const JoinSmem &L, F &&f) {
+rvq_status with_types(const JoinJob &j, F &&f) {
     using C0 = std::integral_constant<int, S16>;
     using C1 = std::integral_constant<int, (int)RVQ_F32>;
-    const auto gate = [&](auto H, auto Y, auto W, auto G) {
+    const auto gate = [&](auto H, auto Y, auto X, auto W) {
         if (j.gate_kind == MOE_GATE_FULL)
-            return f(JoinTypes<4, H.value, Y.value, S16, W.value, H.value, 2, G.value>());
+            return f(JoinTypes<4, H.value, Y.value, X.value, W.value, H.value, 2>());
         if (j.gate_kind == MOE_GATE_CHANNEL)
-            return f(JoinTypes<4, H.value, Y.value, S16, W.value, RVQ_F32, 1, G.value>());
-        return f(JoinTypes<4, H.value, Y.value, S16, W.value, RVQ_F32, 0, G.value>());
+            return f(JoinTypes<4, H.value, Y.value, X.value, W.value, RVQ_F32, 1>());
+        return f(JoinTypes<4, H.value, Y.value, X.value, W.value, RVQ_F32, 0>());
     };
-    using Shared = std::integral_constant<int, 1>;
-    using Global = std::integral_constant<int, 0>;
-    const auto pick_w = [&](auto H, auto Y) {
-        if (j.wdt != RVQ_F32) return gate(H, Y, C0(), Shared());
+    const auto pick_w = [&](auto H, auto Y, auto X) {
+        return j.wdt == RVQ_F32 ? gate(H, Y, X, C1()) : gate(H, Y, X, C0());
+    };
+    const auto pick_x = [&](auto H, auto Y) {
         if constexpr (H.value == (int)RVQ_F32)
-            if (L.w_pre < 0) return gate(H, Y, C1(), Global());
-        return gate(H, Y, C1(), Shared());
+            if (j.xdt == RVQ_F32) return pick_w(H, Y, C1());
+        return pick_w(H, Y, C0());
     };
     const auto pick_y = [&](auto H) {
-        return j.ydt == RVQ_F32 ? pick_w(H, C1()) : pick_w(H, C0());
+        return j.ydt == RVQ_F32 ? pick_x(H, C1()) : pick_x(H, C0());
     };
     return j.hdt == RVQ_F32 ? pick_y(C1()) : pick_y(C0());
 }
@@ -332,10 +334,10 @@ constexpr int kAnyV = 8;
 template <class F>
 rvq_status with_any_types(const JoinJob &j, F &&f) {
     if (j.gate_kind == MOE_GATE_FULL)
-        return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 2, kAny>());
+        return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 2>());
     if (j.gate_kind == MOE_GATE_CHANNEL)
-        return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 1, kAny>());
-    return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 0, kAny>());
+        return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 1>());
+    return f(JoinTypes<kAnyV, kAny, kAny, kAny, kAny, kAny, 0>());
 }
 
 // the walking kernels by 16-bit type (one translation unit each)
@@ -346,10 +348,11 @@ rvq_status join_walk_any(JoinJob &j, const JoinSmem &L, bool bwd, cudaStream_t s
 inline rvq_status join_walk(JoinJob &j, bool bwd, cudaStream_t stream) {
     // types of absent tensors do not matter: take those of the others
     if (!(j.w_post || j.w_pre || j.dw_post || j.dw_pre)) j.wdt = RVQ_F32;
-    if (!(bwd ? j.dxn : j.xn)) j.xdt = j.hdt != RVQ_F32 ? j.hdt : j.ydt != RVQ_F32 ? j.ydt : RVQ_BF16;
+    if (!(bwd ? j.dxn : j.xn)) j.xdt = j.hdt;
     const JoinSmem L = join_ring(j, bwd, 4);
-    if (!join_typed(j, L)) return join_walk_any(j, join_ring(j, bwd, kAnyV), bwd, stream);
-    return j.xdt == RVQ_BF16 ? join_walk_bf16(j, L, bwd, stream) : join_walk_f16(j, L, bwd, stream);
+    if (join_typed(j, L, RVQ_BF16)) return join_walk_bf16(j, L, bwd, stream);
+    if (join_typed(j, L, RVQ_F16)) return join_walk_f16(j, L, bwd, stream);
+    return join_walk_any(j, join_ring(j, bwd, kAnyV), bwd, stream);
 }
 
 }  // namespace rvq

@@ -35,16 +35,20 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
     if (j.gate_kind == MOE_GATE_TOKEN && t < j.n) g_next = ld_elem(j.gate, j.gdt, t);
     int slot_i = 0, flip = 0;
     for (; t < j.n; t += G, flip ^= 2) {
+        if (S == 1 && t >= G) {  // the one row's place is free
+            __syncthreads();
+            fetch(t, 0);
+        }
         if (S) {
             // this row has arrived everywhere, and the row before is read
             cp_wait<0>();
             __syncthreads();
-            fetch(t + G, slot_i ^ 1);
         }
+        if (S == 2) fetch(t + G, slot_i ^ 1);
         const float gt = g_next;
         if (j.gate_kind == MOE_GATE_TOKEN && t + G < j.n) g_next = ld_elem(j.gate, j.gdt, t + G);
         const uint32_t slot = ring + slot_i * L.row;
-        slot_i ^= 1;
+        if (S == 2) slot_i ^= 1;
         const int64_t row = (int64_t)t * j.d;
         const uint32_t at_h = has_h ? slot + L.h : ring + L.zero;
         Four y[V], h[V];
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
             Four g = four(gt), w;
             if (T::GATE == 1) lds4<RVQ_F32>(ring + L.chan, c, RVQ_F32, g);
             if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, j.d, j.gdt, g);
-            gain4<T::W, T::SHARED>(L.w_post, ring, j.w_post, c, j.d, j.wdt, w);
+            gain4<T::W>(S, ring + L.w_post, j.w_post, c, j.d, j.wdt, w);
             h[v] = fma4(g, y[v] * four(r1) * w, four(alpha) * h[v]);
             q = fma4(h[v], h[v], q);
             put4<T::H>(j.h_out, row + c, j.h_out != nullptr && c < j.d, j.hdt, h[v]);
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(512) join_ring_kernel(const JoinJob j, const J
         for (int v = 0; v < V; ++v) {
             const int c = (v * blockDim.x + threadIdx.x) * 4;
             Four w;
-            gain4<T::W, T::SHARED>(L.w_pre, ring, j.w_pre, c, j.d, j.wdt, w);
+            gain4<T::W>(S, ring + L.w_pre, j.w_pre, c, j.d, j.wdt, w);
             put4<T::X>(j.xn, row + c, j.xn != nullptr && c < j.d, j.xdt, h[v] * four(r2) * w);
         }
     }
@@ -142,16 +146,20 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
     scalars(t);
     int slot_i = 0, flip = 0;
     for (; t < j.n; t += G, flip ^= 1) {
+        if (S == 1 && t >= G) {  // the one row's place is free
+            __syncthreads();
+            fetch(t, 0);
+        }
         if (S) {
             // this row has arrived everywhere, and the row before is read
             cp_wait<0>();
             __syncthreads();
-            fetch(t + G, slot_i ^ 1);
         }
+        if (S == 2) fetch(t + G, slot_i ^ 1);
         const float r1 = r1n, r2 = r2n, gt = gn;
         scalars(t + G);
         const uint32_t slot = ring + slot_i * L.row;
-        slot_i ^= 1;
+        if (S == 2) slot_i ^= 1;
         const int64_t row = (int64_t)t * j.d;
         const uint32_t at_h = has_h ? slot + L.h : ring + L.zero;
         const uint32_t at_dh = has_dh ? slot + L.dh : ring + L.zero;
@@ -171,8 +179,8 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
             u.g = four(gt);
             if (T::GATE == 1) lds4<RVQ_F32>(ring + L.chan, c, RVQ_F32, u.g);
             if (T::GATE == 2) row4<T::G>(S, slot + L.gate, j.gate, row, c, j.d, j.gdt, u.g);
-            gain4<T::W, T::SHARED>(L.w_post, ring, j.w_post, c, j.d, j.wdt, u.w);
-            gain4<T::W, T::SHARED>(L.w_pre, ring, j.w_pre, c, j.d, j.wdt, wp);
+            gain4<T::W>(S, ring + L.w_post, j.w_post, c, j.d, j.wdt, u.w);
+            gain4<T::W>(S, ring + L.w_pre, j.w_pre, c, j.d, j.wdt, wp);
             u.yr = y * R1;
             u.z = u.yr * u.w;
             u.ho = fma4(u.g, u.z, AL * h);
@@ -237,7 +245,7 @@ constexpr int kFwdBlocksPerSm = 16;
 template <class T>
 rvq_status walk(JoinJob &j, const JoinSmem &L, bool bwd, cudaStream_t stream) {
     const int threads = join_threads(j.d, 4, T::V);
-    if (bwd) return launch_walk<join_bwd_kernel<T>>(j, L, threads, kBwdBlocksPerSm, stream);
+    if (bwd) return launch_walk<join_bwd_kernel<T>>(j, L, threads, join_bwd_blocks(j.d), stream);
     return launch_walk<join_ring_kernel<T>>(j, L, threads, kFwdBlocksPerSm, stream);
 }
 

@@ -4,7 +4,7 @@
 namespace rvq {
 
 rvq_status join_walk_bf16(JoinJob &j, const JoinSmem &L, bool bwd, cudaStream_t stream) {
-    return with_types<RVQ_BF16>(j, L, [&](auto t) { return walk<decltype(t)>(j, L, bwd, stream); });
+    return with_types<RVQ_BF16>(j, [&](auto t) { return walk<decltype(t)>(j, L, bwd, stream); });
 }
 
 }  // namespace rvq

@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinJob j) {
 
 }  // namespace
 
-int join_bwd_slots(int n) {
-    const int most = kBwdBlocksPerSm * num_sms();
+int join_bwd_slots(int n, int d) {
+    const int most = join_bwd_blocks(d) * num_sms();
     return n < most ? n : most;
 }
 
