@@ -5,12 +5,14 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (RVQ_WS_STATUS_BYTES, moe_bank_init, moe_bank_record_bytes, moe_bank_validate,
-               moe_bank_write_expert, moe_cache_bank, moe_cache_create, moe_cache_destroy,
-               moe_cache_stats, moe_combine, moe_expert_ffn, moe_layer_forward,
-               moe_layer_forward_host, moe_layer_forward_prenorm, moe_layer_forward_streamed,
-               moe_layer_graph_create,
-               moe_rms_norm, moe_route,
+from . import (MOE_ACT_SILU, RVQ_WS_STATUS_BYTES, moe_bank_init, moe_bank_record_bytes,
+               moe_bank_validate, moe_bank_write_expert, moe_cache_bank, moe_cache_create,
+               moe_cache_destroy, moe_cache_stats, moe_combine, moe_expert_ffn,
+               moe_gated_linear, moe_gated_linear_backward, moe_gated_linear_workspace_bytes,
+               moe_layer_forward, moe_layer_forward_host, moe_layer_forward_prenorm,
+               moe_layer_forward_streamed, moe_layer_graph_create, moe_linear,
+               moe_linear_backward, moe_linear_workspace_bytes, moe_norm_join, moe_rms_norm,
+               moe_route,
                moe_router_logits,
                moe_workspace_bytes, rvq_ws_clear, rvq_ws_status)
 
@@ -282,4 +284,112 @@ class MoeStreamedStack:
             pass
 
 
-__all__ = ["MoeLayer", "MoeStack", "MoeStreamedStack", "RVQ_WS_STATUS_BYTES"]
+class SharedExpert:
+    """A dense (unquantised) feed-forward block that every token passes, beside
+    the routed experts: out = (act(x Wg^T) * (x Wu^T)) Wd^T, with gradients.
+    Weights are bf16 or fp16: gate and up [f][d], down [d][f]."""
+
+    def __init__(self, wg, wu, wd, act: int = MOE_ACT_SILU, device: str | torch.device = "cuda"):
+        self.device = torch.device(device)
+        self.wg, self.wu, self.wd = (_dev(w, self.device) for w in (wg, wu, wd))
+        self.f, self.d = self.wg.shape
+        assert self.wu.shape == (self.f, self.d) and self.wd.shape == (self.d, self.f)
+        self.act = act
+        self._bufs = {}
+
+    def buffers(self, n: int, train: bool = False) -> dict:
+        """Outputs and workspace for n tokens, kept; train adds what the
+        gradients need and receive."""
+        b = self._bufs.get((n, train))
+        if b is None:
+            def new(*shape, dtype=self.wg.dtype):
+                return torch.empty(shape, dtype=dtype, device=self.device)
+
+            nbytes = max(moe_gated_linear_workspace_bytes(n, self.f, self.d, train),
+                         moe_linear_workspace_bytes(n, self.d, self.f, train))
+            b = dict(hidden=new(n, self.f), out=new(n, self.d, dtype=torch.float32),
+                     ws=new(nbytes, dtype=torch.uint8))
+            if train:
+                b.update(pre=new(2, n, self.f, dtype=torch.float32), dhidden=new(n, self.f),
+                         dx=new(n, self.d), dwg=torch.empty_like(self.wg),
+                         dwu=torch.empty_like(self.wu), dwd=torch.empty_like(self.wd))
+            rvq_ws_clear(b["ws"])
+            self._bufs[n, train] = b
+        return b
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
+                train: bool = False) -> dict:
+        """out (fp32) = residual + the block of x; with train the gradients'
+        inputs are kept for backward()."""
+        n = x.shape[0]
+        b = self.buffers(n, train)
+        moe_gated_linear(x, self.wg, self.wu, n, self.f, self.d, b["hidden"], b["ws"],
+                         act=self.act, pre=b.get("pre"))
+        moe_linear(b["hidden"], self.wd, n, self.d, self.f, b["out"], b["ws"], residual=residual)
+        return b
+
+    def backward(self, x: torch.Tensor, dout: torch.Tensor) -> dict:
+        """Gradients of a forward(x, train=True): dx, dwg, dwu, dwd from dout (the
+        weights' type); the residual's gradient is dout."""
+        n = x.shape[0]
+        b = self.buffers(n, True)
+        moe_linear_backward(dout, b["hidden"], self.wd, n, self.d, self.f, b["ws"],
+                            dx=b["dhidden"], dw=b["dwd"])
+        moe_gated_linear_backward(b["dhidden"], x, self.wg, self.wu, b["pre"], n, self.f, self.d,
+                                  b["ws"], dx=b["dx"], dwg=b["dwg"], dwu=b["dwu"], act=self.act)
+        return b
+
+    def status(self, n: int, train: bool = False) -> tuple[int, int]:
+        return rvq_ws_status(self.buffers(n, train)["ws"])
+
+
+class SharedExpertStack:
+    """Blocks of routed experts with a shared expert, normed before and after:
+        xn = norm(h) * w_pre;  y = shared(xn) + sum_slot w * expert(xn)
+        h  = alpha * h + gate * norm(y) * w_post
+    for each block (MoeLayer, SharedExpert, dict of w_pre, w_post, gate: tensors
+    or None).  The norm after a block, its gate, the residual's scale and the
+    norm before the next block are one launch (moe_norm_join), and the shared
+    expert's output enters the routed layer as its residual.  h is fp32."""
+
+    def __init__(self, blocks, alpha: float = 1.0, eps: float = 1e-6):
+        assert blocks and all(L.d == S.d == blocks[0][0].d for L, S, _ in blocks)
+        self.blocks, self.alpha, self.eps = list(blocks), alpha, eps
+        self._bufs = {}
+
+    def buffers(self, n: int) -> list[dict]:
+        b = self._bufs.get(n)
+        if b is None:
+            b = []
+            for L, _, _ in self.blocks:
+                bl = L.buffers(n)
+                bl["xn"] = torch.empty((n, L.d), dtype=torch.bfloat16, device=L.device)
+                bl["h"] = torch.empty((n, L.d), dtype=torch.float32, device=L.device)
+                b.append(bl)
+            self._bufs[n] = b
+        return b
+
+    def forward(self, x: torch.Tensor, tc_min_tokens: int = 0) -> list[dict]:
+        """x [n][d] fp32; returns the blocks' buffers ("xn" the normed input,
+        "out" y, "h" the stream after the block)."""
+        n = x.shape[0]
+        bufs = self.buffers(n)
+        first = self.blocks[0]
+        moe_norm_join(x, n, first[0].d, None, bufs[0]["xn"], post_norm=False,
+                      w_pre=first[2].get("w_pre"), eps=self.eps)
+        h = x
+        for i, (L, S, p) in enumerate(self.blocks):
+            b = bufs[i]
+            shared = S.forward(b["xn"])["out"]
+            L.forward(b["xn"], b, tc_min_tokens=tc_min_tokens, residual=shared)
+            last = i + 1 == len(self.blocks)
+            moe_norm_join(b["out"], n, L.d, b["h"], None if last else bufs[i + 1]["xn"], h=h,
+                          alpha=self.alpha, gate=p.get("gate"), w_post=p.get("w_post"),
+                          w_pre=None if last else self.blocks[i + 1][2].get("w_pre"),
+                          eps=self.eps)
+            h = b["h"]
+        return bufs
+
+
+__all__ = ["MoeLayer", "MoeStack", "MoeStreamedStack", "SharedExpert", "SharedExpertStack",
+           "RVQ_WS_STATUS_BYTES"]
