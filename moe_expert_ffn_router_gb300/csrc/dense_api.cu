@@ -114,6 +114,13 @@ WsPlan plan_ws(int mats, int32_t n, int32_t rows, int32_t cols, bool backward) {
     return P;
 }
 
+// the products of dx and dw, each if wanted
+rvq_status launch_gradients(const DenseJob &x, const DenseJob &w, cudaStream_t st) {
+    if (x.out[0] && w.out[0]) return launch_dense_gemm_two(x, w, st);
+    if (x.out[0]) return launch_dense_gemm(x, st);
+    return w.out[0] ? launch_dense_gemm(w, st) : RVQ_OK;
+}
+
 // a gradient's workspace serves the forward call too
 size_t ws_bytes_of(int mats, int32_t n, int32_t rows, int32_t cols, int32_t backward) {
     if (!dense_shape(n, rows, cols)) return 0;
@@ -293,28 +300,24 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
     j.status = (uint32_t *)ws_dev;
     j.partial = (float *)(ws + P.off_partial);
     j.b_t = 1;
-    if (dx_dev) {  // [n][rows] x [rows][cols]
-        j.M = n;
-        j.N = cols;
-        j.K = rows;
-        j.b[0] = w_dev;
-        j.ldb = ldw;
-        j.out[0] = dx_dev;
-        j.ldo = lddx;
-        RVQ_TRY(launch_dense_gemm(j, st));
-    }
-    if (dw_dev) {  // [n][rows]^T x [n][cols]
-        j.a_t = 1;
-        j.M = rows;
-        j.N = cols;
-        j.K = n;
-        j.b[0] = x_dev;
-        j.ldb = ldx;
-        j.out[0] = dw_dev;
-        j.ldo = lddw;
-        RVQ_TRY(launch_dense_gemm(j, st));
-    }
-    return RVQ_OK;
+    // dx: [n][rows] x [rows][cols]; dw: [n][rows]^T x [n][cols]
+    DenseJob w = j;
+    j.M = n;
+    j.N = cols;
+    j.K = rows;
+    j.b[0] = w_dev;
+    j.ldb = ldw;
+    j.out[0] = dx_dev;
+    j.ldo = lddx;
+    w.a_t = 1;
+    w.M = rows;
+    w.N = cols;
+    w.K = n;
+    w.b[0] = x_dev;
+    w.ldb = ldx;
+    w.out[0] = dw_dev;
+    w.ldo = lddw;
+    return launch_gradients(j, w, st);
 }
 
 rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const void *x_dev,
@@ -385,33 +388,27 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
     j.b_t = 1;
     j.status = (uint32_t *)ws_dev;
     j.partial = (float *)(ws + P.off_partial);
-    if (dx_dev) {
-        j.mode = DG_SUM_K;
-        j.M = n;
-        j.N = cols;
-        j.K = rows;
-        j.b[0] = wg_dev;
-        j.b[1] = wu_dev;
-        j.ldb = ldw;
-        j.out[0] = dx_dev;
-        j.ldo = lddx;
-        RVQ_TRY(launch_dense_gemm(j, st));
-    }
-    if (dwg_dev) {
-        j.mode = DG_PAIR_M;
-        j.a_t = 1;
-        j.M = rows;
-        j.N = cols;
-        j.K = n;
-        j.b[0] = x_dev;
-        j.b[1] = nullptr;
-        j.ldb = ldx;
-        j.out[0] = dwg_dev;
-        j.out[1] = dwu_dev;
-        j.ldo = lddw;
-        RVQ_TRY(launch_dense_gemm(j, st));
-    }
-    return RVQ_OK;
+    DenseJob w = j;
+    j.mode = DG_SUM_K;
+    j.M = n;
+    j.N = cols;
+    j.K = rows;
+    j.b[0] = wg_dev;
+    j.b[1] = wu_dev;
+    j.ldb = ldw;
+    j.out[0] = dx_dev;
+    j.ldo = lddx;
+    w.mode = DG_PAIR_M;
+    w.a_t = 1;
+    w.M = rows;
+    w.N = cols;
+    w.K = n;
+    w.b[0] = x_dev;
+    w.ldb = ldx;
+    w.out[0] = dwg_dev;
+    w.out[1] = dwu_dev;
+    w.ldo = lddw;
+    return launch_gradients(j, w, st);
 }
 
 // ---------------------------------------------------------------- norm join

@@ -61,6 +61,15 @@ struct GemmArgs {
     uint32_t *status;
 };
 
+// One product, or two for one launch (the gradients dx and dw, whose tiles alone
+// leave CTA pairs idle), with the tensor maps of their operands.
+template <int JOBS>
+struct GemmParams {
+    CUtensorMap a[JOBS][2], b[JOBS][2];
+    GemmArgs g[JOBS];
+    int bonus;           // see Work
+};
+
 __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
                  : "memory");
@@ -105,21 +114,47 @@ __device__ __forceinline__ void tile_at(const GemmArgs &g, int t, int &m, int &n
 }
 
 // The work of a CTA pair, the same sequence in every role: units of one tile and
-// one run of its slices.
+// one run of its slices, every `pairs`-th unit of the first product, then units of
+// the second.  Pairs that got one unit less of the first (those from U0 mod pairs
+// on) first take `bonus` units of the second alone, as many as that one lasts, so
+// that all pairs end together.
+template <int JOBS>
 struct Work {
-    int unit, pairs, units;
-    int m, n, part, k0, k1;
+    int pair, pairs, unit, round;
+    int job, m, n, part, k0, k1;
 
-    __device__ __forceinline__ Work(const GemmArgs &g, int pair, int pairs_)
-        : unit(pair), pairs(pairs_), units(g.mt * g.nt * g.parts) {}
-    __device__ __forceinline__ bool next(const GemmArgs &g) {
-        if (unit >= units) return false;
+    __device__ __forceinline__ Work(int pair_, int pairs_)
+        : pair(pair_), pairs(pairs_), unit(pair_), round(0), job(0) {}
+    __device__ __forceinline__ bool next(const GemmParams<JOBS> &p) {
+        int u;
+        if (job == 0) {
+            const int units = p.g[0].mt * p.g[0].nt * p.g[0].parts;
+            u = unit;
+            unit += pairs;
+            if (u >= units) {
+                if (JOBS == 1) return false;
+                job = 1;
+            }
+        }
+        if (JOBS > 1 && job == 1) {
+            const int units = p.g[JOBS - 1].mt * p.g[JOBS - 1].nt;
+            const int first = p.g[0].mt * p.g[0].nt % pairs, early = pairs - first;
+            const int e = pair - first;
+            if (round < p.bonus && e >= 0) {
+                u = round * early + e;
+            } else {
+                if (round < p.bonus) round = p.bonus;
+                u = p.bonus * early + (round - p.bonus) * pairs + (e >= 0 ? e : e + pairs);
+            }
+            ++round;
+            if (u >= units) return false;
+        }
+        const GemmArgs &g = p.g[JOBS == 1 ? 0 : job];
         const int tiles = g.mt * g.nt;
-        part = unit / tiles;
-        tile_at(g, unit - part * tiles, m, n);
+        part = u / tiles;
+        tile_at(g, u - part * tiles, m, n);
         k0 = (int)((int64_t)g.slices * part / g.parts);
         k1 = (int)((int64_t)g.slices * (part + 1) / g.parts);
-        unit += pairs;
         return true;
     }
 };
@@ -300,23 +335,22 @@ __device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lan
     turn_rows(turn, lane, out, g.odt, g.ldo, row, g.M, c, width, g.residual ? &res : nullptr, g.rdt);
 }
 
-template <bool GATED>
+template <bool GATED, int JOBS>
 __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
-    const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap ma1,
-    const __grid_constant__ CUtensorMap mb0, const __grid_constant__ CUtensorMap mb1,
-    const __grid_constant__ GemmArgs g) {
+    const __grid_constant__ GemmParams<JOBS> params) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    Work work(g, blockIdx.x >> 1, gridDim.x >> 1);
-    const int mt1 = g.mode == DG_PAIR_M ? g.mt / 2 : g.mt;  // M tiles of one problem
+    Work<JOBS> work(blockIdx.x >> 1, gridDim.x >> 1);
+    const int stages = params.g[0].stages, stage = params.g[0].stage;  // of both products
+    uint32_t *status = params.g[0].status;
     uint8_t *bars = smem + DG_BARS;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * DG_MAX_ST,
                    accfull0 = empty0 + 8 * DG_MAX_ST, accempty0 = accfull0 + 16;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 8 * (2 * DG_MAX_ST + 4));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < g.stages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
@@ -344,25 +378,28 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
 
     if (warp == 0) {
         // producer: this CTA's rows of A and of B for every slice
-        const int bboxes = g.b_t ? (g.half + 63) / 64 : 1;
-        const uint32_t bytes = DG_ABYTES + (g.b_t ? bboxes * 8192 : g.half * 128);
         int s = 0;
         uint32_t lap = 0;  // trips around the ring
         bool ok = true;
-        while (ok && work.next(g)) {
+        while (ok && work.next(params)) {
+            const GemmArgs &g = params.g[JOBS == 1 ? 0 : work.job];
+            const CUtensorMap *ma = params.a[JOBS == 1 ? 0 : work.job];
+            const CUtensorMap *mb = params.b[JOBS == 1 ? 0 : work.job];
+            const uint32_t bytes = DG_ABYTES + g.half * 128;
+            const int mt1 = g.mode == DG_PAIR_M ? g.mt / 2 : g.mt;  // M tiles of one problem
             const bool second = work.m >= mt1;
             const int m0 = (second ? work.m - mt1 : work.m) * 2 * DG_BM + (int)rank * DG_BM;
             const int n0 = GATED ? work.n * g.half : work.n * g.tile_n + (int)rank * g.half;
             for (int k = work.k0; k < work.k1; ++k) {
-                if (lap > 0 && !warp_wait(empty0 + 8 * s, (lap - 1) & 1, abort_flag, g.status)) {
+                if (lap > 0 && !warp_wait(empty0 + 8 * s, (lap - 1) & 1, abort_flag, status)) {
                     ok = false;
                     break;
                 }
                 const bool k2 = k >= g.kb;
                 const int kx = (k2 ? k - g.kb : k) * DG_BK;
-                const CUtensorMap *ta = (second || k2) ? &ma1 : &ma0;
-                const CUtensorMap *tb = (GATED ? rank == 1 : k2) ? &mb1 : &mb0;
-                const uint32_t st = smem_u32(smem + s * g.stage), sb = st + DG_ABYTES;
+                const CUtensorMap *ta = ma + ((second || k2) ? 1 : 0);
+                const CUtensorMap *tb = mb + ((GATED ? rank == 1 : k2) ? 1 : 0);
+                const uint32_t st = smem_u32(smem + s * stage), sb = st + DG_ABYTES;
                 const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
@@ -374,13 +411,13 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                     }
                     if (g.b_t) {
                         tma_pair(sb, tb, n0, kx, bar);
-                        if (bboxes > 1) tma_pair(sb + 8192, tb, n0 + 64, kx, bar);
+                        if (g.half > 64) tma_pair(sb + 8192, tb, n0 + 64, kx, bar);
                     } else {
                         tma_pair(sb, tb, kx, n0, bar);
                     }
                 }
                 __syncwarp();
-                if (++s == g.stages) {
+                if (++s == stages) {
                     s = 0;
                     ++lap;
                 }
@@ -388,35 +425,38 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
         }
     } else if (warp == 1 && rank == 0) {
         // issuer: four 16-deep MMAs per slice
-        const uint32_t da = g.a_t ? 2048u >> 4 : 2u, db = g.b_t ? 2048u >> 4 : 2u;
         int s = 0, done = 0;
         uint32_t lap = 0;
         bool ok = true;
-        for (; ok && work.next(g); ++done) {
+        for (; ok && work.next(params); ++done) {
+            const GemmArgs &g = params.g[JOBS == 1 ? 0 : work.job];
+            const uint32_t da = g.a_t ? 2048u >> 4 : 2u, db = g.b_t ? 2048u >> 4 : 2u;
+            const int a_t = g.a_t, b_t = g.b_t;
+            const uint32_t idesc = g.idesc;
             const int buf = done & 1;
             if (done >= 2 && !warp_wait(accempty0 + 8 * buf, ((done >> 1) - 1) & 1, abort_flag,
-                                        g.status))
+                                        status))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC);
             for (int k = work.k0; k < work.k1; ++k) {
-                if (!warp_wait(full0 + 8 * s, lap & 1, abort_flag, g.status)) {
+                if (!warp_wait(full0 + 8 * s, lap & 1, abort_flag, status)) {
                     ok = false;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t st = smem_u32(smem + s * g.stage);
-                const uint64_t a = operand_desc(st, g.a_t),
-                               b = operand_desc(st + DG_ABYTES, g.b_t);
+                const uint32_t st = smem_u32(smem + s * stage);
+                const uint64_t a = operand_desc(st, a_t),
+                               b = operand_desc(st + DG_ABYTES, b_t);
                 if (elect_one()) {
 #pragma unroll
                     for (int q = 0; q < DG_BK / 16; ++q)
-                        mma_pair(acc, a + q * da, b + q * db, g.idesc,
+                        mma_pair(acc, a + q * da, b + q * db, idesc,
                                  (k > work.k0 || q > 0) ? 1u : 0u);
                     commit_pair(empty0 + 8 * s);
                 }
                 __syncwarp();
-                if (++s == g.stages) {
+                if (++s == stages) {
                     s = 0;
                     ++lap;
                 }
@@ -428,9 +468,11 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
         // epilogue: lanes 32 q .. 32 q + 31 of the accumulator, every other
         // group of 32 columns
         const int q = warp & 3, par = (warp - 4) >> 2;
-        const int per = GATED ? g.half : g.tile_n;  // outputs of a tile's row
         const uint32_t turn = smem_u32(smem + DG_RING) + (uint32_t)(warp - 4) * DG_TURN;
-        for (int done = 0; work.next(g); ++done) {
+        for (int done = 0; work.next(params); ++done) {
+            const GemmArgs &g = params.g[JOBS == 1 ? 0 : work.job];
+            const int per = GATED ? g.half : g.tile_n;  // outputs of a tile's row
+            const int mt1 = g.mode == DG_PAIR_M ? g.mt / 2 : g.mt;
             const bool second = work.m >= mt1;
             const int row =
                 (second ? work.m - mt1 : work.m) * 2 * DG_BM + (int)rank * DG_BM + 32 * q;
@@ -443,7 +485,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                         reinterpret_cast<const char *>(g.residual) +
                         ((int64_t)(row + lane) * g.ldr + work.n * per + c) * e));
             }
-            if (!warp_wait(accfull0 + 8 * buf, (done >> 1) & 1, abort_flag, g.status)) break;
+            if (!warp_wait(accfull0 + 8 * buf, (done >> 1) & 1, abort_flag, status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC) + ((uint32_t)(32 * q) << 16);
             void *out = g.out[second ? 1 : 0];
@@ -625,22 +667,10 @@ size_t dense_gemm_partial_bytes(const DenseJob &job) {
     return partial_bytes(plan_gemm(job, num_sms() / 2), job);
 }
 
-rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
-    if (dense_stream_fits(job)) return launch_dense_stream(job, stream);
-    static std::atomic<int> attr_done[64];  // per device; setting twice is harmless
-    int dev = 0;
-    RVQ_CUDA(cudaGetDevice(&dev));
-    if (dev < 64 && !attr_done[dev]) {
-        RVQ_CUDA(cudaFuncSetAttribute(dense_gemm_kernel<false>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, DG_SMEM));
-        RVQ_CUDA(cudaFuncSetAttribute(dense_gemm_kernel<true>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, DG_SMEM));
-        attr_done[dev] = 1;
-    }
-    const bool gated = job.mode == DG_GATED;
-    const int pairs_max = num_sms() / 2;
-    const GemmPlan plan = plan_gemm(job, pairs_max);
-    GemmArgs g = {};
+// Arguments and tensor maps of a product cut by `plan`.
+static rvq_status fill_args(const DenseJob &job, const GemmPlan &plan, GemmArgs &g,
+                            CUtensorMap (&a)[2], CUtensorMap (&b)[2]) {
+    g = {};
     g.mode = job.mode;
     g.M = job.M;
     g.N = job.N;
@@ -653,12 +683,8 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     g.parts = plan.parts;
     g.tile_n = plan.tile_n;
     g.half = g.tile_n / 2;
-    // B's rows in whole swizzle atoms of 8 rows (1 KB), so every stage starts on one
-    g.stage = DG_ABYTES + g.half * 128;
-    g.stages = DG_RING / g.stage < DG_MAX_ST ? DG_RING / g.stage : DG_MAX_ST;
-    const long long tiles = (long long)g.mt * g.nt;
-    if (tiles > 0x7fffffffll / DG_GROUP) {
-        set_error("dense product: %lld output tiles", tiles);
+    if ((long long)g.mt * g.nt > 0x7fffffffll / DG_GROUP) {
+        set_error("dense product: %lld output tiles", (long long)g.mt * g.nt);
         return RVQ_ENOTIMPL;
     }
     const uint32_t fmt = job.dt == RVQ_BF16 ? 1u : 0u;
@@ -680,18 +706,48 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     }
     g.partial = job.partial;
     g.status = job.status;
-    CUtensorMap ma[2], mb[2];
     for (int i = 0; i < 2; ++i) {
         if (i == 1 && job.a[1] == nullptr)
-            ma[1] = ma[0];
+            a[1] = a[0];
         else
-            RVQ_TRY(encode_operand(&ma[i], job.a[i], job.M, job.K, job.lda, job.a_t, job.dt, DG_BM));
+            RVQ_TRY(encode_operand(&a[i], job.a[i], job.M, job.K, job.lda, job.a_t, job.dt, DG_BM));
         if (i == 1 && job.b[1] == nullptr)
-            mb[1] = mb[0];
+            b[1] = b[0];
         else
-            RVQ_TRY(encode_operand(&mb[i], job.b[i], job.N, job.K, job.ldb, job.b_t, job.dt, g.half));
+            RVQ_TRY(encode_operand(&b[i], job.b[i], job.N, job.K, job.ldb, job.b_t, job.dt, g.half));
     }
-    const long long units = tiles * g.parts, pairs = units < pairs_max ? units : pairs_max;
+    return RVQ_OK;
+}
+
+template <bool GATED, int JOBS>
+static rvq_status launch_products(GemmParams<JOBS> &p, cudaStream_t stream) {
+    static std::atomic<int> attr_done[64];  // per device; setting twice is harmless
+    int dev = 0;
+    RVQ_CUDA(cudaGetDevice(&dev));
+    if (dev < 64 && !attr_done[dev]) {
+        RVQ_CUDA(cudaFuncSetAttribute(dense_gemm_kernel<GATED, JOBS>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, DG_SMEM));
+        attr_done[dev] = 1;
+    }
+    // B's rows come in whole swizzle atoms of 8 rows (1 KB), so every stage starts
+    // on one
+    int half = 0;
+    long long units = 0;
+    for (int i = 0; i < JOBS; ++i) {
+        half = p.g[i].half > half ? p.g[i].half : half;
+        units += (long long)p.g[i].mt * p.g[i].nt * p.g[i].parts;
+    }
+    const int stage = DG_ABYTES + half * 128;
+    for (int i = 0; i < JOBS; ++i) {
+        p.g[i].stage = stage;
+        p.g[i].stages = DG_RING / stage < DG_MAX_ST ? DG_RING / stage : DG_MAX_ST;
+    }
+    const int pairs_max = num_sms() / 2, pairs = units < pairs_max ? (int)units : pairs_max;
+    if (JOBS > 1) {
+        // how many units of the second a unit of the first lasts
+        const long long first = (long long)p.g[0].mt * p.g[0].nt % pairs;
+        p.bonus = first ? p.g[0].slices / p.g[JOBS - 1].slices : 0;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(DG_THREADS);
@@ -706,17 +762,54 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (gated)
-        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_gemm_kernel<true>, ma[0], ma[1], mb[0], mb[1], g));
-    else
-        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_gemm_kernel<false>, ma[0], ma[1], mb[0], mb[1], g));
+    RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_gemm_kernel<GATED, JOBS>, p));
     RVQ_LAUNCHED("dense_gemm");
-    if (g.parts == 1) return RVQ_OK;
+    return RVQ_OK;
+}
+
+rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
+    if (dense_stream_fits(job)) return launch_dense_stream(job, stream);
+    const GemmPlan plan = plan_gemm(job, num_sms() / 2);
+    const bool gated = job.mode == DG_GATED;
+    GemmParams<1> p = {};
+    RVQ_TRY(fill_args(job, plan, p.g[0], p.a[0], p.b[0]));
+    RVQ_TRY((gated ? launch_products<true, 1>(p, stream) : launch_products<false, 1>(p, stream)));
+    if (plan.parts == 1) return RVQ_OK;
     const int64_t threads = (int64_t)job.M * (job.N / 8);
     const dim3 grid((unsigned)((threads + 255) / 256), job.mode == DG_PAIR_M ? 2u : 1u);
-    RVQ_CUDA(gated ? launch_after(dense_parts_kernel<true>, grid, 256, 0, stream, g)
-                   : launch_after(dense_parts_kernel<false>, grid, 256, 0, stream, g));
+    RVQ_CUDA(gated ? launch_after(dense_parts_kernel<true>, grid, 256, 0, stream, p.g[0])
+                   : launch_after(dense_parts_kernel<false>, grid, 256, 0, stream, p.g[0]));
     return RVQ_OK;
+}
+
+rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, cudaStream_t stream) {
+    const long long pairs = num_sms() / 2;
+    const GemmPlan px = plan_gemm(x, (int)pairs), py = plan_gemm(y, (int)pairs);
+    const bool swap = px.slices < py.slices;  // the longer tiles first
+    const GemmPlan &p0 = swap ? py : px, &p1 = swap ? px : py;
+    // slices until the last pair is done, one launch after the other and together
+    // (see Work); together only where that ends sooner (whole training steps, apart
+    // and together: 4096 tokens of 7168 x 2048, 768 slices either way, 484 and 491 us;
+    // 1333 x 1000 x 2048, 53 either way, 57.5 and 54 us; 1777 x 4104 x 1736, 121 and 93,
+    // 114 and 101 us)
+    const long long u0 = (long long)p0.mt * p0.nt, u1 = (long long)p1.mt * p1.nt;
+    const long long s0 = p0.slices, s1 = p1.slices;
+    const long long apart = (u0 + pairs - 1) / pairs * s0 + (u1 + pairs - 1) / pairs * s1;
+    const long long first = u0 % pairs, early = pairs - first, bonus = first ? s0 / s1 : 0;
+    const long long rest = u1 > bonus * early ? u1 - bonus * early : 0;
+    const long long late_end = (u0 / pairs + (first ? 1 : 0)) * s0 +
+                               (rest / pairs + (rest % pairs > early ? 1 : 0)) * s1;
+    const long long early_end = u0 / pairs * s0 + (bonus + (rest + pairs - 1) / pairs) * s1;
+    const long long together = late_end > early_end ? late_end : early_end;
+    // 3 % for operands that are shared less, and a launch of about 12 slices saved
+    if (px.parts > 1 || py.parts > 1 || together * 103 >= (apart + 12) * 100) {
+        RVQ_TRY(launch_dense_gemm(x, stream));
+        return launch_dense_gemm(y, stream);
+    }
+    GemmParams<2> p = {};
+    RVQ_TRY(fill_args(swap ? y : x, p0, p.g[0], p.a[0], p.b[0]));
+    RVQ_TRY(fill_args(swap ? x : y, p1, p.g[1], p.a[1], p.b[1]));
+    return launch_products<false, 2>(p, stream);
 }
 
 }  // namespace rvq
