@@ -35,7 +35,8 @@ constexpr int DG_MAX_ST = 9;  // stages: as many as fit
 constexpr int DG_RING = 192 << 10;
 constexpr int DG_EPI_WARPS = 8;
 constexpr int DG_TURN = 4096;  // staging of an epilogue warp: 32 rows x 32 fp32 columns
-constexpr int DG_BARS = DG_RING + DG_EPI_WARPS * DG_TURN;
+constexpr int DG_BIAS = DG_RING + DG_EPI_WARPS * DG_TURN;  // of two tiles, fp32
+constexpr int DG_BARS = DG_BIAS + 2 * 256 * 4;
 constexpr int DG_SMEM = DG_BARS + 256;
 constexpr int DG_THREADS = 32 * (4 + DG_EPI_WARPS);
 constexpr int DG_ACC = 256;  // TMEM columns per accumulator
@@ -290,17 +291,18 @@ __device__ __forceinline__ void rows_16_plain(uint32_t turn, int lane, void *p, 
         if (8 * j < width && row + 8 * i + r0 < rows) *reinterpret_cast<uint4 *>(q) = o[i];
 }
 
-__device__ __forceinline__ void add_bias32(const void *bias, int dt, int c, int width,
-                                           float (&v)[32]) {
-    if (bias == nullptr) return;
+// adds 32 staged bias values (byte address `at`; the same for every lane)
+__device__ __forceinline__ void add_bias32(uint32_t at, float (&v)[32]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (8 * q < width) {
-            float b[8];
-            ld8(bias, dt, c + 8 * q, b);
+    for (int j = 0; j < 8; ++j) {
+        float b[4];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3])
+                     : "r"(at + 16 * j)
+                     : "memory");
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
-        }
+        for (int e = 0; e < 4; ++e) v[4 * j + e] += b[e];
+    }
 }
 
 // 32 columns of a row per lane, finished and written: v (and w, the up half) are
@@ -308,15 +310,15 @@ __device__ __forceinline__ void add_bias32(const void *bias, int dt, int c, int 
 template <bool GATED>
 __device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lane, void *out, int row,
                                        int c, int width, float (&v)[32], float (&w)[32],
-                                       const Residual &res) {
-    add_bias32(g.bias[0], g.dt, c, width, v);
+                                       const Residual &res, uint32_t bias) {
+    if (g.bias[0]) add_bias32(bias, v);
     if (g.pre[0]) {
         turn_in(turn, lane, v);
         turn_rows(turn, lane, g.pre[0], RVQ_F32, g.N, row, g.M, c, width, nullptr, 0);
     }
     if (g.act != MOE_ACT_NONE) act_group(g.act, v);
     if (GATED) {
-        add_bias32(g.bias[1], g.dt, c, width, w);
+        if (g.bias[1]) add_bias32(bias + g.half * 4, w);
         if (g.pre[1]) {
             turn_in(turn, lane, w);
             turn_rows(turn, lane, g.pre[1], RVQ_F32, g.N, row, g.M, c, width, nullptr, 0);
@@ -485,7 +487,38 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                         reinterpret_cast<const char *>(g.residual) +
                         ((int64_t)(row + lane) * g.ldr + work.n * per + c) * e));
             }
+            // the tile's biases: each warp brings the columns it will read itself
+            // (before the wait) and stages them after it, when no warp still reads
+            // those of the tile before the last
+            constexpr int CH = GATED ? 2 : 4;  // its groups of 32 columns, at most
+            float bias[GATED ? 2 : 1][CH];
+            const bool biased = g.parts == 1 && (g.bias[0] || g.bias[1]);
+            if (biased) {
+#pragma unroll
+                for (int z = 0; z < (GATED ? 2 : 1); ++z)
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const int c = (2 * i + par) * 32 + lane, col = work.n * per + c;
+                        bias[z][i] = g.bias[z] && c < per && col < g.N
+                                         ? ld_elem(g.bias[z], g.dt, col) : 0.f;
+                    }
+            }
             if (!warp_wait(accfull0 + 8 * buf, (done >> 1) & 1, abort_flag, status)) break;
+            const uint32_t bias_at = smem_u32(smem + DG_BIAS) + (uint32_t)buf * 1024;
+            if (biased) {
+#pragma unroll
+                for (int z = 0; z < (GATED ? 2 : 1); ++z)
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const int c = (2 * i + par) * 32 + lane;
+                        if (c < per)
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                                             bias_at + (uint32_t)(z * g.half + c) * 4),
+                                         "f"(bias[z][i])
+                                         : "memory");
+                    }
+                __syncwarp();
+            }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC) + ((uint32_t)(32 * q) << 16);
             void *out = g.out[second ? 1 : 0];
@@ -500,7 +533,8 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                 tmem_ld32(acc + c, v);
                 if (GATED) tmem_ld32(acc + g.half + c, w);
                 if (g.parts == 1) {
-                    finish<GATED>(g, turn, lane, out, row, col, width, v, w, res);
+                    finish<GATED>(g, turn, lane, out, row, col, width, v, w, res,
+                                  bias_at + (uint32_t)c * 4);
                 } else {
                     turn_in(turn, lane, v);
                     turn_rows(turn, lane, plane_of(g, work.part, second ? 1 : 0), RVQ_F32, g.N, row,
