@@ -544,7 +544,7 @@ rvq_status moe_rms_norm(const void *x_dev, rvq_dtype xdt, int32_t n, int32_t d, 
  *
  * Matrices are row-major with a row pitch `ld*` in elements: ld >= columns,
  * ld % 8 == 0, base pointers 16-byte aligned (EALIGN).  n (tokens) is
- * from 1 to 2^24; rows and cols are multiples of 8 up to 2^24 (EINVAL).  Element types are
+ * from 1 to 2^24 - 256; rows and cols are multiples of 8 in that range (EINVAL).  Element types are
  * RVQ_BF16 or RVQ_F16 for the operands of a product (one type for x, w, bias
  * and, in a gradient, dout and every output); products accumulate in fp32 on
  * the tensor cores and each output is rounded once.
@@ -595,7 +595,8 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
 /* Workspace of moe_gated_linear / moe_gated_linear_backward, as above. */
 size_t moe_gated_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols, int32_t backward);
 
-/* The first half of a gated feed-forward block in one kernel:
+/* The first half of a gated feed-forward block in one kernel (a second one adds
+ * partial sums where the tokens are too few to fill the GPU with tiles):
  *   g = x wg^T + bg, u = x wu^T + bu, out = act(g) * u
  *  - x [n][cols], wg and wu [rows][cols] (one pitch ldw), bg and bu [rows] or
  *    NULL (each by itself), out [n][rows], all of dt.

@@ -25,7 +25,7 @@ using namespace rvq;
 namespace {
 
 constexpr int64_t kMaxLd = (int64_t)1 << 36;  // a tensor map's row pitch is below 2^40 bytes
-constexpr int32_t kMaxDim = 1 << 24;
+constexpr int32_t kMaxDim = (1 << 24) - 256;  // 65535 blocks of 256 columns
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -418,7 +418,7 @@ static rvq_status check_join(const char *who, const void *h, rvq_dtype hdt, cons
                              rvq_dtype gdt, int32_t post_norm, const void *w_post,
                              const void *w_pre, rvq_dtype wdt, rvq_dtype xdt) {
     CHECK_ARG(n >= 1 && n <= kMaxDim && d >= 8 && d % 8 == 0 && d <= kJoinMaxD,
-              "%s: n %d, d %d (n from 1 to 2^24; d a multiple of 8, at most %d)", who, n, d,
+              "%s: n %d, d %d (n from 1 to 2^24 - 256; d a multiple of 8, at most %d)", who, n, d,
               kJoinMaxD);
     CHECK_ARG(dtype_any(hdt) && dtype_any(ydt) && dtype_any(gdt) && dtype_any(wdt) &&
                   dtype_any(xdt),

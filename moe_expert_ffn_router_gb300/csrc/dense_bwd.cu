@@ -31,7 +31,7 @@ template <int MATS>
 __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
     __shared__ float red[BW_LANES][MATS][264];
     const int q = threadIdx.x & 31, lane = threadIdx.x >> 5;
-    const int c = (blockIdx.x * 32 + q) * 8;
+    const int c = (blockIdx.y * 32 + q) * 8;
     const bool on = c < j.rows;
     dependency_wait();
     const bool sums = j.dbias[0] || j.dbias[1];
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
         bool ok[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int t = blockIdx.y * kBwdChunkRows + i * BW_LANES + lane;
+            const int t = blockIdx.x * kBwdChunkRows + i * BW_LANES + lane;
             ok[i] = t < j.n;
             at[i] = (int64_t)t * j.rows + c;
             if (!ok[i]) continue;
@@ -86,13 +86,13 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) red[lane][m][q * 8 + e] = acc[m][e];
     __syncthreads();
-    const int col = blockIdx.x * 256 + threadIdx.x;
+    const int col = blockIdx.y * 256 + threadIdx.x;
     if (col >= j.rows) return;
     for (int m = 0; m < MATS; ++m) {
         float s = 0.f;
 #pragma unroll
         for (int l = 0; l < BW_LANES; ++l) s += red[l][m][threadIdx.x];
-        j.part[((int64_t)blockIdx.y * MATS + m) * j.rows + col] = s;
+        j.part[((int64_t)blockIdx.x * MATS + m) * j.rows + col] = s;
     }
 }
 
@@ -121,11 +121,7 @@ __global__ void __launch_bounds__(1024) dense_bias_sum_kernel(const DenseBwdJob 
 
 rvq_status launch_dense_bwd(const DenseBwdJob &job, cudaStream_t stream) {
     const int chunks = dense_bwd_chunks(job.n);
-    if (chunks > 65535) {
-        set_error("dense gradient: %d tokens (at most %d)", job.n, 65535 * kBwdChunkRows);
-        return RVQ_ENOTIMPL;
-    }
-    const dim3 grid((unsigned)((job.rows + 255) / 256), (unsigned)chunks);
+    const dim3 grid((unsigned)chunks, (unsigned)((job.rows + 255) / 256));
     DenseBwdJob j = job;
     j.wide = (((uintptr_t)job.pre[0] | (uintptr_t)job.pre[1]) & 31) == 0;
     RVQ_CUDA(job.mats == 2 ? launch_after(dense_bwd_kernel<2>, grid, 256, 0, stream, j)

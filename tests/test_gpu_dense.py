@@ -136,6 +136,37 @@ def test_gated_forward(n, rows, cols, dtype):
     assert rvq.rvq_ws_status(ws) == (0, 0)
 
 
+@pytest.mark.parametrize("n,rows,cols", [(193, 256, 1024), (257, 520, 4096), (112, 7168, 1024),
+                                         (113, 512, 1024), (65, 512, 2048), (600, 1000, 2048)])
+def test_every_way_of_a_product(n, rows, cols):
+    """Tokens at the ends of the stream of weights and of tiles cut by slices:
+    the same epilogue in each (bias, activation, scale, residual, pre)."""
+    g = gen(n)
+    x, w, w2 = normal(g, (n, cols), BF), normal(g, (rows, cols), BF, cols ** -0.5), \
+        normal(g, (rows, cols), BF, cols ** -0.5)
+    bias, bias2, res = normal(g, (rows,), BF), normal(g, (rows,), BF), normal(g, (n, rows), F32)
+    ws = workspace(n, rows, cols)
+    out, big = hole((n, rows), BF, 8)
+    pre = torch.empty((n, rows), dtype=F32, device=DEV)
+    rvq.moe_linear(x, w, n, rows, cols, out, ws, bias=bias, act=rvq.MOE_ACT_GELU, alpha=0.5,
+                   residual=res, pre=pre)
+    want, wpre = R.linear(x, w, bias, "gelu", 0.5, res, BF)
+    R.check(out, want, "out")
+    R.check(pre, wpre, "pre")
+    assert untouched(big, out)
+    ws2 = workspace(n, rows, cols, True)
+    gout, gbig = hole((n, rows), BF, 8)
+    pre2 = torch.empty((2, n, rows), dtype=F32, device=DEV)
+    rvq.moe_gated_linear(x, w, w2, n, rows, cols, gout, ws2, bg=bias, bu=bias2,
+                         act=rvq.MOE_ACT_GELU_TANH, pre=pre2)
+    wg, (g0, e0), (g1, e1) = R.gated(x, w, w2, bias, bias2, "gelu_tanh")
+    R.check(gout, wg, "gated out")
+    R.check(pre2[0], (g0, e0), "g")
+    R.check(pre2[1], (g1, e1), "u")
+    assert untouched(gbig, gout)
+    assert rvq.rvq_ws_status(ws) == (0, 0) and rvq.rvq_ws_status(ws2) == (0, 0)
+
+
 def linear_train(n, rows, cols, dtype, act, bias, alpha=1.0, seed=0, extra=0):
     g = gen(seed)
     x = padded(normal(g, (n, cols), dtype), extra)

@@ -174,6 +174,60 @@ def test_join_every_type_mix():
         check_backward(s, 4, 136, 0.5, True, hdt, ydt, xdt, wdt, rstd)
 
 
+# many rows (blocks that walk over them), at the limit of the block-per-row
+# kernel, and the layouts of a walking block: two rows in shared memory, one (fp32
+# with a full gate), none (long rows), types that no instance has
+WALKS = [(304, 520, F32, BF, BF, BF, "token"), (305, 520, BF, BF, BF, BF, "channel"),
+         (900, 8, BF, BF, BF, BF, "full"), (613, 136, HF, F32, HF, HF, "scalar"),
+         (500, 7168, F32, F32, BF, F32, "full"), (333, 8192, F32, F32, F32, F32, "full"),
+         (400, 8192, F32, F32, HF, HF, "channel"), (310, 8200, F32, F32, F32, F32, "channel"),
+         (306, 16384, F32, F32, F32, F32, "full"), (306, 16384, BF, BF, BF, BF, "token"),
+         (700, 264, BF, HF, F32, HF, "full"), (350, 2048, HF, BF, BF, F32, "none")]
+
+
+@pytest.mark.parametrize("n,d,hdt,ydt,xdt,wdt,gate", WALKS)
+def test_join_many_rows(n, d, hdt, ydt, xdt, wdt, gate):
+    for post in (True, False):
+        s = make(n, d, hdt, ydt, wdt, gate, post, seed=n)
+        rstd = check_forward(s, n, d, 0.5, post, hdt, xdt)
+        check_backward(s, n, d, 0.5, post, hdt, ydt, xdt, wdt, rstd)
+
+
+def test_join_many_rows_full_gate_of_another_type():
+    n, d = 320, 264
+    s = make(n, d, F32, BF, F32, "full", True, seed=5)
+    s["gate"] = s["gate"].to(BF)
+    rstd = check_forward(s, n, d, 1.0, True, F32, BF)
+    check_backward(s, n, d, 1.0, True, F32, BF, BF, F32, rstd)
+
+
+def test_join_many_rows_without_some_tensors():
+    n, d = 777, 1000
+    for which, with_h in (("dho", True), ("dxn", False), ("both", False)):
+        s = make(n, d, BF, BF, BF, "token", True, gains=which == "dxn", seed=4, with_h=with_h)
+        rstd = check_forward(s, n, d, 1.0, True, BF, BF)
+        wdt = BF if s["w_pre"] is not None else F32
+        check_backward(s, n, d, 1.0, True, BF, BF, BF, wdt, rstd, which=which)
+    # outputs over inputs, as for few rows
+    s = make(n, d, BF, BF, BF, "channel", True, seed=2)
+    ho, xn, rstd = forward(s, n, d, 1.0, True, BF, BF)
+    for over in ("h", "y"):
+        t = {k: None if v is None else v.clone() for k, v in s.items()}
+        xn2 = torch.empty_like(xn)
+        rvq.moe_norm_join(t["y"], n, d, t[over], xn2, h=t["h"], gate=t["gate"],
+                          w_post=t["w_post"], w_pre=t["w_pre"], eps=EPS)
+        assert torch.equal(t[over], ho) and torch.equal(xn2, xn)
+    g = gen(3)
+    dho, dxn = ((torch.randn((n, d), device=DEV, generator=g)).to(BF) for _ in range(2))
+    ws = torch.empty(rvq.moe_norm_join_workspace_bytes(n, d), dtype=torch.uint8, device=DEV)
+    kw = dict(h=s["h"], gate=s["gate"], w_post=s["w_post"], w_pre=s["w_pre"])
+    dh, dy = torch.empty_like(dho), torch.empty_like(dho)
+    rvq.moe_norm_join_backward(dho, dxn, s["y"], n, d, rstd, ws, dh=dh, dy=dy, **kw)
+    a, b = dho.clone(), dxn.clone()
+    rvq.moe_norm_join_backward(a, b, s["y"], n, d, rstd, ws, dh=a, dy=b, **kw)
+    assert torch.equal(a, dh) and torch.equal(b, dy)
+
+
 def test_join_aliases_and_partial_outputs():
     n, d = 6, 7168
     s = make(n, d, F32, F32, BF, "token", True, seed=2)
