@@ -1,7 +1,8 @@
 // Elementwise gradients in front of the backward products of moe_linear and
 // moe_gated_linear, with the bias gradients' sums over tokens.
 //
-// Memory-bound: dout and the saved fp32 pre-activations are read once, dp is
+// Memory-bound (4096 x 2048, gated: 117 MB in 20 us, 5.9 TB/s; 1777 x 4104 with GELU:
+// 58 MB in 15 us): dout and the saved fp32 pre-activations are read once, dp is
 // written once, 16 or 32 bytes per thread and access.  A block takes 32 rows x
 // 256 columns (32 groups of eight columns x 8 row lanes, four rows each), so a
 // bias gradient leaves one fp32 partial per 32 rows and column, added in row

@@ -8,8 +8,8 @@
 //    one thread issues cta_group::2 MMAs on both halves.  Pairing halves the
 //    shared memory and L2 traffic of B per operation.
 //  * Both operands arrive by TMA in 64-deep slices (one 128-byte swizzled row
-//    of 16-bit elements), seven 32 KB stages per CTA (more of a narrower tile); the slices of both CTAs
-//    complete on the leader's barrier.
+//    of 16-bit elements), six 32 KB stages per CTA (more of a narrower tile); the
+//    slices of both CTAs complete on the leader's barrier.
 //  * A transposed operand (stored [K][rows]) is loaded as it lies, in boxes of
 //    64 rows x 64 deep, and read through MN-major descriptors, so the gradients
 //    need no transposed copies.
@@ -18,8 +18,22 @@
 //  * A gated product loads its gate half from B0 (leader) and its up half from
 //    B1 (follower), so both projections of an output lie in one accumulator row
 //    and act(g) * u is formed in registers.
+//  * Outputs are turned from a row per lane into rows of 64 or 128 contiguous
+//    bytes through 4 KB of staging per warp; biases are staged once per tile.
+//  * Tiles too few for half the pairs are cut by slices into parts, which a second
+//    launch adds in order; the products of dx and dw share a launch where their
+//    tiles fill the pairs better together.
 // Rows, columns and depth past the ends are zero-filled by TMA and not stored.
 // Each output is rounded once, from fp32.  Every wait is bounded (1 s).
+//
+// Measured (GB300, operands rotated through more than L2): 2048 tokens through
+// the gated projection 7168 -> 2048 70.5 us (1.70 PFLOP/s; 80 us in a loop of half
+// a second, where the power cap holds a library product of the same size at
+// 74-77), 4096^2 x 8192 154 us (1.79).  A slice of a 256-wide tile takes 528 cycles
+// against 512 of its MMAs; a narrower one is bound by the operand fill (about 55
+// bytes per cycle and SM) and the issue.  Around the slices a tile costs 2200
+// cycles to its first operands and, at the end, 4800 for the outputs, when all
+// SMs write at once.
 #include "dense_tc.cuh"
 
 #include <cudaTypedefs.h>
@@ -621,8 +635,9 @@ struct GemmPlan {
     int tile_n, mt, nt, slices, parts;
 };
 
-// Cycles of a 64-deep slice of a 256 x tile_n tile, as measured: the MMAs' 2 per
-// column, or, for narrower tiles, the issue and the operand fill.
+// Cycles of a 64-deep slice of a 256 x tile_n tile: the MMAs' 2 per column, or, for
+// narrower tiles, the issue and the operand fill (measured 508 at 128 columns, 530
+// at 192 and 224).
 double slice_cycles(int tile_n) {
     const double fill = 460.0 + 0.375 * tile_n;
     return 2.0 * tile_n > fill ? 2.0 * tile_n : fill;

@@ -15,7 +15,15 @@
 //  * The partial tiles (fp32) go to shared memory, and each CTA of the cluster
 //    adds its share of the rows over the cluster in rank order (distributed
 //    shared memory): no workspace, no atomics, results repeat bit for bit.
+//  * Launched programmatically: while the kernel before it ends, a CTA brings its
+//    first slices of weights into L2 (13.4 -> 12.4 us below).
 // Every wait is bounded (1 s).
+//
+// Measured (GB300, weights rotated through more than L2, launches back to back):
+// one token through the gated projection 7168 -> 2048 12.4 us (58.7 MB, 4.7 TB/s;
+// 8.7 us at the copy rate), 64 tokens 15.6 us; 2048 -> 7168 7.9 and 10.8 us; 512 -> 256
+// 3.4 us.  Once the stream runs it moves 7 TB/s; the rest is the first load (1.7 us,
+// part of it hidden) and the tail of MMA, cluster barrier and joining (2.5 us).
 #include "dense_tc.cuh"
 
 namespace rvq {

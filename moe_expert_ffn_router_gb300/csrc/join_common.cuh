@@ -1,6 +1,6 @@
-// Shared parts of moe_norm_join (norm_join.cu) and its gradients
-// (norm_join_bwd.cu): sums over a block, a ring of rows in shared memory, and
-// the launch of blocks that walk over the rows.
+// Shared parts of moe_norm_join and its gradients (norm_join.cu, join_walk.cuh):
+// sums over a block, a ring of rows in shared memory, and the launch of blocks
+// that walk over the rows.
 //
 // A walking block's thread owns the same columns of every row: groups of four,
 // a block's width apart, so that a warp's accesses are contiguous for every
@@ -9,6 +9,12 @@
 // absent tensor is a row of zeros.  With types looked up at run time every
 // load's latency was exposed: 56 us against 36 us for 2048 rows of 7168 (fp32 h
 // and y, bf16 xn).
+//
+// Measured (GB300): forward of 2048 x 7168 36 us (fp32 h and y, bf16 xn: 206 MB,
+// 5.7 TB/s) and 26 us (bf16: 118 MB, 4.5 TB/s), of 4099 x 2048 (bf16) 16 us; forward and
+// gradients 83 us and 45 us.  The forward call is bound by memory; the gradients
+// by issue and latency (57 % of the issue slots with 16 warps an SM; the sums over
+// rows hold 48 registers a thread).
 #pragma once
 
 #include <type_traits>
