@@ -474,19 +474,22 @@ def moe_rms_norm(x, n, d, out, eps=1e-6, stream=None):
 _DTYPES = {torch.float32: RVQ_F32, torch.bfloat16: RVQ_BF16, torch.float16: RVQ_F16}
 
 
-def _dt_any(t) -> int:
-    """dtype code of a dense operator's tensor (None: fp32, unused)."""
-    if t is None:
-        return RVQ_F32
+def _code(dtype) -> int:
+    """dtype code of a dense operator's tensors."""
     try:
-        return _DTYPES[t.dtype]
+        return _DTYPES[dtype]
     except KeyError:
-        raise TypeError(f"unsupported dtype {t.dtype} (bf16, fp16 or fp32)") from None
+        raise TypeError(f"unsupported dtype {dtype} (bf16, fp16 or fp32)") from None
+
+
+def _dt_any(t) -> int:
+    """dtype code of a tensor (None: fp32, unused)."""
+    return RVQ_F32 if t is None else _code(t.dtype)
 
 
 # The dense calls take a few microseconds on the GPU at decode sizes, so their
-# host side asks torch for as little as it can: raw stream handles, plain
-# integers, one look at each tensor's shape, strides and type.
+# host side asks torch for as little as it can: raw stream handles, one look at
+# each tensor's shape, strides and type, addresses taken along with the checks.
 def _raw_stream(stream) -> int:
     """cudaStream_t of `stream`, or of the current device's current stream
     (the caller's CUDA tensors have initialised torch's CUDA state)."""
@@ -495,29 +498,36 @@ def _raw_stream(stream) -> int:
     return stream.cuda_stream
 
 
-def _mat(t, rows, cols, what, dtype=None) -> int:
-    """Row pitch of a [rows][cols] matrix; columns must be contiguous."""
+def _mat(t, rows, cols, what, dtype=None):
+    """(address, row pitch) of a [rows][cols] matrix with contiguous columns, or
+    (None, 0)."""
     if t is None:
-        return 0
+        return None, 0
     if t.shape != (rows, cols):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
     pitch, step = t.stride()
     if step != 1:
         raise ValueError(f"{what}: columns are not contiguous (strides {t.stride()})")
-    return pitch if rows > 1 else max(cols, pitch // 8 * 8)
+    return t.data_ptr(), pitch if rows > 1 else max(cols, pitch // 8 * 8)
 
 
 def _vec(t, numel, what, dtype=None):
-    """A contiguous tensor of numel elements (or None)."""
+    """Address of a contiguous tensor of numel elements, or None."""
     if t is None:
-        return
+        return None
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{what}: {tuple(t.shape)} with strides {t.stride()}, expected {numel} "
                          "contiguous elements")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    return t.data_ptr()
+
+
+def _same_pitch(a, b, what):
+    if a != b:
+        raise ValueError(f"{what} have different row pitches")
 
 
 def moe_linear_workspace_bytes(n, rows, cols, backward=False) -> int:
@@ -529,15 +539,17 @@ def moe_linear(x, w, n, rows, cols, out, ws, bias=None, act=MOE_ACT_NONE, alpha=
     """out = residual + alpha * act(x w^T + bias); x [n][cols], w [rows][cols]
     (bf16 or fp16, any row pitch), out and residual [n][rows].  pre (fp32
     [n][rows]) keeps x w^T + bias for moe_linear_backward."""
-    ldx, ldw = _mat(x, n, cols, "x"), _mat(w, rows, cols, "w", x.dtype)
-    ldo, ldr = _mat(out, n, rows, "out"), _mat(residual, n, rows, "residual")
-    _vec(bias, rows, "bias", x.dtype)
-    _vec(pre, n * rows, "pre", torch.float32)
-    _check("moe_linear",
-           _lib.moe_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, _p(bias), _dt_any(x), n, rows,
-                           cols, act, alpha, _p(residual), _dt_any(residual), ldr, out.data_ptr(),
-                           _dt_any(out), ldo, _p(pre), ws.data_ptr(), ws.nbytes,
-                           _raw_stream(stream)))
+    dt = x.dtype
+    px, ldx = _mat(x, n, cols, "x")
+    pw, ldw = _mat(w, rows, cols, "w", dt)
+    po, ldo = _mat(out, n, rows, "out")
+    pr, ldr = _mat(residual, n, rows, "residual")
+    rc = _lib.moe_linear(px, ldx, pw, ldw, _vec(bias, rows, "bias", dt), _dt_any(x), n, rows, cols,
+                         act, alpha, pr, _dt_any(residual), ldr, po, _dt_any(out), ldo,
+                         _vec(pre, n * rows, "pre", torch.float32), ws.data_ptr(), ws.nbytes,
+                         _raw_stream(stream))
+    if rc:
+        _check("moe_linear", rc)
 
 
 def moe_linear_backward(dout, x, w, n, rows, cols, ws, dx=None, dw=None, dbias=None, pre=None,
@@ -545,16 +557,18 @@ def moe_linear_backward(dout, x, w, n, rows, cols, ws, dx=None, dw=None, dbias=N
     """Gradients of moe_linear (those given a tensor): dx [n][cols], dw
     [rows][cols], dbias [rows]; the residual's gradient is dout itself."""
     dt = dout.dtype
-    ldd, ldx, ldw = (_mat(dout, n, rows, "dout"), _mat(x, n, cols, "x", dt),
-                     _mat(w, rows, cols, "w", dt))
-    lddx, lddw = _mat(dx, n, cols, "dx", dt), _mat(dw, rows, cols, "dw", dt)
-    _vec(dbias, rows, "dbias", dt)
-    _vec(pre, n * rows, "pre", torch.float32)
-    _check("moe_linear_backward",
-           _lib.moe_linear_backward(dout.data_ptr(), ldd, _p(x), ldx, _p(w), ldw, _p(pre),
-                                    _dt_any(dout), n, rows, cols, act, alpha, _p(dx), lddx,
-                                    _p(dw), lddw,
-                                    _p(dbias), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+    pd, ldd = _mat(dout, n, rows, "dout")
+    px, ldx = _mat(x, n, cols, "x", dt)
+    pw, ldw = _mat(w, rows, cols, "w", dt)
+    pdx, lddx = _mat(dx, n, cols, "dx", dt)
+    pdw, lddw = _mat(dw, rows, cols, "dw", dt)
+    rc = _lib.moe_linear_backward(pd, ldd, px, ldx, pw, ldw,
+                                  _vec(pre, n * rows, "pre", torch.float32), _dt_any(dout), n,
+                                  rows, cols, act, alpha, pdx, lddx, pdw, lddw,
+                                  _vec(dbias, rows, "dbias", dt), ws.data_ptr(), ws.nbytes,
+                                  _raw_stream(stream))
+    if rc:
+        _check("moe_linear_backward", rc)
 
 
 def moe_gated_linear_workspace_bytes(n, rows, cols, backward=False) -> int:
@@ -563,21 +577,21 @@ def moe_gated_linear_workspace_bytes(n, rows, cols, backward=False) -> int:
 
 def moe_gated_linear(x, wg, wu, n, rows, cols, out, ws, bg=None, bu=None, act=MOE_ACT_SILU,
                      pre=None, stream=None):
-    """out = act(x wg^T + bg) * (x wu^T + bu) in one kernel.  wg and wu share
-    their row pitch (two halves of one tensor do).  pre (fp32 [2][n][rows])
-    keeps both projections for moe_gated_linear_backward."""
+    """out = act(x wg^T + bg) * (x wu^T + bu).  wg and wu share their row pitch
+    (two halves of one tensor do).  pre (fp32 [2][n][rows]) keeps both projections
+    for moe_gated_linear_backward."""
     dt = x.dtype
-    ldx, ldw = _mat(x, n, cols, "x"), _mat(wg, rows, cols, "wg", dt)
-    if _mat(wu, rows, cols, "wu", dt) != ldw:
-        raise ValueError("wg and wu have different row pitches")
-    ldo = _mat(out, n, rows, "out", dt)
-    _vec(bg, rows, "bg", dt)
-    _vec(bu, rows, "bu", dt)
-    _vec(pre, 2 * n * rows, "pre", torch.float32)
-    _check("moe_gated_linear",
-           _lib.moe_gated_linear(x.data_ptr(), ldx, wg.data_ptr(), wu.data_ptr(), ldw, _p(bg),
-                                 _p(bu), _dt_any(x), n, rows, cols, act, out.data_ptr(), ldo,
-                                 _p(pre), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+    px, ldx = _mat(x, n, cols, "x")
+    pg, ldw = _mat(wg, rows, cols, "wg", dt)
+    pu, ldu = _mat(wu, rows, cols, "wu", dt)
+    _same_pitch(ldw, ldu, "wg and wu")
+    po, ldo = _mat(out, n, rows, "out", dt)
+    rc = _lib.moe_gated_linear(px, ldx, pg, pu, ldw, _vec(bg, rows, "bg", dt),
+                               _vec(bu, rows, "bu", dt), _dt_any(x), n, rows, cols, act, po, ldo,
+                               _vec(pre, 2 * n * rows, "pre", torch.float32), ws.data_ptr(),
+                               ws.nbytes, _raw_stream(stream))
+    if rc:
+        _check("moe_gated_linear", rc)
 
 
 def moe_gated_linear_backward(dout, x, wg, wu, pre, n, rows, cols, ws, dx=None, dwg=None, dwu=None,
@@ -585,21 +599,23 @@ def moe_gated_linear_backward(dout, x, wg, wu, pre, n, rows, cols, ws, dx=None, 
     """Gradients of moe_gated_linear (those given a tensor) from the forward
     call's inputs and `pre`."""
     dt = dout.dtype
-    ldd, ldx, ldw = (_mat(dout, n, rows, "dout"), _mat(x, n, cols, "x", dt),
-                     _mat(wg, rows, cols, "wg", dt))
-    if _mat(wu, rows, cols, "wu", dt) != ldw:
-        raise ValueError("wg and wu have different row pitches")
-    lddx, lddw = _mat(dx, n, cols, "dx", dt), _mat(dwg, rows, cols, "dwg", dt)
-    if _mat(dwu, rows, cols, "dwu", dt) != lddw:
-        raise ValueError("dwg and dwu have different row pitches")
-    _vec(dbg, rows, "dbg", dt)
-    _vec(dbu, rows, "dbu", dt)
-    _vec(pre, 2 * n * rows, "pre", torch.float32)
-    _check("moe_gated_linear_backward",
-           _lib.moe_gated_linear_backward(dout.data_ptr(), ldd, _p(x), ldx, _p(wg), _p(wu), ldw,
-                                          _p(pre), _dt_any(dout), n, rows, cols, act, _p(dx), lddx, _p(dwg),
-                                          _p(dwu), lddw, _p(dbg), _p(dbu), ws.data_ptr(), ws.nbytes,
-                                          _raw_stream(stream)))
+    pd, ldd = _mat(dout, n, rows, "dout")
+    px, ldx = _mat(x, n, cols, "x", dt)
+    pg, ldw = _mat(wg, rows, cols, "wg", dt)
+    pu, ldu = _mat(wu, rows, cols, "wu", dt)
+    _same_pitch(ldw, ldu, "wg and wu")
+    pdx, lddx = _mat(dx, n, cols, "dx", dt)
+    pdg, lddw = _mat(dwg, rows, cols, "dwg", dt)
+    pdu, lddu = _mat(dwu, rows, cols, "dwu", dt)
+    _same_pitch(lddw, lddu, "dwg and dwu")
+    rc = _lib.moe_gated_linear_backward(pd, ldd, px, ldx, pg, pu, ldw,
+                                        _vec(pre, 2 * n * rows, "pre", torch.float32),
+                                        _dt_any(dout), n, rows, cols, act, pdx, lddx, pdg, pdu,
+                                        lddw, _vec(dbg, rows, "dbg", dt),
+                                        _vec(dbu, rows, "dbu", dt), ws.data_ptr(), ws.nbytes,
+                                        _raw_stream(stream))
+    if rc:
+        _check("moe_gated_linear_backward", rc)
 
 
 def _gate_kind(gate, n, d) -> int:
@@ -609,16 +625,16 @@ def _gate_kind(gate, n, d) -> int:
         return MOE_GATE_NONE
     if not gate.is_contiguous():
         raise ValueError(f"gate: not contiguous (strides {gate.stride()})")
-    shape = tuple(gate.shape)
-    if shape == (n, d):
-        return MOE_GATE_FULL
-    if shape in ((d,), (1, d)):
-        return MOE_GATE_CHANNEL
+    shape = gate.shape
     if shape == (n, 1):
         return MOE_GATE_TOKEN
+    if shape == (n, d):
+        return MOE_GATE_FULL
+    if shape == (d,) or shape == (1, d):
+        return MOE_GATE_CHANNEL
     if gate.numel() == 1:
         return MOE_GATE_SCALAR
-    raise ValueError(f"gate: shape {shape} does not broadcast over ({n}, {d})")
+    raise ValueError(f"gate: shape {tuple(shape)} does not broadcast over ({n}, {d})")
 
 
 def moe_norm_join(y, n, d, h_out, xn, h=None, alpha=1.0, gate=None, post_norm=True, w_post=None,
@@ -626,23 +642,29 @@ def moe_norm_join(y, n, d, h_out, xn, h=None, alpha=1.0, gate=None, post_norm=Tr
     """h_out = alpha * h + gate * norm(y) * w_post (post_norm; else y itself),
     xn = norm(h_out) * w_pre.  gate broadcasts over [n][d]; gains None are 1.
     h_out or xn may be None.  rstd (fp32 [2][n]) is kept for the gradients."""
-    for t, what in ((y, "y"), (h, "h"), (h_out, "h_out"), (xn, "xn")):
-        _vec(t, n * d, what)
-    if h is not None and h_out is not None and h.dtype != h_out.dtype:
-        raise TypeError(f"h_out: dtype {h_out.dtype}, expected {h.dtype}")
-    _vec(w_post, d, "w_post")
-    _vec(w_pre, d, "w_pre", None if w_post is None else w_post.dtype)
-    _vec(rstd, 2 * n, "rstd", torch.float32)
-    _check("moe_norm_join",
-           _lib.moe_norm_join(_p(h), _dt_any(h if h is not None else h_out), y.data_ptr(),
-                              _dt_any(y), n, d, alpha, _p(gate), _gate_kind(gate, n, d), _dt_any(gate),
-                              int(post_norm), _p(w_post), _p(w_pre),
-                              _dt_any(w_post if w_post is not None else w_pre), eps, _p(h_out),
-                              _p(xn), _dt_any(xn), _p(rstd), _raw_stream(stream)))
+    nd = n * d
+    ho = h if h is not None else h_out
+    wdt = w_post if w_post is not None else w_pre
+    rc = _lib.moe_norm_join(
+        _vec(h, nd, "h"), _dt_any(ho), _vec(y, nd, "y"), _dt_any(y), n, d, alpha,
+        None if gate is None else gate.data_ptr(), _gate_kind(gate, n, d), _dt_any(gate),
+        int(post_norm), _vec(w_post, d, "w_post"),
+        _vec(w_pre, d, "w_pre", None if wdt is w_pre else wdt.dtype), _dt_any(wdt), eps,
+        _vec(h_out, nd, "h_out", None if ho is h_out else ho.dtype), _vec(xn, nd, "xn"),
+        _dt_any(xn), _vec(rstd, 2 * n, "rstd", torch.float32), _raw_stream(stream))
+    if rc:
+        _check("moe_norm_join", rc)
 
 
 def moe_norm_join_workspace_bytes(n, d) -> int:
     return int(_lib.moe_norm_join_workspace_bytes(n, d))
+
+
+def _first_dtype(*tensors):
+    for t in tensors:
+        if t is not None:
+            return t.dtype
+    return torch.float32
 
 
 def moe_norm_join_backward(dh_out, dxn, y, n, d, rstd, ws, h=None, alpha=1.0, gate=None,
@@ -650,26 +672,23 @@ def moe_norm_join_backward(dh_out, dxn, y, n, d, rstd, ws, h=None, alpha=1.0, ga
                            dw_post=None, dw_pre=None, stream=None):
     """Gradients of moe_norm_join (those given a tensor) from its inputs and
     rstd.  dh_out or dxn may be None."""
-    for t, what in ((y, "y"), (h, "h"), (dh_out, "dh_out"), (dxn, "dxn")):
-        _vec(t, n * d, what)
-    hdt = next((t.dtype for t in (h, dh_out, dh) if t is not None), torch.float32)
-    _vec(dh_out, n * d, "dh_out", hdt)
-    _vec(dh, n * d, "dh", hdt)
-    _vec(dy, n * d, "dy", y.dtype)
-    wdt = next((t.dtype for t in (w_post, w_pre, dw_post, dw_pre) if t is not None), torch.float32)
-    for t, what in ((w_post, "w_post"), (w_pre, "w_pre"), (dw_post, "dw_post"),
-                    (dw_pre, "dw_pre")):
-        _vec(t, d, what, wdt)
-    _vec(rstd, 2 * n, "rstd", torch.float32)
-    if gate is not None:
-        _vec(dgate, gate.numel(), "dgate", gate.dtype)
-    _check("moe_norm_join_backward",
-           _lib.moe_norm_join_backward(_p(dh_out), _p(dxn), _dt_any(dxn), _p(h), _DTYPES[hdt],
-                                       y.data_ptr(), _dt_any(y), n, d, alpha, _p(gate),
-                                       _gate_kind(gate, n, d), _dt_any(gate), int(post_norm),
-                                       _p(w_post), _p(w_pre), _DTYPES[wdt], _p(rstd), _p(dh),
-                                       _p(dy), _p(dgate), _p(dw_post), _p(dw_pre), ws.data_ptr(),
-                                       ws.nbytes, _raw_stream(stream)))
+    nd = n * d
+    hdt = _first_dtype(h, dh_out, dh)
+    wdt = _first_dtype(w_post, w_pre, dw_post, dw_pre)
+    if gate is None:
+        pg, pdg = None, None if dgate is None else dgate.data_ptr()
+    else:
+        pg, pdg = gate.data_ptr(), _vec(dgate, gate.numel(), "dgate", gate.dtype)
+    rc = _lib.moe_norm_join_backward(
+        _vec(dh_out, nd, "dh_out", hdt), _vec(dxn, nd, "dxn"), _dt_any(dxn), _vec(h, nd, "h", hdt),
+        _code(hdt), _vec(y, nd, "y"), _dt_any(y), n, d, alpha, pg, _gate_kind(gate, n, d),
+        _dt_any(gate), int(post_norm), _vec(w_post, d, "w_post", wdt),
+        _vec(w_pre, d, "w_pre", wdt), _code(wdt), _vec(rstd, 2 * n, "rstd", torch.float32),
+        _vec(dh, nd, "dh", hdt), _vec(dy, nd, "dy", y.dtype), pdg,
+        _vec(dw_post, d, "dw_post", wdt), _vec(dw_pre, d, "dw_pre", wdt), ws.data_ptr(), ws.nbytes,
+        _raw_stream(stream))
+    if rc:
+        _check("moe_norm_join_backward", rc)
 
 
 def rvq_ws_clear(ws, stream=None):
