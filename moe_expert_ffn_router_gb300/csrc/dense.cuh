@@ -261,10 +261,11 @@ struct DenseJob {
 };
 size_t dense_gemm_partial_bytes(const DenseJob &job);
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream);
-// two products without a common output in one launch (not GATED; one dt)
+// two products without a common output (not GATED; one dt), in one launch where
+// that is faster; one whose out[0] is NULL is not wanted
 rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, cudaStream_t stream);
-// launch_dense_gemm for few tokens (PLAIN and GATED, nothing transposed): the weights
-// streamed past the batch (dense_stream.cu)
+// launch_dense_gemm for few tokens as the rows of A: the weights streamed past the
+// batch (dense_stream.cu)
 constexpr int kStreamMaxTokens = 192;
 bool dense_stream_fits(const DenseJob &job);
 rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream);

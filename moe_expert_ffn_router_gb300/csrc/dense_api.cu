@@ -114,13 +114,6 @@ WsPlan plan_ws(int mats, int32_t n, int32_t rows, int32_t cols, bool backward) {
     return P;
 }
 
-// the products of dx and dw, each if wanted
-rvq_status launch_gradients(const DenseJob &x, const DenseJob &w, cudaStream_t st) {
-    if (x.out[0] && w.out[0]) return launch_dense_gemm_two(x, w, st);
-    if (x.out[0]) return launch_dense_gemm(x, st);
-    return w.out[0] ? launch_dense_gemm(w, st) : RVQ_OK;
-}
-
 // a gradient's workspace serves the forward call too
 size_t ws_bytes_of(int mats, int32_t n, int32_t rows, int32_t cols, int32_t backward) {
     if (!dense_shape(n, rows, cols)) return 0;
@@ -317,7 +310,7 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
     w.ldb = ldx;
     w.out[0] = dw_dev;
     w.ldo = lddw;
-    return launch_gradients(j, w, st);
+    return launch_dense_gemm_two(j, w, st);
 }
 
 rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const void *x_dev,
@@ -408,7 +401,7 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
     w.out[0] = dwg_dev;
     w.out[1] = dwu_dev;
     w.ldo = lddw;
-    return launch_gradients(j, w, st);
+    return launch_dense_gemm_two(j, w, st);
 }
 
 // ---------------------------------------------------------------- norm join

@@ -633,6 +633,7 @@ __global__ void __launch_bounds__(256) dense_parts_kernel(const __grid_constant_
 // How a product is cut: tile width, and the parts of a tile.
 struct GemmPlan {
     int tile_n, mt, nt, slices, parts;
+    double cycles;
 };
 
 // Cycles of a 64-deep slice of a 256 x tile_n tile: the MMAs' 2 per column, or, for
@@ -643,13 +644,22 @@ double slice_cycles(int tile_n) {
     return 2.0 * tile_n > fill ? 2.0 * tile_n : fill;
 }
 
-// The cheapest of the tile widths: (waves of pairs) x (slices of a tile).  Where
-// not even half the pairs would have a tile, the tiles' slices are cut into parts
-// for the others, which costs the parts' way through L2 and a second launch.
-GemmPlan plan_gemm(const DenseJob &j, int pairs) {
-    constexpr double kTile = 600.0, kParts = 6000.0;
+// A tile's share of a pair's time: its slices, or, of a short depth, its outputs'
+// way out, which the next tile's slices would have hidden.
+double tile_cycles(int slices, int tile_n) {
+    const double in = slices * slice_cycles(tile_n) + 600.0, out = 18.0 * tile_n;
+    return in > out ? in : out;
+}
+
+// The cheapest of the tile widths: (waves of pairs) x (a tile's time).  Where not
+// even half the pairs would have a tile, the tiles' slices are cut into (up to
+// `most`) parts for the others, which costs the parts' way through L2 and a second
+// launch.
+constexpr int kMaxParts = 8;
+GemmPlan plan_gemm(const DenseJob &j, int pairs, int most = kMaxParts) {
+    constexpr double kParts = 6000.0;
     GemmPlan best = {};
-    double cost = 1e300;
+    best.cycles = 1e300;
     const int mt = (j.M + 2 * DG_BM - 1) / (2 * DG_BM) * (j.mode == DG_PAIR_M ? 2 : 1);
     const int kb = (j.K + DG_BK - 1) / DG_BK, slices = j.mode == DG_SUM_K ? 2 * kb : kb;
     const double planes = j.mode == DG_GATED || j.mode == DG_PAIR_M ? 2.0 : 1.0;
@@ -658,23 +668,13 @@ GemmPlan plan_gemm(const DenseJob &j, int pairs) {
         const int per = j.mode == DG_GATED ? tn / 2 : tn;
         const int nt = (j.N + per - 1) / per;
         const double tiles = (double)mt * nt;
-        int parts = 1;
-        for (; parts <= 8 && tiles * parts <= pairs && slices >= 8 * parts; ++parts) {
-            const double waves = parts > 1 ? 1.0 : ceil(tiles / pairs);
+        for (int parts = 1; parts <= most; ++parts) {
+            if (parts > 1 && (tiles * parts > pairs || slices < 8 * parts)) break;
             // the parts' bytes, written and read at about 5 KB per cycle
             const double join = parts > 1 ? kParts + parts * planes * j.M * j.N * 8.0 / 5000.0 : 0.0;
-            const double t = waves * (ceil((double)slices / parts) * slice_cycles(tn) + kTile) + join;
-            if (t < cost * 0.999) {
-                cost = t;
-                best = {tn, mt, nt, slices, parts};
-            }
-        }
-        if (parts == 1) {  // more tiles than pairs, or few slices
-            const double t = ceil(tiles / pairs) * (slices * slice_cycles(tn) + kTile);
-            if (t < cost * 0.999) {
-                cost = t;
-                best = {tn, mt, nt, slices, 1};
-            }
+            const double t =
+                ceil(tiles * parts / pairs) * tile_cycles((slices + parts - 1) / parts, tn) + join;
+            if (t < best.cycles * 0.999) best = {tn, mt, nt, slices, parts, t};
         }
     }
     return best;
@@ -792,11 +792,6 @@ static rvq_status launch_products(GemmParams<JOBS> &p, cudaStream_t stream) {
         p.g[i].stages = DG_RING / stage < DG_MAX_ST ? DG_RING / stage : DG_MAX_ST;
     }
     const int pairs_max = num_sms() / 2, pairs = units < pairs_max ? (int)units : pairs_max;
-    if (JOBS > 1) {
-        // how many units of the second a unit of the first lasts
-        const long long first = (long long)p.g[0].mt * p.g[0].nt % pairs;
-        p.bonus = first ? p.g[0].slices / p.g[JOBS - 1].slices : 0;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(DG_THREADS);
@@ -816,9 +811,10 @@ static rvq_status launch_products(GemmParams<JOBS> &p, cudaStream_t stream) {
     return RVQ_OK;
 }
 
-rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
+// one product, its tiles cut into up to `most` parts
+static rvq_status launch_one(const DenseJob &job, int most, cudaStream_t stream) {
     if (dense_stream_fits(job)) return launch_dense_stream(job, stream);
-    const GemmPlan plan = plan_gemm(job, num_sms() / 2);
+    const GemmPlan plan = plan_gemm(job, num_sms() / 2, most);
     const bool gated = job.mode == DG_GATED;
     GemmParams<1> p = {};
     RVQ_TRY(fill_args(job, plan, p.g[0], p.a[0], p.b[0]));
@@ -831,33 +827,44 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     return RVQ_OK;
 }
 
+rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
+    return launch_one(job, kMaxParts, stream);
+}
+
 rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, cudaStream_t stream) {
     const long long pairs = num_sms() / 2;
-    const GemmPlan px = plan_gemm(x, (int)pairs), py = plan_gemm(y, (int)pairs);
-    const bool swap = px.slices < py.slices;  // the longer tiles first
+    const GemmPlan px = plan_gemm(x, (int)pairs, 1), py = plan_gemm(y, (int)pairs, 1);
+    const double tx = tile_cycles(px.slices, px.tile_n), ty = tile_cycles(py.slices, py.tile_n);
+    const bool swap = tx < ty;  // the longer tiles first
     const GemmPlan &p0 = swap ? py : px, &p1 = swap ? px : py;
-    // slices until the last pair is done, one launch after the other and together
+    const double t0 = swap ? ty : tx, t1 = swap ? tx : ty;
+    // Cycles until the last pair is done, one launch after the other and together
     // (see Work); together only where that ends sooner (whole training steps, apart
-    // and together: 4096 tokens of 7168 x 2048, 768 slices either way, 484 and 491 us;
-    // 1333 x 1000 x 2048, 53 either way, 57.5 and 54 us; 1777 x 4104 x 1736, 121 and 93,
-    // 114 and 101 us)
+    // and together: 4096 tokens of 7168 x 2048, equal waves, 484 and 491 us, so 3 %
+    // are taken for operands that are shared less; 1333 x 1000 x 2048, equal waves,
+    // 57.5 and 54 us, so 6500 cycles for a launch; 1777 x 4104 x 1736, 121 slices and
+    // 93, 114 and 101 us).
+    const double apart = plan_gemm(x, (int)pairs).cycles + plan_gemm(y, (int)pairs).cycles + 6500.0;
     const long long u0 = (long long)p0.mt * p0.nt, u1 = (long long)p1.mt * p1.nt;
-    const long long s0 = p0.slices, s1 = p1.slices;
-    const long long apart = (u0 + pairs - 1) / pairs * s0 + (u1 + pairs - 1) / pairs * s1;
-    const long long first = u0 % pairs, early = pairs - first, bonus = first ? s0 / s1 : 0;
+    const long long first = u0 % pairs, early = pairs - first;
+    const int bonus = first ? (int)(t0 / t1) : 0;
     const long long rest = u1 > bonus * early ? u1 - bonus * early : 0;
-    const long long late_end = (u0 / pairs + (first ? 1 : 0)) * s0 +
-                               (rest / pairs + (rest % pairs > early ? 1 : 0)) * s1;
-    const long long early_end = u0 / pairs * s0 + (bonus + (rest + pairs - 1) / pairs) * s1;
-    const long long together = late_end > early_end ? late_end : early_end;
-    // 3 % for operands that are shared less, and a launch of about 12 slices saved
-    if (px.parts > 1 || py.parts > 1 || together * 103 >= (apart + 12) * 100) {
-        RVQ_TRY(launch_dense_gemm(x, stream));
-        return launch_dense_gemm(y, stream);
+    const double late_end = (double)(u0 / pairs + (first ? 1 : 0)) * t0 +
+                            (double)(rest / pairs + (rest % pairs > early ? 1 : 0)) * t1;
+    const double early_end = (double)(u0 / pairs) * t0 +
+                             (double)(bonus + (rest + pairs - 1) / pairs) * t1;
+    const double together = late_end > early_end ? late_end : early_end;
+    const bool one = !dense_stream_fits(x) && !dense_stream_fits(y) && together * 1.03 < apart;
+    if (!one || !x.out[0] || !y.out[0]) {
+        // a product wanted alone is cut as it would be beside the other: the same sums
+        const int most = one ? 1 : kMaxParts;
+        if (x.out[0]) RVQ_TRY(launch_one(x, most, stream));
+        return y.out[0] ? launch_one(y, most, stream) : RVQ_OK;
     }
     GemmParams<2> p = {};
     RVQ_TRY(fill_args(swap ? y : x, p0, p.g[0], p.a[0], p.b[0]));
     RVQ_TRY(fill_args(swap ? x : y, p1, p.g[1], p.a[1], p.b[1]));
+    p.bonus = bonus;
     return launch_products<false, 2>(p, stream);
 }
 

@@ -1,5 +1,5 @@
-// The forward products of the dense operators for few tokens (decode batches):
-// moe_linear and moe_gated_linear as a stream of the weights.
+// The products of the dense operators for few tokens (decode batches) as a stream
+// of the weights: moe_linear, moe_gated_linear and the gradients of their inputs.
 //
 // Memory-bound: rows x cols weights are read once and a handful of tokens are
 // multiplied with each, so the weights take the place of the M operand (128 of
@@ -12,6 +12,9 @@
 //  * Weights and tokens arrive by TMA in 64-deep slices through a ring of about
 //    190 KB per CTA, or 96 KB where there are enough CTAs for two per SM; one
 //    thread issues the MMAs.
+//  * For the gradient of the input the weights are read as they lie ([depth][row]),
+//    through MN-major descriptors, and the gate's and the up half's products follow
+//    one another in depth.
 //  * The partial tiles (fp32) go to shared memory, and each CTA of the cluster
 //    adds its share of the rows over the cluster in rank order (distributed
 //    shared memory): no workspace, no atomics, results repeat bit for bit.
@@ -37,7 +40,9 @@ constexpr int DS_MAX_ST = 10;
 constexpr int DS_PITCH = DS_ROWS + 4;  // floats between tokens of a partial tile
 
 struct StreamArgs {
-    int n, rows, kb;      // tokens, rows of one matrix, 64-deep slices
+    int n, rows, kb;      // tokens, rows of one matrix, 64-deep slices of a product
+    int slices;           // kb, or 2 kb (a sum of two products)
+    int w_t;              // weights stored [depth][row]
     int npad;             // tokens padded to a multiple of 16
     int stages, split;    // ring depth; CTAs of a cluster
     int ahead;            // slices prefetched before the kernel may read
@@ -97,15 +102,16 @@ __device__ __forceinline__ void ld2(const void *p, int dt, int64_t i, float (&v)
 template <bool GATED>
 __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
     const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
-    const __grid_constant__ CUtensorMap mx, const __grid_constant__ StreamArgs g) {
+    const __grid_constant__ CUtensorMap mx0, const __grid_constant__ CUtensorMap mx1,
+    const __grid_constant__ StreamArgs g) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int TR = GATED ? DS_ROWS / 2 : DS_ROWS;  // rows of one matrix in a tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int tile = blockIdx.x / g.split;
     const int r0 = tile * TR;
-    const int k0 = (int)((int64_t)g.kb * rank / g.split);
-    const int k1 = (int)((int64_t)g.kb * (rank + 1) / g.split);
+    const int k0 = (int)((int64_t)g.slices * rank / g.split);
+    const int k1 = (int)((int64_t)g.slices * (rank + 1) / g.split);
     const int stage = DS_ABYTES + g.npad * DS_BK * 2;
     __shared__ __align__(8) uint64_t bars[2 * DS_MAX_ST + 1];
     __shared__ uint32_t tslot;
@@ -137,8 +143,15 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
         // While the kernel before this one ends, bring the first weights into L2
         // (whatever that kernel writes is read coherently after the wait).
         for (int k = k0; k < k1 && k < k0 + g.ahead; ++k) {
-            tma_prefetch(&mw0, k * DS_BK, r0);
-            if (GATED) tma_prefetch(&mw1, k * DS_BK, r0);
+            const int kx = (k < g.kb ? k : k - g.kb) * DS_BK;
+            const CUtensorMap *mw = k < g.kb ? &mw0 : &mw1;
+            if (g.w_t) {
+                tma_prefetch(mw, r0, kx);
+                tma_prefetch(mw, r0 + 64, kx);
+            } else {
+                tma_prefetch(mw, kx, r0);
+                if (GATED) tma_prefetch(&mw1, kx, r0);
+            }
         }
     }
     dependency_wait();
@@ -151,11 +164,18 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
                                              g.status))
                 break;
             const uint32_t st = smem_u32(smem + s * stage), bar = full0 + 8 * s;
+            const int kx = (k < g.kb ? k : k - g.kb) * DS_BK;
+            const CUtensorMap *mw = k < g.kb ? &mw0 : &mw1, *mx = k < g.kb ? &mx0 : &mx1;
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar, (uint32_t)stage);
-                tma_load(st, &mw0, k * DS_BK, r0, bar);
-                if (GATED) tma_load(st + DS_ABYTES / 2, &mw1, k * DS_BK, r0, bar);
-                tma_load(st + DS_ABYTES, &mx, k * DS_BK, 0, bar);
+                if (g.w_t) {
+                    tma_load(st, mw, r0, kx, bar);
+                    tma_load(st + 8192, mw, r0 + 64, kx, bar);
+                } else {
+                    tma_load(st, mw, kx, r0, bar);
+                    if (GATED) tma_load(st + DS_ABYTES / 2, &mw1, kx, r0, bar);
+                }
+                tma_load(st + DS_ABYTES, mx, kx, 0, bar);
             }
             __syncwarp();
         }
@@ -165,11 +185,12 @@ __global__ void __launch_bounds__(DS_THREADS, 2) dense_stream_kernel(
             if (!warp_wait(full0 + 8 * s, (it / g.stages) & 1, abort_flag, g.status)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t st = smem_u32(smem + s * stage);
-            const uint64_t a = operand_desc(st, 0), b = operand_desc(st + DS_ABYTES, 0);
+            const uint64_t a = operand_desc(st, g.w_t), b = operand_desc(st + DS_ABYTES, 0);
+            const uint32_t da = g.w_t ? 2048u >> 4 : 2u;
             if (elect_one()) {
 #pragma unroll
                 for (int q = 0; q < DS_BK / 16; ++q)
-                    mma_one(tmem, a + 2 * q, b + 2 * q, g.idesc, (it > 0 || q > 0) ? 1u : 0u);
+                    mma_one(tmem, a + q * da, b + 2 * q, g.idesc, (it > 0 || q > 0) ? 1u : 0u);
                 mma_commit(empty0 + 8 * s);
             }
             __syncwarp();
@@ -290,12 +311,13 @@ int stream_tiles(const DenseJob &j) {
 // us, stream / tiled: gated 7168 -> 2048, 192 tokens 20.5 / 21.8, 256 23.9 / 22.2;
 // gated 1736 -> 1000, 128 8.7 / 9.9, 192 10.7 / 10.4; plain 2048 -> 7168, 96 12.8 /
 // 13.6, 128 14.3 / 13.6; 1736 -> 4104, 128 11.4 / 12.1; 512 -> 2048, 48 4.9 / 5.0,
-// 64 5.4 / 5.0).
+// 64 5.4 / 5.0; gradient of the input, 7168 x 2048, 1 9.4 / 15.2, 96 15.9 / 15.9).
 // 64 tokens is the end for few rows, which are split eightfold up to there (7168 ->
 // 512: 64 9.0 / 9.7, 96 14.7 / 10.1).
 bool dense_stream_fits(const DenseJob &j) {
-    if (j.a_t || j.b_t || (j.mode != DG_GATED && j.mode != DG_PLAIN)) return false;
-    const int most = j.mode == DG_GATED ? kStreamMaxTokens : j.K >= 1024 ? 112 : 48;
+    if (j.a_t || j.mode == DG_PAIR_M) return false;
+    const int depth = j.mode == DG_SUM_K ? 2 * j.K : j.K;
+    const int most = j.mode == DG_GATED ? kStreamMaxTokens : depth >= 1024 ? 112 : 48;
     return j.M <= (stream_tiles(j) * 8 <= num_sms() / 2 && most > 64 ? 64 : most);
 }
 
@@ -315,19 +337,23 @@ rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream) {
     g.n = job.M;
     g.rows = job.N;
     g.kb = (job.K + DS_BK - 1) / DS_BK;
+    g.slices = job.mode == DG_SUM_K ? 2 * g.kb : g.kb;
+    g.w_t = job.b_t;
     g.npad = (job.M + 15) / 16 * 16;
     const int tile_rows = gated ? DS_ROWS / 2 : DS_ROWS;
     const int tiles = stream_tiles(job);
     // Depth split: as many CTAs as are resident at once (two per SM up to 128
     // tokens), each with two slices or more.  Past 16 tokens at most four, since
     // the joined tile grows (64 tokens, 7168 -> 2 x 2048: 15.7 us with 128 CTAs
-    // of large rings, 18.5 us with 256 of small ones), unless tiles are few (64
-    // tokens, 7168 -> 512).  Clusters of eight take small rings: with one CTA per
-    // SM a GPC's SMs do not divide by eight.
+    // of large rings, 18.5 us with 256 of small ones), unless tiles are few and deep
+    // (64 tokens, 7168 -> 2048 13.1 us in eight parts, 14.8 in four; 1736 -> 2 x 1000
+    // 9.7 and 7.0).  Clusters of eight take small rings: with one CTA per SM a GPC's
+    // SMs do not divide by eight.
     const int sms = num_sms(), slots = g.npad <= 128 ? 2 * sms : sms;
-    const int most = g.npad <= 16 || (g.npad <= 64 && tiles * 8 <= sms / 2) ? 8 : 4;
+    const bool deep = tiles * 4 <= sms / 2 && g.slices >= 64;
+    const int most = g.npad <= 16 || (g.npad <= 64 && deep) ? 8 : 4;
     g.split = 1;
-    while (g.split < most && tiles * g.split * 2 <= slots && g.kb >= g.split * 4) g.split *= 2;
+    while (g.split < most && tiles * g.split * 2 <= slots && g.slices >= g.split * 4) g.split *= 2;
     const bool two = g.npad <= 128 && (tiles * g.split > sms || g.split == 8);
     const int ring = two ? kRingSmall : kRingLarge;
     const int stage = DS_ABYTES + g.npad * DS_BK * 2;
@@ -336,7 +362,8 @@ rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream) {
     g.cols = 32;
     while ((int)g.cols < g.npad) g.cols *= 2;
     const uint32_t fmt = job.dt == RVQ_BF16 ? 1u : 0u;
-    g.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(g.npad >> 3) << 17) |
+    g.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)job.b_t << 15) |
+              ((uint32_t)(g.npad >> 3) << 17) |
               ((uint32_t)(DS_ROWS >> 4) << 24);
     g.dt = job.dt;
     g.act = job.act;
@@ -352,13 +379,18 @@ rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream) {
         g.pre[i] = job.pre[i];
     }
     g.status = job.status;
-    CUtensorMap mw[2], mx;
-    RVQ_TRY(encode_operand(&mw[0], job.b[0], job.N, job.K, job.ldb, 0, job.dt, tile_rows));
-    if (gated)
-        RVQ_TRY(encode_operand(&mw[1], job.b[1], job.N, job.K, job.ldb, 0, job.dt, tile_rows));
-    else
-        mw[1] = mw[0];
-    RVQ_TRY(encode_operand(&mx, job.a[0], job.M, job.K, job.lda, 0, job.dt, g.npad));
+    CUtensorMap mw[2], mx[2];
+    for (int i = 0; i < 2; ++i) {
+        if (i == 1 && (job.b[1] == nullptr || job.mode == DG_PLAIN))
+            mw[1] = mw[0];
+        else
+            RVQ_TRY(encode_operand(&mw[i], job.b[i], job.N, job.K, job.ldb, job.b_t, job.dt,
+                                   tile_rows));
+        if (i == 1 && job.mode != DG_SUM_K)
+            mx[1] = mx[0];
+        else
+            RVQ_TRY(encode_operand(&mx[i], job.a[i], job.M, job.K, job.lda, 0, job.dt, g.npad));
+    }
     // the ring, or the partial tile that takes its place
     const int part = g.n * DS_PITCH * 4, dyn = g.stages * stage > part ? g.stages * stage : part;
     cudaLaunchConfig_t cfg = {};
@@ -376,9 +408,9 @@ rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (gated)
-        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_stream_kernel<true>, mw[0], mw[1], mx, g));
+        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_stream_kernel<true>, mw[0], mw[1], mx[0], mx[1], g));
     else
-        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_stream_kernel<false>, mw[0], mw[1], mx, g));
+        RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_stream_kernel<false>, mw[0], mw[1], mx[0], mx[1], g));
     RVQ_LAUNCHED("dense_stream");
     return RVQ_OK;
 }
