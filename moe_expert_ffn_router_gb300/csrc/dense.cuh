@@ -261,9 +261,19 @@ struct DenseJob {
 };
 size_t dense_gemm_partial_bytes(const DenseJob &job);
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream);
-// two products without a common output (not GATED; one dt), in one launch where
-// that is faster; one whose out[0] is NULL is not wanted
-rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, cudaStream_t stream);
+// Sums of a bias gradient still to be added: dbias[m][col] (NULL: not wanted) from
+// the fp32 partials part[chunk][m][col].
+struct BiasSums {
+    const float *part;
+    int chunks, mats, rows, dt;
+    void *dbias[2];
+    __host__ __device__ bool wanted() const { return dbias[0] || dbias[1]; }
+};
+// Two products without a common output (not GATED; one dt), in one launch where
+// that is faster; one whose out[0] is NULL is not wanted.  Adds the bias gradients
+// along with them.
+rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const BiasSums &sums,
+                                 cudaStream_t stream);
 // launch_dense_gemm for few tokens as the rows of A: the weights streamed past the
 // batch (dense_stream.cu)
 constexpr int kStreamMaxTokens = 192;
@@ -274,7 +284,8 @@ rvq_status launch_dense_stream(const DenseJob &job, cudaStream_t stream);
 //   mats 2: dp0 = dout * pre1 * act'(pre0), dp1 = dout * act(pre0)
 //   mats 1: dp0 = alpha * dout * act'(pre0)      (pre0 NULL: act' = 1)
 // dp (16-bit [n][rows] each, NULL: not written) and, with dbias[i] set, the
-// sums over the n rows through fp32 partials ([chunks][mats][rows] in part).
+// partial sums over the n rows (fp32 [chunks][mats][rows] in part), which
+// launch_dense_gemm_two or launch_bias_sums adds.
 struct DenseBwdJob {
     int mats, n, rows, act;
     float alpha;
@@ -290,6 +301,27 @@ struct DenseBwdJob {
 constexpr int kBwdChunkRows = 32;  // rows per partial of a bias gradient
 inline int dense_bwd_chunks(int n) { return (n + kBwdChunkRows - 1) / kBwdChunkRows; }
 rvq_status launch_dense_bwd(const DenseBwdJob &job, cudaStream_t stream);
+// Adds the partials of bias gradients: eight columns per warp and turn, the chunks
+// dealt to four lanes each, whose sums are added in a fixed order.
+__device__ __forceinline__ void add_bias_sums(const BiasSums &s, int warp, int warps, int lane) {
+    const int col = lane & 7, first = lane >> 3;
+    const int groups = s.rows / 8;
+    const int64_t step = (int64_t)s.mats * s.rows;
+    for (int i = warp; i < s.mats * groups; i += warps) {
+        const int m = i / groups, c = (i - m * groups) * 8 + col;
+        if (s.dbias[m] == nullptr) continue;
+        const float *p = s.part + (int64_t)m * s.rows + c;
+        float sum = 0.f;
+#pragma unroll 8
+        for (int k = first; k < s.chunks; k += 4) sum += p[k * step];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (first == 0) st_elem(s.dbias[m], s.dt, c, sum);
+    }
+}
+
+BiasSums bias_sums_of(const DenseBwdJob &job);
+rvq_status launch_bias_sums(const BiasSums &s, cudaStream_t stream);
 
 // ---------------------------------------------------------------- norm join
 struct JoinJob {

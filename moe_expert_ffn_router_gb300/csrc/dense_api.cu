@@ -267,6 +267,7 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
     // without an activation the products read dout itself (alpha goes into
     // their epilogues), so nothing is rounded on the way
     const bool direct = act == MOE_ACT_NONE;
+    BiasSums sums = {};
     if (!direct || dbias_dev) {
         DenseBwdJob b = {};
         b.mats = 1;
@@ -282,6 +283,7 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
         b.dbias[0] = dbias_dev;
         b.part = (float *)(ws + P.off_part);
         RVQ_TRY(launch_dense_bwd(b, st));
+        sums = bias_sums_of(b);
     }
     DenseJob j = {};
     j.mode = DG_PLAIN;
@@ -310,7 +312,7 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
     w.ldb = ldx;
     w.out[0] = dw_dev;
     w.ldo = lddw;
-    return launch_dense_gemm_two(j, w, st);
+    return launch_dense_gemm_two(j, w, sums, st);
 }
 
 rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const void *x_dev,
@@ -401,7 +403,7 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
     w.out[0] = dwg_dev;
     w.out[1] = dwu_dev;
     w.ldo = lddw;
-    return launch_dense_gemm_two(j, w, st);
+    return launch_dense_gemm_two(j, w, bias_sums_of(b), st);
 }
 
 // ---------------------------------------------------------------- norm join

@@ -6,8 +6,10 @@
 // written once, 16 or 32 bytes per thread and access.  A block takes 32 rows x
 // 256 columns (32 groups of eight columns x 8 row lanes, four rows each), so a
 // bias gradient leaves one fp32 partial per 32 rows and column, added in row
-// order; a second launch adds the partials in chunk order (no atomics: results
-// repeat bit for bit).
+// order.  The partials are added in a fixed order (no atomics: results repeat
+// bit for bit) by idle warps of the products that follow, which hides them (whole
+// training step, 1333 x 1000 x 2048: @@ us; with a launch of their own @@), or by a
+// launch of their own where no such product is wanted.
 #include "dense.cuh"
 
 namespace rvq {
@@ -97,25 +99,9 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
     }
 }
 
-// Adds the chunks' partials: 32 columns x 32 lanes, a lane's chunks in order,
-// then the lanes in order.
-__global__ void __launch_bounds__(1024) dense_bias_sum_kernel(const DenseBwdJob j, int chunks) {
-    __shared__ float red[32][33];
-    const int q = threadIdx.x & 31, lane = threadIdx.x >> 5, m = blockIdx.y;
-    const int col = blockIdx.x * 32 + q;
+__global__ void __launch_bounds__(256) dense_bias_sum_kernel(const BiasSums s) {
     dependency_wait();
-    if (j.dbias[m] == nullptr) return;
-    float s = 0.f;
-    if (col < j.rows)
-#pragma unroll 4
-        for (int k = lane; k < chunks; k += 32) s += j.part[((int64_t)k * j.mats + m) * j.rows + col];
-    red[lane][q] = s;
-    __syncthreads();
-    if (lane != 0 || col >= j.rows) return;
-    s = 0.f;
-#pragma unroll
-    for (int l = 0; l < 32; ++l) s += red[l][q];
-    st_elem(j.dbias[m], j.dt, col, s);
+    add_bias_sums(s, (int)blockIdx.x * 8 + (threadIdx.x >> 5), (int)gridDim.x * 8, threadIdx.x & 31);
 }
 
 }  // namespace
@@ -127,11 +113,17 @@ rvq_status launch_dense_bwd(const DenseBwdJob &job, cudaStream_t stream) {
     j.wide = (((uintptr_t)job.pre[0] | (uintptr_t)job.pre[1]) & 31) == 0;
     RVQ_CUDA(job.mats == 2 ? launch_after(dense_bwd_kernel<2>, grid, 256, 0, stream, j)
                            : launch_after(dense_bwd_kernel<1>, grid, 256, 0, stream, j));
-    if (job.dbias[0] || job.dbias[1]) {
-        RVQ_CUDA(launch_after(dense_bias_sum_kernel,
-                              dim3((unsigned)((job.rows + 31) / 32), (unsigned)job.mats), 1024, 0,
-                              stream, job, chunks));
-    }
+    return RVQ_OK;
+}
+
+BiasSums bias_sums_of(const DenseBwdJob &job) {
+    return {job.part, dense_bwd_chunks(job.n), job.mats, job.rows, job.dt,
+            {job.dbias[0], job.dbias[1]}};
+}
+
+rvq_status launch_bias_sums(const BiasSums &s, cudaStream_t stream) {
+    const int groups = s.mats * (s.rows / 8);  // a warp each
+    RVQ_CUDA(launch_after(dense_bias_sum_kernel, (unsigned)((groups + 7) / 8), 256, 0, stream, s));
     return RVQ_OK;
 }
 

@@ -83,6 +83,7 @@ struct GemmParams {
     CUtensorMap a[JOBS][2], b[JOBS][2];
     GemmArgs g[JOBS];
     int bonus;           // see Work
+    BiasSums sums;       // added beside the products
 };
 
 __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
@@ -480,6 +481,9 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
             if (elect_one()) commit_pair(accfull0 + 8 * buf);
             __syncwarp();
         }
+    } else if (warp == 2 || warp == 3) {
+        if (!GATED && params.sums.wanted())
+            add_bias_sums(params.sums, (int)blockIdx.x * 2 + warp - 2, (int)gridDim.x * 2, lane);
     } else if (warp >= 4) {
         // epilogue: lanes 32 q .. 32 q + 31 of the accumulator, every other
         // group of 32 columns
@@ -812,11 +816,16 @@ static rvq_status launch_products(GemmParams<JOBS> &p, cudaStream_t stream) {
 }
 
 // one product, its tiles cut into up to `most` parts
-static rvq_status launch_one(const DenseJob &job, int most, cudaStream_t stream) {
-    if (dense_stream_fits(job)) return launch_dense_stream(job, stream);
+static rvq_status launch_one(const DenseJob &job, int most, const BiasSums &sums,
+                             cudaStream_t stream) {
+    if (dense_stream_fits(job)) {
+        RVQ_TRY(launch_dense_stream(job, stream));
+        return sums.wanted() ? launch_bias_sums(sums, stream) : RVQ_OK;
+    }
     const GemmPlan plan = plan_gemm(job, num_sms() / 2, most);
     const bool gated = job.mode == DG_GATED;
     GemmParams<1> p = {};
+    p.sums = sums;
     RVQ_TRY(fill_args(job, plan, p.g[0], p.a[0], p.b[0]));
     RVQ_TRY((gated ? launch_products<true, 1>(p, stream) : launch_products<false, 1>(p, stream)));
     if (plan.parts == 1) return RVQ_OK;
@@ -828,10 +837,11 @@ static rvq_status launch_one(const DenseJob &job, int most, cudaStream_t stream)
 }
 
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
-    return launch_one(job, kMaxParts, stream);
+    return launch_one(job, kMaxParts, BiasSums{}, stream);
 }
 
-rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, cudaStream_t stream) {
+rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const BiasSums &sums,
+                                 cudaStream_t stream) {
     const long long pairs = num_sms() / 2;
     const GemmPlan px = plan_gemm(x, (int)pairs, 1), py = plan_gemm(y, (int)pairs, 1);
     const double tx = tile_cycles(px.slices, px.tile_n), ty = tile_cycles(py.slices, py.tile_n);
@@ -858,13 +868,15 @@ rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, cudaStrea
     if (!one || !x.out[0] || !y.out[0]) {
         // a product wanted alone is cut as it would be beside the other: the same sums
         const int most = one ? 1 : kMaxParts;
-        if (x.out[0]) RVQ_TRY(launch_one(x, most, stream));
-        return y.out[0] ? launch_one(y, most, stream) : RVQ_OK;
+        if (x.out[0]) RVQ_TRY(launch_one(x, most, y.out[0] ? BiasSums{} : sums, stream));
+        if (y.out[0]) return launch_one(y, most, sums, stream);
+        return !x.out[0] && sums.wanted() ? launch_bias_sums(sums, stream) : RVQ_OK;
     }
     GemmParams<2> p = {};
     RVQ_TRY(fill_args(swap ? y : x, p0, p.g[0], p.a[0], p.b[0]));
     RVQ_TRY(fill_args(swap ? x : y, p1, p.g[1], p.a[1], p.b[1]));
     p.bonus = bonus;
+    p.sums = sums;
     return launch_products<false, 2>(p, stream);
 }
 

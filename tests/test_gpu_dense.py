@@ -405,3 +405,35 @@ def test_offsets_beyond_32_bits():
     rvq.moe_linear_backward(strided, x, w, n, rows, cols, ws, dx=dx)
     rvq.moe_linear_backward(plain, x, w, n, rows, cols, ws, dx=dx2)
     assert torch.equal(dx, dx2)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(3, 264, 200), (300, 1000, 136), (5000, 8, 72),
+                                         (700, 4104, 264)])
+def test_bias_gradients_beside_any_product(n, rows, cols):
+    """The sums of a bias gradient are the same with both products, one or none,
+    and with the other bias left out."""
+    g = gen(n)
+    x, wg, wu = (normal(g, s, BF, v) for s, v in (((n, cols), 1.0), ((rows, cols), cols ** -0.5),
+                                                  ((rows, cols), cols ** -0.5)))
+    bg, bu = normal(g, (rows,), BF), normal(g, (rows,), BF)
+    dout = normal(g, (n, rows), BF, 0.5)
+    ws = workspace(n, rows, cols, True)
+    out = torch.empty((n, rows), dtype=BF, device=DEV)
+    pre = torch.empty((2, n, rows), dtype=F32, device=DEV)
+    rvq.moe_gated_linear(x, wg, wu, n, rows, cols, out, ws, bg=bg, bu=bu, pre=pre)
+    dg, edg, du, edu = gated_dp(x, wg, wu, bg, bu, dout, "silu")
+    _, outs = R.grads([dg, du], [edg, edu], x, [wg, wu], BF)
+    first = None
+    for products in (("dx", "dwg", "dwu"), ("dx",), ("dwg", "dwu"), ()):
+        for biases in (("dbg", "dbu"), ("dbg",), ("dbu",)):
+            kw = {k: torch.full((n if k == "dx" else rows, cols), float("nan"), dtype=BF, device=DEV)
+                  for k in products}
+            kw.update({k: torch.full((rows,), float("nan"), dtype=BF, device=DEV) for k in biases})
+            rvq.moe_gated_linear_backward(dout, x, wg, wu, pre, n, rows, cols, ws, **kw)
+            assert rvq.rvq_ws_status(ws) == (0, 0)
+            if first is None:
+                first = kw
+                R.check(kw["dbg"], outs[0][1], "dbg")
+                R.check(kw["dbu"], outs[1][1], "dbu")
+            for k in biases:
+                assert torch.equal(kw[k], first[k]), (products, k)
