@@ -14,9 +14,10 @@ namespace rvq {
 // The dense operators' kernels are launched programmatically: a kernel's blocks
 // may start as those of the kernel before it on the stream end, and touch memory
 // only after dependency_wait(), which waits for that kernel's end.  Only short
-// kernels call dependents_may_start(): waiting blocks of the next kernel hold
-// shared memory, and with the walking kernels of moe_norm_join that cost more
-// than the launch (forward and gradients of 4099 x 2048: 70 us, 54 us without).
+// kernels call dependents_may_start() (those for few rows, and the elementwise
+// gradients, whose products then start 1 to 2 us sooner): waiting blocks of the next
+// kernel hold shared memory, and with the walking kernels of moe_norm_join that cost
+// more than the launch (forward and gradients of 4099 x 2048: 70 us, 54 us without).
 __device__ __forceinline__ void dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -98,11 +98,11 @@ __global__ void __launch_bounds__(1024) join_row_kernel(const JoinJob j) {
     }
 }
 
-// Adds the blocks' sums: 32 columns x 32 lanes, a lane's blocks in order, then
-// the lanes in order.
+// Adds the blocks' sums: 32 columns (a quad per thread) x up to 128 lanes, a lane's
+// blocks in order, then the lanes in a fixed order.
 __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinJob j) {
-    __shared__ float red[32][33];
-    const int k = blockIdx.y, q = threadIdx.x & 31, lane = threadIdx.x >> 5;
+    __shared__ float red[32][32];
+    const int k = blockIdx.y, q = threadIdx.x & 7, lane = threadIdx.x >> 3, lanes = blockDim.x >> 3;
     void *dst = k == 0 ? j.dw_post : k == 1 ? j.dw_pre
                 : j.gate_kind == MOE_GATE_CHANNEL ? j.dgate : nullptr;
     dependency_wait();
@@ -117,18 +117,31 @@ __global__ void __launch_bounds__(1024) join_sum_kernel(const JoinJob j) {
         return;
     }
     if (dst == nullptr) return;
-    const int c = blockIdx.x * 32 + q;
-    float s = 0.f;
-    if (c < j.d)
-#pragma unroll 4
-        for (int i = lane; i < j.slots; i += 32) s += j.part[((int64_t)i * 3 + k) * j.d + c];
-    red[lane][q] = s;
-    __syncthreads();
-    if (lane == 0 && c < j.d) {
-        s = 0.f;
+    const int c = blockIdx.x * 32 + q * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < j.d) {
+        const float *p = j.part + (int64_t)k * j.d + c;
+#pragma unroll 8
+        for (int i = lane; i < j.slots; i += lanes) {
+            const float4 o = *reinterpret_cast<const float4 *>(p + (int64_t)i * 3 * j.d);
+            s = make_float4(s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w);
+        }
+    }
 #pragma unroll
-        for (int l = 0; l < 32; ++l) s += red[l][q];
-        st_elem(dst, k == 2 ? j.gdt : j.wdt, c, s);
+    for (int o = 8; o < 32; o *= 2) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+        s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+        s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    }
+    if ((threadIdx.x & 31) < 8) *reinterpret_cast<float4 *>(&red[threadIdx.x >> 5][q * 4]) = s;
+    __syncthreads();
+    const int col = blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && col < j.d) {
+        float t = 0.f;
+#pragma unroll 8
+        for (int w = 0; w < lanes / 4; ++w) t += red[w][threadIdx.x];
+        st_elem(dst, k == 2 ? j.gdt : j.wdt, col, t);
     }
 }
 
@@ -158,8 +171,9 @@ rvq_status launch_norm_join_bwd(const JoinJob &job, cudaStream_t stream) {
     const bool gate = j.dgate && (j.gate_kind == MOE_GATE_CHANNEL || j.gate_kind == MOE_GATE_SCALAR);
     if (j.dw_post || j.dw_pre || gate) {
         // the blocks' sums over rows, in order (no atomics: results repeat)
-        RVQ_CUDA(launch_after(join_sum_kernel, dim3((unsigned)((j.d + 31) / 32), 3), 1024, 0, stream,
-                              j));
+        const int lanes = j.slots < 256 ? 32 : 128;
+        RVQ_CUDA(launch_after(join_sum_kernel, dim3((unsigned)((j.d + 31) / 32), 3), 8 * lanes, 0,
+                              stream, j));
     }
     return RVQ_OK;
 }
