@@ -228,6 +228,15 @@ inline int join_bwd_blocks(int d) {
     const int b = 512 / (((d / 4 + 3) / 4 + 31) / 32 * 32);
     return b < 4 ? 4 : b;
 }
+// Whether a thread of the gradients' kernel takes two groups of columns instead of
+// four, for twice the warps: where the rows' bytes leave an SM few blocks, or a block
+// few warps, or there is a row per SM at most (forward and gradients, four and two:
+// fp32 2000 x 2048 39.5 and 31.8 us, 1500 x 4096 57.3 and 49.2; bf16 3000 x 1000 28.6
+// and 27.0, 100 x 2048 11.0 and 10.1, but 4099 x 2048 40.0 and 42.2).  Past 4096
+// columns the registers of so many threads do not suffice.
+inline bool join_bwd_narrow(const JoinJob &j) {
+    return j.d <= 4096 && (j.hdt == RVQ_F32 || j.d <= 1024 || j.n <= num_sms());
+}
 constexpr int kSmemMax = 225 << 10;  // of a block, beside its static part
 
 inline int join_threads(int d, int group, int v) {

@@ -245,6 +245,13 @@ constexpr int kFwdBlocksPerSm = 16;
 template <class T>
 rvq_status walk(JoinJob &j, const JoinSmem &L, bool bwd, cudaStream_t stream) {
     const int threads = join_threads(j.d, 4, T::V);
+    if constexpr (T::V == 4) {
+        if (bwd && join_bwd_narrow(j)) {
+            using U = JoinTypes<2, T::H, T::Y, T::X, T::W, T::G, T::GATE>;
+            return launch_walk<join_bwd_kernel<U>>(j, join_ring(j, true, 2), join_threads(j.d, 4, 2),
+                                                   join_bwd_blocks(j.d), stream);
+        }
+    }
     if (bwd) return launch_walk<join_bwd_kernel<T>>(j, L, threads, join_bwd_blocks(j.d), stream);
     return launch_walk<join_ring_kernel<T>>(j, L, threads, kFwdBlocksPerSm, stream);
 }
