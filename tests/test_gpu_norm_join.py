@@ -357,3 +357,23 @@ def test_join_repeats_streams_and_graphs():
     torch.cuda.synchronize()
     for k in a:
         assert torch.equal(a[k], b[k]) and torch.equal(a[k], c[k]), k
+
+
+@pytest.mark.parametrize("half", [BF, HF])
+@pytest.mark.parametrize("gate", ["token", "channel", "full"])
+def test_join_threads_with_four_groups_of_columns(half, gate):
+    """The gradients where a thread takes four groups of columns instead of two: 16-bit
+    h with more rows than SMs and more than 1024 columns, fp32 h past 4096 columns."""
+    for k, (hdt, ydt, xdt, wdt) in enumerate(itertools.product((F32, half), repeat=4)):
+        n, d = (3, 4104) if hdt == F32 else (160, 1032)
+        s = make(n, d, hdt, ydt, wdt, gate, True, seed=k)
+        rstd = check_forward(s, n, d, 0.5, True, hdt, xdt)
+        check_backward(s, n, d, 0.5, True, hdt, ydt, xdt, wdt, rstd)
+
+
+@pytest.mark.parametrize("n,d,dtype", [(152, 2048, BF), (153, 2048, BF), (300, 1024, BF),
+                                       (300, 1032, BF), (300, 4096, F32), (300, 4104, F32)])
+def test_join_at_the_limits_of_narrow_threads(n, d, dtype):
+    s = make(n, d, dtype, dtype, dtype, "channel", True, seed=d)
+    rstd = check_forward(s, n, d, 0.75, True, dtype, BF)
+    check_backward(s, n, d, 0.75, True, dtype, dtype, BF, dtype, rstd)
