@@ -20,9 +20,14 @@
 //    and act(g) * u is formed in registers.
 //  * Outputs are turned from a row per lane into rows of 64 or 128 contiguous
 //    bytes through 4 KB of staging per warp; biases are staged once per tile.
-//  * Tiles too few for half the pairs are cut by slices into parts, which a second
-//    launch adds in order; the products of dx and dw share a launch where their
-//    tiles fill the pairs better together.
+//  * A tile of too few for half the pairs is split among the two or four pairs of a
+//    cluster, which multiply a run of its slices each and exchange the sums through
+//    distributed shared memory (512 x 2048 x 2048 13.7 -> 11.8 us, 250 x 856 x 1240
+//    10.4 -> 8.1), or, where the depth is long, cut by slices into parts, which a
+//    second launch adds in order (512 tokens, gated 7168 -> 2048 27.7 us, split 30.5).
+//    The products of dx and dw share a launch where their tiles fill the pairs better
+//    together.  (Tiles of 256 columns are not split: what the pairs send takes a third
+//    of the ring, 256 x 7168 x 2048 14.9 -> 17.5 us.)
 // Rows, columns and depth past the ends are zero-filled by TMA and not stored.
 // Each output is rounded once, from fp32.  Every wait is bounded (1 s).
 //
@@ -52,6 +57,7 @@ constexpr int DG_TURN = 4096;  // staging of an epilogue warp: 32 rows x 32 fp32
 constexpr int DG_BIAS = DG_RING + DG_EPI_WARPS * DG_TURN;  // of two tiles, fp32
 constexpr int DG_BARS = DG_BIAS + 2 * 256 * 4;
 constexpr int DG_SMEM = DG_BARS + 256;
+constexpr int kSumsMax = 48 << 10;        // of the ring, for sums of a split tile
 constexpr int DG_THREADS = 32 * (4 + DG_EPI_WARPS);
 constexpr int DG_ACC = 256;  // TMEM columns per accumulator
 constexpr int DG_GROUP = 8;  // M tiles walked together (operand reuse in L2)
@@ -83,6 +89,7 @@ struct GemmParams {
     CUtensorMap a[JOBS][2], b[JOBS][2];
     GemmArgs g[JOBS];
     int bonus;           // see Work
+    int split;           // pairs that share a unit's slices (a cluster), or 1
     BiasSums sums;       // added beside the products
 };
 
@@ -111,11 +118,11 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
 
 // arrives on the barrier at this offset in both CTAs once the MMAs issued so
 // far are done
-__device__ __forceinline__ void commit_pair(uint32_t mbar) {
+__device__ __forceinline__ void commit_pair(uint32_t mbar, uint32_t lead) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(mbar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << lead))
         : "memory");
 }
 
@@ -134,7 +141,9 @@ __device__ __forceinline__ void tile_at(const GemmArgs &g, int t, int &m, int &n
 // the second.  Pairs that got one unit less of the first (those from U0 mod pairs
 // on) first take `bonus` units of the second alone, as many as that one lasts, so
 // that all pairs end together.
-template <int JOBS>
+// With SPLIT a cluster of `split` pairs has one unit, and pair `part` of it a run of
+// its slices.
+template <int JOBS, bool SPLIT>
 struct Work {
     int pair, pairs, unit, round;
     int job, m, n, part, k0, k1;
@@ -143,6 +152,21 @@ struct Work {
         : pair(pair_), pairs(pairs_), unit(pair_), round(0), job(0) {}
     __device__ __forceinline__ bool next(const GemmParams<JOBS> &p) {
         int u;
+        if (SPLIT) {
+            if (round++) return false;
+            u = pair / p.split;
+            part = pair - u * p.split;
+            const int units = p.g[0].mt * p.g[0].nt;
+            if (JOBS > 1 && u >= units) {
+                job = 1;
+                u -= units;
+            }
+            const GemmArgs &g = p.g[JOBS == 1 ? 0 : job];
+            tile_at(g, u, m, n);
+            k0 = (int)((int64_t)g.slices * part / p.split);
+            k1 = (int)((int64_t)g.slices * (part + 1) / p.split);
+            return true;
+        }
         if (job == 0) {
             const int units = p.g[0].mt * p.g[0].nt * p.g[0].parts;
             u = unit;
@@ -352,13 +376,54 @@ __device__ __forceinline__ void finish(const GemmArgs &g, uint32_t turn, int lan
     turn_rows(turn, lane, out, g.odt, g.ldo, row, g.M, c, width, g.residual ? &res : nullptr, g.rdt);
 }
 
-template <bool GATED, int JOBS>
+// Bytes that a CTA receives from the other pairs of its cluster, at the end of the
+// ring: per sender and group of 32 columns that it finishes, 128 rows (twice for a
+// gated product).
+__host__ __device__ __forceinline__ int sums_bytes(int split, int per, bool gated) {
+    const int groups = (per + 31) / 32;
+    return (split - 1) * ((groups + split - 1) / split) * (gated ? 2 : 1) * 4 * DG_TURN;
+}
+
+template <bool GATED>
+__device__ __forceinline__ uint32_t sums_at(const uint8_t *smem, int split, int per, int from,
+                                            int to, int c, int q) {
+    const int groups = ((per + 31) / 32 + split - 1) / split;
+    const int block = (from < to ? from : from - 1) * groups + (c >> 5) / split;
+    return smem_u32(smem + DG_RING - sums_bytes(split, per, GATED)) +
+           (uint32_t)((block * (GATED ? 2 : 1) * 4 + q) * DG_TURN);
+}
+
+// Sums of a split tile on their way between the pairs of a cluster: 32 columns of 32
+// rows, 16 bytes per lane and access (contiguous for a warp, both ways).
+__device__ __forceinline__ void send32(uint32_t addr, int lane, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr + j * 512 +
+                                                                               lane * 16),
+                     "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                     : "memory");
+}
+
+__device__ __forceinline__ void add_sent32(uint32_t addr, int lane, float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float b[4];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3])
+                     : "r"(addr + j * 512 + lane * 16)
+                     : "memory");
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * j + e] += b[e];
+    }
+}
+
+template <bool GATED, int JOBS, bool SPLIT>
 __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     const __grid_constant__ GemmParams<JOBS> params) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    Work<JOBS> work(blockIdx.x >> 1, gridDim.x >> 1);
+    const uint32_t rank = cluster_rank() & 1u, lead = cluster_rank() & ~1u;
+    Work<JOBS, SPLIT> work(blockIdx.x >> 1, gridDim.x >> 1);
     const int stages = params.g[0].stages, stage = params.g[0].stage;  // of both products
     uint32_t *status = params.g[0].status;
     uint8_t *bars = smem + DG_BARS;
@@ -393,6 +458,9 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     const uint32_t tmem = *tslot;
     dependency_wait();
 
+    const int q = warp & 3, par = (warp - 4) >> 2;  // of an epilogue warp
+    const uint32_t turn = smem_u32(smem + DG_RING) + (uint32_t)(warp - 4) * DG_TURN;
+    bool sent = false;
     if (warp == 0) {
         // producer: this CTA's rows of A and of B for every slice
         int s = 0;
@@ -417,7 +485,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                 const CUtensorMap *ta = ma + ((second || k2) ? 1 : 0);
                 const CUtensorMap *tb = mb + ((GATED ? rank == 1 : k2) ? 1 : 0);
                 const uint32_t st = smem_u32(smem + s * stage), sb = st + DG_ABYTES;
-                const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
+                const uint32_t bar = cluster_addr(full0 + 8 * s, lead);
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
                     if (g.a_t) {
@@ -470,7 +538,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                     for (int q = 0; q < DG_BK / 16; ++q)
                         mma_pair(acc, a + q * da, b + q * db, idesc,
                                  (k > work.k0 || q > 0) ? 1u : 0u);
-                    commit_pair(empty0 + 8 * s);
+                    commit_pair(empty0 + 8 * s, lead);
                 }
                 __syncwarp();
                 if (++s == stages) {
@@ -478,7 +546,7 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
                     ++lap;
                 }
             }
-            if (elect_one()) commit_pair(accfull0 + 8 * buf);
+            if (elect_one()) commit_pair(accfull0 + 8 * buf, lead);
             __syncwarp();
         }
     } else if (warp == 2 || warp == 3) {
@@ -487,8 +555,6 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
     } else if (warp >= 4) {
         // epilogue: lanes 32 q .. 32 q + 31 of the accumulator, every other
         // group of 32 columns
-        const int q = warp & 3, par = (warp - 4) >> 2;
-        const uint32_t turn = smem_u32(smem + DG_RING) + (uint32_t)(warp - 4) * DG_TURN;
         for (int done = 0; work.next(params); ++done) {
             const GemmArgs &g = params.g[JOBS == 1 ? 0 : work.job];
             const int per = GATED ? g.half : g.tile_n;  // outputs of a tile's row
@@ -541,6 +607,24 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
             const uint32_t acc = tmem + (uint32_t)(buf * DG_ACC) + ((uint32_t)(32 * q) << 16);
             void *out = g.out[second ? 1 : 0];
             float v[32], w[32];
+            if (SPLIT) {
+                // group c / 32 is finished by pair c / 32 mod split: the others send theirs
+                for (int c = par * 32; c < per; c += 64) {
+                    const int owner = (c >> 5) % params.split;
+                    if (owner == work.part) continue;
+                    const uint32_t to = cluster_addr(
+                        sums_at<GATED>(smem, params.split, per, work.part, owner, c, q),
+                        2 * owner + rank);
+                    tmem_ld32(acc + c, v);
+                    send32(to, lane, v);
+                    if (GATED) {
+                        tmem_ld32(acc + g.half + c, w);
+                        send32(to + 4 * DG_TURN, lane, w);
+                    }
+                }
+                sent = true;
+                break;
+            }
             for (int c = par * 32; c < per; c += 64) {
                 const int col = work.n * per + c;
                 const int width = min(min(32, per - c), g.N - col);
@@ -566,10 +650,43 @@ __global__ void __launch_bounds__(DG_THREADS, 1) dense_gemm_kernel(
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
-            if (lane == 0) arrive_cluster(cluster_addr(accempty0 + 8 * buf, 0));
+            if (lane == 0) arrive_cluster(cluster_addr(accempty0 + 8 * buf, lead));
         }
     }
     __syncwarp();
+    if (SPLIT) {
+        cluster_sync();  // the sums have arrived
+        if (warp >= 4 && sent) {
+            // this pair's share of the columns, the pairs' sums added in order
+            const GemmArgs &g = params.g[JOBS == 1 ? 0 : work.job];
+            const int per = GATED ? g.half : g.tile_n;
+            const int mt1 = g.mode == DG_PAIR_M ? g.mt / 2 : g.mt;
+            const bool second = work.m >= mt1;
+            const int row =
+                (second ? work.m - mt1 : work.m) * 2 * DG_BM + (int)rank * DG_BM + 32 * q;
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
+            float v[32], w[32];
+            for (int c = par * 32; c < per; c += 64) {
+                const int col = work.n * per + c;
+                const int width = min(min(32, per - c), g.N - col);
+                if ((c >> 5) % params.split != work.part || row >= g.M || width <= 0) continue;
+                Residual res;
+                if (!GATED && g.residual)
+                    res.load(g.residual, g.rdt, g.ldr, lane, row, g.M, col, width);
+                tmem_ld32(acc + c, v);
+                if (GATED) tmem_ld32(acc + g.half + c, w);
+                for (int from = 0; from < params.split; ++from) {
+                    if (from == work.part) continue;
+                    const uint32_t at =
+                        sums_at<GATED>(smem, params.split, per, from, work.part, c, q);
+                    add_sent32(at, lane, v);
+                    if (GATED) add_sent32(at + 4 * DG_TURN, lane, w);
+                }
+                finish<GATED>(g, turn, lane, g.out[second ? 1 : 0], row, col, width, v, w, res,
+                              smem_u32(smem + DG_BIAS) + (uint32_t)c * 4);
+            }
+        }
+    }
     __syncthreads();
     if (*abort_flag) {
         // copies and MMAs still in flight end well within this time
@@ -636,7 +753,7 @@ __global__ void __launch_bounds__(256) dense_parts_kernel(const __grid_constant_
 
 // How a product is cut: tile width, and the parts of a tile.
 struct GemmPlan {
-    int tile_n, mt, nt, slices, parts;
+    int tile_n, mt, nt, slices, parts, split;
     double cycles;
 };
 
@@ -655,32 +772,71 @@ double tile_cycles(int slices, int tile_n) {
     return in > out ? in : out;
 }
 
+// Clusters of `split` pairs that the device holds at once (0: none).
+int max_clusters(int split);
+
+// A product cut into tiles of tile_n columns, each split among `split` pairs; cycles:
+// those of one tile, without its way out (18 a column).  The pairs of a split tile
+// send each other the sums that they do not write out (about 35 a column).
+GemmPlan cut(const DenseJob &j, int tile_n, int split) {
+    GemmPlan p = {};
+    p.tile_n = tile_n;
+    p.parts = 1;
+    p.split = split;
+    p.mt = (j.M + 2 * DG_BM - 1) / (2 * DG_BM) * (j.mode == DG_PAIR_M ? 2 : 1);
+    const int per = j.mode == DG_GATED ? tile_n / 2 : tile_n;
+    p.nt = (j.N + per - 1) / per;
+    const int kb = (j.K + DG_BK - 1) / DG_BK;
+    p.slices = j.mode == DG_SUM_K ? 2 * kb : kb;
+    p.cycles = tile_cycles((p.slices + split - 1) / split, tile_n);
+    if (split > 1) {
+        const int groups = (per + 31) / 32, mine = (groups + split - 1) / split;
+        const double sent = tile_n * (1.0 - (double)mine / groups);
+        p.cycles = ((p.slices + split - 1) / split) * slice_cycles(tile_n) + 600.0 + 1200.0 +
+                   35.0 * sent - 18.0 * sent;
+    }
+    return p;
+}
+
+bool split_fits(const GemmPlan &p, bool gated) {
+    return p.slices >= 2 * p.split &&
+           sums_bytes(p.split, gated ? p.tile_n / 2 : p.tile_n, gated) <= kSumsMax;
+}
+
 // The cheapest of the tile widths: (waves of pairs) x (a tile's time).  Where not
-// even half the pairs would have a tile, the tiles' slices are cut into (up to
-// `most`) parts for the others, which costs the parts' way through L2 and a second
-// launch.
+// even half the pairs would have a tile, its slices are split among the pairs of a
+// cluster, or cut into (up to `most`) parts, which costs the parts' way through L2
+// and a second launch.
 constexpr int kMaxParts = 8;
-GemmPlan plan_gemm(const DenseJob &j, int pairs, int most = kMaxParts) {
+GemmPlan plan_gemm(const DenseJob &j, int pairs, int most = kMaxParts, int max_split = 4) {
     constexpr double kParts = 6000.0;
-    GemmPlan best = {};
-    best.cycles = 1e300;
-    const int mt = (j.M + 2 * DG_BM - 1) / (2 * DG_BM) * (j.mode == DG_PAIR_M ? 2 : 1);
-    const int kb = (j.K + DG_BK - 1) / DG_BK, slices = j.mode == DG_SUM_K ? 2 * kb : kb;
+    GemmPlan best = {}, shared = {};
+    best.cycles = shared.cycles = 1e300;
     const double planes = j.mode == DG_GATED || j.mode == DG_PAIR_M ? 2.0 : 1.0;
     for (int tn = 256; tn >= 64; tn -= 32) {
         if (j.b_t && tn != 256 && tn != 128) continue;  // whole 64-row boxes per CTA
-        const int per = j.mode == DG_GATED ? tn / 2 : tn;
-        const int nt = (j.N + per - 1) / per;
-        const double tiles = (double)mt * nt;
+        GemmPlan p = cut(j, tn, 1);
+        const double tiles = (double)p.mt * p.nt;
         for (int parts = 1; parts <= most; ++parts) {
-            if (parts > 1 && (tiles * parts > pairs || slices < 8 * parts)) break;
+            if (parts > 1 && (tiles * parts > pairs || p.slices < 8 * parts)) break;
             // the parts' bytes, written and read at about 5 KB per cycle
             const double join = parts > 1 ? kParts + parts * planes * j.M * j.N * 8.0 / 5000.0 : 0.0;
-            const double t =
-                ceil(tiles * parts / pairs) * tile_cycles((slices + parts - 1) / parts, tn) + join;
-            if (t < best.cycles * 0.999) best = {tn, mt, nt, slices, parts, t};
+            p.parts = parts;
+            p.cycles =
+                ceil(tiles * parts / pairs) * tile_cycles((p.slices + parts - 1) / parts, tn) + join;
+            if (p.cycles < best.cycles * 0.999) best = p;
+        }
+        for (int split = 2; split <= max_split; split *= 2) {
+            const GemmPlan q = cut(j, tn, split);
+            if (tiles <= max_clusters(split) && split_fits(q, j.mode == DG_GATED) &&
+                q.cycles + 18.0 * tn < shared.cycles + 18.0 * shared.tile_n)
+                shared = q;
         }
     }
+    // a tile's way out counts here: a split one's is shared.  Parts are estimated
+    // high by about a tenth.
+    const double most_cycles = (best.cycles + 18.0 * best.tile_n) * (best.parts > 1 ? 0.9 : 1.0);
+    if (shared.cycles + 18.0 * shared.tile_n < most_cycles) return shared;
     return best;
 }
 
@@ -772,30 +928,33 @@ static rvq_status fill_args(const DenseJob &job, const GemmPlan &plan, GemmArgs 
     return RVQ_OK;
 }
 
-template <bool GATED, int JOBS>
+template <bool GATED, int JOBS, bool SPLIT>
 static rvq_status launch_products(GemmParams<JOBS> &p, cudaStream_t stream) {
     static std::atomic<int> attr_done[64];  // per device; setting twice is harmless
     int dev = 0;
     RVQ_CUDA(cudaGetDevice(&dev));
     if (dev < 64 && !attr_done[dev]) {
-        RVQ_CUDA(cudaFuncSetAttribute(dense_gemm_kernel<GATED, JOBS>,
+        RVQ_CUDA(cudaFuncSetAttribute(dense_gemm_kernel<GATED, JOBS, SPLIT>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, DG_SMEM));
         attr_done[dev] = 1;
     }
     // B's rows come in whole swizzle atoms of 8 rows (1 KB), so every stage starts
     // on one
-    int half = 0;
+    int half = 0, ring = DG_RING;
     long long units = 0;
     for (int i = 0; i < JOBS; ++i) {
+        const int sums = SPLIT ? sums_bytes(p.split, GATED ? p.g[i].half : p.g[i].tile_n, GATED) : 0;
+        ring = DG_RING - sums < ring ? DG_RING - sums : ring;
         half = p.g[i].half > half ? p.g[i].half : half;
         units += (long long)p.g[i].mt * p.g[i].nt * p.g[i].parts;
     }
     const int stage = DG_ABYTES + half * 128;
     for (int i = 0; i < JOBS; ++i) {
         p.g[i].stage = stage;
-        p.g[i].stages = DG_RING / stage < DG_MAX_ST ? DG_RING / stage : DG_MAX_ST;
+        p.g[i].stages = ring / stage < DG_MAX_ST ? ring / stage : DG_MAX_ST;
     }
-    const int pairs_max = num_sms() / 2, pairs = units < pairs_max ? (int)units : pairs_max;
+    const int pairs_max = num_sms() / 2;
+    const int pairs = SPLIT ? (int)units * p.split : units < pairs_max ? (int)units : pairs_max;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(DG_THREADS);
@@ -803,31 +962,35 @@ static rvq_status launch_products(GemmParams<JOBS> &p, cudaStream_t stream) {
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = SPLIT ? 2 * p.split : 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_gemm_kernel<GATED, JOBS>, p));
+    RVQ_CUDA(cudaLaunchKernelEx(&cfg, dense_gemm_kernel<GATED, JOBS, SPLIT>, p));
     RVQ_LAUNCHED("dense_gemm");
     return RVQ_OK;
 }
 
-// one product, its tiles cut into up to `most` parts
-static rvq_status launch_one(const DenseJob &job, int most, const BiasSums &sums,
+// one product, cut by `plan`
+static rvq_status launch_one(const DenseJob &job, const GemmPlan &plan, const BiasSums &sums,
                              cudaStream_t stream) {
     if (dense_stream_fits(job)) {
         RVQ_TRY(launch_dense_stream(job, stream));
         return sums.wanted() ? launch_bias_sums(sums, stream) : RVQ_OK;
     }
-    const GemmPlan plan = plan_gemm(job, num_sms() / 2, most);
     const bool gated = job.mode == DG_GATED;
     GemmParams<1> p = {};
     p.sums = sums;
     RVQ_TRY(fill_args(job, plan, p.g[0], p.a[0], p.b[0]));
-    RVQ_TRY((gated ? launch_products<true, 1>(p, stream) : launch_products<false, 1>(p, stream)));
+    p.split = plan.split;
+    if (plan.split > 1)
+        return gated ? launch_products<true, 1, true>(p, stream)
+                     : launch_products<false, 1, true>(p, stream);
+    RVQ_TRY((gated ? launch_products<true, 1, false>(p, stream)
+                   : launch_products<false, 1, false>(p, stream)));
     if (plan.parts == 1) return RVQ_OK;
     const int64_t threads = (int64_t)job.M * (job.N / 8);
     const dim3 grid((unsigned)((threads + 255) / 256), job.mode == DG_PAIR_M ? 2u : 1u);
@@ -836,14 +999,59 @@ static rvq_status launch_one(const DenseJob &job, int most, const BiasSums &sums
     return RVQ_OK;
 }
 
+namespace {
+int max_clusters(int split) {
+    static std::atomic<int> cached[64][2];  // per device, plus one
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+    std::atomic<int> &known = cached[dev][split == 4];
+    if (known) return known - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms() / (2 * split) * 2 * split));
+    cfg.blockDim = dim3(DG_THREADS);
+    cfg.dynamicSmemBytes = DG_SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(dense_gemm_kernel<false, 1, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, DG_SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, dense_gemm_kernel<false, 1, true>, &cfg) != cudaSuccess)
+        n = 0;
+    known = n + 1;
+    return n;
+}
+}  // namespace
+
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
-    return launch_one(job, kMaxParts, BiasSums{}, stream);
+    return launch_one(job, plan_gemm(job, num_sms() / 2), BiasSums{}, stream);
 }
 
 rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const BiasSums &sums,
                                  cudaStream_t stream) {
     const long long pairs = num_sms() / 2;
-    const GemmPlan px = plan_gemm(x, (int)pairs, 1), py = plan_gemm(y, (int)pairs, 1);
+    const GemmPlan ax = plan_gemm(x, (int)pairs), ay = plan_gemm(y, (int)pairs);
+    const double apart = ax.cycles + ay.cycles + 6500.0;
+    const bool streamed = dense_stream_fits(x) || dense_stream_fits(y);
+    // together with every tile split among a cluster's pairs
+    GemmPlan sx = {}, sy = {};
+    double split_cycles = 1e300;
+    for (int split = 2; split <= 4 && !streamed; split *= 2)
+        for (int c = 0; c < 4; ++c) {
+            const GemmPlan p = cut(x, c & 1 ? 128 : 256, split), q = cut(y, c & 2 ? 128 : 256, split);
+            const double t = p.cycles > q.cycles ? p.cycles : q.cycles;
+            if (split_fits(p, false) && split_fits(q, false) && t < split_cycles &&
+                (long long)p.mt * p.nt + (long long)q.mt * q.nt <= max_clusters(split)) {
+                sx = p;
+                sy = q;
+                split_cycles = t;
+            }
+        }
+    const GemmPlan px = plan_gemm(x, (int)pairs, 1, 1), py = plan_gemm(y, (int)pairs, 1, 1);
     const double tx = tile_cycles(px.slices, px.tile_n), ty = tile_cycles(py.slices, py.tile_n);
     const bool swap = tx < ty;  // the longer tiles first
     const GemmPlan &p0 = swap ? py : px, &p1 = swap ? px : py;
@@ -854,7 +1062,6 @@ rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const Bia
     // are taken for operands that are shared less; 1333 x 1000 x 2048, equal waves,
     // 57.5 and 54 us, so 6500 cycles for a launch; 1777 x 4104 x 1736, 121 slices and
     // 93, 114 and 101 us).
-    const double apart = plan_gemm(x, (int)pairs).cycles + plan_gemm(y, (int)pairs).cycles + 6500.0;
     const long long u0 = (long long)p0.mt * p0.nt, u1 = (long long)p1.mt * p1.nt;
     const long long first = u0 % pairs, early = pairs - first;
     const int bonus = first ? (int)(t0 / t1) : 0;
@@ -864,20 +1071,30 @@ rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const Bia
     const double early_end = (double)(u0 / pairs) * t0 +
                              (double)(bonus + (rest + pairs - 1) / pairs) * t1;
     const double together = late_end > early_end ? late_end : early_end;
-    const bool one = !dense_stream_fits(x) && !dense_stream_fits(y) && together * 1.03 < apart;
-    if (!one || !x.out[0] || !y.out[0]) {
+    const bool one = !streamed && together * 1.03 < apart && together <= split_cycles;
+    const bool split = !streamed && split_cycles < apart && !one;
+    if (!(one || split) || !x.out[0] || !y.out[0]) {
         // a product wanted alone is cut as it would be beside the other: the same sums
-        const int most = one ? 1 : kMaxParts;
-        if (x.out[0]) RVQ_TRY(launch_one(x, most, y.out[0] ? BiasSums{} : sums, stream));
-        if (y.out[0]) return launch_one(y, most, sums, stream);
+        const GemmPlan &lx = one ? px : split ? sx : ax, &ly = one ? py : split ? sy : ay;
+        if (x.out[0]) RVQ_TRY(launch_one(x, lx, y.out[0] ? BiasSums{} : sums, stream));
+        if (y.out[0]) return launch_one(y, ly, sums, stream);
         return !x.out[0] && sums.wanted() ? launch_bias_sums(sums, stream) : RVQ_OK;
+    }
+    if (split) {
+        GemmParams<2> p = {};
+        RVQ_TRY(fill_args(x, sx, p.g[0], p.a[0], p.b[0]));
+        RVQ_TRY(fill_args(y, sy, p.g[1], p.a[1], p.b[1]));
+        p.split = sx.split;
+        p.sums = sums;
+        return launch_products<false, 2, true>(p, stream);
     }
     GemmParams<2> p = {};
     RVQ_TRY(fill_args(swap ? y : x, p0, p.g[0], p.a[0], p.b[0]));
     RVQ_TRY(fill_args(swap ? x : y, p1, p.g[1], p.a[1], p.b[1]));
     p.bonus = bonus;
     p.sums = sums;
-    return launch_products<false, 2>(p, stream);
+    p.split = 1;
+    return launch_products<false, 2, false>(p, stream);
 }
 
 }  // namespace rvq

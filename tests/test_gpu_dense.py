@@ -437,3 +437,47 @@ def test_bias_gradients_beside_any_product(n, rows, cols):
                 R.check(kw["dbu"], outs[1][1], "dbu")
             for k in biases:
                 assert torch.equal(kw[k], first[k]), (products, k)
+
+
+# tiles split among the pairs of a cluster (two or four), ragged and whole
+SPLITS = [(250, 856, 1240), (512, 2048, 2048), (1000, 1000, 2040), (385, 712, 2048),
+          (129, 520, 3000)]
+
+
+@pytest.mark.parametrize("n,rows,cols", SPLITS)
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_linear_split_tiles(n, rows, cols, act):
+    g = gen(n)
+    x, w = normal(g, (n, cols), BF), normal(g, (rows, cols), BF, cols ** -0.5)
+    b, res = normal(g, (rows,), BF), normal(g, (n, rows), F32)
+    ws = workspace(n, rows, cols)
+    out, bo = hole((n, rows), F32 if act == "none" else BF, 8)
+    pre = torch.empty((n, rows), dtype=F32, device=DEV)
+    rvq.moe_linear(x, w, n, rows, cols, out, ws, bias=b, act=rvq.MOE_ACTS[act], alpha=-0.5,
+                   residual=res, pre=pre)
+    assert rvq.rvq_ws_status(ws) == (0, 0) and untouched(bo, out)
+    p, ep = R.product(R.d(x), R.d(w))
+    p = p + R.d(b)
+    ep = ep + 2 * R.U32 * p.abs()
+    assert ((pre.double() - p).abs() <= ep).all()
+    a = R.act(act, p)
+    ea = (1.2 * ep + 16 * R.U32 * p.abs()) * 0.5 + 4 * R.U32 * (a.abs() + res.double().abs())
+    want = res.double() - 0.5 * a
+    tol = ea + torch.finfo(out.dtype).eps / 2 * (want.abs() + ea)
+    assert ((out.double() - want).abs() <= tol).all()
+    again = torch.empty_like(out)
+    rvq.moe_linear(x, w, n, rows, cols, again, ws, bias=b, act=rvq.MOE_ACTS[act], alpha=-0.5,
+                   residual=res)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(757, 2000, 336), (300, 1000, 1000), (2999, 256, 264),
+                                         (512, 2048, 2048), (161, 520, 1040)])
+def test_linear_gradients_split_tiles(n, rows, cols):
+    linear_train(n, rows, cols, BF if n % 2 else HF, "silu", True, alpha=0.5, extra=8, seed=n)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(662, 472, 1344), (400, 800, 3000), (256, 1024, 2048),
+                                         (1688, 320, 512), (200, 264, 7168)])
+def test_gated_gradients_split_tiles(n, rows, cols):
+    test_gated_gradients(n, rows, cols)
