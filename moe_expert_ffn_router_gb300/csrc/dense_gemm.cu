@@ -798,6 +798,9 @@ GemmPlan cut(const DenseJob &j, int tile_n, int split) {
     return p;
 }
 
+// A tile of fewer slices than that gains less than the exchange costs.
+constexpr int kSplitSlices = 12;
+
 bool split_fits(const GemmPlan &p, bool gated) {
     return p.slices >= 2 * p.split &&
            sums_bytes(p.split, gated ? p.tile_n / 2 : p.tile_n, gated) <= kSumsMax;
@@ -826,10 +829,11 @@ GemmPlan plan_gemm(const DenseJob &j, int pairs, int most = kMaxParts, int max_s
                 ceil(tiles * parts / pairs) * tile_cycles((p.slices + parts - 1) / parts, tn) + join;
             if (p.cycles < best.cycles * 0.999) best = p;
         }
-        for (int split = 2; split <= max_split; split *= 2) {
+        for (int split = 2; split <= max_split && p.slices >= kSplitSlices; split *= 2) {
             const GemmPlan q = cut(j, tn, split);
-            if (tiles <= max_clusters(split) && split_fits(q, j.mode == DG_GATED) &&
-                q.cycles + 18.0 * tn < shared.cycles + 18.0 * shared.tile_n)
+            if (tiles * split <= pairs && split_fits(q, j.mode == DG_GATED) &&
+                q.cycles + 18.0 * tn < shared.cycles + 18.0 * shared.tile_n &&
+                tiles <= max_clusters(split))
                 shared = q;
         }
     }
@@ -977,10 +981,6 @@ static rvq_status launch_products(GemmParams<JOBS> &p, cudaStream_t stream) {
 // one product, cut by `plan`
 static rvq_status launch_one(const DenseJob &job, const GemmPlan &plan, const BiasSums &sums,
                              cudaStream_t stream) {
-    if (dense_stream_fits(job)) {
-        RVQ_TRY(launch_dense_stream(job, stream));
-        return sums.wanted() ? launch_bias_sums(sums, stream) : RVQ_OK;
-    }
     const bool gated = job.mode == DG_GATED;
     GemmParams<1> p = {};
     p.sums = sums;
@@ -1028,24 +1028,42 @@ int max_clusters(int split) {
 }  // namespace
 
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
+    if (dense_stream_fits(job)) return launch_dense_stream(job, stream);
     return launch_one(job, plan_gemm(job, num_sms() / 2), BiasSums{}, stream);
 }
 
 rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const BiasSums &sums,
                                  cudaStream_t stream) {
     const long long pairs = num_sms() / 2;
+    if (dense_stream_fits(x) || dense_stream_fits(y)) {
+        // few tokens: each its own way, the bias gradients beside the tiled one
+        const DenseJob *jobs[2] = {&x, &y};
+        bool added = !sums.wanted();
+        for (int i = 1; i >= 0; --i) {
+            const DenseJob &j = *jobs[i];
+            if (!j.out[0]) continue;
+            if (dense_stream_fits(j)) {
+                RVQ_TRY(launch_dense_stream(j, stream));
+            } else {
+                RVQ_TRY(launch_one(j, plan_gemm(j, (int)pairs), added ? BiasSums{} : sums, stream));
+                added = true;
+            }
+        }
+        return added ? RVQ_OK : launch_bias_sums(sums, stream);
+    }
     const GemmPlan ax = plan_gemm(x, (int)pairs), ay = plan_gemm(y, (int)pairs);
     const double apart = ax.cycles + ay.cycles + 6500.0;
-    const bool streamed = dense_stream_fits(x) || dense_stream_fits(y);
     // together with every tile split among a cluster's pairs
     GemmPlan sx = {}, sy = {};
     double split_cycles = 1e300;
-    for (int split = 2; split <= 4 && !streamed; split *= 2)
+    for (int split = 2; split <= 4 && (ax.slices >= kSplitSlices || ay.slices >= kSplitSlices);
+         split *= 2)
         for (int c = 0; c < 4; ++c) {
             const GemmPlan p = cut(x, c & 1 ? 128 : 256, split), q = cut(y, c & 2 ? 128 : 256, split);
             const double t = p.cycles > q.cycles ? p.cycles : q.cycles;
-            if (split_fits(p, false) && split_fits(q, false) && t < split_cycles &&
-                (long long)p.mt * p.nt + (long long)q.mt * q.nt <= max_clusters(split)) {
+            const long long units = (long long)p.mt * p.nt + (long long)q.mt * q.nt;
+            if (units * split <= pairs && t < split_cycles && split_fits(p, false) &&
+                split_fits(q, false) && units <= max_clusters(split)) {
                 sx = p;
                 sy = q;
                 split_cycles = t;
@@ -1071,8 +1089,8 @@ rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const Bia
     const double early_end = (double)(u0 / pairs) * t0 +
                              (double)(bonus + (rest + pairs - 1) / pairs) * t1;
     const double together = late_end > early_end ? late_end : early_end;
-    const bool one = !streamed && together * 1.03 < apart && together <= split_cycles;
-    const bool split = !streamed && split_cycles < apart && !one;
+    const bool one = together * 1.03 < apart && together <= split_cycles;
+    const bool split = split_cycles < apart && !one;
     if (!(one || split) || !x.out[0] || !y.out[0]) {
         // a product wanted alone is cut as it would be beside the other: the same sums
         const GemmPlan &lx = one ? px : split ? sx : ax, &ly = one ? py : split ? sy : ay;
