@@ -12,9 +12,10 @@
 //
 // Measured (GB300): forward of 2048 x 7168 36 us (fp32 h and y, bf16 xn: 206 MB,
 // 5.7 TB/s) and 26 us (bf16: 118 MB, 4.5 TB/s), of 4099 x 2048 (bf16) 16 us; forward and
-// gradients 83 us and 45 us.  The forward call is bound by memory; the gradients
+// gradients 126, 82 and 45 us.  The forward call is bound by memory; the gradients
 // by issue and latency (57 % of the issue slots with 16 warps an SM; the sums over
-// rows hold 48 registers a thread).
+// rows hold up to 48 registers a thread), of fp32 rows past 6400 columns by copies
+// that wait for the row before.
 #pragma once
 
 #include <type_traits>
