@@ -80,6 +80,33 @@ bool disjoint(const void *a, int64_t lda, int32_t ra, int32_t ca, size_t ea, con
     return a1 <= b0 || b1 <= a0;
 }
 
+// A row-major matrix, or (vector()) contiguous values; NULL: absent.
+struct Span {
+    const void *p;
+    int64_t ld;
+    int32_t rows, cols;
+    size_t e;
+};
+
+Span vector(const void *p, int32_t n, size_t e) { return {p, n, 1, n, e}; }
+
+bool apart(const Span &a, const Span &b) {
+    return disjoint(a.p, a.ld, a.rows, a.cols, a.e, b.p, b.ld, b.rows, b.cols, b.e);
+}
+
+// Outputs that one launch may write while it reads the inputs: none overlaps an
+// input or another output.
+template <int O, int I>
+bool all_apart(const Span (&out)[O], const Span (&in)[I]) {
+    for (int o = 0; o < O; ++o) {
+        for (int i = 0; i < I; ++i)
+            if (!apart(out[o], in[i])) return false;
+        for (int i = 0; i < o; ++i)
+            if (!apart(out[o], out[i])) return false;
+    }
+    return true;
+}
+
 // Workspace: status | partial sums of split products | and for a gradient dp
 // 16-bit [mats][n][rows] | bias partials.  The calls' products run one after
 // another and share the partial sums' place.
@@ -253,14 +280,13 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
     CHECK_ALIGN(dbias_dev, who, "dbias");
     CHECK_ALIGN(pre_dev, who, "pre");
     RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(1, n, rows, cols, 1)));
-    CHECK_ARG((dx_dev == nullptr ||
-               (disjoint(dx_dev, lddx, n, cols, 2, dout_dev, lddo, n, rows, 2) &&
-                disjoint(dx_dev, lddx, n, cols, 2, w_dev, ldw, rows, cols, 2) &&
-                (dw_dev == nullptr || disjoint(dx_dev, lddx, n, cols, 2, x_dev, ldx, n, cols, 2)))) &&
-                  (dw_dev == nullptr ||
-                   (disjoint(dw_dev, lddw, rows, cols, 2, dout_dev, lddo, n, rows, 2) &&
-                    disjoint(dw_dev, lddw, rows, cols, 2, x_dev, ldx, n, cols, 2))),
-              "%s: a gradient overlaps an input", who);
+    // The products of dx and dw may run in one launch, the bias sums beside either.
+    const Span out[] = {{dx_dev, lddx, n, cols, 2}, {dw_dev, lddw, rows, cols, 2},
+                        vector(dbias_dev, rows, 2)};
+    const Span in[] = {{dx_dev || dw_dev ? dout_dev : nullptr, lddo, n, rows, 2},
+                       {dx_dev ? w_dev : nullptr, ldw, rows, cols, 2},
+                       {dw_dev ? x_dev : nullptr, ldx, n, cols, 2}};
+    CHECK_ARG(all_apart(out, in), "%s: a gradient overlaps an input or another gradient", who);
     const WsPlan P = plan_ws(1, n, rows, cols, true);
     uint8_t *ws = (uint8_t *)ws_dev;
     cudaStream_t st = (cudaStream_t)stream;
@@ -342,15 +368,14 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
         RVQ_TRY(check_matrix(who, "dwu", dwu_dev, lddw, cols));
     }
     RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(2, n, rows, cols, 1)));
-    CHECK_ARG((dx_dev == nullptr ||
-               (disjoint(dx_dev, lddx, n, cols, 2, wg_dev, ldw, rows, cols, 2) &&
-                disjoint(dx_dev, lddx, n, cols, 2, wu_dev, ldw, rows, cols, 2) &&
-                (dwg_dev == nullptr || disjoint(dx_dev, lddx, n, cols, 2, x_dev, ldx, n, cols, 2)))) &&
-                  (dwg_dev == nullptr ||
-                   (disjoint(dwg_dev, lddw, rows, cols, 2, x_dev, ldx, n, cols, 2) &&
-                    disjoint(dwu_dev, lddw, rows, cols, 2, x_dev, ldx, n, cols, 2) &&
-                    disjoint(dwu_dev, lddw, rows, cols, 2, dwg_dev, lddw, rows, cols, 2))),
-              "%s: a gradient overlaps an input or the other gradient", who);
+    // As in moe_linear_backward; dout is read before the products.
+    const Span out[] = {{dx_dev, lddx, n, cols, 2}, {dwg_dev, lddw, rows, cols, 2},
+                        {dwu_dev, lddw, rows, cols, 2}, vector(dbg_dev, rows, 2),
+                        vector(dbu_dev, rows, 2)};
+    const Span in[] = {{dx_dev ? wg_dev : nullptr, ldw, rows, cols, 2},
+                       {dx_dev ? wu_dev : nullptr, ldw, rows, cols, 2},
+                       {dwg_dev ? x_dev : nullptr, ldx, n, cols, 2}};
+    CHECK_ARG(all_apart(out, in), "%s: a gradient overlaps an input or another gradient", who);
     const WsPlan P = plan_ws(2, n, rows, cols, true);
     uint8_t *ws = (uint8_t *)ws_dev;
     cudaStream_t st = (cudaStream_t)stream;

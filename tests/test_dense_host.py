@@ -172,3 +172,38 @@ def test_binding_refusals():
     assert [rvq._gate_kind(g, 4, 64) for g in
             (None, torch.zeros(1), torch.zeros(4, 1), torch.zeros(64), torch.zeros(1, 64),
              torch.zeros(4, 64))] == [0, 1, 2, 3, 3, 4]
+
+
+@pytest.mark.parametrize("n", [1, 4, 300])
+def test_gradients_refuse_racing_overlaps(n):
+    """The products of a gradient call may run in one launch: a gradient over an
+    input of the other product, or over another gradient, is refused."""
+    at = [A + i * 0x10000000 for i in range(16)]
+    base = dict(do=at[0], ldd=32, x=at[1], ldx=64, w=at[2], ldw=64, pre=at[3], dt=BF16, n=n,
+                rows=32, cols=64, act=2, alpha=1.0, dx=at[4], lddx=64, dw=at[5], lddw=64,
+                db=at[6], ws=at[7], wsb=1, st=None)
+
+    def back(**kw):
+        return lib.moe_linear_backward(*{**base, "wsb": 1 << 24, **kw}.values())
+
+    assert lib.moe_linear_backward(*base.values()) == ENOMEM   # else it is accepted
+    last = (32 * 64 - 8) * 2        # the last 16 bytes of w and dw
+    for bad in (dict(dw=at[2]), dict(dw=at[2] + last), dict(dw=at[2] - last), dict(dw=at[4]),
+                dict(dx=at[5] + 64), dict(db=at[4]), dict(db=at[5] + last), dict(db=at[2]),
+                dict(db=at[1]), dict(db=at[0]), dict(db=at[0], act=0, pre=None)):
+        assert back(**bad) == EINVAL, bad
+        assert b"overlaps" in lib.rvq_last_error(), bad
+    base = dict(do=at[0], ldd=32, x=at[1], ldx=64, wg=at[2], wu=at[3], ldw=64, pre=at[4], dt=BF16,
+                n=n, rows=32, cols=64, act=2, dx=at[5], lddx=64, dwg=at[6], dwu=at[7], lddw=64,
+                dbg=at[8], dbu=at[9], ws=at[10], wsb=1, st=None)
+
+    def gback(**kw):
+        return lib.moe_gated_linear_backward(*{**base, "wsb": 1 << 24, **kw}.values())
+
+    assert lib.moe_gated_linear_backward(*base.values()) == ENOMEM
+    for bad in (dict(dwg=at[2]), dict(dwg=at[3]), dict(dwu=at[2] + last), dict(dwu=at[3]),
+                dict(dwg=at[5]), dict(dwu=at[5]), dict(dx=at[7] - 16), dict(dbg=at[5]),
+                dict(dbg=at[6]), dict(dbg=at[2]), dict(dbu=at[7] + last), dict(dbu=at[3]),
+                dict(dbu=at[8]), dict(dbu=at[8] + 48), dict(dbg=at[1])):
+        assert gback(**bad) == EINVAL, bad
+        assert b"overlaps" in lib.rvq_last_error(), bad
