@@ -570,7 +570,8 @@ size_t moe_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols, int32_t
  *  - x [n][cols], w [rows][cols] of dt; bias [rows] of dt or NULL.
  *  - residual [n][rows] of rdt, or NULL; out [n][rows] of odt; rdt and odt are
  *    fp32 or 16-bit (any mix).  out may alias residual if type and pitch agree
- *    (each element is read before it is written); no other overlap.
+ *    (each element is read before it is written); out and pre overlap nothing
+ *    else (EINVAL).
  *  - pre: fp32 [n][rows] without padding, or NULL; receives x w^T + bias, which
  *    moe_linear_backward needs for act != MOE_ACT_NONE. */
 rvq_status moe_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t ldw,
@@ -602,7 +603,8 @@ size_t moe_gated_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols, i
  *   g = x wg^T + bg, u = x wu^T + bu, out = act(g) * u
  *  - x [n][cols], wg and wu [rows][cols] (one pitch ldw), bg and bu [rows] or
  *    NULL (each by itself), out [n][rows], all of dt.
- *  - pre: fp32 [2][n][rows] or NULL; receives g and u for the gradients. */
+ *  - pre: fp32 [2][n][rows] or NULL; receives g and u for the gradients.
+ *  - out and pre overlap nothing (EINVAL). */
 rvq_status moe_gated_linear(const void *x_dev, int64_t ldx, const void *wg_dev,
                             const void *wu_dev, int64_t ldw, const void *bg_dev,
                             const void *bu_dev, rvq_dtype dt, int32_t n, int32_t rows,

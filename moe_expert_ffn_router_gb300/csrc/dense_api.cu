@@ -180,12 +180,14 @@ rvq_status moe_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t
     CHECK_ALIGN(pre_dev, who, "pre");
     RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(1, n, rows, cols, 0)));
     const size_t oe = elem_bytes(odt);
-    CHECK_ARG(disjoint(out_dev, ldo, n, rows, oe, x_dev, ldx, n, cols, 2) &&
-                  disjoint(out_dev, ldo, n, rows, oe, w_dev, ldw, rows, cols, 2) &&
-                  disjoint(out_dev, ldo, n, rows, oe, pre_dev, rows, n, rows, 4),
-              "%s: out overlaps another matrix", who);
+    const Span o = {out_dev, ldo, n, rows, oe}, pre = {pre_dev, rows, n, rows, 4};
+    const Span in[] = {{x_dev, ldx, n, cols, 2}, {w_dev, ldw, rows, cols, 2},
+                       vector(bias_dev, rows, 2)};
+    const Span res = {residual_dev, ldr, n, rows, elem_bytes(rdt)};
+    CHECK_ARG(all_apart({o, pre}, in) && apart(pre, res), "%s: out or pre overlaps another matrix",
+              who);
     CHECK_ARG((residual_dev == out_dev && rdt == odt && ldr == ldo) ||
-                  disjoint(out_dev, ldo, n, rows, oe, residual_dev, ldr, n, rows, elem_bytes(rdt)),
+                  apart(o, res),
               "%s: out overlaps the residual with another type, place or pitch", who);
     DenseJob j = {};
     j.mode = DG_PLAIN;
@@ -227,12 +229,12 @@ rvq_status moe_gated_linear(const void *x_dev, int64_t ldx, const void *wg_dev,
     CHECK_ALIGN(bu_dev, who, "bu");
     CHECK_ALIGN(pre_dev, who, "pre");
     RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(2, n, rows, cols, 0)));
-    CHECK_ARG(disjoint(out_dev, ldo, n, rows, 2, x_dev, ldx, n, cols, 2) &&
-                  disjoint(out_dev, ldo, n, rows, 2, wg_dev, ldw, rows, cols, 2) &&
-                  disjoint(out_dev, ldo, n, rows, 2, wu_dev, ldw, rows, cols, 2) &&
-                  (pre_dev == nullptr ||
-                   disjoint(out_dev, ldo, n, rows, 2, pre_dev, rows, 2 * n, rows, 4)),
-              "%s: out overlaps another matrix", who);
+    const Span out[] = {{out_dev, ldo, n, rows, 2}, {pre_dev, rows, n, rows, 4},
+                        {pre_dev ? pre_dev + (size_t)n * rows : nullptr, rows, n, rows, 4}};
+    const Span in[] = {{x_dev, ldx, n, cols, 2}, {wg_dev, ldw, rows, cols, 2},
+                       {wu_dev, ldw, rows, cols, 2}, vector(bg_dev, rows, 2),
+                       vector(bu_dev, rows, 2)};
+    CHECK_ARG(all_apart(out, in), "%s: out or pre overlaps another matrix", who);
     DenseJob j = {};
     j.mode = DG_GATED;
     j.M = n;

@@ -207,3 +207,28 @@ def test_gradients_refuse_racing_overlaps(n):
                 dict(dbu=at[8]), dict(dbu=at[8] + 48), dict(dbg=at[1])):
         assert gback(**bad) == EINVAL, bad
         assert b"overlaps" in lib.rvq_last_error(), bad
+
+
+@pytest.mark.parametrize("n", [1, 4, 300])
+def test_outputs_over_inputs_are_refused(n):
+    """The saved pre-activations and the biases too: some blocks still read what
+    others write."""
+    at = [A + i * 0x10000000 for i in range(16)]
+    base = dict(x=at[0], ldx=64, w=at[1], ldw=64, bias=at[2], dt=BF16, n=n, rows=32, cols=64,
+                act=2, alpha=1.0, res=at[3], rdt=BF16, ldr=32, out=at[4], odt=BF16, ldo=32,
+                pre=at[5], ws=at[6], wsb=1, st=None)
+    assert lib.moe_linear(*base.values()) == ENOMEM    # else it is accepted
+    for bad in (dict(pre=at[0]), dict(pre=at[1]), dict(pre=at[1] + (32 * 64 - 8) * 2),
+                dict(pre=at[2]), dict(pre=at[3]), dict(pre=at[4]), dict(out=at[2]),
+                dict(out=at[2] + 48), dict(out=at[0]), dict(out=at[5])):
+        assert lib.moe_linear(*{**base, "wsb": 1 << 24, **bad}.values()) == EINVAL, bad
+        assert b"overlaps" in lib.rvq_last_error(), bad
+    base = dict(x=at[0], ldx=64, wg=at[1], wu=at[2], ldw=64, bg=at[3], bu=at[4], dt=BF16, n=n,
+                rows=32, cols=64, act=2, out=at[5], ldo=32, pre=at[6], ws=at[7], wsb=1, st=None)
+    assert lib.moe_gated_linear(*base.values()) == ENOMEM
+    half = n * 32 * 4               # bytes of pre's first plane
+    for bad in (dict(pre=at[0]), dict(pre=at[1]), dict(pre=at[2]), dict(pre=at[2] - half),
+                dict(pre=at[3]), dict(pre=at[4] - half), dict(pre=at[5] - half),
+                dict(out=at[3]), dict(out=at[4] + 48), dict(out=at[6]), dict(out=at[6] + half)):
+        assert lib.moe_gated_linear(*{**base, "wsb": 1 << 24, **bad}.values()) == EINVAL, bad
+        assert b"overlaps" in lib.rvq_last_error(), bad
