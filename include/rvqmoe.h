@@ -645,9 +645,10 @@ typedef enum moe_gate {
  *  - h may be NULL (no residual), h_out or xn may be NULL (not both).
  *  - rstd: fp32 [2][n] or NULL; receives 1/rms of y (1 without a post norm) and
  *    of h_out, for the gradients.
- *  - h_out may alias h or y, and xn may alias y, if their types agree; xn must
- *    not alias h_out.  Sums and statistics are fp32.  eps >= 0; a row of zeros
- *    with eps = 0 gives NaN, as the formula does. */
+ *  - h_out and xn may each take the place of h, y or a full gate of the same
+ *    type; the outputs (rstd too) overlap nothing else (EINVAL).  Sums and
+ *    statistics are fp32.  eps >= 0; a row of zeros with eps = 0 gives NaN, as
+ *    the formula does. */
 rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rvq_dtype ydt,
                          int32_t n, int32_t d, float alpha, const void *gate_dev,
                          moe_gate gate_kind, rvq_dtype gdt, int32_t post_norm,
@@ -666,8 +667,10 @@ size_t moe_norm_join_workspace_bytes(int32_t n, int32_t d);
  *   dz     = gate e;  dw_post = sum_t dz y r1;  dw_pre = sum_t dxn h_out r2 (wdt)
  *   dy     = post_norm ? r1 (dz w_post) - y r1^3 mean(dz w_post y) : dz  (ydt)
  * h_out is recomputed from h, y and rstd.  Outputs are NULL when not wanted.
- * Sums over tokens run in a fixed order: results repeat bit for bit.  dh may
- * alias dh_out, and dy may alias dxn, if their types agree. */
+ * Sums over tokens run in a fixed order: results repeat bit for bit.  dh, dy and
+ * dgate (per token or full) may each take the place of h, y, gate, dh_out or dxn of
+ * the same type and shape, and overlap no other input; the gradients do not overlap
+ * each other (EINVAL). */
 rvq_status moe_norm_join_backward(const void *dh_out_dev, const void *dxn_dev, rvq_dtype xdt,
                                   const void *h_dev, rvq_dtype hdt, const void *y_dev,
                                   rvq_dtype ydt, int32_t n, int32_t d, float alpha,

@@ -458,11 +458,28 @@ static rvq_status check_join(const char *who, const void *h, rvq_dtype hdt, cons
     return RVQ_OK;
 }
 
-// a and b are the same rows of the same type, or do not overlap
-static bool same_or_disjoint(const void *a, rvq_dtype adt, const void *b, rvq_dtype bdt, int32_t n,
-                             int32_t d) {
-    return (a == b && adt == bdt) ||
-           disjoint(a, d, n, d, elem_bytes(adt), b, d, n, d, elem_bytes(bdt));
+// A tensor of the join: n rows of d values, or values over tokens or channels
+// (len); kept apart from others, or over rows of its own type.
+struct JoinSpan {
+    const void *p;
+    rvq_dtype dt;
+    int32_t rows, cols;
+};
+
+static bool apart(const JoinSpan &a, const JoinSpan &b) {
+    return disjoint(a.p, a.cols, a.rows, a.cols, elem_bytes(a.dt), b.p, b.cols, b.rows, b.cols,
+                    elem_bytes(b.dt));
+}
+
+// Every block reads its rows before it writes them: an output may take the place of
+// rows of the same type.
+static bool same_or_apart(const JoinSpan &a, const JoinSpan &b) {
+    return (a.p == b.p && a.dt == b.dt && a.rows == b.rows && a.cols == b.cols) || apart(a, b);
+}
+
+static JoinSpan gate_span(const void *p, rvq_dtype dt, int kind, int32_t n, int32_t d) {
+    return {p, dt, kind == MOE_GATE_TOKEN || kind == MOE_GATE_FULL ? n : 1,
+            kind == MOE_GATE_CHANNEL || kind == MOE_GATE_FULL ? d : 1};
 }
 
 rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rvq_dtype ydt,
@@ -479,13 +496,21 @@ rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rv
     CHECK_ALIGN(h_out_dev, who, "h_out");
     CHECK_ALIGN(xn_dev, who, "xn");
     CHECK_ALIGN(rstd_dev, who, "rstd");
-    CHECK_ARG(same_or_disjoint(h_out_dev, hdt, h_dev, hdt, n, d) &&
-                  same_or_disjoint(h_out_dev, hdt, y_dev, ydt, n, d) &&
-                  same_or_disjoint(xn_dev, xdt, y_dev, ydt, n, d) &&
-                  same_or_disjoint(xn_dev, xdt, h_dev, hdt, n, d) &&
-                  disjoint(xn_dev, d, n, d, elem_bytes(xdt), h_out_dev, d, n, d,
-                           elem_bytes(hdt)),
-              "%s: an output overlaps an input of another type or place, or the other output",
+    const JoinSpan out[] = {{h_out_dev, hdt, n, d}, {xn_dev, xdt, n, d}};
+    const JoinSpan rstd = {rstd_dev, RVQ_F32, 2, n};
+    const JoinSpan rows[] = {{h_dev, hdt, n, d}, {y_dev, ydt, n, d},
+                             gate_span(gate_dev, gdt, (int)gate_kind, n, d)};
+    const JoinSpan gains[] = {{w_post_dev, wdt, 1, d}, {w_pre_dev, wdt, 1, d}};
+    bool ok = apart(out[0], out[1]);
+    for (const JoinSpan &o : out) {
+        for (const JoinSpan &r : rows)
+            ok = ok && (r.rows == n && r.cols == d ? same_or_apart(o, r) : apart(o, r));
+        for (const JoinSpan &g : gains) ok = ok && apart(o, g);
+        ok = ok && apart(o, rstd);
+    }
+    for (const JoinSpan &r : rows) ok = ok && apart(rstd, r);
+    for (const JoinSpan &g : gains) ok = ok && apart(rstd, g);
+    CHECK_ARG(ok, "%s: an output overlaps an input of another type or place, or another output",
               who);
     JoinJob j = {};
     j.n = n;
@@ -544,12 +569,24 @@ rvq_status moe_norm_join_backward(const void *dh_out_dev, const void *dxn_dev, r
     static const char *const names[] = {"dh_out", "dxn", "rstd", "dh", "dy", "dgate", "dw_post",
                                         "dw_pre"};
     for (int i = 0; i < 8; ++i) CHECK_ALIGN(al[i], who, names[i]);
-    CHECK_ARG(same_or_disjoint(dh_dev, hdt, dh_out_dev, hdt, n, d) &&
-                  same_or_disjoint(dh_dev, hdt, dxn_dev, xdt, n, d) &&
-                  same_or_disjoint(dy_dev, ydt, dh_out_dev, hdt, n, d) &&
-                  same_or_disjoint(dy_dev, ydt, dxn_dev, xdt, n, d) &&
-                  disjoint(dh_dev, d, n, d, elem_bytes(hdt), dy_dev, d, n, d, elem_bytes(ydt)),
-              "%s: a gradient overlaps an input of another type or place, or the other gradient",
+    // dgate per row and dh, dy are written while other blocks read their rows; the
+    // gains' and the other gates' gradients after the last row.
+    const JoinSpan gate = gate_span(gate_dev, gdt, (int)gate_kind, n, d);
+    const JoinSpan out[] = {{dh_dev, hdt, n, d}, {dy_dev, ydt, n, d},
+                            gate_span(dgate_dev, gdt, (int)gate_kind, n, d),
+                            {dw_post_dev, wdt, 1, d}, {dw_pre_dev, wdt, 1, d}};
+    const JoinSpan in[] = {{h_dev, hdt, n, d}, {y_dev, ydt, n, d}, gate, {dh_out_dev, hdt, n, d},
+                           {dxn_dev, xdt, n, d}, {rstd_dev, RVQ_F32, 2, n},
+                           {w_post_dev, wdt, 1, d}, {w_pre_dev, wdt, 1, d}};
+    const bool gate_rows = gate_kind == MOE_GATE_TOKEN || gate_kind == MOE_GATE_FULL;
+    bool ok = true;
+    for (int o = 0; o < 5; ++o) {
+        for (int i = 0; i < o; ++i) ok = ok && apart(out[o], out[i]);
+        if (o > 2 || (o == 2 && !gate_rows)) continue;
+        for (int i = 0; i < 8; ++i) ok = ok && (i < 5 ? same_or_apart(out[o], in[i])
+                                                      : apart(out[o], in[i]));
+    }
+    CHECK_ARG(ok, "%s: a gradient overlaps an input of another type or place, or another gradient",
               who);
     RVQ_TRY(check_ws(who, ws_dev, ws_bytes, moe_norm_join_workspace_bytes(n, d)));
     JoinJob j = {};

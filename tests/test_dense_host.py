@@ -232,3 +232,45 @@ def test_outputs_over_inputs_are_refused(n):
                 dict(out=at[3]), dict(out=at[4] + 48), dict(out=at[6]), dict(out=at[6] + half)):
         assert lib.moe_gated_linear(*{**base, "wsb": 1 << 24, **bad}.values()) == EINVAL, bad
         assert b"overlaps" in lib.rvq_last_error(), bad
+
+
+@pytest.mark.parametrize("n,d", [(4, 64), (1000, 264)])
+def test_join_refuses_racing_overlaps(n, d):
+    """Rows are read before they are written by the block that owns them, so an
+    output may take the place of rows of its type; any other overlap is refused."""
+    at = [A + i * 0x10000000 for i in range(16)]
+    base = dict(h=at[0], hdt=F32, y=at[1], ydt=F32, n=n, d=d, alpha=1.0, gate=at[2], kind=4,
+                gdt=F32, post=1, wpost=at[3], wpre=at[4], wdt=F32, eps=1e-6, ho=at[5], xn=at[6],
+                xdt=F32, rstd=at[7], st=None)
+    row = d * 4
+    for bad in (dict(ho=at[2] + row), dict(xn=at[2] + row), dict(ho=at[2], gdt=BF16),
+                dict(ho=at[2], kind=3), dict(xn=at[2], kind=2), dict(ho=at[2], kind=1),
+                dict(ho=at[3]), dict(xn=at[4] + 16), dict(rstd=at[0]), dict(rstd=at[1] + row),
+                dict(rstd=at[2]), dict(rstd=at[3]), dict(rstd=at[5]), dict(rstd=at[6] + row),
+                dict(xn=at[5] + row), dict(ho=at[0] + row), dict(xn=at[1] - row)):
+        assert lib.moe_norm_join(*{**base, **bad}.values()) == EINVAL, bad
+        assert b"overlaps" in lib.rvq_last_error(), bad
+    base = dict(dho=at[0], dxn=at[1], xdt=F32, h=at[2], hdt=F32, y=at[3], ydt=F32, n=n, d=d,
+                alpha=1.0, gate=at[4], kind=4, gdt=F32, post=1, wpost=at[5], wpre=at[6], wdt=F32,
+                rstd=at[7], dh=at[8], dy=at[9], dgate=at[10], dwpost=at[11], dwpre=at[12],
+                ws=at[13], wsb=1, st=None)
+
+    def back(**kw):
+        return lib.moe_norm_join_backward(*{**base, **kw}.values())
+
+    ok = (dict(), dict(dh=at[0]), dict(dh=at[1]), dict(dh=at[2]), dict(dh=at[3], dy=at[2]),
+          dict(dy=at[4], dgate=at[3]), dict(dgate=at[4]), dict(kind=2, dgate=at[4]),
+          dict(kind=3, dgate=at[4]), dict(kind=1, dgate=at[4]), dict(dwpost=at[5], dwpre=at[6]))
+    for kw in ok:
+        assert back(**kw) == ENOMEM, kw     # past the checks of overlaps
+    for bad in (dict(dh=at[2] + row), dict(dh=at[3] + row), dict(dh=at[4] + row),
+                dict(dy=at[2] + row), dict(dy=at[3] - row), dict(dh=at[2], hdt=F32, dy=at[2]),
+                dict(dh=at[3], ydt=BF16), dict(dh=at[4], kind=3), dict(dy=at[4], kind=2),
+                dict(dgate=at[8]), dict(dgate=at[9] + row), dict(dgate=at[2] + row),
+                dict(dgate=at[4] + row), dict(dgate=at[7]), dict(dgate=at[5]),
+                dict(dgate=at[7], kind=2), dict(dgate=at[3] + 16, kind=2),
+                dict(dgate=at[8], kind=3), dict(dgate=at[9], kind=1), dict(dwpost=at[8]),
+                dict(dwpre=at[9] + row), dict(dwpost=at[12]), dict(dwpre=at[10]),
+                dict(dh=at[5]), dict(dy=at[6]), dict(dh=at[7]), dict(dgate=at[11], kind=3)):
+        assert back(**bad, wsb=1 << 26) == EINVAL, bad
+        assert b"overlaps" in lib.rvq_last_error(), bad

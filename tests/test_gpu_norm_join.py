@@ -377,3 +377,33 @@ def test_join_at_the_limits_of_narrow_threads(n, d, dtype):
     s = make(n, d, dtype, dtype, dtype, "channel", True, seed=d)
     rstd = check_forward(s, n, d, 0.75, True, dtype, BF)
     check_backward(s, n, d, 0.75, True, dtype, dtype, BF, dtype, rstd)
+
+
+@pytest.mark.parametrize("n,d", [(6, 264), (400, 264), (400, 7168), (306, 16384)])
+@pytest.mark.parametrize("gate", ["token", "full"])
+def test_join_outputs_in_the_place_of_inputs(n, d, gate):
+    """Rows of the same type may be written over: h, y and a full gate by the
+    outputs, and h, y and a gate per row by the gradients."""
+    s = make(n, d, F32, F32, F32, gate, True, seed=n)
+    ho, xn, rstd = forward(s, n, d, 1.0, True, F32, F32)
+    full = gate == "full"
+    for a, b in [("h", "y"), ("y", "h")] + ([("gate", "h"), ("y", "gate")] if full else []):
+        t = {k: v.clone() for k, v in s.items()}
+        rvq.moe_norm_join(t["y"], n, d, t[a], t[b], h=t["h"], gate=t["gate"], w_post=t["w_post"],
+                          w_pre=t["w_pre"], eps=EPS)
+        assert torch.equal(t[a], ho) and torch.equal(t[b], xn), (a, b)
+    g = gen(3)
+    dho, dxn = (torch.randn((n, d), device=DEV, generator=g) for _ in range(2))
+    ws = torch.empty(rvq.moe_norm_join_workspace_bytes(n, d), dtype=torch.uint8, device=DEV)
+
+    def back(t, dh, dy, dgate):
+        rvq.moe_norm_join_backward(dho, dxn, t["y"], n, d, rstd, ws, h=t["h"], gate=t["gate"],
+                                   w_post=t["w_post"], w_pre=t["w_pre"], dh=dh, dy=dy, dgate=dgate)
+
+    want = torch.empty_like(ho), torch.empty_like(ho), torch.empty_like(s["gate"])
+    back(s, *want)
+    for order in [("h", "y", "gate"), ("y", "h", "gate")] + ([("gate", "h", "y")] if full else []):
+        t = {k: v.clone() for k, v in s.items()}
+        back(t, *(t[k] for k in order))
+        for k, w in zip(order, want):
+            assert torch.equal(t[k], w), (order, k)
