@@ -18,10 +18,12 @@ namespace {
 constexpr int BW_LANES = 8;
 static_assert(kBwdChunkRows % BW_LANES == 0, "rows of a chunk per lane");
 
-// eight fp32 values; `wide`: at a multiple of 32 bytes, one load per lane
+// eight fp32 values; `wide`: at a multiple of 32 bytes, one load per lane.  A plain
+// load, as of dout below: blocks may be resident while the kernel before still writes
+// these values, and the read-only path is for data that no one writes meanwhile.
 __device__ __forceinline__ void ld32(const float *p, int wide, float (&v)[8]) {
     if (wide) {
-        asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
                        "=f"(v[6]), "=f"(v[7])
                      : "l"(p));
@@ -53,8 +55,8 @@ __global__ void __launch_bounds__(256) dense_bwd_kernel(const DenseBwdJob j) {
             ok[i] = t < j.n;
             at[i] = (int64_t)t * j.rows + c;
             if (!ok[i]) continue;
-            d_raw[i] = __ldg(reinterpret_cast<const uint4 *>(
-                reinterpret_cast<const uint16_t *>(j.dout) + (int64_t)t * j.ldd + c));
+            d_raw[i] = *reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const uint16_t *>(j.dout) + (int64_t)t * j.ldd + c);
             if (j.pre[0]) ld32(j.pre[0] + at[i], j.wide, g[i]);
             if (MATS == 2) ld32(j.pre[1] + at[i], j.wide, u[i]);
         }

@@ -201,7 +201,7 @@ __device__ __forceinline__ void fill_smem(uint8_t *smem, const JoinJob &j, const
         const int n16 = j.d * esize(j.wdt) / 16;
         for (int i = threadIdx.x; i < n16; i += blockDim.x)
             reinterpret_cast<uint4 *>(smem + at)[i] =
-                src ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(one, one, one, one);
+                src ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(one, one, one, one);
     };
     gain(L.w_post, j.w_post);
     gain(L.w_pre, j.w_pre);

@@ -1,6 +1,7 @@
 """Host side of the dense operators (no GPU): workspace sizes and refusals
 before any launch, in the library and in the binding."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -274,3 +275,15 @@ def test_join_refuses_racing_overlaps(n, d):
                 dict(dh=at[5]), dict(dy=at[6]), dict(dh=at[7]), dict(dgate=at[11], kind=3)):
         assert back(**bad, wsb=1 << 26) == EINVAL, bad
         assert b"overlaps" in lib.rvq_last_error(), bad
+
+
+def test_no_read_only_loads_beside_a_running_kernel():
+    """The dense operators' kernels are launched programmatically: their blocks may be
+    resident while the kernel before them writes what they will read.  The read-only
+    path (ld.global.nc, __ldg) is defined for data that no one writes meanwhile."""
+    csrc = os.path.join(os.path.dirname(rvq.__file__), "csrc")
+    files = [f for f in sorted(os.listdir(csrc)) if f.startswith(("dense", "join", "norm_join"))]
+    assert len(files) >= 10
+    for f in files:
+        code = open(os.path.join(csrc, f)).read()
+        assert "__ldg(" not in code and "global.nc" not in code and "__restrict__" not in code, f
