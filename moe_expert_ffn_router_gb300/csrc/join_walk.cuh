@@ -199,7 +199,9 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinJob j, const Jo
         }
         float s[3] = {sum4(s0), sum4(sA), sum4(sB)};
         block_sum(s, red[flip]);
-        const float cS = r2 * r2 * r2 * inv_d * s[0];
+        // r2 s[0] is of the order of d: in this order no factor leaves fp32 where c S
+        // does not (r2^3 alone does for rows of 1e-13 or 1e13)
+        const float cS = r2 * (r2 * (r2 * s[0] * inv_d));
         const float ez = s[1] - cS * s[2];  // sum e z (one gate per row) or sum e gate z
         if (T::GATE == 0 && j.dgate && threadIdx.x == 0) {
             if (j.gate_kind == MOE_GATE_TOKEN)

@@ -407,3 +407,33 @@ def test_join_outputs_in_the_place_of_inputs(n, d, gate):
         back(t, *(t[k] for k in order))
         for k, w in zip(order, want):
             assert torch.equal(t[k], w), (order, k)
+
+
+@pytest.mark.parametrize("n,d", [(3, 264), (400, 264), (310, 8200)])
+@pytest.mark.parametrize("scale", [1e-14, 1.0, 1e14])
+def test_join_gradients_of_any_scale(n, d, scale):
+    """Rows whose norm is far from 1 (eps 0): the gradient's third power of 1/rms is
+    beyond fp32, the gradient itself is not."""
+    g = gen(n)
+    h, y = (torch.randn((n, d), device=DEV, generator=g) * scale for _ in range(2))
+    w_pre = torch.randn((d,), device=DEV, generator=g) * 0.1 + 1
+    dxn = torch.randn((n, d), device=DEV, generator=g)
+    xn, rstd = torch.empty_like(h), torch.empty((2, n), device=DEV)
+    rvq.moe_norm_join(y, n, d, None, xn, h=h, alpha=0.5, post_norm=False, w_pre=w_pre, eps=0.0,
+                      rstd=rstd)
+    ws = torch.empty(rvq.moe_norm_join_workspace_bytes(n, d), dtype=torch.uint8, device=DEV)
+    dh, dy, dw = torch.empty_like(h), torch.empty_like(h), torch.empty_like(w_pre)
+    rvq.moe_norm_join_backward(None, dxn, y, n, d, rstd, ws, h=h, alpha=0.5, post_norm=False,
+                               w_pre=w_pre, dh=dh, dy=dy, dw_pre=dw)
+    ho = 0.5 * h.double() + y.double()
+    r = 1 / torch.sqrt((ho * ho).mean(1, keepdim=True))
+    q = dxn.double() * w_pre.double()
+    e = r * q - ho * r ** 3 * (q * ho).mean(1, keepdim=True)
+    # magnitudes of the terms times the errors met on the way: 1/rms and the row's sum
+    # are each good to 64 half steps, the rest are a dozen operations
+    mag = r * q.abs() + ho.abs() * r ** 3 * (q * ho).abs().mean(1, keepdim=True)
+    err = 4 * 80 * U * mag
+    R.check(dh, (0.5 * e, 0.5 * err), "dh")
+    R.check(dy, (e, err), "dy")
+    t = dxn.double() * ho * r
+    R.check(dw, (t.sum(0), (80 + n) * U * t.abs().sum(0)), "dw_pre")
