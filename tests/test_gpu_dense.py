@@ -481,3 +481,77 @@ def test_linear_gradients_split_tiles(n, rows, cols):
                                          (1688, 320, 512), (200, 264, 7168)])
 def test_gated_gradients_split_tiles(n, rows, cols):
     test_gated_gradients(n, rows, cols)
+
+
+def act_error(name, v):
+    """Relative error of an activation's evaluation in fp32, in its own terms: the
+    hardware exponential is good to 2 + 1.2 |a| units of the last place (2^-23) of
+    exp(a), a's own rounding moves it by up to 3 |a| half steps, a division takes two
+    units, and a polynomial and the remaining products a few."""
+    a = {"silu": v.abs(), "gelu": v * v / 2,
+         "gelu_tanh": 1.5957691216057308 * (v + 0.044715 * v ** 3).abs()}[name]
+    return (16 + 3 * a) * 2.0 ** -23
+
+
+def sweep(lo=-9.0, hi=9.0, count=4096):
+    """Values as the sum of two bf16 ones, which the products with 1 add up again."""
+    v = torch.linspace(lo, hi, count, device=DEV)
+    a = v.to(BF)
+    b = (v - a.float()).to(BF)
+    return a, b
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("tokens_are", ["few", "many"])
+def test_activations_are_accurate_in_the_tails(act, tokens_are):
+    """Outputs in fp32 are within the evaluation's own relative error of the formula,
+    for every pre-activation from -9 to 9."""
+    a, b = sweep()
+    ones = torch.zeros((8, 8), dtype=BF, device=DEV)
+    ones[:, :2] = 1
+    wide = torch.zeros((a.numel(), 8), dtype=BF, device=DEV)
+    wide[:, 0], wide[:, 1] = a, b
+    x, w = (ones[:1].clone(), wide) if tokens_are == "few" else (wide, ones)
+    n, rows = x.shape[0], w.shape[0]
+    ws = workspace(n, rows, 8)
+    out, pre = (torch.empty((n, rows), device=DEV) for _ in range(2))
+    rvq.moe_linear(x, w, n, rows, 8, out, ws, act=rvq.MOE_ACTS[act], pre=pre)
+    v = (a.double() + b.double()) if tokens_are == "few" else (a.double() + b.double())[:, None]
+    assert ((pre.double() - v).abs() <= 2.0 ** -22 * v.abs()).all()
+    want = R.act(act, pre.double())
+    if act == "gelu_tanh":     # 1 + tanh loses its last digits at -1 in any precision
+        want = pre.double() * torch.sigmoid(
+            1.5957691216057308 * (pre.double() + 0.044715 * pre.double() ** 3))
+    err = (out.double() - want).abs()
+    over = err - (act_error(act, pre.double()) * want.abs() + R.tiny(F32))
+    i = over.argmax()
+    assert (over <= 0).all(), (pre.reshape(-1)[i].item(), out.reshape(-1)[i].item(),
+                               want.reshape(-1)[i].item())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_are_accurate_in_the_tails(act):
+    """dp = dout act'(pre) in bf16, for pre from -9 to 9: half a step, and the
+    evaluation's error of the slope's two terms."""
+    a, b = sweep()
+    n = a.numel()
+    pre = (a.float() + b.float())[:, None].expand(n, 8).contiguous()
+    eye = torch.eye(8, dtype=BF, device=DEV)
+    dx = torch.empty((n, 8), dtype=BF, device=DEV)
+    ws = workspace(n, 8, 8)
+    rvq.moe_linear_backward(torch.ones((n, 8), dtype=BF, device=DEV), None, eye, n, 8, 8, ws,
+                            dx=dx, pre=pre, act=rvq.MOE_ACTS[act])
+    v = pre.double()
+    arg = {"silu": v, "gelu": None,
+           "gelu_tanh": 1.5957691216057308 * (v + 0.044715 * v ** 3)}[act]
+    if act == "gelu":
+        one, two = 0.5 * torch.special.erfc(-v / 2 ** 0.5), \
+            v * torch.exp(-0.5 * v * v) / (2 * torch.pi) ** 0.5
+    else:
+        da = 1.0 if act == "silu" else 1.5957691216057308 * (1 + 3 * 0.044715 * v * v)
+        one = torch.sigmoid(arg)
+        two = v * one * torch.sigmoid(-arg) * da
+    want = one + two
+    # 1 - s of a sigmoid near 1 is good to a half step of 1 only
+    err = 2 * act_error(act, v) * (one.abs() + two.abs()) + 4 * R.U32 * (v * v).clamp(min=1) * one
+    assert ((dx.double() - want).abs() <= R.half_step(BF) * (want.abs() + err) + err).all()
