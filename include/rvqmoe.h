@@ -566,8 +566,8 @@ typedef enum moe_act {
 } moe_act;
 
 /* Workspace of moe_linear (backward = 0), or of moe_linear_backward and
- * moe_linear (1).  It depends on the current device's SM count.  0 for a shape
- * the calls refuse. */
+ * moe_linear (1), for up to n tokens.  It depends on the current device's SM count.
+ * 0 for a shape the calls refuse. */
 size_t moe_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols, int32_t backward);
 
 /* out[t][r] = residual[t][r] + alpha * act(sum_c x[t][c] w[r][c] + bias[r])

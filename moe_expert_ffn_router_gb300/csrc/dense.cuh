@@ -266,7 +266,7 @@ struct DenseJob {
     uint32_t *status;       // the workspace's status block
     float *partial;         // dense_gemm_partial_bytes of workspace
 };
-size_t dense_gemm_partial_bytes(const DenseJob &job);
+size_t dense_gemm_partial_bytes(const DenseJob &job);  // grows with M, N and K
 rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream);
 // Sums of a bias gradient still to be added: dbias[m][col] (NULL: not wanted) from
 // the fp32 partials part[chunk][m][col].

@@ -844,11 +844,6 @@ GemmPlan plan_gemm(const DenseJob &j, int pairs, int most = kMaxParts, int max_s
     return best;
 }
 
-size_t partial_bytes(const GemmPlan &p, const DenseJob &j) {
-    const size_t planes = j.mode == DG_GATED || j.mode == DG_PAIR_M ? 2 : 1;
-    return p.parts > 1 ? (size_t)p.parts * planes * j.M * j.N * 4 : 0;
-}
-
 }  // namespace
 
 rvq_status encode_operand(CUtensorMap *map, const void *p, int rows, int K, int64_t ld, int t, int dt,
@@ -875,9 +870,18 @@ rvq_status encode_operand(CUtensorMap *map, const void *p, int rows, int K, int6
     return RVQ_OK;
 }
 
+// Partial sums of any cut that plan_gemm may choose for up to these M, N and K, so
+// that a workspace serves fewer tokens too (which may be cut where more are not).  A
+// tile of 256 x 256 at most holds a pair's part, and there are no more parts than pairs.
 size_t dense_gemm_partial_bytes(const DenseJob &job) {
-    if (dense_stream_fits(job)) return 0;
-    return partial_bytes(plan_gemm(job, num_sms() / 2), job);
+    if (dense_stream_fits(job)) return 0;  // and so does every smaller M
+    const int kb = (job.K + DG_BK - 1) / DG_BK, slices = job.mode == DG_SUM_K ? 2 * kb : kb;
+    const int parts = slices / 8 < kMaxParts ? slices / 8 : kMaxParts;
+    if (parts < 2) return 0;
+    const size_t planes = job.mode == DG_GATED || job.mode == DG_PAIR_M ? 2 : 1;
+    const size_t all = (size_t)parts * planes * job.M * job.N * 4;
+    const size_t most = (size_t)(num_sms() / 2) * 2 * DG_BM * DG_ACC * 4;
+    return all < most ? all : most;
 }
 
 // Arguments and tensor maps of a product cut by `plan`.

@@ -287,3 +287,19 @@ def test_no_read_only_loads_beside_a_running_kernel():
     for f in files:
         code = open(os.path.join(csrc, f)).read()
         assert "__ldg(" not in code and "global.nc" not in code and "__restrict__" not in code, f
+
+
+@pytest.mark.parametrize("rows,cols", [(2048, 7168), (7168, 2048), (1000, 2048), (256, 512),
+                                       (360, 688), (264, 7168), (8, 8)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_a_workspace_serves_fewer_tokens(rows, cols, backward):
+    """A program allocates for its largest batch: no smaller batch needs more, nor
+    does the forward call need more than the gradients."""
+    tokens = sorted(set(list(range(1, 520, 7)) + [2 ** i + j for i in range(8, 15) for j in (-1, 0, 1)]
+                        + list(range(512, 5000, 97))))
+    for f in (rvq.moe_linear_workspace_bytes, rvq.moe_gated_linear_workspace_bytes):
+        need = [f(n, rows, cols, backward) for n in tokens]
+        assert all(a <= b for a, b in zip(need, need[1:]))
+        assert all(f(n, rows, cols) <= b for n, b in zip(tokens, need))
+    need = [rvq.moe_norm_join_workspace_bytes(n, cols) for n in tokens]
+    assert all(a <= b for a, b in zip(need, need[1:]))

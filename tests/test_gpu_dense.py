@@ -555,3 +555,26 @@ def test_slopes_are_accurate_in_the_tails(act):
     # 1 - s of a sigmoid near 1 is good to a half step of 1 only
     err = 2 * act_error(act, v) * (one.abs() + two.abs()) + 4 * R.U32 * (v * v).clamp(min=1) * one
     assert ((dx.double() - want).abs() <= R.half_step(BF) * (want.abs() + err) + err).all()
+
+
+def test_one_workspace_for_every_batch():
+    """A workspace made for the largest batch serves the smaller ones, which are cut
+    otherwise, with the same results as one of their own."""
+    rows, cols, most = 1000, 4096, 2048
+    g = gen(1)
+    x, dout = normal(g, (most, cols), BF), normal(g, (most, rows), BF)
+    wg, wu = (normal(g, (rows, cols), BF, cols ** -0.5) for _ in range(2))
+    big = workspace(most, rows, cols, True)
+    for n in (most, 700, 400, 200, 30, 1):
+        got = []
+        for ws in (big, workspace(n, rows, cols, True)):
+            out = torch.empty((n, rows), dtype=BF, device=DEV)
+            pre = torch.empty((2, n, rows), dtype=F32, device=DEV)
+            dx, dwg, dwu = (torch.empty(s, dtype=BF, device=DEV)
+                            for s in ((n, cols), (rows, cols), (rows, cols)))
+            rvq.moe_gated_linear(x[:n], wg, wu, n, rows, cols, out, ws, pre=pre)
+            rvq.moe_gated_linear_backward(dout[:n], x[:n], wg, wu, pre, n, rows, cols, ws, dx=dx,
+                                          dwg=dwg, dwu=dwu)
+            assert rvq.rvq_ws_status(ws) == (0, 0)
+            got.append((out, pre, dx, dwg, dwu))
+        assert all(torch.equal(a, b) for a, b in zip(*got)), n
