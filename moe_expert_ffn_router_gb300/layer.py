@@ -149,6 +149,15 @@ class MoeLayer:
         return rvq_ws_status(self.workspace(n))
 
 
+def _share_workspace(layers: list[MoeLayer], n: int):
+    """One workspace for layers that run one after another on one stream (24 GB for
+    a K3-shaped layer at 2048 tokens)."""
+    ws = layers[0].workspace(n)
+    for L in layers[1:]:
+        if moe_workspace_bytes(L.bank, n, L.k) <= ws.numel():
+            L._ws[n] = ws
+
+
 class MoeStack:
     """Layers applied in order to a residual stream h (the first layer's
     input, then each layer's fp32 output): layer i computes
@@ -165,12 +174,7 @@ class MoeStack:
     def buffers(self, n: int) -> list[dict]:
         b = self._bufs.get(n)
         if b is None:
-            # the layers run one after another on one stream, so they share
-            # one workspace (24 GB per K3-shaped layer at 2048 tokens)
-            ws = self.layers[0].workspace(n)
-            for L in self.layers[1:]:
-                if moe_workspace_bytes(L.bank, n, L.k) <= ws.numel():
-                    L._ws[n] = ws
+            _share_workspace(self.layers, n)
             b = [L.buffers(n) for L in self.layers]
             for L, bl in zip(self.layers, b):
                 bl["xn"] = torch.empty((n, L.d), dtype=torch.bfloat16, device=L.device)
@@ -361,6 +365,7 @@ class SharedExpertStack:
         b = self._bufs.get(n)
         if b is None:
             b = []
+            _share_workspace([L for L, _, _ in self.blocks], n)
             for L, _, _ in self.blocks:
                 bl = L.buffers(n)
                 bl["xn"] = torch.empty((n, L.d), dtype=torch.bfloat16, device=L.device)

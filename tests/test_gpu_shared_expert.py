@@ -112,3 +112,14 @@ def test_example_runs():
     line = [v for v in r.stdout.splitlines() if v.startswith("training loss:")][0]
     losses = [float(v) for v in line.split(":")[1].split()]
     assert len(losses) == 5 and losses[-1] < losses[0]
+
+
+def test_blocks_share_a_workspace():
+    """The routed layers run one after another: one workspace (24 GB for a K3-shaped
+    layer at 2048 tokens) serves them all."""
+    stack, _ = build(3)
+    for n in (3, 70):
+        bufs = stack.forward(torch.randn((n, D), device=DEV))
+        assert len({b["ws"].data_ptr() for b in bufs}) == 1
+        for L, S, _ in stack.blocks:
+            assert L.status(n) == (0, 0) and S.status(n) == (0, 0)
