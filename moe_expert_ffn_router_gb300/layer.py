@@ -298,6 +298,9 @@ class SharedExpert:
         self.wg, self.wu, self.wd = (_dev(w, self.device) for w in (wg, wu, wd))
         self.f, self.d = self.wg.shape
         assert self.wu.shape == (self.f, self.d) and self.wd.shape == (self.d, self.f)
+        for name, w in (("wg", self.wg), ("wu", self.wu), ("wd", self.wd)):
+            if w.dtype not in (torch.bfloat16, torch.float16) or w.dtype != self.wg.dtype:
+                raise TypeError(f"{name}: {w.dtype} (bf16 or fp16, one type for all three)")
         self.act = act
         self._bufs = {}
 
@@ -354,10 +357,15 @@ class SharedExpertStack:
     for each block (MoeLayer, SharedExpert, dict of w_pre, w_post, gate: tensors
     or None).  The norm after a block, its gate, the residual's scale and the
     norm before the next block are one launch (moe_norm_join), and the shared
-    expert's output enters the routed layer as its residual.  h is fp32."""
+    expert's output enters the routed layer as its residual.  h is fp32, xn bf16 (the
+    routed layers take no fp16), so the shared experts are bf16 (TypeError)."""
 
     def __init__(self, blocks, alpha: float = 1.0, eps: float = 1e-6):
         assert blocks and all(L.d == S.d == blocks[0][0].d for L, S, _ in blocks)
+        for i, (_, S, _) in enumerate(blocks):
+            if S.wg.dtype != torch.bfloat16:
+                raise TypeError(f"block {i}: shared expert of {S.wg.dtype}, and the normed stream "
+                                "that the routed experts read too is bf16")
         self.blocks, self.alpha, self.eps = list(blocks), alpha, eps
         self._bufs = {}
 

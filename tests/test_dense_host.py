@@ -303,3 +303,22 @@ def test_a_workspace_serves_fewer_tokens(rows, cols, backward):
         assert all(f(n, rows, cols) <= b for n, b in zip(tokens, need))
     need = [rvq.moe_norm_join_workspace_bytes(n, cols) for n in tokens]
     assert all(a <= b for a, b in zip(need, need[1:]))
+
+
+def test_shared_expert_types_are_refused_where_they_are_built():
+    """Not in the first call: a weight type that the products do not take, mixed types,
+    and fp16 experts in a stack, whose normed stream is bf16."""
+    from moe_expert_ffn_router_gb300.layer import SharedExpert, SharedExpertStack
+
+    def expert(*dtypes):
+        shapes = ((16, 32), (16, 32), (32, 16))
+        return SharedExpert(*(torch.zeros(s, dtype=t) for s, t in zip(shapes, dtypes)), device="cpu")
+
+    bf, hf, f32 = torch.bfloat16, torch.float16, torch.float32
+    for bad in ((f32, f32, f32), (bf, bf, hf), (hf, bf, hf)):
+        with pytest.raises(TypeError, match="bf16 or fp16"):
+            expert(*bad)
+    layer = type("Layer", (), dict(d=32))()
+    SharedExpertStack([(layer, expert(bf, bf, bf), {})])
+    with pytest.raises(TypeError, match="block 1"):
+        SharedExpertStack([(layer, expert(bf, bf, bf), {}), (layer, expert(hf, hf, hf), {})])
