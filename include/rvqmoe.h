@@ -544,7 +544,9 @@ rvq_status moe_rms_norm(const void *x_dev, rvq_dtype xdt, int32_t n, int32_t d, 
  *
  * Matrices are row-major with a row pitch `ld*` in elements: ld >= columns,
  * ld % 8 == 0, base pointers 16-byte aligned (EALIGN).  n (tokens) is
- * from 1 to 2^24 - 256; rows and cols are multiples of 8 in that range (EINVAL).  Element types are
+ * from 1 to 2^24 - 256; rows and cols are multiples of 8 in that range (EINVAL).
+ * Matrices of one pitch in different columns of a wider one do not overlap.
+ * Element types are
  * RVQ_BF16 or RVQ_F16 for the operands of a product (one type for x, w, bias
  * and, in a gradient, dout and every output); products accumulate in fp32 on
  * the tensor cores and each output is rounded once.

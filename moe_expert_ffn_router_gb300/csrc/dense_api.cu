@@ -70,14 +70,21 @@ rvq_status check_ws(const char *who, const void *ws, size_t bytes, size_t need) 
     return RVQ_OK;
 }
 
-// Byte ranges of two row-major matrices do not overlap.
+// Two row-major matrices do not overlap.
 bool disjoint(const void *a, int64_t lda, int32_t ra, int32_t ca, size_t ea, const void *b,
               int64_t ldb, int32_t rb, int32_t cb, size_t eb) {
     if (a == nullptr || b == nullptr) return true;
     const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
     const uintptr_t a1 = a0 + ((uint64_t)(ra - 1) * (uint64_t)lda + (uint64_t)ca) * ea;
     const uintptr_t b1 = b0 + ((uint64_t)(rb - 1) * (uint64_t)ldb + (uint64_t)cb) * eb;
-    return a1 <= b0 || b1 <= a0;
+    if (a1 <= b0 || b1 <= a0) return true;
+    // of one row pitch, in different columns: parts of one wider matrix
+    const uint64_t wa = (uint64_t)ca * ea, wb = (uint64_t)cb * eb;
+    const uint64_t pa = (uint64_t)lda * ea, pb = (uint64_t)ldb * eb;
+    const uint64_t pitch = ra > 1 ? pa : pb;
+    if ((ra > 1 && rb > 1 && pa != pb) || pitch == 0) return false;
+    const uint64_t at = b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;
+    return at >= wa && at + wb <= pitch;
 }
 
 // A row-major matrix, or (vector()) contiguous values; NULL: absent.
@@ -178,7 +185,6 @@ rvq_status moe_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t
     }
     CHECK_ALIGN(bias_dev, who, "bias");
     CHECK_ALIGN(pre_dev, who, "pre");
-    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(1, n, rows, cols, 0)));
     const size_t oe = elem_bytes(odt);
     const Span o = {out_dev, ldo, n, rows, oe}, pre = {pre_dev, rows, n, rows, 4};
     const Span in[] = {{x_dev, ldx, n, cols, 2}, {w_dev, ldw, rows, cols, 2},
@@ -189,6 +195,7 @@ rvq_status moe_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t
     CHECK_ARG((residual_dev == out_dev && rdt == odt && ldr == ldo) ||
                   apart(o, res),
               "%s: out overlaps the residual with another type, place or pitch", who);
+    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(1, n, rows, cols, 0)));
     DenseJob j = {};
     j.mode = DG_PLAIN;
     j.M = n;
@@ -228,13 +235,13 @@ rvq_status moe_gated_linear(const void *x_dev, int64_t ldx, const void *wg_dev,
     CHECK_ALIGN(bg_dev, who, "bg");
     CHECK_ALIGN(bu_dev, who, "bu");
     CHECK_ALIGN(pre_dev, who, "pre");
-    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(2, n, rows, cols, 0)));
     const Span out[] = {{out_dev, ldo, n, rows, 2}, {pre_dev, rows, n, rows, 4},
                         {pre_dev ? pre_dev + (size_t)n * rows : nullptr, rows, n, rows, 4}};
     const Span in[] = {{x_dev, ldx, n, cols, 2}, {wg_dev, ldw, rows, cols, 2},
                        {wu_dev, ldw, rows, cols, 2}, vector(bg_dev, rows, 2),
                        vector(bu_dev, rows, 2)};
     CHECK_ARG(all_apart(out, in), "%s: out or pre overlaps another matrix", who);
+    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(2, n, rows, cols, 0)));
     DenseJob j = {};
     j.mode = DG_GATED;
     j.M = n;
@@ -281,7 +288,6 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
     }
     CHECK_ALIGN(dbias_dev, who, "dbias");
     CHECK_ALIGN(pre_dev, who, "pre");
-    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(1, n, rows, cols, 1)));
     // The products of dx and dw may run in one launch, the bias sums beside either.
     const Span out[] = {{dx_dev, lddx, n, cols, 2}, {dw_dev, lddw, rows, cols, 2},
                         vector(dbias_dev, rows, 2)};
@@ -289,6 +295,7 @@ rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x
                        {dx_dev ? w_dev : nullptr, ldw, rows, cols, 2},
                        {dw_dev ? x_dev : nullptr, ldx, n, cols, 2}};
     CHECK_ARG(all_apart(out, in), "%s: a gradient overlaps an input or another gradient", who);
+    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(1, n, rows, cols, 1)));
     const WsPlan P = plan_ws(1, n, rows, cols, true);
     uint8_t *ws = (uint8_t *)ws_dev;
     cudaStream_t st = (cudaStream_t)stream;
@@ -369,7 +376,6 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
         RVQ_TRY(check_matrix(who, "dwg", dwg_dev, lddw, cols));
         RVQ_TRY(check_matrix(who, "dwu", dwu_dev, lddw, cols));
     }
-    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(2, n, rows, cols, 1)));
     // As in moe_linear_backward; dout is read before the products.
     const Span out[] = {{dx_dev, lddx, n, cols, 2}, {dwg_dev, lddw, rows, cols, 2},
                         {dwu_dev, lddw, rows, cols, 2}, vector(dbg_dev, rows, 2),
@@ -378,6 +384,7 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
                        {dx_dev ? wu_dev : nullptr, ldw, rows, cols, 2},
                        {dwg_dev ? x_dev : nullptr, ldx, n, cols, 2}};
     CHECK_ARG(all_apart(out, in), "%s: a gradient overlaps an input or another gradient", who);
+    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, ws_bytes_of(2, n, rows, cols, 1)));
     const WsPlan P = plan_ws(2, n, rows, cols, true);
     uint8_t *ws = (uint8_t *)ws_dev;
     cudaStream_t st = (cudaStream_t)stream;

@@ -322,3 +322,25 @@ def test_shared_expert_types_are_refused_where_they_are_built():
     SharedExpertStack([(layer, expert(bf, bf, bf), {})])
     with pytest.raises(TypeError, match="block 1"):
         SharedExpertStack([(layer, expert(bf, bf, bf), {}), (layer, expert(hf, hf, hf), {})])
+
+
+def test_columns_of_one_wider_matrix_do_not_overlap():
+    """Matrices of one pitch that lie beside each other in a wider one are accepted (the
+    next refusal is the workspace's); a shared column, or another pitch, is not."""
+    # x in columns 0 .. 63, out 64 .. 95, the residual 96 .. 127 of 128, 300 rows
+    beside = dict(n=300, x=A, ldx=128, out=A + 128, ldo=128, res=A + 192, rdt=BF16, ldr=128, wsb=1)
+    assert lin(**beside) == ENOMEM
+    assert lin(**{**beside, "n": 1}) == ENOMEM
+    # a narrow fp32 output in the same bytes: columns 64 .. 127 of 256 bytes
+    assert lin(**{**beside, "res": None, "odt": F32, "ldo": 64}) == ENOMEM
+    for bad in (dict(out=A + 112), dict(out=A + 144), dict(res=A + 176), dict(ldo=136),
+                dict(ldr=120), dict(out=A + 240), dict(x=A + 16), dict(odt=F32, ldo=64)):
+        assert lin(**{**beside, **bad}) == EINVAL, bad
+    # the gradients of two halves of a matrix [rows][2 cols], into such a matrix
+    both = dict(do=A, ldd=32, x=B, ldx=64, wg=C, wu=C + 128, ldw=128, pre=D, dt=BF16, n=40, rows=32,
+                cols=64, act=2, dx=E_, lddx=64, dwg=F, dwu=F + 128, lddw=128, dbg=None, dbu=None,
+                ws=F + 0x10000000, wsb=1, st=None)
+    assert lib.moe_gated_linear_backward(*both.values()) == ENOMEM
+    for bad in (dict(dwu=F + 112), dict(dwu=F + 144), dict(dx=C + 128, lddx=128),
+                dict(dwg=C, dwu=F)):
+        assert lib.moe_gated_linear_backward(*{**both, **bad}.values()) == EINVAL, bad

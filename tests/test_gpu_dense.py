@@ -578,3 +578,28 @@ def test_one_workspace_for_every_batch():
             assert rvq.rvq_ws_status(ws) == (0, 0)
             got.append((out, pre, dx, dwg, dwu))
         assert all(torch.equal(a, b) for a, b in zip(*got)), n
+
+
+@pytest.mark.parametrize("n", [3, 300])
+def test_columns_of_one_wider_matrix(n):
+    """Input, output and residual beside each other in one matrix, and both weight
+    gradients in one."""
+    rows, cols = 72, 136
+    g = gen(n)
+    x, res = normal(g, (n, cols), BF), normal(g, (n, rows), BF)
+    wide = torch.full((n, cols + 2 * rows), float("nan"), dtype=BF, device=DEV)
+    xs, out, rs = wide[:, :cols], wide[:, cols:cols + rows], wide[:, cols + rows:]
+    xs.copy_(x)
+    rs.copy_(res)
+    wg, wu = (normal(g, (rows, cols), BF, cols ** -0.5) for _ in range(2))
+    ws = workspace(n, rows, cols, True)
+    rvq.moe_linear(xs, wg, n, rows, cols, out, ws, residual=rs)
+    R.check(out, R.linear(x, wg, None, "none", 1.0, res, BF)[0], "out")
+    assert torch.equal(xs, x) and torch.equal(rs, res)
+    pre = torch.empty((2, n, rows), dtype=F32, device=DEV)
+    rvq.moe_gated_linear(xs, wg, wu, n, rows, cols, out, ws, pre=pre)
+    dw = torch.empty((rows, 2 * cols), dtype=BF, device=DEV)
+    apart = [torch.empty((rows, cols), dtype=BF, device=DEV) for _ in range(2)]
+    for a, b in ((dw[:, :cols], dw[:, cols:]), apart):
+        rvq.moe_gated_linear_backward(res, xs, wg, wu, pre, n, rows, cols, ws, dwg=a, dwu=b)
+    assert torch.equal(dw, torch.cat(apart, 1))
