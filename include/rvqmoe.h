@@ -687,6 +687,20 @@ rvq_status moe_norm_join_backward(const void *dh_out_dev, const void *dxn_dev, r
                                   void *dw_pre_dev, void *ws_dev, size_t ws_bytes,
                                   rvq_stream_t stream);
 
+/* How the current device computes the products of moe_linear or (gated)
+ * moe_gated_linear, or (backward) those of their gradients, both wanted: lets a test
+ * say which way it ran.  Launches nothing.  out[0]: 1 if dx and dw share a launch; then for
+ * the forward product or dx, and (backward) for dw: a moe_way, the parts or the pairs
+ * of CTAs that a tile is cut into, the tile's columns (0 for MOE_WAY_STREAM). */
+typedef enum moe_way {
+    MOE_WAY_STREAM = 0, /* weights streamed past the tokens                     */
+    MOE_WAY_TILES = 1,  /* whole tiles                                          */
+    MOE_WAY_PARTS = 2,  /* tiles cut by depth, added by a second launch         */
+    MOE_WAY_SPLIT = 3   /* tiles split by depth among the pairs of a cluster    */
+} moe_way;
+rvq_status rvq_selftest_dense_plan(int32_t gated, int32_t backward, int32_t n, int32_t rows,
+                                   int32_t cols, int32_t out[7]);
+
 /* Self-test of the failure path of the tensor-core kernel (no counterpart in
  * the pages): launches the prefill GEMM on one zero token routed to expert 0
  * with its MMA role first waiting for an mbarrier arrival that nothing makes.

@@ -27,6 +27,7 @@ RVQMOE_PREFILL_MIN_TOKENS = 6
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 MOE_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU,
             "gelu": MOE_ACT_GELU, "gelu_tanh": MOE_ACT_GELU_TANH}
+MOE_WAYS = ("stream", "tiles", "parts", "split")
 (MOE_GATE_NONE, MOE_GATE_SCALAR, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL) = range(5)
 DEV_ERR_INDEX, DEV_ERR_NONFINITE, DEV_ERR_CORRUPT, DEV_ERR_TIMEOUT = 1, 2, 4, 8
 STATUS = {0: "RVQ_OK", 1: "RVQ_EINVAL", 2: "RVQ_EALIGN", 3: "RVQ_ENOMEM", 4: "RVQ_ECORRUPT",
@@ -130,6 +131,7 @@ _SIGS = {
     "moe_norm_join_backward": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp,
                                       _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _sz, _vp]),
+    "rvq_selftest_dense_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
     "rvq_selftest_prefill_timeout": (_i32, [_BANKP, _vp, _sz, _vp]),
     "rvq_ws_clear": (_i32, [_vp, _vp]),
     "rvq_ws_status": (_i32, [_vp, ctypes.POINTER(_u32), _vp]),
@@ -616,6 +618,18 @@ def moe_gated_linear_backward(dout, x, wg, wu, pre, n, rows, cols, ws, dx=None, 
                                         _raw_stream(stream))
     if rc:
         _check("moe_gated_linear_backward", rc)
+
+
+def rvq_selftest_dense_plan(gated, backward, n, rows, cols) -> tuple[bool, list[tuple[str, int, int]]]:
+    """How the products of moe_linear or (gated) moe_gated_linear, or of their
+    gradients, are computed: whether dx and dw share a launch, and for each product
+    (the forward's; dx, dw) its way ("stream", "tiles", "parts" or "split"), the parts
+    or CTA pairs a tile is cut into, and the tile's columns."""
+    out = (_i32 * 7)()
+    _check("rvq_selftest_dense_plan",
+           _lib.rvq_selftest_dense_plan(int(gated), int(backward), n, rows, cols, out))
+    ways = [(MOE_WAYS[out[i]], out[i + 1], out[i + 2]) for i in (1, 4)]
+    return bool(out[0]), ways if backward else ways[:1]
 
 
 def _gate_kind(gate, n, d) -> int:

@@ -281,6 +281,8 @@ struct BiasSums {
 // along with them.
 rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const BiasSums &sums,
                                  cudaStream_t stream);
+// rvq_selftest_dense_plan's answer for one product or the two of a gradient
+void dense_plan_of(const DenseJob &x, const DenseJob *y, int32_t (&out)[7]);
 // launch_dense_gemm for few tokens as the rows of A: the weights streamed past the
 // batch (dense_stream.cu)
 constexpr int kStreamMaxTokens = 192;

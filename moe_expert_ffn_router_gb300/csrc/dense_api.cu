@@ -121,7 +121,7 @@ struct WsPlan {
     size_t off_partial, off_dp, off_part, total;
 };
 
-size_t product_partial(int mode, int32_t M, int32_t N, int32_t K, int a_t, int b_t) {
+DenseJob product_of(int mode, int32_t M, int32_t N, int32_t K, int a_t, int b_t) {
     DenseJob j = {};
     j.mode = mode;
     j.M = M;
@@ -129,7 +129,18 @@ size_t product_partial(int mode, int32_t M, int32_t N, int32_t K, int a_t, int b
     j.K = K;
     j.a_t = a_t;
     j.b_t = b_t;
-    return dense_gemm_partial_bytes(j);
+    return j;
+}
+
+// The products of a call, by their sizes: the forward's, or dx and dw.
+DenseJob forward_product(int mats, int32_t n, int32_t rows, int32_t cols) {
+    return product_of(mats == 2 ? DG_GATED : DG_PLAIN, n, rows, cols, 0, 0);
+}
+DenseJob dx_product(int mats, int32_t n, int32_t rows, int32_t cols) {
+    return product_of(mats == 2 ? DG_SUM_K : DG_PLAIN, n, cols, rows, 0, 1);
+}
+DenseJob dw_product(int mats, int32_t n, int32_t rows, int32_t cols) {
+    return product_of(mats == 2 ? DG_PAIR_M : DG_PLAIN, rows, cols, n, 1, 1);
 }
 
 WsPlan plan_ws(int mats, int32_t n, int32_t rows, int32_t cols, bool backward) {
@@ -137,11 +148,11 @@ WsPlan plan_ws(int mats, int32_t n, int32_t rows, int32_t cols, bool backward) {
     P.off_partial = RVQ_WS_STATUS_BYTES;
     if (!backward) {
         P.total = up256(P.off_partial +
-                        product_partial(mats == 2 ? DG_GATED : DG_PLAIN, n, rows, cols, 0, 0));
+                        dense_gemm_partial_bytes(forward_product(mats, n, rows, cols)));
         return P;
     }
-    const size_t dx = product_partial(mats == 2 ? DG_SUM_K : DG_PLAIN, n, cols, rows, 0, 1);
-    const size_t dw = product_partial(mats == 2 ? DG_PAIR_M : DG_PLAIN, rows, cols, n, 1, 1);
+    const size_t dx = dense_gemm_partial_bytes(dx_product(mats, n, rows, cols));
+    const size_t dw = dense_gemm_partial_bytes(dw_product(mats, n, rows, cols));
     P.off_dp = up256(P.off_partial + (dx > dw ? dx : dw));
     P.off_part = up256(P.off_dp + (size_t)mats * n * rows * 2);
     P.total = up256(P.off_part + (size_t)dense_bwd_chunks(n) * mats * rows * 4);
@@ -438,6 +449,23 @@ rvq_status moe_gated_linear_backward(const void *dout_dev, int64_t lddo, const v
     w.out[1] = dwu_dev;
     w.ldo = lddw;
     return launch_dense_gemm_two(j, w, bias_sums_of(b), st);
+}
+
+rvq_status rvq_selftest_dense_plan(int32_t gated, int32_t backward, int32_t n, int32_t rows,
+                                   int32_t cols, int32_t out[7]) {
+    const char *who = "rvq_selftest_dense_plan";
+    CHECK_ARG(dense_shape(n, rows, cols) && out, "%s: n %d, rows %d, cols %d, out %p", who, n, rows,
+              cols, (void *)out);
+    const int mats = gated ? 2 : 1;
+    int32_t plan[7];
+    if (backward) {
+        const DenseJob dw = dw_product(mats, n, rows, cols);
+        dense_plan_of(dx_product(mats, n, rows, cols), &dw, plan);
+    } else {
+        dense_plan_of(forward_product(mats, n, rows, cols), nullptr, plan);
+    }
+    for (int i = 0; i < 7; ++i) out[i] = plan[i];
+    return RVQ_OK;
 }
 
 // ---------------------------------------------------------------- norm join

@@ -1038,25 +1038,15 @@ rvq_status launch_dense_gemm(const DenseJob &job, cudaStream_t stream) {
     return launch_one(job, plan_gemm(job, num_sms() / 2), BiasSums{}, stream);
 }
 
-rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const BiasSums &sums,
-                                 cudaStream_t stream) {
-    const long long pairs = num_sms() / 2;
-    if (dense_stream_fits(x) || dense_stream_fits(y)) {
-        // few tokens: each its own way, the bias gradients beside the tiled one
-        const DenseJob *jobs[2] = {&x, &y};
-        bool added = !sums.wanted();
-        for (int i = 1; i >= 0; --i) {
-            const DenseJob &j = *jobs[i];
-            if (!j.out[0]) continue;
-            if (dense_stream_fits(j)) {
-                RVQ_TRY(launch_dense_stream(j, stream));
-            } else {
-                RVQ_TRY(launch_one(j, plan_gemm(j, (int)pairs), added ? BiasSums{} : sums, stream));
-                added = true;
-            }
-        }
-        return added ? RVQ_OK : launch_bias_sums(sums, stream);
-    }
+// How two products without a common output are cut, for one launch or (together
+// false) one each.
+struct TwoPlan {
+    GemmPlan x, y;
+    bool together, split, swap;  // split: every tile among the pairs of a cluster
+    int bonus;                   // see Work
+};
+
+static TwoPlan plan_two(const DenseJob &x, const DenseJob &y, long long pairs) {
     const GemmPlan ax = plan_gemm(x, (int)pairs), ay = plan_gemm(y, (int)pairs);
     const double apart = ax.cycles + ay.cycles + 6500.0;
     // together with every tile split among a cluster's pairs
@@ -1097,28 +1087,67 @@ rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const Bia
     const double together = late_end > early_end ? late_end : early_end;
     const bool one = together * 1.03 < apart && together <= split_cycles;
     const bool split = split_cycles < apart && !one;
-    if (!(one || split) || !x.out[0] || !y.out[0]) {
+    const bool both = one || split;
+    return {one ? px : split ? sx : ax, one ? py : split ? sy : ay, both, split, swap && one, bonus};
+}
+
+rvq_status launch_dense_gemm_two(const DenseJob &x, const DenseJob &y, const BiasSums &sums,
+                                 cudaStream_t stream) {
+    const long long pairs = num_sms() / 2;
+    if (dense_stream_fits(x) || dense_stream_fits(y)) {
+        // few tokens: each its own way, the bias gradients beside the tiled one
+        const DenseJob *jobs[2] = {&x, &y};
+        bool added = !sums.wanted();
+        for (int i = 1; i >= 0; --i) {
+            const DenseJob &j = *jobs[i];
+            if (!j.out[0]) continue;
+            if (dense_stream_fits(j)) {
+                RVQ_TRY(launch_dense_stream(j, stream));
+            } else {
+                RVQ_TRY(launch_one(j, plan_gemm(j, (int)pairs), added ? BiasSums{} : sums, stream));
+                added = true;
+            }
+        }
+        return added ? RVQ_OK : launch_bias_sums(sums, stream);
+    }
+    const TwoPlan t = plan_two(x, y, pairs);
+    if (!t.together || !x.out[0] || !y.out[0]) {
         // a product wanted alone is cut as it would be beside the other: the same sums
-        const GemmPlan &lx = one ? px : split ? sx : ax, &ly = one ? py : split ? sy : ay;
-        if (x.out[0]) RVQ_TRY(launch_one(x, lx, y.out[0] ? BiasSums{} : sums, stream));
-        if (y.out[0]) return launch_one(y, ly, sums, stream);
+        if (x.out[0]) RVQ_TRY(launch_one(x, t.x, y.out[0] ? BiasSums{} : sums, stream));
+        if (y.out[0]) return launch_one(y, t.y, sums, stream);
         return !x.out[0] && sums.wanted() ? launch_bias_sums(sums, stream) : RVQ_OK;
     }
-    if (split) {
-        GemmParams<2> p = {};
-        RVQ_TRY(fill_args(x, sx, p.g[0], p.a[0], p.b[0]));
-        RVQ_TRY(fill_args(y, sy, p.g[1], p.a[1], p.b[1]));
-        p.split = sx.split;
-        p.sums = sums;
-        return launch_products<false, 2, true>(p, stream);
-    }
+    const DenseJob &j0 = t.swap ? y : x, &j1 = t.swap ? x : y;
     GemmParams<2> p = {};
-    RVQ_TRY(fill_args(swap ? y : x, p0, p.g[0], p.a[0], p.b[0]));
-    RVQ_TRY(fill_args(swap ? x : y, p1, p.g[1], p.a[1], p.b[1]));
-    p.bonus = bonus;
+    RVQ_TRY(fill_args(j0, t.swap ? t.y : t.x, p.g[0], p.a[0], p.b[0]));
+    RVQ_TRY(fill_args(j1, t.swap ? t.x : t.y, p.g[1], p.a[1], p.b[1]));
     p.sums = sums;
-    p.split = 1;
-    return launch_products<false, 2, false>(p, stream);
+    p.split = t.x.split;
+    p.bonus = t.bonus;
+    return t.split ? launch_products<false, 2, true>(p, stream)
+                   : launch_products<false, 2, false>(p, stream);
+}
+
+void dense_plan_of(const DenseJob &x, const DenseJob *y, int32_t (&out)[7]) {
+    const int pairs = num_sms() / 2;
+    const auto way = [](const DenseJob &j, const GemmPlan &p, int32_t *o) {
+        const bool streamed = dense_stream_fits(j);
+        o[0] = streamed ? MOE_WAY_STREAM
+               : p.split > 1 ? MOE_WAY_SPLIT
+               : p.parts > 1 ? MOE_WAY_PARTS : MOE_WAY_TILES;
+        o[1] = streamed ? 0 : p.split > 1 ? p.split : p.parts;
+        o[2] = streamed ? 0 : p.tile_n;
+    };
+    for (int32_t &v : out) v = 0;
+    if (y == nullptr || dense_stream_fits(x) || dense_stream_fits(*y)) {
+        way(x, plan_gemm(x, pairs), out + 1);
+        if (y) way(*y, plan_gemm(*y, pairs), out + 4);
+        return;
+    }
+    const TwoPlan t = plan_two(x, *y, pairs);
+    out[0] = t.together;
+    way(x, t.x, out + 1);
+    way(*y, t.y, out + 4);
 }
 
 }  // namespace rvq

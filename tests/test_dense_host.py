@@ -344,3 +344,19 @@ def test_columns_of_one_wider_matrix_do_not_overlap():
     for bad in (dict(dwu=F + 112), dict(dwu=F + 144), dict(dx=C + 128, lddx=128),
                 dict(dwg=C, dwu=F)):
         assert lib.moe_gated_linear_backward(*{**both, **bad}.values()) == EINVAL, bad
+
+
+def test_plan_of_a_product():
+    """What the planner says without a GPU: shapes are checked, decode batches stream
+    the weights, many tokens take whole tiles, gradients report both products."""
+    out = (ctypes.c_int32 * 7)()
+    for bad in ((0, 0, 0, 8, 8), (0, 1, 1, 12, 8), (1, 0, 1, 8, 0)):
+        assert lib.rvq_selftest_dense_plan(*bad, out) == EINVAL
+    assert lib.rvq_selftest_dense_plan(0, 0, 1, 8, 8, None) == EINVAL
+    for gated in (False, True):
+        assert rvq.rvq_selftest_dense_plan(gated, False, 1, 2048, 7168) == (False, [("stream", 0, 0)])
+        joint, ((way, cut, cols),) = rvq.rvq_selftest_dense_plan(gated, False, 4096, 2048, 7168)
+        assert (joint, way, cut) == (False, "tiles", 1) and cols % 32 == 0
+        joint, ways = rvq.rvq_selftest_dense_plan(gated, True, 1, 2048, 7168)
+        assert not joint and [w[0] for w in ways] == ["stream", "tiles"]
+        assert len(rvq.rvq_selftest_dense_plan(gated, True, 4096, 2048, 7168)[1]) == 2

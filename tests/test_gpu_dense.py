@@ -603,3 +603,59 @@ def test_columns_of_one_wider_matrix(n):
     for a, b in ((dw[:, :cols], dw[:, cols:]), apart):
         rvq.moe_gated_linear_backward(res, xs, wg, wu, pre, n, rows, cols, ws, dwg=a, dwu=b)
     assert torch.equal(dw, torch.cat(apart, 1))
+
+
+# Every way of computing a product, and every pairing of ways of dx and dw that is not
+# rare, at sizes that are not near another way: (n, rows, cols), whether dx and dw share
+# a launch, and each product's way with the CTA pairs that split a tile.
+FORWARD_WAYS = [
+    (False, (7, 256, 512), "stream", 0), (False, (256, 512, 256), "tiles", 0),
+    (False, (66, 8, 3968), "parts", 0), (False, (5300, 8, 872), "split", 2),
+    (False, (50, 8, 864), "split", 4), (False, (250, 472, 1240), "split", 4),
+    (True, (7, 256, 512), "stream", 0), (True, (256, 512, 256), "tiles", 0),
+    (True, (71, 8, 2056), "parts", 0), (True, (257, 520, 4096), "parts", 0),
+    (True, (69, 8, 752), "split", 2), (True, (113, 512, 1024), "split", 2)]
+GRADIENT_WAYS = [
+    (False, (31, 72, 1000), False, ("stream", 0), ("tiles", 0)),
+    (False, (129, 264, 136), True, ("tiles", 0), ("tiles", 0)),
+    (False, (709, 200, 8), True, ("split", 2), ("split", 2)),
+    (False, (487, 928, 256), True, ("split", 4), ("split", 4)),
+    (False, (3864, 3720, 312), False, ("parts", 0), ("parts", 0)),
+    (False, (829, 5536, 8), False, ("parts", 0), ("split", 2)),
+    (False, (70, 3112, 8), False, ("parts", 0), ("tiles", 0)),
+    (False, (67, 1968, 8), False, ("split", 4), ("tiles", 0)),
+    (False, (3062, 8, 8), False, ("tiles", 0), ("parts", 0)),
+    (False, (1865, 8, 8), False, ("tiles", 0), ("split", 4)),
+    (True, (31, 72, 1000), False, ("stream", 0), ("tiles", 0)),
+    (True, (129, 264, 136), True, ("tiles", 0), ("tiles", 0)),
+    (True, (256, 512, 256), True, ("split", 2), ("split", 2)),
+    (True, (709, 200, 8), True, ("split", 4), ("split", 4)),
+    (True, (3506, 2848, 8), False, ("parts", 0), ("parts", 0)),
+    (True, (707, 2864, 8), False, ("parts", 0), ("split", 2)),
+    (True, (71, 1616, 8), False, ("parts", 0), ("tiles", 0)),
+    (True, (65, 904, 8), False, ("split", 4), ("tiles", 0)),
+    (True, (3711, 360, 688), False, ("tiles", 0), ("parts", 0)),
+    (True, (1865, 8, 8), False, ("tiles", 0), ("split", 4))]
+
+
+def pairs_of(way):
+    return way[0], way[1] if way[0] == "split" else 0
+
+
+@pytest.mark.parametrize("gated,size,way,pairs", FORWARD_WAYS)
+def test_forward_ways(gated, size, way, pairs):
+    """The way is the one that the size is here for, and its results are right."""
+    _, (w,) = rvq.rvq_selftest_dense_plan(gated, False, *size)
+    assert pairs_of(w) == (way, pairs)
+    test_every_way_of_a_product(*size)
+
+
+@pytest.mark.parametrize("gated,size,joint,dx,dw", GRADIENT_WAYS)
+def test_gradient_ways(gated, size, joint, dx, dw):
+    together, ways = rvq.rvq_selftest_dense_plan(gated, True, *size)
+    assert together == joint and [pairs_of(w) for w in ways] == [dx, dw]
+    if gated:
+        test_gated_gradients(*size)
+    else:
+        linear_train(*size, BF if size[0] % 2 else HF, "silu", True, alpha=0.5, extra=8,
+                     seed=size[0])
