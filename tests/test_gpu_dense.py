@@ -659,3 +659,44 @@ def test_gradient_ways(gated, size, joint, dx, dw):
     else:
         linear_train(*size, BF if size[0] % 2 else HF, "silu", True, alpha=0.5, extra=8,
                      seed=size[0])
+
+
+def test_two_streams_at_once():
+    """Calls of several ways on two streams with a workspace each, in flight together."""
+    sizes = [(1, 2048, 2048), (40, 1000, 1736), (300, 520, 2048), (900, 1000, 1096)]
+    g = gen(11)
+    jobs = []
+    for n, rows, cols in sizes:
+        x, dout = normal(g, (n, cols), BF), normal(g, (n, rows), BF)
+        wg, wu = (normal(g, (rows, cols), BF, cols ** -0.5) for _ in range(2))
+        jobs.append((n, rows, cols, x, wg, wu, dout, [workspace(n, rows, cols, True)
+                                                     for _ in range(2)]))
+
+    def outputs(n, rows, cols):
+        return [torch.zeros(s, dtype=t, device=DEV) for s, t in
+                (((n, rows), BF), ((2, n, rows), F32), ((n, cols), BF), ((rows, cols), BF),
+                 ((rows, cols), BF))]
+
+    def step(job, i, o, stream=None):
+        n, rows, cols, x, wg, wu, dout, ws = job
+        rvq.moe_gated_linear(x, wg, wu, n, rows, cols, o[0], ws[i], pre=o[1], stream=stream)
+        rvq.moe_gated_linear_backward(dout, x, wg, wu, o[1], n, rows, cols, ws[i], dx=o[2],
+                                      dwg=o[3], dwu=o[4], stream=stream)
+
+    want = [outputs(*j[:3]) for j in jobs]
+    for j, o in zip(jobs, want):
+        step(j, 0, o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[outputs(*j[:3]) for j in jobs] for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for k in range(len(jobs)):
+            for i, s in enumerate(streams):
+                m = (k + i) % len(jobs)     # different calls at the same time
+                step(jobs[m], i, got[i][m], s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j, a, b in zip(jobs, got[i], want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b)), (i, j[:3])
+            assert rvq.rvq_ws_status(j[7][i]) == (0, 0)

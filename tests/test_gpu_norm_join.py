@@ -437,3 +437,14 @@ def test_join_gradients_of_any_scale(n, d, scale):
     R.check(dy, (e, err), "dy")
     t = dxn.double() * ho * r
     R.check(dw, (t.sum(0), (80 + n) * U * t.abs().sum(0)), "dw_pre")
+
+
+@pytest.mark.parametrize("d,wdt", [(5632, F32), (6144, F32), (6152, F32), (7168, BF), (7176, BF)])
+def test_join_where_the_ring_gets_shorter(d, wdt):
+    """fp32 rows at the ends of two of them in shared memory for the gradients: 6144
+    columns with fp32 gains and 16-bit xn, 7168 with 16-bit gains."""
+    n = 320
+    for xdt in (BF, F32):
+        s = make(n, d, F32, F32, wdt, "token", True, seed=d)
+        rstd = check_forward(s, n, d, 1.0, True, F32, xdt)
+        check_backward(s, n, d, 1.0, True, F32, F32, xdt, wdt, rstd)
