@@ -591,7 +591,8 @@ rvq_status moe_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t
  * dout [n][rows]; dx [n][cols], dw [rows][cols], dbias [rows], all of dt, each
  * NULL when not wanted (one at least is).  The gradient of the residual is dout
  * itself.  pre: as written by the forward call (NULL for MOE_ACT_NONE).  With
- * an activation dp is rounded to dt once as an operand of the products.
+ * an activation dp is rounded to dt once as an operand of the products (fp16: a dp
+ * beyond 65504 becomes infinite there, as any fp16 gradient does; scale dout).
  * The gradients overlap neither each other nor dout, nor w (with dx), nor x
  * (with dw): the products may run in one launch (EINVAL). */
 rvq_status moe_linear_backward(const void *dout_dev, int64_t lddo, const void *x_dev, int64_t ldx,
@@ -618,7 +619,8 @@ rvq_status moe_gated_linear(const void *x_dev, int64_t ldx, const void *wg_dev,
                             void *ws_dev, size_t ws_bytes, rvq_stream_t stream);
 
 /* Gradients of moe_gated_linear, with dg = dout * u * act'(g) and
- * du = dout * act(g) (each rounded to dt once as an operand of the products):
+ * du = dout * act(g) (each rounded to dt once as an operand of the products, as dp
+ * of moe_linear_backward):
  *   dx = dg wg + du wu, dwg = dg^T x, dwu = du^T x, dbg, dbu = sums over t
  * Outputs are NULL when not wanted; dwg and dwu go together (one pitch lddw).
  * The gradients overlap neither each other, nor wg and wu (with dx), nor x (with

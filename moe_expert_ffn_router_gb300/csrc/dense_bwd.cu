@@ -1,6 +1,11 @@
 // Elementwise gradients in front of the backward products of moe_linear and
 // moe_gated_linear, with the bias gradients' sums over tokens.
 //
+// dp is rounded to 16 bits here, once: the products' operands are of one 16-bit type,
+// and dp in two such parts would double their time.  It is the second of the two
+// roundings of dx and dw (error against 64 bits 2.4e-3 in bf16, 1.7e-3 with the last
+// rounding alone); bias gradients are summed before it.
+//
 // Memory-bound (4096 x 2048, gated: 117 MB in 20 us, 5.9 TB/s; 1777 x 4104 with GELU:
 // 58 MB in 15 us): dout and the saved fp32 pre-activations are read once, dp is
 // written once, 16 or 32 bytes per thread and access.  A block takes 32 rows x

@@ -759,14 +759,16 @@ struct GemmPlan {
 
 // Cycles of a 64-deep slice of a 256 x tile_n tile: the MMAs' 2 per column, or, for
 // narrower tiles, the issue and the operand fill (measured 508 at 128 columns, 530
-// at 192 and 224).
+// at 192 and 224).  Of rows on 128-byte lines: others touch five 32-byte sectors for
+// every four (663 at 256 columns), which the model leaves out.
 double slice_cycles(int tile_n) {
     const double fill = 460.0 + 0.375 * tile_n;
     return 2.0 * tile_n > fill ? 2.0 * tile_n : fill;
 }
 
 // A tile's share of a pair's time: its slices, or, of a short depth, its outputs'
-// way out, which the next tile's slices would have hidden.
+// way out, which the next tile's slices would have hidden (18 cycles a column for a
+// plain 16-bit output; pre, an activation and a residual take more, left out).
 double tile_cycles(int slices, int tile_n) {
     const double in = slices * slice_cycles(tile_n) + 600.0, out = 18.0 * tile_n;
     return in > out ? in : out;

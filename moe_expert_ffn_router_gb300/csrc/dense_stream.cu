@@ -309,7 +309,8 @@ int stream_tiles(const DenseJob &j) {
 
 // Up to how many tokens the stream of weights beats the tiled product (measured,
 // us, stream / tiled: gated 7168 -> 2048, 192 tokens 20.5 / 21.8, 256 23.9 / 22.2;
-// gated 1736 -> 1000, 128 8.7 / 9.9, 192 10.7 / 10.4; plain 2048 -> 7168, 96 12.8 /
+// gated 1736 -> 1000, 128 8.7 / 9.9, 192 10.7 / 10.4, which one limit for every gated
+// product gives away; plain 2048 -> 7168, 96 12.8 /
 // 13.6, 128 14.3 / 13.6; 1736 -> 4104, 128 11.4 / 12.1; 512 -> 2048, 48 4.9 / 5.0,
 // 64 5.4 / 5.0; gradient of the input, 7168 x 2048, 1 9.4 / 15.2, 96 15.9 / 15.9).
 // 64 tokens is the end for few rows, which are split eightfold up to there (7168 ->

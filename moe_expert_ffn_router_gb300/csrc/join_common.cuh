@@ -14,8 +14,9 @@
 // 5.7 TB/s) and 26 us (bf16: 118 MB, 4.5 TB/s), of 4099 x 2048 (bf16) 16 us; forward and
 // gradients 126, 82 and 45 us.  The forward call is bound by memory; the gradients
 // by issue and latency (57 % of the issue slots with 16 warps an SM; the sums over
-// rows hold up to 48 registers a thread), of fp32 rows past 6400 columns by copies
-// that wait for the row before.
+// rows hold up to 48 registers a thread), of long fp32 rows by copies that wait
+// for the row before, where two rows do not fit (join_ring): past 6144 columns with
+// fp32 gains and a 16-bit xn, 7168 with 16-bit gains too.
 #pragma once
 
 #include <type_traits>
