@@ -689,6 +689,62 @@ rvq_status moe_norm_join_backward(const void *dh_out_dev, const void *dxn_dev, r
                                   void *dw_pre_dev, void *ws_dev, size_t ws_bytes,
                                   rvq_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Microscaled operators: the dense operators above for matrices held in 8 or 4 bits
+ * (the pages have no counterpart; formats as in the Open Compute Project's
+ * "Microscaling Formats (MX)" specification, 1.0).  Blocks of 32 values along a row
+ * share a scale 2^(byte - 127); a value is its code times that scale.  A block with
+ * scale byte 255 is NaN.
+ *  - codes: uint8, row-major, columns padded to a multiple of 128 (the padding holds
+ *    zeros): one byte per MOE_MX_F8 value, one for two MOE_MX_F4 values, the lower
+ *    column in the lower half.  moe_mx_code_bytes(fmt, rows, cols) bytes.
+ *  - scales: uint8, in tiles of 128 rows x 4 blocks (128 columns), 512 bytes each;
+ *    tile (r / 128, c / 128) is number (r / 128) * ceil(cols / 128) + c / 128, and in it
+ *    row r, column c has byte (r % 32) * 16 + (r / 32 % 4) * 4 + c / 32 % 4.
+ *    moe_mx_scale_bytes(rows, cols) bytes.  Bytes of rows behind the last are neither
+ *    written nor used; those of padded columns are written (0).
+ * Both start on 32 bytes (EALIGN).  Rows from 1, columns multiples of 8, up to
+ * 2^24 - 256 each.  Other matrices have row pitches as in the dense operators.
+ * ------------------------------------------------------------------------ */
+typedef enum moe_mx {
+    MOE_MX_F8 = 0, /* e4m3: 4-bit exponent, 3-bit mantissa, up to 448           */
+    MOE_MX_F4 = 1  /* e2m1: 0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives      */
+} moe_mx;
+
+/* 0 for a shape or format that the calls refuse. */
+size_t moe_mx_code_bytes(moe_mx fmt, int32_t rows, int32_t cols);
+size_t moe_mx_scale_bytes(int32_t rows, int32_t cols);
+
+/* x [rows][cols] of xdt (fp32, bf16 or fp16) -> codes and scales.  With m the largest
+ * magnitude of a block, its scale is 2^(floor(log2 m) - 8) (F8) or 2^(floor(log2 m) - 2)
+ * (F4), at least 2^-127 (so too where m = 0); values over their scale are rounded to
+ * the nearest code, ties to even, and end at the largest one.  A block that holds a
+ * NaN or an infinity gets scale 255 and codes 0.  No sums: the result is exact.
+ * codes and scales overlap neither x nor each other (EINVAL). */
+rvq_status moe_mx_quantize(const void *x_dev, int64_t ldx, rvq_dtype xdt, int32_t rows,
+                           int32_t cols, moe_mx fmt, uint8_t *codes_dev, uint8_t *scales_dev,
+                           rvq_stream_t stream);
+
+/* The inverse: out [rows][cols] of odt = codes times scales (in fp32, rounded once). */
+rvq_status moe_mx_dequantize(const uint8_t *codes_dev, const uint8_t *scales_dev, moe_mx fmt,
+                             int32_t rows, int32_t cols, void *out_dev, rvq_dtype odt, int64_t ldo,
+                             rvq_stream_t stream);
+
+/* moe_norm_join with the normed rows microscaled on the way out: h_out as there, and
+ * codes, scales = moe_mx_quantize(norm(h_out) * w_pre), of the fp32 values.
+ *  - h_out and xn (those values in xdt, for a router or routed experts beside the
+ *    microscaled product) may be NULL; codes and scales ([n][d]) may not, and overlap
+ *    nothing.  Other arguments and overlaps as in moe_norm_join.
+ *  - rstd as there: moe_norm_join_backward takes it, with the gradient of the
+ *    microscaled rows in dxn (straight through the rounding). */
+rvq_status moe_norm_join_mx(const void *h_dev, rvq_dtype hdt, const void *y_dev, rvq_dtype ydt,
+                            int32_t n, int32_t d, float alpha, const void *gate_dev,
+                            moe_gate gate_kind, rvq_dtype gdt, int32_t post_norm,
+                            const void *w_post_dev, const void *w_pre_dev, rvq_dtype wdt, float eps,
+                            void *h_out_dev, void *xn_dev, rvq_dtype xdt, moe_mx fmt,
+                            uint8_t *codes_dev, uint8_t *scales_dev, float *rstd_dev,
+                            rvq_stream_t stream);
+
 /* How the current device computes the products of moe_linear or (gated)
  * moe_gated_linear, or (backward) those of their gradients, both wanted: lets a test
  * say which way it ran.  Launches nothing.  out[0]: 1 if dx and dw share a launch; then for

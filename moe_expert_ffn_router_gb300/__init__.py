@@ -28,6 +28,8 @@ MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = rang
 MOE_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU,
             "gelu": MOE_ACT_GELU, "gelu_tanh": MOE_ACT_GELU_TANH}
 MOE_WAYS = ("stream", "tiles", "parts", "split")
+MOE_MX_F8, MOE_MX_F4 = range(2)
+MOE_MX = {"f8": MOE_MX_F8, "f4": MOE_MX_F4}
 (MOE_GATE_NONE, MOE_GATE_SCALAR, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL) = range(5)
 DEV_ERR_INDEX, DEV_ERR_NONFINITE, DEV_ERR_CORRUPT, DEV_ERR_TIMEOUT = 1, 2, 4, 8
 STATUS = {0: "RVQ_OK", 1: "RVQ_EINVAL", 2: "RVQ_EALIGN", 3: "RVQ_ENOMEM", 4: "RVQ_ECORRUPT",
@@ -131,6 +133,12 @@ _SIGS = {
     "moe_norm_join_backward": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp,
                                       _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _sz, _vp]),
+    "moe_mx_code_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_mx_scale_bytes": (_sz, [_i32, _i32]),
+    "moe_mx_quantize": (_i32, [_vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "moe_mx_dequantize": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _vp]),
+    "moe_norm_join_mx": (_i32, [_vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _i32, _i32, _i32, _vp,
+                                _vp, _i32, _f32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp]),
     "rvq_selftest_dense_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
     "rvq_selftest_prefill_timeout": (_i32, [_BANKP, _vp, _sz, _vp]),
     "rvq_ws_clear": (_i32, [_vp, _vp]),
@@ -703,6 +711,66 @@ def moe_norm_join_backward(dh_out, dxn, y, n, d, rstd, ws, h=None, alpha=1.0, ga
         _raw_stream(stream))
     if rc:
         _check("moe_norm_join_backward", rc)
+
+
+# ------------------------------------------------------------------ microscaled operators
+
+def moe_mx_code_bytes(fmt, rows, cols) -> int:
+    return int(_lib.moe_mx_code_bytes(fmt, rows, cols))
+
+
+def moe_mx_scale_bytes(rows, cols) -> int:
+    return int(_lib.moe_mx_scale_bytes(rows, cols))
+
+
+def _mx(codes, scales, rows, cols, fmt, what):
+    """Addresses of a microscaled matrix's codes and scales (contiguous uint8 tensors
+    of their sizes, any shape), or (None, None)."""
+    if codes is None and scales is None:
+        return None, None
+    tiles = -(-cols // 128)
+    return (_vec(codes, rows * tiles * (64 if fmt == MOE_MX_F4 else 128), what, torch.uint8),
+            _vec(scales, -(-rows // 128) * tiles * 512, what + " scales", torch.uint8))
+
+
+def moe_mx_quantize(x, rows, cols, codes, scales, fmt=MOE_MX_F8, stream=None):
+    """codes, scales (uint8, moe_mx_code_bytes and moe_mx_scale_bytes long) = x [rows][cols]
+    in a microscaled format."""
+    px, ldx = _mat(x, rows, cols, "x")
+    pc, ps = _mx(codes, scales, rows, cols, fmt, "codes")
+    rc = _lib.moe_mx_quantize(px, ldx, _dt_any(x), rows, cols, fmt, pc, ps, _raw_stream(stream))
+    if rc:
+        _check("moe_mx_quantize", rc)
+
+
+def moe_mx_dequantize(codes, scales, rows, cols, out, fmt=MOE_MX_F8, stream=None):
+    """out [rows][cols] (bf16, fp16 or fp32) = the values of a microscaled matrix."""
+    pc, ps = _mx(codes, scales, rows, cols, fmt, "codes")
+    po, ldo = _mat(out, rows, cols, "out")
+    rc = _lib.moe_mx_dequantize(pc, ps, fmt, rows, cols, po, _dt_any(out), ldo,
+                                _raw_stream(stream))
+    if rc:
+        _check("moe_mx_dequantize", rc)
+
+
+def moe_norm_join_mx(y, n, d, h_out, codes, scales, fmt=MOE_MX_F8, xn=None, h=None, alpha=1.0,
+                     gate=None, post_norm=True, w_post=None, w_pre=None, eps=1e-6, rstd=None,
+                     stream=None):
+    """moe_norm_join whose normed rows go into a microscaled matrix (codes, scales), and
+    into xn too if it is given.  h_out may be None."""
+    nd = n * d
+    ho = h if h is not None else h_out
+    wdt = w_post if w_post is not None else w_pre
+    pc, ps = _mx(codes, scales, n, d, fmt, "codes")
+    rc = _lib.moe_norm_join_mx(
+        _vec(h, nd, "h"), _dt_any(ho), _vec(y, nd, "y"), _dt_any(y), n, d, alpha,
+        None if gate is None else gate.data_ptr(), _gate_kind(gate, n, d), _dt_any(gate),
+        int(post_norm), _vec(w_post, d, "w_post"),
+        _vec(w_pre, d, "w_pre", None if wdt is w_pre else wdt.dtype), _dt_any(wdt), eps,
+        _vec(h_out, nd, "h_out", None if ho is h_out else ho.dtype), _vec(xn, nd, "xn"),
+        _dt_any(xn), fmt, pc, ps, _vec(rstd, 2 * n, "rstd", torch.float32), _raw_stream(stream))
+    if rc:
+        _check("moe_norm_join_mx", rc)
 
 
 def rvq_ws_clear(ws, stream=None):

@@ -3,35 +3,11 @@
 // Host code only.
 #include <math.h>
 
-#include "dense.cuh"
+#include "arg_check.cuh"
 
 using namespace rvq;
 
-#define CHECK_ARG(cond, ...)          \
-    do {                              \
-        if (!(cond)) {                \
-            set_error(__VA_ARGS__);   \
-            return RVQ_EINVAL;        \
-        }                             \
-    } while (0)
-#define CHECK_ALIGN(p, who, what)                                                          \
-    do {                                                                                   \
-        if (((uintptr_t)(p) & 15u) != 0) {                                                 \
-            set_error("%s: %s %p is not 16-byte aligned", who, what, (const void *)(p));   \
-            return RVQ_EALIGN;                                                             \
-        }                                                                                  \
-    } while (0)
-
 namespace {
-
-constexpr int64_t kMaxLd = (int64_t)1 << 36;  // a tensor map's row pitch is below 2^40 bytes
-constexpr int32_t kMaxDim = (1 << 24) - 256;  // 65535 blocks of 256 columns
-
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
-bool dtype16(rvq_dtype t) { return t == RVQ_BF16 || t == RVQ_F16; }
-bool dtype_any(rvq_dtype t) { return t == RVQ_F32 || dtype16(t); }
-size_t elem_bytes(rvq_dtype t) { return t == RVQ_F32 ? 4 : 2; }
 
 bool dense_shape(int32_t n, int32_t rows, int32_t cols) {
     return n >= 1 && rows >= 8 && cols >= 8 && rows % 8 == 0 && cols % 8 == 0 && n <= kMaxDim &&
@@ -46,72 +22,6 @@ rvq_status check_dense_shape(const char *who, int32_t n, int32_t rows, int32_t c
     CHECK_ARG(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, "%s: activation %d", who, act);
     CHECK_ARG(dtype16(dt), "%s: dtype %d (bf16 or fp16)", who, (int)dt);
     return RVQ_OK;
-}
-
-// A row-major matrix: not NULL, 16-byte aligned, pitch >= columns and a
-// multiple of 8 elements.
-rvq_status check_matrix(const char *who, const char *what, const void *p, int64_t ld,
-                        int32_t cols) {
-    CHECK_ARG(p != nullptr, "%s: null %s", who, what);
-    CHECK_ARG(ld >= cols && ld % 8 == 0 && ld < kMaxLd,
-              "%s: %s row pitch %lld for %d columns (>= columns, a multiple of 8)", who, what,
-              (long long)ld, cols);
-    CHECK_ALIGN(p, who, what);
-    return RVQ_OK;
-}
-
-rvq_status check_ws(const char *who, const void *ws, size_t bytes, size_t need) {
-    CHECK_ARG(ws != nullptr && ((uintptr_t)ws & 255u) == 0,
-              "%s: workspace must be 256-byte aligned and not null", who);
-    if (bytes < need) {
-        set_error("%s: workspace %zu < %zu bytes", who, bytes, need);
-        return RVQ_ENOMEM;
-    }
-    return RVQ_OK;
-}
-
-// Two row-major matrices do not overlap.
-bool disjoint(const void *a, int64_t lda, int32_t ra, int32_t ca, size_t ea, const void *b,
-              int64_t ldb, int32_t rb, int32_t cb, size_t eb) {
-    if (a == nullptr || b == nullptr) return true;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    const uintptr_t a1 = a0 + ((uint64_t)(ra - 1) * (uint64_t)lda + (uint64_t)ca) * ea;
-    const uintptr_t b1 = b0 + ((uint64_t)(rb - 1) * (uint64_t)ldb + (uint64_t)cb) * eb;
-    if (a1 <= b0 || b1 <= a0) return true;
-    // of one row pitch, in different columns: parts of one wider matrix
-    const uint64_t wa = (uint64_t)ca * ea, wb = (uint64_t)cb * eb;
-    const uint64_t pa = (uint64_t)lda * ea, pb = (uint64_t)ldb * eb;
-    const uint64_t pitch = ra > 1 ? pa : pb;
-    if ((ra > 1 && rb > 1 && pa != pb) || pitch == 0) return false;
-    const uint64_t at = b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;
-    return at >= wa && at + wb <= pitch;
-}
-
-// A row-major matrix, or (vector()) contiguous values; NULL: absent.
-struct Span {
-    const void *p;
-    int64_t ld;
-    int32_t rows, cols;
-    size_t e;
-};
-
-Span vector(const void *p, int32_t n, size_t e) { return {p, n, 1, n, e}; }
-
-bool apart(const Span &a, const Span &b) {
-    return disjoint(a.p, a.ld, a.rows, a.cols, a.e, b.p, b.ld, b.rows, b.cols, b.e);
-}
-
-// Outputs that one launch may write while it reads the inputs: none overlaps an
-// input or another output.
-template <int O, int I>
-bool all_apart(const Span (&out)[O], const Span (&in)[I]) {
-    for (int o = 0; o < O; ++o) {
-        for (int i = 0; i < I; ++i)
-            if (!apart(out[o], in[i])) return false;
-        for (int i = 0; i < o; ++i)
-            if (!apart(out[o], out[i])) return false;
-    }
-    return true;
 }
 
 // Workspace: status | partial sums of split products | and for a gradient dp
@@ -470,53 +380,6 @@ rvq_status rvq_selftest_dense_plan(int32_t gated, int32_t backward, int32_t n, i
 
 // ---------------------------------------------------------------- norm join
 
-static rvq_status check_join(const char *who, const void *h, rvq_dtype hdt, const void *y,
-                             rvq_dtype ydt, int32_t n, int32_t d, const void *gate, int kind,
-                             rvq_dtype gdt, int32_t post_norm, const void *w_post,
-                             const void *w_pre, rvq_dtype wdt, rvq_dtype xdt) {
-    CHECK_ARG(n >= 1 && n <= kMaxDim && d >= 8 && d % 8 == 0 && d <= kJoinMaxD,
-              "%s: n %d, d %d (n from 1 to 2^24 - 256; d a multiple of 8, at most %d)", who, n, d,
-              kJoinMaxD);
-    CHECK_ARG(dtype_any(hdt) && dtype_any(ydt) && dtype_any(gdt) && dtype_any(wdt) &&
-                  dtype_any(xdt),
-              "%s: dtypes %d, %d, %d, %d, %d", who, (int)hdt, (int)ydt, (int)gdt, (int)wdt,
-              (int)xdt);
-    CHECK_ARG(y != nullptr, "%s: null y", who);
-    CHECK_ARG(kind >= MOE_GATE_NONE && kind <= MOE_GATE_FULL && (kind == MOE_GATE_NONE) == !gate,
-              "%s: gate kind %d %s a gate", who, kind, gate ? "with" : "without");
-    CHECK_ARG(post_norm || !w_post, "%s: w_post without post_norm", who);
-    CHECK_ALIGN(h, who, "h");
-    CHECK_ALIGN(y, who, "y");
-    CHECK_ALIGN(gate, who, "gate");
-    CHECK_ALIGN(w_post, who, "w_post");
-    CHECK_ALIGN(w_pre, who, "w_pre");
-    return RVQ_OK;
-}
-
-// A tensor of the join: n rows of d values, or values over tokens or channels
-// (len); kept apart from others, or over rows of its own type.
-struct JoinSpan {
-    const void *p;
-    rvq_dtype dt;
-    int32_t rows, cols;
-};
-
-static bool apart(const JoinSpan &a, const JoinSpan &b) {
-    return disjoint(a.p, a.cols, a.rows, a.cols, elem_bytes(a.dt), b.p, b.cols, b.rows, b.cols,
-                    elem_bytes(b.dt));
-}
-
-// Every block reads its rows before it writes them: an output may take the place of
-// rows of the same type.
-static bool same_or_apart(const JoinSpan &a, const JoinSpan &b) {
-    return (a.p == b.p && a.dt == b.dt && a.rows == b.rows && a.cols == b.cols) || apart(a, b);
-}
-
-static JoinSpan gate_span(const void *p, rvq_dtype dt, int kind, int32_t n, int32_t d) {
-    return {p, dt, kind == MOE_GATE_TOKEN || kind == MOE_GATE_FULL ? n : 1,
-            kind == MOE_GATE_CHANNEL || kind == MOE_GATE_FULL ? d : 1};
-}
-
 rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rvq_dtype ydt,
                          int32_t n, int32_t d, float alpha, const void *gate_dev,
                          moe_gate gate_kind, rvq_dtype gdt, int32_t post_norm,
@@ -531,22 +394,12 @@ rvq_status moe_norm_join(const void *h_dev, rvq_dtype hdt, const void *y_dev, rv
     CHECK_ALIGN(h_out_dev, who, "h_out");
     CHECK_ALIGN(xn_dev, who, "xn");
     CHECK_ALIGN(rstd_dev, who, "rstd");
-    const JoinSpan out[] = {{h_out_dev, hdt, n, d}, {xn_dev, xdt, n, d}};
-    const JoinSpan rstd = {rstd_dev, RVQ_F32, 2, n};
-    const JoinSpan rows[] = {{h_dev, hdt, n, d}, {y_dev, ydt, n, d},
-                             gate_span(gate_dev, gdt, (int)gate_kind, n, d)};
-    const JoinSpan gains[] = {{w_post_dev, wdt, 1, d}, {w_pre_dev, wdt, 1, d}};
-    bool ok = apart(out[0], out[1]);
-    for (const JoinSpan &o : out) {
-        for (const JoinSpan &r : rows)
-            ok = ok && (r.rows == n && r.cols == d ? same_or_apart(o, r) : apart(o, r));
-        for (const JoinSpan &g : gains) ok = ok && apart(o, g);
-        ok = ok && apart(o, rstd);
-    }
-    for (const JoinSpan &r : rows) ok = ok && apart(rstd, r);
-    for (const JoinSpan &g : gains) ok = ok && apart(rstd, g);
-    CHECK_ARG(ok, "%s: an output overlaps an input of another type or place, or another output",
-              who);
+    const JoinSpan in[] = {{h_dev, hdt, n, d}, {y_dev, ydt, n, d},
+                           gate_span(gate_dev, gdt, (int)gate_kind, n, d),
+                           {w_post_dev, wdt, 1, d}, {w_pre_dev, wdt, 1, d}};
+    CHECK_ARG(join_outputs_ok(in, {h_out_dev, hdt, n, d}, {xn_dev, xdt, n, d},
+                              {rstd_dev, RVQ_F32, 2, n}),
+              "%s: an output overlaps an input of another type or place, or another output", who);
     JoinJob j = {};
     j.n = n;
     j.d = d;

@@ -1,0 +1,129 @@
+"""Host side of the microscaled operators (no GPU): sizes and refusals before any
+launch, in the library and in the binding; the tests' own definition of the formats."""
+import pytest
+import torch
+
+import moe_expert_ffn_router_gb300 as rvq
+from tests import mx_ref as X
+
+lib = rvq._lib
+A = 0x10000000       # fake, aligned "device" addresses far apart (never dereferenced)
+B, C, D, E_, F = (A + i * 0x10000000 for i in range(1, 6))
+OK, EINVAL, EALIGN, ENOMEM = 0, 1, 2, 3
+F32, BF16, F16 = 0, 1, 2
+F8, F4 = rvq.MOE_MX_F8, rvq.MOE_MX_F4
+
+
+def test_sizes():
+    assert rvq.moe_mx_code_bytes(F8, 1, 8) == 128 and rvq.moe_mx_code_bytes(F4, 1, 8) == 64
+    assert rvq.moe_mx_code_bytes(F8, 5, 136) == 5 * 256
+    assert rvq.moe_mx_code_bytes(F4, 2048, 7168) == 2048 * 3584
+    assert rvq.moe_mx_scale_bytes(1, 8) == 512 and rvq.moe_mx_scale_bytes(129, 136) == 4 * 512
+    assert rvq.moe_mx_scale_bytes(2048, 7168) == 2048 * 7168 // 32
+    # past 2^31 and 2^32 bytes
+    assert rvq.moe_mx_code_bytes(F8, 1 << 20, 1 << 16) == 1 << 36
+    for r, c in ((0, 8), (-1, 8), (1, 0), (1, 12), (1 << 24, 8), (1, 1 << 24), (1 << 23, 1 << 23)):
+        assert rvq.moe_mx_code_bytes(F8, r, c) == 0 and rvq.moe_mx_scale_bytes(r, c) == 0
+    assert rvq.moe_mx_code_bytes(2, 1, 8) == 0
+
+
+def test_quantize_refusals():
+    base = dict(x=A, ldx=64, xdt=BF16, rows=4, cols=64, fmt=F8, codes=B, scales=C, st=None)
+
+    def q(**kw):
+        return lib.moe_mx_quantize(*{**base, **kw}.values())
+
+    for bad in (dict(rows=0), dict(cols=60), dict(cols=0), dict(xdt=3), dict(x=None), dict(ldx=56),
+                dict(ldx=65), dict(fmt=2), dict(fmt=-1), dict(codes=None), dict(scales=None),
+                dict(codes=A), dict(scales=A + 480), dict(scales=B + 512 - 32),
+                dict(codes=A - 4 * 128 + 32), dict(codes=C + 480)):
+        assert q(**bad) == EINVAL, bad
+    for bad in (dict(x=A + 8), dict(codes=B + 16), dict(scales=C + 16)):
+        assert q(**bad) == EALIGN, bad
+    assert b"aligned" in lib.rvq_last_error()
+
+
+def test_dequantize_refusals():
+    base = dict(codes=A, scales=B, fmt=F4, rows=4, cols=64, out=C, odt=BF16, ldo=64, st=None)
+
+    def q(**kw):
+        return lib.moe_mx_dequantize(*{**base, **kw}.values())
+
+    for bad in (dict(rows=0), dict(cols=4), dict(odt=9), dict(out=None), dict(ldo=32), dict(fmt=7),
+                dict(codes=None), dict(scales=None), dict(out=A + 192), dict(out=B)):
+        assert q(**bad) == EINVAL, bad
+    for bad in (dict(out=C + 8), dict(codes=A + 16), dict(scales=B + 8)):
+        assert q(**bad) == EALIGN, bad
+
+
+def test_join_refusals():
+    base = dict(h=A, hdt=F32, y=B, ydt=BF16, n=4, d=64, alpha=1.0, gate=None, kind=0, gdt=F32,
+                post=1, wpost=None, wpre=None, wdt=F32, eps=1e-6, ho=C, xn=D, xdt=BF16, fmt=F8,
+                codes=E_, scales=F, rstd=None, st=None)
+
+    def join(**kw):
+        return lib.moe_norm_join_mx(*{**base, **kw}.values())
+
+    for bad in (dict(n=0), dict(d=60), dict(d=16392), dict(hdt=3), dict(ydt=-1), dict(y=None),
+                dict(kind=2), dict(gate=E_, kind=0), dict(post=0, wpost=A + 0x100000),
+                dict(eps=-1.0), dict(eps=float("inf")), dict(fmt=3), dict(codes=None),
+                dict(scales=None), dict(ho=B), dict(xn=A), dict(ho=C, xn=C), dict(codes=A),
+                dict(codes=B), dict(codes=C), dict(codes=D), dict(scales=E_), dict(scales=C),
+                dict(rstd=C), dict(rstd=E_), dict(wpre=E_), dict(wpre=C),
+                dict(gate=F, kind=2), dict(ho=A + 16)):
+        assert join(**bad) == EINVAL, bad
+    for bad in (dict(h=A + 4), dict(y=B + 8), dict(ho=C + 8), dict(xn=D + 8), dict(codes=E_ + 16),
+                dict(scales=F + 16), dict(wpre=E_ + 0x100008), dict(rstd=A + 0x100004)):
+        assert join(**bad) == EALIGN, bad
+
+
+def test_binding_refusals():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    codes, scales = torch.zeros(512, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x: shape"):
+        rvq.moe_mx_quantize(x, 4, 72, codes, scales)
+    with pytest.raises(ValueError, match="codes"):
+        rvq.moe_mx_quantize(x, 4, 64, codes[:256], scales)
+    with pytest.raises(ValueError, match="codes scales"):
+        rvq.moe_mx_quantize(x, 4, 64, codes, scales[:256])
+    with pytest.raises(TypeError, match="codes"):
+        rvq.moe_mx_quantize(x, 4, 64, codes.view(torch.int8), scales)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        rvq.moe_mx_quantize(x.double(), 4, 64, codes, scales)
+    with pytest.raises(ValueError, match="contiguous"):
+        rvq.moe_mx_dequantize(codes, scales, 4, 64, x.t().contiguous().t())
+    with pytest.raises(ValueError, match="y"):
+        rvq.moe_norm_join_mx(x, 4, 128, None, codes, scales)
+
+
+def test_definition():
+    """The tests' formats: every value a fixed point, ties, ends, padding, layout."""
+    v4 = X.values(F4)
+    assert v4.tolist() == [0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6]
+    v8 = X.values(F8)
+    assert v8[126] == 448 and v8[1] == 2.0 ** -9 and torch.isnan(v8[127])
+    for t, v in ((torch.float8_e4m3fn, v8),):
+        assert torch.equal(torch.arange(256, dtype=torch.uint8).view(t).double().nan_to_num(-1),
+                           v.nan_to_num(-1))
+    for fmt, v in ((F8, v8), (F4, v4)):
+        f = v[torch.isfinite(v)]
+        assert torch.equal(X.round_code(f, fmt), f)
+    assert X.round_code(torch.tensor([.25, .75, 2.5, 3.5, 5., 7.]).double(), F4).tolist() == \
+        [0, 1, 2, 4, 4, 6]
+    x = torch.zeros((130, 136))
+    x[0, 0], x[1, 33], x[129, 135] = 3.0, -448.0, 2.0 ** -126
+    for fmt in (F8, F4):
+        q, b = X.quantize(x, fmt)
+        assert q.shape == (130, 256) and b.shape == (130, 8)
+        assert b[0, 0] == 1 - X.LEAD[fmt] + 127 and b[1, 1] == 8 - X.LEAD[fmt] + 127
+        assert b[129, 4] == 0 and b[2, 3] == 0
+        tiles = X.to_tiles(b)
+        assert tiles.numel() == rvq.moe_mx_scale_bytes(130, 136)
+        assert torch.equal(X.from_tiles(tiles, 130, 136), b)
+        assert tiles[(1 * 2 + 1) * 512 + 1 * 16 + 0] == b[129, 4]
+        codes = X.pack(q, fmt)
+        assert codes.numel() == rvq.moe_mx_code_bytes(fmt, 130, 136)
+        got = X.dequantize(codes.view(-1), tiles, 130, 136, fmt)
+        # 448 over its F4 scale is 7: ends at 6
+        assert got[0, 0] == 3 and got[1, 33] == (-448 if fmt == F8 else -384)
+        X.check_quantized(codes, tiles, 130, 136, fmt, x.double(), torch.zeros(130, 136), "self")
