@@ -730,6 +730,39 @@ rvq_status moe_mx_dequantize(const uint8_t *codes_dev, const uint8_t *scales_dev
                              int32_t rows, int32_t cols, void *out_dev, rvq_dtype odt, int64_t ldo,
                              rvq_stream_t stream);
 
+/* Workspaces of the products below, for up to n tokens.  0 for a shape they refuse. */
+size_t moe_mx_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols);
+size_t moe_mx_gated_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols);
+
+/* out[t][r] = residual[t][r] + alpha * act(sum_c x[t][c] w[r][c] + bias[r])
+ *  - x [n][cols] and w [rows][cols] microscaled, each in either format (two MOE_MX_F4
+ *    operands are multiplied at twice the rate); bias fp32 [rows] or NULL.
+ *  - residual [n][rows] of rdt, or NULL; out [n][rows] of odt; rdt and odt are fp32 or
+ *    16-bit (any mix).  out may alias residual if type and pitch agree (each element is
+ *    read before it is written) and overlaps nothing else (EINVAL).
+ * Products of codes are exact, sums are fp32 on the tensor cores, and each output is
+ * rounded once.  A block of NaN makes its token's (or its weight row's) outputs NaN. */
+rvq_status moe_mx_linear(const uint8_t *x_dev, const uint8_t *x_scales_dev, moe_mx xfmt,
+                         const uint8_t *w_dev, const uint8_t *w_scales_dev, moe_mx wfmt,
+                         const float *bias_dev, int32_t n, int32_t rows, int32_t cols, moe_act act,
+                         float alpha, const void *residual_dev, rvq_dtype rdt, int64_t ldr,
+                         void *out_dev, rvq_dtype odt, int64_t ldo, void *ws_dev, size_t ws_bytes,
+                         rvq_stream_t stream);
+
+/* The first half of a gated feed-forward block:
+ *   g = x wg^T + bg, u = x wu^T + bu, act(g) * u
+ * into out [n][rows] of odt (fp32 or 16-bit), or, with out NULL, microscaled in ofmt
+ * (codes, scales: moe_mx_quantize of the fp32 values) for the next product.
+ * wg and wu [rows][cols] share wfmt; bg, bu fp32 [rows] or NULL, each by itself.  The
+ * outputs overlap nothing (EINVAL). */
+rvq_status moe_mx_gated_linear(const uint8_t *x_dev, const uint8_t *x_scales_dev, moe_mx xfmt,
+                               const uint8_t *wg_dev, const uint8_t *wg_scales_dev,
+                               const uint8_t *wu_dev, const uint8_t *wu_scales_dev, moe_mx wfmt,
+                               const float *bg_dev, const float *bu_dev, int32_t n, int32_t rows,
+                               int32_t cols, moe_act act, void *out_dev, rvq_dtype odt, int64_t ldo,
+                               uint8_t *codes_dev, uint8_t *scales_dev, moe_mx ofmt, void *ws_dev,
+                               size_t ws_bytes, rvq_stream_t stream);
+
 /* moe_norm_join with the normed rows microscaled on the way out: h_out as there, and
  * codes, scales = moe_mx_quantize(norm(h_out) * w_pre), of the fp32 values.
  *  - h_out and xn (those values in xdt, for a router or routed experts beside the

@@ -137,6 +137,12 @@ _SIGS = {
     "moe_mx_scale_bytes": (_sz, [_i32, _i32]),
     "moe_mx_quantize": (_i32, [_vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
     "moe_mx_dequantize": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _vp]),
+    "moe_mx_linear_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_mx_gated_linear_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_mx_linear": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _f32,
+                             _vp, _i32, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
+    "moe_mx_gated_linear": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
+                                   _i32, _i32, _vp, _i32, _i64, _vp, _vp, _i32, _vp, _sz, _vp]),
     "moe_norm_join_mx": (_i32, [_vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _i32, _i32, _i32, _vp,
                                 _vp, _i32, _f32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp]),
     "rvq_selftest_dense_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
@@ -751,6 +757,53 @@ def moe_mx_dequantize(codes, scales, rows, cols, out, fmt=MOE_MX_F8, stream=None
                                 _raw_stream(stream))
     if rc:
         _check("moe_mx_dequantize", rc)
+
+
+def moe_mx_linear_workspace_bytes(n, rows, cols) -> int:
+    return int(_lib.moe_mx_linear_workspace_bytes(n, rows, cols))
+
+
+def moe_mx_gated_linear_workspace_bytes(n, rows, cols) -> int:
+    return int(_lib.moe_mx_gated_linear_workspace_bytes(n, rows, cols))
+
+
+def moe_mx_linear(x, x_scales, w, w_scales, n, rows, cols, out, ws, xfmt=MOE_MX_F8,
+                  wfmt=MOE_MX_F4, bias=None, act=MOE_ACT_NONE, alpha=1.0, residual=None,
+                  stream=None):
+    """out = residual + alpha * act(x w^T + bias) of microscaled x [n][cols] and w
+    [rows][cols] (codes and scales); bias fp32, out and residual [n][rows] in bf16, fp16
+    or fp32."""
+    px, pxs = _mx(x, x_scales, n, cols, xfmt, "x")
+    pw, pws = _mx(w, w_scales, rows, cols, wfmt, "w")
+    po, ldo = _mat(out, n, rows, "out")
+    pr, ldr = _mat(residual, n, rows, "residual")
+    rc = _lib.moe_mx_linear(px, pxs, xfmt, pw, pws, wfmt, _vec(bias, rows, "bias", torch.float32),
+                            n, rows, cols, act, alpha, pr, _dt_any(residual), ldr, po,
+                            _dt_any(out), ldo, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+    if rc:
+        _check("moe_mx_linear", rc)
+
+
+def moe_mx_gated_linear(x, x_scales, wg, wg_scales, wu, wu_scales, n, rows, cols, out, ws,
+                        xfmt=MOE_MX_F8, wfmt=MOE_MX_F4, bg=None, bu=None, act=MOE_ACT_SILU,
+                        out_scales=None, ofmt=MOE_MX_F8, stream=None):
+    """act(x wg^T + bg) * (x wu^T + bu) of microscaled matrices: into out [n][rows] (bf16,
+    fp16 or fp32), or, with out_scales, into out and out_scales as codes and scales."""
+    px, pxs = _mx(x, x_scales, n, cols, xfmt, "x")
+    pg, pgs = _mx(wg, wg_scales, rows, cols, wfmt, "wg")
+    pu, pus = _mx(wu, wu_scales, rows, cols, wfmt, "wu")
+    if out_scales is None:
+        po, ldo = _mat(out, n, rows, "out")
+        odt, pc, ps = _dt_any(out), None, None
+    else:
+        po, ldo, odt = None, 0, RVQ_F32
+        pc, ps = _mx(out, out_scales, n, rows, ofmt, "out")
+    rc = _lib.moe_mx_gated_linear(px, pxs, xfmt, pg, pgs, pu, pus, wfmt,
+                                  _vec(bg, rows, "bg", torch.float32),
+                                  _vec(bu, rows, "bu", torch.float32), n, rows, cols, act, po, odt,
+                                  ldo, pc, ps, ofmt, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+    if rc:
+        _check("moe_mx_gated_linear", rc)
 
 
 def moe_norm_join_mx(y, n, d, h_out, codes, scales, fmt=MOE_MX_F8, xn=None, h=None, alpha=1.0,

@@ -3,7 +3,7 @@
 #include <math.h>
 
 #include "arg_check.cuh"
-#include "mx.cuh"
+#include "mx_tc.cuh"
 
 using namespace rvq;
 
@@ -50,6 +50,35 @@ Span scales_of(const void *p, int32_t rows, int32_t cols) {
     return {p, kMxTileBytes, (int32_t)(mx_tiles(rows) * mx_tiles(cols)), kMxTileBytes, 1};
 }
 
+bool mx_product_shape(int32_t n, int32_t rows, int32_t cols) {
+    return mx_shape(n, cols) && mx_shape(rows, cols) && rows >= 8 && rows % 8 == 0 &&
+           mx_shape(n, rows);
+}
+
+rvq_status check_mx_product(const char *who, int32_t n, int32_t rows, int32_t cols, int act) {
+    CHECK_ARG(mx_product_shape(n, rows, cols),
+              "%s: n %d, rows %d, cols %d (n >= 1; rows and cols multiples of 8)", who, n, rows,
+              cols);
+    CHECK_ARG(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, "%s: activation %d", who, act);
+    return RVQ_OK;
+}
+
+MxJob mx_job(int mats, int32_t n, int32_t rows, int32_t cols, const uint8_t *x, const uint8_t *xs,
+             int xfmt, int wfmt, int act, void *ws) {
+    MxJob j = {};
+    j.mats = mats;
+    j.n = n;
+    j.rows = rows;
+    j.cols = cols;
+    j.x = x;
+    j.xs = xs;
+    j.xfmt = xfmt;
+    j.wfmt = wfmt;
+    j.act = act;
+    j.status = (uint32_t *)ws;
+    return j;
+}
+
 }  // namespace
 
 extern "C" {
@@ -92,6 +121,101 @@ rvq_status moe_mx_dequantize(const uint8_t *codes_dev, const uint8_t *scales_dev
     CHECK_ARG(all_apart(out, in), "%s: out overlaps the codes or scales", who);
     return launch_mx_dequantize({codes_dev, scales_dev, rows, cols, (int)fmt, out_dev, ldo, (int)odt},
                                 (cudaStream_t)stream);
+}
+
+size_t moe_mx_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols) {
+    return mx_product_shape(n, rows, cols) ? RVQ_WS_STATUS_BYTES : 0;
+}
+
+size_t moe_mx_gated_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols) {
+    return moe_mx_linear_workspace_bytes(n, rows, cols);
+}
+
+rvq_status moe_mx_linear(const uint8_t *x_dev, const uint8_t *x_scales_dev, moe_mx xfmt,
+                         const uint8_t *w_dev, const uint8_t *w_scales_dev, moe_mx wfmt,
+                         const float *bias_dev, int32_t n, int32_t rows, int32_t cols, moe_act act,
+                         float alpha, const void *residual_dev, rvq_dtype rdt, int64_t ldr,
+                         void *out_dev, rvq_dtype odt, int64_t ldo, void *ws_dev, size_t ws_bytes,
+                         rvq_stream_t stream) {
+    const char *who = "moe_mx_linear";
+    RVQ_TRY(check_mx_product(who, n, rows, cols, (int)act));
+    RVQ_TRY(check_mx(who, "x", x_dev, x_scales_dev, (int)xfmt));
+    RVQ_TRY(check_mx(who, "w", w_dev, w_scales_dev, (int)wfmt));
+    CHECK_ARG(dtype_any(odt), "%s: out dtype %d", who, (int)odt);
+    RVQ_TRY(check_matrix(who, "out", out_dev, ldo, rows));
+    if (residual_dev) {
+        CHECK_ARG(dtype_any(rdt), "%s: residual dtype %d", who, (int)rdt);
+        RVQ_TRY(check_matrix(who, "residual", residual_dev, ldr, rows));
+    }
+    CHECK_ALIGN(bias_dev, who, "bias");
+    const Span out[] = {{out_dev, ldo, n, rows, elem_bytes(odt)}};
+    const Span in[] = {codes_of(x_dev, (int)xfmt, n, cols), scales_of(x_scales_dev, n, cols),
+                       codes_of(w_dev, (int)wfmt, rows, cols), scales_of(w_scales_dev, rows, cols),
+                       vector(bias_dev, rows, 4)};
+    CHECK_ARG(all_apart(out, in), "%s: out overlaps an input", who);
+    CHECK_ARG((residual_dev == out_dev && rdt == odt && ldr == ldo) ||
+                  apart(out[0], {residual_dev, ldr, n, rows, elem_bytes(rdt)}),
+              "%s: out overlaps the residual with another type, place or pitch", who);
+    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, moe_mx_linear_workspace_bytes(n, rows, cols)));
+    MxJob j = mx_job(1, n, rows, cols, x_dev, x_scales_dev, (int)xfmt, (int)wfmt, (int)act, ws_dev);
+    j.w[0] = w_dev;
+    j.ws[0] = w_scales_dev;
+    j.bias[0] = bias_dev;
+    j.alpha = alpha;
+    j.residual = residual_dev;
+    j.rdt = (int)rdt;
+    j.ldr = ldr;
+    j.out = out_dev;
+    j.odt = (int)odt;
+    j.ldo = ldo;
+    return launch_mx_product(j, (cudaStream_t)stream);
+}
+
+rvq_status moe_mx_gated_linear(const uint8_t *x_dev, const uint8_t *x_scales_dev, moe_mx xfmt,
+                               const uint8_t *wg_dev, const uint8_t *wg_scales_dev,
+                               const uint8_t *wu_dev, const uint8_t *wu_scales_dev, moe_mx wfmt,
+                               const float *bg_dev, const float *bu_dev, int32_t n, int32_t rows,
+                               int32_t cols, moe_act act, void *out_dev, rvq_dtype odt, int64_t ldo,
+                               uint8_t *codes_dev, uint8_t *scales_dev, moe_mx ofmt, void *ws_dev,
+                               size_t ws_bytes, rvq_stream_t stream) {
+    const char *who = "moe_mx_gated_linear";
+    RVQ_TRY(check_mx_product(who, n, rows, cols, (int)act));
+    RVQ_TRY(check_mx(who, "x", x_dev, x_scales_dev, (int)xfmt));
+    RVQ_TRY(check_mx(who, "wg", wg_dev, wg_scales_dev, (int)wfmt));
+    RVQ_TRY(check_mx(who, "wu", wu_dev, wu_scales_dev, (int)wfmt));
+    CHECK_ARG((out_dev != nullptr) != (codes_dev != nullptr || scales_dev != nullptr),
+              "%s: either out or codes and scales", who);
+    if (out_dev) {
+        CHECK_ARG(dtype_any(odt), "%s: out dtype %d", who, (int)odt);
+        RVQ_TRY(check_matrix(who, "out", out_dev, ldo, rows));
+    } else {
+        RVQ_TRY(check_mx(who, "output", codes_dev, scales_dev, (int)ofmt));
+    }
+    CHECK_ALIGN(bg_dev, who, "bg");
+    CHECK_ALIGN(bu_dev, who, "bu");
+    const Span out[] = {{out_dev, ldo, n, rows, elem_bytes(odt)},
+                        codes_of(codes_dev, (int)ofmt, n, rows), scales_of(scales_dev, n, rows)};
+    const Span in[] = {codes_of(x_dev, (int)xfmt, n, cols), scales_of(x_scales_dev, n, cols),
+                       codes_of(wg_dev, (int)wfmt, rows, cols), scales_of(wg_scales_dev, rows, cols),
+                       codes_of(wu_dev, (int)wfmt, rows, cols), scales_of(wu_scales_dev, rows, cols),
+                       vector(bg_dev, rows, 4), vector(bu_dev, rows, 4)};
+    CHECK_ARG(all_apart(out, in), "%s: an output overlaps an input or another output", who);
+    RVQ_TRY(check_ws(who, ws_dev, ws_bytes, moe_mx_gated_linear_workspace_bytes(n, rows, cols)));
+    MxJob j = mx_job(2, n, rows, cols, x_dev, x_scales_dev, (int)xfmt, (int)wfmt, (int)act, ws_dev);
+    j.w[0] = wg_dev;
+    j.w[1] = wu_dev;
+    j.ws[0] = wg_scales_dev;
+    j.ws[1] = wu_scales_dev;
+    j.bias[0] = bg_dev;
+    j.bias[1] = bu_dev;
+    j.alpha = 1.f;
+    j.out = out_dev;
+    j.odt = (int)odt;
+    j.ldo = ldo;
+    j.codes = codes_dev;
+    j.scales = scales_dev;
+    j.ofmt = (int)ofmt;
+    return launch_mx_product(j, (cudaStream_t)stream);
 }
 
 rvq_status moe_norm_join_mx(const void *h_dev, rvq_dtype hdt, const void *y_dev, rvq_dtype ydt,

@@ -127,3 +127,78 @@ def test_definition():
         # 448 over its F4 scale is 7: ends at 6
         assert got[0, 0] == 3 and got[1, 33] == (-448 if fmt == F8 else -384)
         X.check_quantized(codes, tiles, 130, 136, fmt, x.double(), torch.zeros(130, 136), "self")
+
+
+def test_product_sizes():
+    for f in (rvq.moe_mx_linear_workspace_bytes, rvq.moe_mx_gated_linear_workspace_bytes):
+        for n, r, c in ((1, 8, 8), (7, 256, 512), (4096, 2048, 7168)):
+            assert f(n, r, c) >= 256
+        for n, r, c in ((0, 8, 8), (1, 12, 8), (1, 8, 12), (1, 0, 8), (-1, 8, 8), (1 << 24, 8, 8)):
+            assert f(n, r, c) == 0
+
+
+def test_linear_refusals():
+    base = dict(x=A, xs=B, xf=F8, w=C, wsc=D, wf=F4, bias=None, n=4, rows=32, cols=64, act=0,
+                alpha=1.0, res=None, rdt=F32, ldr=0, out=E_, odt=BF16, ldo=32, ws=F, wsb=1 << 20,
+                st=None)
+
+    def lin(**kw):
+        return lib.moe_mx_linear(*{**base, **kw}.values())
+
+    G = F + 0x10000000
+    for bad in (dict(n=0), dict(rows=12), dict(cols=60), dict(rows=0), dict(xf=2), dict(wf=-1),
+                dict(act=5), dict(act=-1), dict(x=None), dict(xs=None), dict(w=None),
+                dict(wsc=None), dict(out=None), dict(ldo=24), dict(ldo=31), dict(odt=7),
+                dict(res=G, rdt=5, ldr=32), dict(res=G, ldr=24), dict(ws=None), dict(ws=F + 16),
+                dict(out=A), dict(out=B + 64), dict(out=A + 4 * 128 - 16), dict(out=D),
+                dict(out=C + 32 * 64 - 16), dict(bias=E_),
+                dict(res=E_, rdt=F32, ldr=32), dict(res=E_ + 16, rdt=BF16, ldr=32),
+                dict(res=E_, rdt=BF16, ldr=40)):
+        assert lin(**bad) == EINVAL, bad
+    for bad in (dict(x=A + 16), dict(xs=B + 16), dict(w=C + 8), dict(wsc=D + 16), dict(out=E_ + 4),
+                dict(bias=G + 4), dict(res=G + 8, ldr=32)):
+        assert lin(**bad) == EALIGN, bad
+    assert lin(wsb=255) == ENOMEM
+
+
+def test_gated_refusals():
+    G = F + 0x10000000
+    base = dict(x=A, xs=A + 0x100000, xf=F8, wg=B, wgs=B + 0x100000, wu=C, wus=C + 0x100000, wf=F4,
+                bg=None, bu=None, n=4, rows=32, cols=64, act=2, out=D, odt=BF16, ldo=32, codes=None,
+                scales=None, of=F8, ws=F, wsb=1 << 20, st=None)
+
+    def gat(**kw):
+        return lib.moe_mx_gated_linear(*{**base, **kw}.values())
+
+    mx = dict(out=None, codes=E_, scales=G)
+    for bad in (dict(n=0), dict(rows=4), dict(cols=4), dict(xf=5), dict(wf=2), dict(act=9),
+                dict(x=None), dict(wg=None), dict(wus=None), dict(out=None), dict(ldo=16),
+                dict(odt=3), dict(out=A), dict(out=B), dict(out=C + 0x100000), dict(ws=None),
+                dict(codes=E_, scales=G), dict(codes=E_), dict(**mx, of=2),
+                dict(out=None, codes=E_), dict(out=None, scales=E_),
+                dict(out=None, codes=E_, scales=E_), dict(out=None, codes=A, scales=G),
+                dict(out=None, codes=E_, scales=C), dict(bg=D), dict(bu=D)):
+        assert gat(**bad) == EINVAL, bad
+    for bad in (dict(x=A + 16), dict(wu=C + 8), dict(out=D + 8), dict(bg=G + 8), dict(bu=G + 8),
+                dict(out=None, codes=E_ + 16, scales=G)):
+        assert gat(**bad) == EALIGN, bad
+    assert gat(wsb=0) == ENOMEM
+
+
+def test_product_binding_refusals():
+    u8 = torch.uint8
+    x, xs = torch.zeros(512, dtype=u8), torch.zeros(512, dtype=u8)
+    w, ws_ = torch.zeros(8 * 64, dtype=u8), torch.zeros(512, dtype=u8)
+    out, ws = torch.zeros((4, 8)), torch.zeros(256, dtype=u8)
+    with pytest.raises(ValueError, match="x:"):
+        rvq.moe_mx_linear(x[:256], xs, w, ws_, 4, 8, 64, out, ws)
+    with pytest.raises(ValueError, match="w:"):
+        rvq.moe_mx_linear(x, xs, w, ws_, 4, 8, 64, out, ws, wfmt=F8)
+    with pytest.raises(ValueError, match="out"):
+        rvq.moe_mx_linear(x, xs, w, ws_, 4, 8, 64, out[:3], ws)
+    with pytest.raises(TypeError, match="bias"):
+        rvq.moe_mx_linear(x, xs, w, ws_, 4, 8, 64, out, ws, bias=torch.zeros(8).double())
+    with pytest.raises(ValueError, match="wu scales"):
+        rvq.moe_mx_gated_linear(x, xs, w, ws_, w, ws_[:256], 4, 8, 64, out, ws)
+    with pytest.raises(ValueError, match="out scales"):
+        rvq.moe_mx_gated_linear(x, xs, w, ws_, w, ws_, 4, 8, 64, x, ws, out_scales=ws)
