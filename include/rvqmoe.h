@@ -362,6 +362,49 @@ rvq_status moe_route(const float *logits_dev, int32_t n, int32_t E, int32_t k,
                      int32_t *topk_idx_dev, float *topk_w_dev, int32_t *offsets_dev,
                      int32_t *pairs_dev, void *ws_dev, size_t ws_bytes, rvq_stream_t stream);
 
+/* Routing by scores with a balance bias and groups of experts (moe_route's selection by
+ * logits is the pages' reading; this call is an addition for routers trained so):
+ *   p_e = softmax(l)_e over all E, or sigmoid(l_e);   c_e = p_e + bias[e]
+ *   the E experts are `groups` runs of equal size; a group's value is the sum of its two
+ *   largest c (its c where it is one expert); the top_groups groups of largest value stay
+ *   the k largest c of those groups are chosen, in descending order
+ *   w_j = scale * p_j, or with renorm scale * p_j / sum_i p_i of the chosen
+ * Ties go to the lower group and the lower expert.  The choice is that of 64-bit
+ * arithmetic (without a bias experts are compared by their logits); weights are fp32.
+ * The bias takes part in the choice alone.  Renormalised sigmoids of very negative logits
+ * keep their ratios. */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct moe_route_rule {
+    moe_score score;
+    const float *bias_dev;       /* fp32 [E] (dev), or NULL                      */
+    int32_t groups, top_groups;  /* 1 <= top_groups <= groups <= 32, E % groups == 0 */
+    int32_t renorm;
+    float scale;
+} moe_route_rule;
+
+/* 0 for sizes the call refuses; for up to n tokens. */
+size_t moe_route_scored_workspace_bytes(int32_t n, int32_t E);
+
+/* topk_idx int32 [n][k], topk_w fp32 [n][k], offsets int32 [E+1], pairs int32 [n*k] as
+ * moe_route writes them; logits fp32 [n][E] (all dev).  1 <= k <= min(32, experts of
+ * top_groups groups), E <= 256, n <= 262144.  The outputs overlap nothing (EINVAL); ws
+ * 256-byte aligned, moe_route_scored_workspace_bytes long.  A logit or bias that is not
+ * finite sets RVQ_DEV_ERR_NONFINITE and counts as 0. */
+rvq_status moe_route_scored(const float *logits_dev, int32_t n, int32_t E, int32_t k,
+                            const moe_route_rule *rule, int32_t *topk_idx_dev, float *topk_w_dev,
+                            int32_t *offsets_dev, int32_t *pairs_dev, void *ws_dev,
+                            size_t ws_bytes, rvq_stream_t stream);
+
+/* Gradient of the logits (fp32 [n][E], every element written) from that of topk_w, for
+ * the choice topk_idx (which has no gradient; indices outside 0 .. E-1 take no part):
+ *   dp_j = scale dw_j, or with renorm scale (dw_j - sum_i dw_i p_i / P) / P, P = sum_i p_i
+ *   sigmoid: dl_j = dp_j p_j (1 - p_j);  softmax: dl_e = p_e (dp_e - sum_j dp_j p_j)
+ * dlogits may take the place of logits and overlaps nothing else (EINVAL). */
+rvq_status moe_route_scored_backward(const float *dtopk_w_dev, const float *logits_dev,
+                                     const int32_t *topk_idx_dev, int32_t n, int32_t E, int32_t k,
+                                     const moe_route_rule *rule, float *dlogits_dev,
+                                     rvq_stream_t stream);
+
 /* --------------------------------------------------------------------------
  * Expert FFN on the grouped pairs: for every pair entry p = t*k + slot with
  * expert e, y_pair[p] = Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), silu(g) =
@@ -443,6 +486,17 @@ rvq_status moe_layer_forward_ex(const rvq_moe_bank *bank, const float *wr_dev,
                                 float *out_dev, void *ws_dev, size_t ws_bytes,
                                 const void *residual_dev, rvq_dtype rdt, int32_t tc_min_tokens,
                                 void **events, rvq_stream_t stream);
+
+/* moe_layer_forward_ex with the experts chosen by `rule` (moe_route_scored) in the
+ * place of moe_route; bias_dev is the router's own bias, added to the logits. */
+rvq_status moe_layer_forward_scored(const rvq_moe_bank *bank, const float *wr_dev,
+                                    const float *bias_dev, const moe_route_rule *rule,
+                                    const void *x_dev, rvq_dtype xdt, int32_t n, int32_t k,
+                                    float *logits_dev, int32_t *topk_idx_dev, float *topk_w_dev,
+                                    int32_t *offsets_dev, int32_t *pairs_dev, float *out_dev,
+                                    void *ws_dev, size_t ws_bytes, const void *residual_dev,
+                                    rvq_dtype rdt, int32_t tc_min_tokens, void **events,
+                                    rvq_stream_t stream);
 
 /* One whole MoE layer with its input and output in host memory, for callers
  * whose tokens arrive from and leave to the host.  The call queues, all on

@@ -28,6 +28,8 @@ MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = rang
 MOE_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU,
             "gelu": MOE_ACT_GELU, "gelu_tanh": MOE_ACT_GELU_TANH}
 MOE_WAYS = ("stream", "tiles", "parts", "split")
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = range(2)
+MOE_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 MOE_MX_F8, MOE_MX_F4 = range(2)
 MOE_MX = {"f8": MOE_MX_F8, "f4": MOE_MX_F4}
 (MOE_GATE_NONE, MOE_GATE_SCALAR, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL) = range(5)
@@ -49,6 +51,12 @@ class RvqMoeBank(ctypes.Structure):
                 ("f", ctypes.c_int32), ("layer", ctypes.c_int32)]
 
 
+class MoeRouteRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class RvqCacheStats(ctypes.Structure):
     _fields_ = [("hits", ctypes.c_uint64), ("misses", ctypes.c_uint64),
                 ("prefetched", ctypes.c_uint64), ("prefetch_used", ctypes.c_uint64),
@@ -65,6 +73,7 @@ _vp, _i32, _u32, _u64, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32,
 _i64, _f32 = ctypes.c_int64, ctypes.c_float
 _lib = ctypes.CDLL(LIB_PATH)
 _BANKP = ctypes.POINTER(RvqMoeBank)
+_RULEP = ctypes.POINTER(MoeRouteRule)
 _SIGS = {
     "rvq_status_string": (ctypes.c_char_p, [_i32]),
     "rvq_last_error": (ctypes.c_char_p, []),
@@ -97,6 +106,9 @@ _SIGS = {
     "moe_router_logits": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),
     "moe_route_max_tokens": (_i32, [_i32]),
     "moe_route": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_scored_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_route_scored": (_i32, [_vp, _i32, _i32, _i32, _RULEP, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_scored_backward": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _RULEP, _vp, _vp]),
     "moe_workspace_bytes": (_sz, [_BANKP, _i32, _i32]),
     "moe_expert_ffn": (_i32, [_BANKP, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_expert_ffn_ex": (_i32, [_BANKP, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _i32,
@@ -106,6 +118,8 @@ _SIGS = {
                                  _vp, _vp, _vp, _sz, _vp, _vp]),
     "moe_layer_forward_ex": (_i32, [_BANKP, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
                                     _vp, _vp, _vp, _vp, _sz, _vp, _i32, _i32, _vp, _vp]),
+    "moe_layer_forward_scored": (_i32, [_BANKP, _vp, _vp, _RULEP, _vp, _i32, _i32, _i32, _vp, _vp,
+                                        _vp, _vp, _vp, _vp, _vp, _sz, _vp, _i32, _i32, _vp, _vp]),
     "moe_layer_forward_host": (_i32, [_BANKP, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp]),
     "moe_layer_graph_create": (_i32, [_BANKP, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
@@ -388,13 +402,69 @@ def moe_combine(y_pair, topk_w, n, k, d, residual, out, stream=None):
                                            _dt(residual), _p(out), _stream(stream)))
 
 
+def moe_route_rule(E, score=MOE_SCORE_SIGMOID, bias=None, groups=1, top_groups=1, renorm=True,
+                   scale=1.0) -> MoeRouteRule:
+    """How moe_route_scored chooses among E experts; keeps a reference to the bias
+    (fp32 [E])."""
+    rule = MoeRouteRule(score, _vec(bias, E, "bias", torch.float32), groups, top_groups,
+                        int(renorm), scale)
+    rule.keep = bias
+    return rule
+
+
+def moe_route_scored_workspace_bytes(n, E) -> int:
+    return int(_lib.moe_route_scored_workspace_bytes(n, E))
+
+
+def moe_route_scored(logits, n, E, k, topk_idx, topk_w, offsets, pairs, ws,
+                     score=MOE_SCORE_SIGMOID, bias=None, groups=1, top_groups=1, renorm=True,
+                     scale=1.0, stream=None):
+    """The k of E experts with the largest score plus bias in the top_groups best groups
+    (a group's value: its two largest), weights from the scores, and the grouping of
+    moe_route.  logits fp32 [n][E]."""
+    rule = MoeRouteRule(score, _vec(bias, E, "bias", torch.float32), groups, top_groups,
+                        int(renorm), scale)
+    f32, i32 = torch.float32, torch.int32
+    rc = _lib.moe_route_scored(_vec(logits, n * E, "logits", f32), n, E, k, rule,
+                               _vec(topk_idx, n * k, "topk_idx", i32),
+                               _vec(topk_w, n * k, "topk_w", f32),
+                               _vec(offsets, E + 1, "offsets", i32),
+                               _vec(pairs, n * k, "pairs", i32), ws.data_ptr(), ws.nbytes,
+                               _raw_stream(stream))
+    if rc:
+        _check("moe_route_scored", rc)
+
+
+def moe_route_scored_backward(dtopk_w, logits, topk_idx, n, E, k, dlogits,
+                              score=MOE_SCORE_SIGMOID, renorm=True, scale=1.0, stream=None):
+    """dlogits (fp32 [n][E], may be logits itself) from the gradient of topk_w."""
+    rule = MoeRouteRule(score, None, 1, 1, int(renorm), scale)
+    f32 = torch.float32
+    rc = _lib.moe_route_scored_backward(_vec(dtopk_w, n * k, "dtopk_w", f32),
+                                        _vec(logits, n * E, "logits", f32),
+                                        _vec(topk_idx, n * k, "topk_idx", torch.int32), n, E, k,
+                                        rule, _vec(dlogits, n * E, "dlogits", f32),
+                                        _raw_stream(stream))
+    if rc:
+        _check("moe_route_scored_backward", rc)
+
+
 def moe_layer_forward(bank, wr, bias, x, n, k, logits, topk_idx, topk_w, offsets, pairs, out,
-                      ws, events=None, stream=None, tc_min_tokens=0, residual=None):
+                      ws, events=None, stream=None, tc_min_tokens=0, residual=None, rule=None):
+    """rule (moe_route_rule): experts chosen by moe_route_scored instead of moe_route."""
     ev = None
     if events is not None:
         assert len(events) == MOE_LAYER_EVENTS
         ev = (ctypes.c_void_p * MOE_LAYER_EVENTS)(*[e.cuda_event for e in events])
     rdt = _dt(residual) if residual is not None else _dt(x)
+    if rule is not None:
+        _check("moe_layer_forward_scored",
+               _lib.moe_layer_forward_scored(ctypes.byref(bank), _p(wr), _p(bias), rule, _p(x),
+                                             _dt(x), n, k, _p(logits), _p(topk_idx), _p(topk_w),
+                                             _p(offsets), _p(pairs), _p(out), _p(ws), _nbytes(ws),
+                                             _p(residual), rdt, int(tc_min_tokens), ev,
+                                             _stream(stream)))
+        return
     _check("moe_layer_forward",
            _lib.moe_layer_forward_ex(ctypes.byref(bank), _p(wr), _p(bias), _p(x), _dt(x), n, k,
                                      _p(logits), _p(topk_idx), _p(topk_w), _p(offsets),

@@ -10,6 +10,7 @@
 #include <new>
 
 #include "internal.cuh"
+#include "route_scored.cuh"
 
 namespace rvq {
 
@@ -741,7 +742,8 @@ static rvq_status layer_after_router(const rvq_moe_bank *bank, const void *x_dev
                                      int32_t *offsets_dev, int32_t *pairs_dev, float *out_dev,
                                      void *ws_dev, const void *residual_dev, rvq_dtype rdt,
                                      int32_t tc_min_tokens, void **events, cudaStream_t st,
-                                     const FfnPlan &P, float *out2 = nullptr);
+                                     const FfnPlan &P, float *out2 = nullptr,
+                                     const RouteRule *rule = nullptr);
 
 // moe_layer_forward_ex, with out2 (optional) a second copy of the output that
 // the combine writes (a host buffer the GPU maps).
@@ -751,7 +753,8 @@ static rvq_status layer_forward(const rvq_moe_bank *bank, const float *wr_dev,
                                 float *topk_w_dev, int32_t *offsets_dev, int32_t *pairs_dev,
                                 float *out_dev, void *ws_dev, size_t ws_bytes,
                                 const void *residual_dev, rvq_dtype rdt, int32_t tc_min_tokens,
-                                void **events, rvq_stream_t stream, float *out2) {
+                                void **events, rvq_stream_t stream, float *out2,
+                                const RouteRule *rule = nullptr) {
     RVQ_TRY(check_ffn_args(bank, x_dev, xdt, n, k, ws_dev, ws_bytes, "moe_layer_forward"));
     if (!residual_dev) {
         residual_dev = x_dev;
@@ -789,7 +792,7 @@ static rvq_status layer_forward(const rvq_moe_bank *bank, const float *wr_dev,
     RVQ_TRY(mark(1));
     return layer_after_router(bank, x_dev, xdt, n, k, logits_dev, topk_idx_dev, topk_w_dev,
                               offsets_dev, pairs_dev, out_dev, ws_dev, residual_dev, rdt,
-                              tc_min_tokens, events, st, P, out2);
+                              tc_min_tokens, events, st, P, out2, rule);
 }
 
 rvq_status moe_layer_forward_ex(const rvq_moe_bank *bank, const float *wr_dev,
@@ -804,6 +807,27 @@ rvq_status moe_layer_forward_ex(const rvq_moe_bank *bank, const float *wr_dev,
                          residual_dev, rdt, tc_min_tokens, events, stream, nullptr);
 }
 
+rvq_status moe_layer_forward_scored(const rvq_moe_bank *bank, const float *wr_dev,
+                                    const float *bias_dev, const moe_route_rule *rule,
+                                    const void *x_dev, rvq_dtype xdt, int32_t n, int32_t k,
+                                    float *logits_dev, int32_t *topk_idx_dev, float *topk_w_dev,
+                                    int32_t *offsets_dev, int32_t *pairs_dev, float *out_dev,
+                                    void *ws_dev, size_t ws_bytes, const void *residual_dev,
+                                    rvq_dtype rdt, int32_t tc_min_tokens, void **events,
+                                    rvq_stream_t stream) {
+    const char *who = "moe_layer_forward_scored";
+    RVQ_TRY(check_ffn_args(bank, x_dev, xdt, n, k, ws_dev, ws_bytes, who));
+    RouteRule r;
+    RVQ_TRY(check_rule(who, rule, bank->n_experts, k, r));
+    if (ws_bytes < RVQ_WS_STATUS_BYTES + route_scored_hist_bytes(n, bank->n_experts)) {
+        set_error("%s: workspace %zu too small for the router", who, ws_bytes);
+        return RVQ_ENOMEM;
+    }
+    return layer_forward(bank, wr_dev, bias_dev, x_dev, xdt, n, k, logits_dev, topk_idx_dev,
+                         topk_w_dev, offsets_dev, pairs_dev, out_dev, ws_dev, ws_bytes,
+                         residual_dev, rdt, tc_min_tokens, events, stream, nullptr, &r);
+}
+
 // Routing, expert FFN and combine of a layer whose logits are computed.
 static rvq_status layer_after_router(const rvq_moe_bank *bank, const void *x_dev, rvq_dtype xdt,
                                      int32_t n, int32_t k, float *logits_dev,
@@ -811,7 +835,7 @@ static rvq_status layer_after_router(const rvq_moe_bank *bank, const void *x_dev
                                      int32_t *offsets_dev, int32_t *pairs_dev, float *out_dev,
                                      void *ws_dev, const void *residual_dev, rvq_dtype rdt,
                                      int32_t tc_min_tokens, void **events, cudaStream_t st,
-                                     const FfnPlan &P, float *out2) {
+                                     const FfnPlan &P, float *out2, const RouteRule *rule) {
     const bool pdl = events == nullptr;
     auto mark = [&](int i) -> rvq_status {
         if (events) RVQ_CUDA(cudaEventRecord((cudaEvent_t)events[i], st));
@@ -819,13 +843,22 @@ static rvq_status layer_after_router(const rvq_moe_bank *bank, const void *x_dev
     };
     // decode batches on the lookup-table path: the routing block also writes
     // the GEMV's pair plan (one launch less on the critical path)
-    const bool fuse_plan = tc_min_tokens <= 0 && decode_pair_plan(P, n);
+    const bool fuse_plan = !rule && tc_min_tokens <= 0 && decode_pair_plan(P, n);
+    if (rule) {
+        // the counts of its runs take the place of partial sums that come later
+        const RouteScoredJob j = {logits_dev, n, bank->n_experts, k, *rule, topk_idx_dev,
+                                  topk_w_dev, offsets_dev, pairs_dev, (uint32_t *)ws_dev,
+                                  (int32_t *)((uint8_t *)ws_dev + RVQ_WS_STATUS_BYTES)};
+        RVQ_TRY(launch_route_scored(j, st));
+    }
     LutJob plan = {};
     if (fuse_plan)
         plan = ffn_job(bank, record_layout(bank->d, bank->f), n * k, ws_dev, nullptr, 0);
-    RVQ_TRY(launch_route(logits_dev, n, bank->n_experts, k, topk_idx_dev, topk_w_dev, offsets_dev,
-                         pairs_dev, (uint32_t *)ws_dev, st, pdl, fuse_plan ? &plan : nullptr,
-                         fuse_plan ? (int4 *)((uint8_t *)ws_dev + P.off_desc_gu) : nullptr));
+    if (!rule)
+        RVQ_TRY(launch_route(logits_dev, n, bank->n_experts, k, topk_idx_dev, topk_w_dev,
+                             offsets_dev, pairs_dev, (uint32_t *)ws_dev, st, pdl,
+                             fuse_plan ? &plan : nullptr,
+                             fuse_plan ? (int4 *)((uint8_t *)ws_dev + P.off_desc_gu) : nullptr));
     RVQ_TRY(mark(2));
     if (tc_min_tokens <= 0) {
         // lookup-table path only; the down partials are reduced inside the combine

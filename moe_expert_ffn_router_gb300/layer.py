@@ -5,14 +5,14 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (MOE_ACT_SILU, RVQ_WS_STATUS_BYTES, moe_bank_init, moe_bank_record_bytes,
+from . import (MOE_ACT_SILU, MOE_SCORE_SIGMOID, RVQ_WS_STATUS_BYTES, moe_bank_init, moe_bank_record_bytes,
                moe_bank_validate, moe_bank_write_expert, moe_cache_bank, moe_cache_create,
                moe_cache_destroy, moe_cache_stats, moe_combine, moe_expert_ffn,
                moe_gated_linear, moe_gated_linear_backward, moe_gated_linear_workspace_bytes,
                moe_layer_forward, moe_layer_forward_host, moe_layer_forward_prenorm,
                moe_layer_forward_streamed, moe_layer_graph_create, moe_linear,
                moe_linear_backward, moe_linear_workspace_bytes, moe_norm_join, moe_rms_norm,
-               moe_route,
+               moe_route, moe_route_rule, moe_route_scored,
                moe_router_logits,
                moe_workspace_bytes, rvq_ws_clear, rvq_ws_status)
 
@@ -41,6 +41,7 @@ class MoeLayer:
         self.bank = moe_bank_init(self.buf, n_experts, d, f, layer)
         self.wr = None
         self.bias = None
+        self.rule = None
         self._ws = {}
 
     # ---------------------------------------------------------------- loading
@@ -60,6 +61,18 @@ class MoeLayer:
         self.wr = _dev(wr, self.device, torch.float32)
         assert self.wr.shape == (self.E, self.d)
         self.bias = None if bias is None else _dev(bias, self.device, torch.float32)
+
+    def set_scoring(self, score: int = MOE_SCORE_SIGMOID, bias=None, groups: int = 1,
+                    top_groups: int = 1, renorm: bool = True, scale: float = 1.0):
+        """Experts chosen by scores plus a balance bias (fp32 [E]) from the best groups
+        (moe_route_scored) in forward() and forward_steps()."""
+        bias = None if bias is None else _dev(bias, self.device, torch.float32)
+        self.rule = moe_route_rule(self.E, score, bias, groups, top_groups, renorm, scale)
+
+    def _by_logits(self, what: str):
+        if self.rule is not None:
+            raise ValueError(f"{what}: the layer scores its experts (set_scoring), and this call "
+                             "chooses by logits")
 
     def validate(self):
         moe_bank_validate(self.bank)
@@ -98,7 +111,7 @@ class MoeLayer:
         b = bufs or self.buffers(n)
         moe_layer_forward(self.bank, self.wr, self.bias, x, n, self.k, b["logits"], b["idx"],
                           b["w"], b["offsets"], b["pairs"], b["out"], b["ws"], events=events,
-                          tc_min_tokens=tc_min_tokens, residual=residual)
+                          tc_min_tokens=tc_min_tokens, residual=residual, rule=self.rule)
         return b
 
     def forward_host(self, x_host: torch.Tensor, out_host: torch.Tensor, bufs: dict | None = None,
@@ -106,6 +119,7 @@ class MoeLayer:
         """The layer with its input read from and its output written to host
         tensors (pinned for asynchronous copies), through the library's
         host-buffer call; asynchronous on the current stream."""
+        self._by_logits("forward_host")
         n = x_host.shape[0]
         b = bufs or self.buffers(n)
         xd = b.get("x_dev")
@@ -122,6 +136,7 @@ class MoeLayer:
         copy of x_host into x_dev before it and of the output to out_host
         after it), recorded on a side stream; launch() runs it on the current
         stream."""
+        self._by_logits("graph")
         side = torch.cuda.Stream(device=self.device)
         side.wait_stream(torch.cuda.current_stream())
         g = moe_layer_graph_create(self.bank, self.wr, self.bias, x_dev.shape[0], self.k, x_dev,
@@ -137,8 +152,14 @@ class MoeLayer:
         n = x.shape[0]
         b = self.buffers(n)
         moe_router_logits(self.wr, self.bias, x, n, self.E, self.d, b["logits"])
-        moe_route(b["logits"], n, self.E, self.k, b["idx"], b["w"], b["offsets"], b["pairs"],
-                  b["ws"])
+        if self.rule is None:
+            moe_route(b["logits"], n, self.E, self.k, b["idx"], b["w"], b["offsets"], b["pairs"],
+                      b["ws"])
+        else:
+            r = self.rule
+            moe_route_scored(b["logits"], n, self.E, self.k, b["idx"], b["w"], b["offsets"],
+                             b["pairs"], b["ws"], r.score, r.keep, r.groups, r.top_groups,
+                             r.renorm, r.scale)
         y = torch.empty((n * self.k, self.d), dtype=torch.float32, device=self.device)
         moe_expert_ffn(self.bank, x, n, self.k, b["offsets"], b["pairs"], y, b["ws"])
         moe_combine(y, b["w"], n, self.k, self.d, x, b["out"])
@@ -189,10 +210,12 @@ class MoeStack:
         h = x
         for i, L in enumerate(self.layers):
             b = bufs[i]
-            if events is not None and i == 0:
-                # per-kernel timing marks: the norm and the layer as separate calls
+            if L.rule is not None or (events is not None and i == 0):
+                # scored experts, or per-kernel timing marks: the norm and the layer as
+                # separate calls
                 moe_rms_norm(h, n, L.d, b["xn"], eps=self.eps)
-                L.forward(b["xn"], b, events=events, tc_min_tokens=tc_min_tokens, residual=h)
+                L.forward(b["xn"], b, events=events if i == 0 else None,
+                          tc_min_tokens=tc_min_tokens, residual=h)
             else:
                 moe_layer_forward_prenorm(L.bank, L.wr, L.bias, h, n, L.k, self.eps, b["xn"],
                                           b["logits"], b["idx"], b["w"], b["offsets"], b["pairs"],
@@ -212,6 +235,8 @@ class MoeStreamedStack:
                  eps: float = 1e-6):
         assert layers and all(L.d == layers[0].d and L.f == layers[0].f and L.E == layers[0].E
                               for L in layers)
+        for L in layers:
+            L._by_logits("MoeStreamedStack")
         L0 = layers[0]
         self.n_layers, self.E, self.d, self.f, self.k = len(layers), L0.E, L0.d, L0.f, L0.k
         self.device = L0.device
