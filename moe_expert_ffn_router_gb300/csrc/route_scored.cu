@@ -26,11 +26,8 @@ namespace rvq {
 namespace {
 
 constexpr int RS_NT = 256;
+constexpr int RS_PLACE = 1024;  // threads of a placing block
 constexpr int RS_Q = 8;  // experts per lane
-
-template <class F> struct KeyOf;
-template <> struct KeyOf<float> { using type = uint32_t; };
-template <> struct KeyOf<double> { using type = uint64_t; };
 
 // Order-preserving keys (after -0 -> +0): larger value, larger key, never 0.
 __device__ __forceinline__ uint32_t to_key(float f) {
@@ -53,8 +50,8 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     const uint32_t lo = warp_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
     return ((uint64_t)hi << 32) | lo;
 }
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+
+__device__ __forceinline__ float finite_or_0(float v) { return isfinite(v) ? v : 0.f; }
 
 template <class F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -63,192 +60,296 @@ __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
-// Scores of this lane's experts (0 past the last).
+// 1 / (1 + e^-l): expf's two units, half a step of the sum, two of the quotient's
+__device__ __forceinline__ float sigmoid32(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
+__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
+
+// Groups of a row that stay, as bits: lane g holds the value of group g.
 template <class F>
-__device__ __forceinline__ void scores(const float (&l)[RS_Q], int E, int lane, int score,
-                                       F (&p)[RS_Q]) {
-    if (score == MOE_SCORE_SIGMOID) {
-#pragma unroll
-        for (int q = 0; q < RS_Q; ++q)
-            p[q] = lane + 32 * q < E ? F(1) / (F(1) + exp_of(-F(l[q]))) : F(0);
-        return;
+__device__ __forceinline__ uint32_t best_groups(F mine, const RouteRule &rule, int lane) {
+    int place = 0;
+    for (int g = 0; g < rule.groups; ++g) {
+        const F v = __shfl_sync(0xffffffffu, mine, g);
+        if (v > mine || (v == mine && g < lane)) ++place;
     }
-    uint32_t top = 0;
-#pragma unroll
-    for (int q = 0; q < RS_Q; ++q)
-        if (lane + 32 * q < E) top = max(top, to_key(l[q]));
-    const F m = F(from_key(warp_max(top)));
-    F z = F(0);
-#pragma unroll
-    for (int q = 0; q < RS_Q; ++q) {
-        p[q] = lane + 32 * q < E ? exp_of(F(l[q]) - m) : F(0);
-        z += p[q];
-    }
-    z = warp_sum(z);
-#pragma unroll
-    for (int q = 0; q < RS_Q; ++q) p[q] /= z;
+    return __ballot_sync(0xffffffffu, lane < rule.groups && place < rule.top_groups);
 }
 
-// The k experts of a row: lane s < k gets the s-th.  Returns whether two values that
-// decide are closer than the arithmetic tells apart (F float).
+// The choice in 64 bits, from the start: for the rows that 32 bits leave open.  Rolled
+// loops over keys in shared memory: it runs seldom, and long straight code would cost
+// more to fetch than to run.
+__device__ __noinline__ int choose_64(const float *row, const float *bias, int E, int k,
+                                      const RouteRule &rule, int lane, uint64_t *key) {
+    double m = 0.0, z = 1.0;
+    if (rule.score == MOE_SCORE_SOFTMAX) {
+        uint32_t top = 0;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32) top = max(top, to_key(finite_or_0(row[e])));
+        m = (double)from_key(warp_max(top));
+        z = 0.0;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32) z += exp((double)finite_or_0(row[e]) - m);
+        z = warp_sum(z);
+    }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+        const float l = finite_or_0(row[e]);
+        const double p = rule.score == MOE_SCORE_SIGMOID ? sigmoid64(l) : exp((double)l - m) / z;
+        key[e] = to_key(bias ? p + (double)finite_or_0(bias[e]) : p);
+    }
+    __syncwarp();
+    uint32_t kept = 0xffffffffu;
+    const int size = E / rule.groups;
+    if (rule.top_groups < rule.groups) {
+        double mine = 0.0;
+        if (lane < rule.groups) {
+            uint64_t a1 = 0, a2 = 0;
+#pragma unroll 1
+            for (int e = lane * size; e < (lane + 1) * size; ++e) {
+                const uint64_t c = key[e];
+                a2 = c > a1 ? a1 : c > a2 ? c : a2;
+                a1 = c > a1 ? c : a1;
+            }
+            mine = from_key(a1) + (size > 1 ? from_key(a2) : 0.0);
+        }
+        kept = best_groups(mine, rule, lane);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+        if (!((kept >> (e / size)) & 1u) && rule.top_groups < rule.groups)
+            key[e] = 0;
+        else if (!bias)
+            key[e] = to_key((double)finite_or_0(row[e]));
+    }
+    __syncwarp();
+    int my_idx = 0;
+#pragma unroll 1
+    for (int s = 0; s < k; ++s) {
+        uint64_t best = 0;
+        int at = 0x7fffffff;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32)
+            if (key[e] > best) { best = key[e]; at = e; }
+        const uint64_t top = warp_max(best);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)at : 0x7fffffffu);
+        if (lane == s) my_idx = (int)e;
+        if ((int)(e & 31) == lane) key[e] = 0;
+        __syncwarp();
+    }
+    return my_idx;
+}
+
+// The k experts of a row: lane s < k gets the s-th.  l, b: logits and biases of the
+// lane's experts, finite.
 //
-// Error of a 32-bit score: sigmoid 2 units of expf, one of the sum, a half of the
-// quotient, at most 4e-7; softmax p (6 + |l - m|) 2^-23 with p |l - m| <= 0.37, and 14
-// half steps of the sum, at most 1.7e-6; both of p <= 1.  Two values c are told apart by
-// more than twice that and a step of the larger |c|; sums of two by twice as much.
-template <class F>
-__device__ __forceinline__ bool choose(const float (&l)[RS_Q], const float (&b)[RS_Q], int E, int k,
-                                       const RouteRule &rule, int lane, int &my_idx) {
-    using Key = typename KeyOf<F>::type;
+// Error of a 32-bit score: sigmoid p (1 - p) 2.4e-7 and p 3e-7, at most 4e-7; softmax
+// p (6 + |l - m|) 2^-23 with p |l - m| <= 0.37, and 14 half steps of the sum, at most
+// 1.7e-6.  Two values c are told apart by more than twice that and a step of the larger
+// |c|; sums of two by twice as much.
+__device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[RS_Q],
+                                      const float *row, int E, int k, const RouteRule &rule,
+                                      int lane, uint64_t *scratch) {
     const bool biased = rule.bias != nullptr, grouped = rule.top_groups < rule.groups;
-    constexpr bool kCheck = sizeof(F) == 4;
-    bool near = false;
-    Key key[RS_Q];
-    float big = 0.f;
-    if (biased || grouped) {
-        F p[RS_Q];
-        scores<F>(l, E, lane, rule.score, p);
-#pragma unroll
-        for (int q = 0; q < RS_Q; ++q) {
-            const F c = biased ? p[q] + F(b[q]) : p[q];
-            key[q] = lane + 32 * q < E ? to_key(c) : Key(0);
-            if (kCheck) big = fmaxf(big, fabsf((float)c));
-        }
-    }
+    const int size = E / rule.groups;
+    uint32_t key[RS_Q];
     float apart = 0.f;
-    if (kCheck && (biased || grouped))
-        apart = 3.4e-6f + 2.4e-7f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    bool in[RS_Q];
+    if (biased || grouped) {
+        float p[RS_Q];
+        if (rule.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-    for (int q = 0; q < RS_Q; ++q) in[q] = lane + 32 * q < E;
-    if (grouped) {
-        const int size = E / rule.groups;
-        F mine = F(0);
-        for (int g = 0; g < rule.groups; ++g) {
-            const int lo = g * size - lane, hi = lo + size;  // 32 q of its members
-            Key a1 = 0, a2 = 0;
-#pragma unroll
-            for (int q = 0; q < RS_Q; ++q) {
-                if (32 * q < lo || 32 * q >= hi) continue;
-                if (key[q] > a1) {
-                    a2 = a1;
-                    a1 = key[q];
-                } else if (key[q] > a2) {
-                    a2 = key[q];
-                }
-            }
-            const Key v1 = warp_max(a1);
-            const int winner = __ffs(__ballot_sync(0xffffffffu, a1 == v1)) - 1;
-            F v = from_key(v1);
-            if (size > 1) v += from_key(warp_max(lane == winner ? a2 : a1));
-            if (lane == g) mine = v;
-        }
-        int place = 0;  // of group `lane`
-        F worst = F(0), best = F(0);
-        for (int g = 0; g < rule.groups; ++g) {
-            const F v = __shfl_sync(0xffffffffu, mine, g);
-            if (v > mine || (v == mine && g < lane)) ++place;
-        }
-        const uint32_t kept =
-            __ballot_sync(0xffffffffu, lane < rule.groups && place < rule.top_groups);
-        if (kCheck) {
-            bool any_w = false, any_b = false;
-            for (int g = 0; g < rule.groups; ++g) {
-                const F v = __shfl_sync(0xffffffffu, mine, g);
-                if ((kept >> g) & 1u) {
-                    if (!any_w || v < worst) worst = v;
-                    any_w = true;
-                } else {
-                    if (!any_b || v > best) best = v;
-                    any_b = true;
-                }
-            }
-            near = !((float)worst - (float)best > 2.f * apart);
-        }
-#pragma unroll
-        for (int q = 0; q < RS_Q; ++q) {
-            const int e = lane + 32 * q;
-            in[q] = e < E && ((kept >> (e / size)) & 1u);
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < RS_Q; ++q) {
-        if (!biased) key[q] = to_key(F(l[q]));
-        if (!in[q]) key[q] = 0;
-    }
-    // lane-local best (ties: lower q = lower expert index)
-    uint32_t taken = 0u;
-    Key lk = 0, last = 0;
-    int lq = 0;
-#pragma unroll
-    for (int q = 0; q < RS_Q; ++q)
-        if (key[q] > lk) { lk = key[q]; lq = q; }
-    my_idx = 0;
-    const int picks = kCheck && biased ? k + 1 : k;  // the next one too, to be told apart
-    for (int s = 0; s < picks; ++s) {
-        const Key kmax = warp_max(lk);
-        if (kCheck && biased && s > 0 && kmax != 0 &&
-            !((float)from_key(last) - (float)from_key(kmax) > apart))
-            near = true;
-        last = kmax;
-        const uint32_t cand = lk == kmax ? (uint32_t)(lane + 32 * lq) : 0xffffffffu;
-        const uint32_t e = __reduce_min_sync(0xffffffffu, cand);
-        if (s < k && lane == s) my_idx = (int)e;
-        if ((int)(e & 31) == lane) {
-            taken |= 1u << (e >> 5);
-            lk = 0;
-            lq = 0;
+            for (int q = 0; q < RS_Q; ++q) p[q] = sigmoid32(l[q]);
+        } else {
+            uint32_t top = 0;
 #pragma unroll
             for (int q = 0; q < RS_Q; ++q)
-                if (!((taken >> q) & 1u) && key[q] > lk) { lk = key[q]; lq = q; }
+                if (lane + 32 * q < E) top = max(top, to_key(l[q]));
+            const float m = from_key(warp_max(top));
+            float z = 0.f;
+#pragma unroll
+            for (int q = 0; q < RS_Q; ++q) {
+                p[q] = lane + 32 * q < E ? expf(l[q] - m) : 0.f;
+                z += p[q];
+            }
+            const float inv = 1.f / warp_sum(z);
+#pragma unroll
+            for (int q = 0; q < RS_Q; ++q) p[q] *= inv;
+        }
+        uint32_t big = 0;
+#pragma unroll
+        for (int q = 0; q < RS_Q; ++q) {
+            const float c = p[q] + b[q];
+            key[q] = lane + 32 * q < E ? to_key(c) : 0u;
+            big = max(big, __float_as_uint(c) & 0x7FFFFFFFu);
+        }
+        apart = 3.6e-6f + 2.4e-7f * __uint_as_float(warp_max(big));
+    }
+    const bool whole = size % 32 == 0;  // register q is of group 32 q / size
+    uint32_t stays = 0xffu;             // bit q: expert lane + 32 q is of a group that stays
+    if (grouped) {
+        uint32_t v1 = 0, v2 = 0;  // of group `lane`
+        if (whole) {
+            uint32_t a1 = 0, a2 = 0;
+            int next = size / 32, g = 0;
+#pragma unroll
+            for (int q = 0; q < RS_Q; ++q) {
+                a2 = max(a2, min(a1, key[q]));
+                a1 = max(a1, key[q]);
+                if (q + 1 == next) {
+                    const uint32_t t1 = warp_max(a1);
+                    const int winner = __ffs(__ballot_sync(0xffffffffu, a1 == t1)) - 1;
+                    const uint32_t t2 = warp_max(lane == winner ? a2 : a1);
+                    if (lane == g) { v1 = t1; v2 = t2; }
+                    a1 = a2 = 0;
+                    ++g;
+                    next += size / 32;
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int g = 0; g < rule.groups; ++g) {
+                const int lo = g * size - lane;  // 32 q of its members: lo .. lo + size - 1
+                uint32_t a1 = 0, a2 = 0;
+#pragma unroll
+                for (int q = 0; q < RS_Q; ++q) {
+                    const uint32_t c = (uint32_t)(32 * q - lo) < (uint32_t)size ? key[q] : 0u;
+                    a2 = max(a2, min(a1, c));
+                    a1 = max(a1, c);
+                }
+                const uint32_t t1 = warp_max(a1);
+                const int winner = __ffs(__ballot_sync(0xffffffffu, a1 == t1)) - 1;
+                const uint32_t t2 = warp_max(lane == winner ? a2 : a1);
+                if (lane == g) { v1 = t1; v2 = t2; }
+            }
+        }
+        const float mine = lane < rule.groups ? from_key(v1) + (size > 1 ? from_key(v2) : 0.f) : 0.f;
+        const uint32_t kept = best_groups(mine, rule, lane);
+        const bool in = (kept >> lane) & 1u;
+        const float worst = from_key(__reduce_min_sync(0xffffffffu, in ? to_key(mine) : 0xffffffffu));
+        const float best = from_key(warp_max(!in && lane < rule.groups ? to_key(mine) : 0u));
+        if (!(worst - best > 2.f * apart)) return choose_64(row, rule.bias, E, k, rule, lane, scratch);
+        stays = 0;
+        int g = whole ? 0 : lane / size, left = whole ? size : size - lane % size;
+#pragma unroll
+        for (int q = 0; q < RS_Q; ++q) {
+            stays |= ((kept >> (g & 31)) & 1u) << q;
+            for (left -= 32; left <= 0; left += size) ++g;
         }
     }
-    return near;
-}
-
-__device__ __noinline__ int choose_64(const float (&l)[RS_Q], const float (&b)[RS_Q], int E, int k,
-                                      const RouteRule &rule, int lane) {
-    int idx;
-    choose<double>(l, b, E, k, rule, lane, idx);
+    uint32_t id[RS_Q];
+#pragma unroll
+    for (int q = 0; q < RS_Q; ++q) {
+        const int e = lane + 32 * q;
+        if (!biased) key[q] = to_key(l[q]);
+        if (e >= E || !((stays >> q) & 1u)) key[q] = 0;
+        id[q] = (uint32_t)e;
+    }
+    // the lane's experts, best first (equal ones by index): an odd-even merge network
+#define RVQ_CE(i, j)                                                     \
+    {                                                                    \
+        const bool s = key[i] < key[j] || (key[i] == key[j] && id[i] > id[j]); \
+        const uint32_t x = key[i], y = id[i];                            \
+        key[i] = s ? key[j] : x;                                         \
+        id[i] = s ? id[j] : y;                                           \
+        key[j] = s ? x : key[j];                                         \
+        id[j] = s ? y : id[j];                                           \
+    }
+    RVQ_CE(0, 1) RVQ_CE(2, 3) RVQ_CE(4, 5) RVQ_CE(6, 7)
+    RVQ_CE(0, 2) RVQ_CE(1, 3) RVQ_CE(4, 6) RVQ_CE(5, 7)
+    RVQ_CE(1, 2) RVQ_CE(5, 6)
+    RVQ_CE(0, 4) RVQ_CE(1, 5) RVQ_CE(2, 6) RVQ_CE(3, 7)
+    RVQ_CE(2, 4) RVQ_CE(3, 5)
+    RVQ_CE(1, 2) RVQ_CE(3, 4) RVQ_CE(5, 6)
+#undef RVQ_CE
+    // lane s takes the s-th pick and its key; with a bias one more than k (up to 32)
+    uint32_t my_id = 0, my_key = 0;
+    const int most = biased ? min(k + 1, 32) : k;
+    const auto pick = [&](int s) {
+        const uint32_t top = warp_max(key[0]);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, key[0] == top ? id[0] : 0xffffu);
+        if (lane == s) {
+            my_id = e;
+            my_key = top;
+        }
+        if (id[0] == e) {
+#pragma unroll
+            for (int q = 0; q + 1 < RS_Q; ++q) {
+                key[q] = key[q + 1];
+                id[q] = id[q + 1];
+            }
+            key[RS_Q - 1] = 0;
+        }
+    };
+#pragma unroll 1
+    for (int s = 0; s < most; ++s) pick(s);
+    if (!biased) return (int)my_id;
+    // bit s: the pick after the s-th is not told apart from it
+    const auto open_after = [&](int picked) {
+        uint32_t next = __shfl_down_sync(0xffffffffu, my_key, 1);
+        if (picked == 32) {  // the one after the last pick
+            const uint32_t top = warp_max(key[0]);
+            if (lane == 31) next = top;
+        }
+        return __ballot_sync(0xffffffffu, lane < picked && lane <= 31 && next != 0 &&
+                                              !(from_key(my_key) - from_key(next) > apart));
+    };
+    if ((open_after(most) & (0xffffffffu >> (32 - k))) == 0) return (int)my_id;
+    if (rule.score != MOE_SCORE_SIGMOID) return choose_64(row, rule.bias, E, k, rule, lane, scratch);
+    // on until a pick is told apart from the next: the first `cut` are the candidates
+    for (int s = most; s < 32; ++s) pick(s);
+    const uint32_t after = ~open_after(32) >> (k - 1);
+    if (after == 0) return choose_64(row, rule.bias, E, k, rule, lane, scratch);
+    const int cut = k - 1 + __ffs(after);
+    // the first `cut` values again in 64 bits, one per lane, and their order
+    const double c = lane < cut ? sigmoid64(finite_or_0(row[my_id])) +
+                                      (double)finite_or_0(rule.bias[my_id])
+                                : 0.0;
+    int place = 0;
+#pragma unroll 1
+    for (int s = 0; s < cut; ++s) {
+        const double o = __shfl_sync(0xffffffffu, c, s);
+        const uint32_t e = __shfl_sync(0xffffffffu, my_id, s);
+        if (o > c || (o == c && e < my_id)) ++place;
+    }
+    int idx = 0;
+#pragma unroll 1
+    for (int s = 0; s < cut; ++s) {
+        const int at = __shfl_sync(0xffffffffu, place, s);
+        const uint32_t e = __shfl_sync(0xffffffffu, my_id, s);
+        if (at == lane) idx = (int)e;
+    }
     return idx;
 }
 
 // Chosen expert and weight of lane s < k.
 __device__ __forceinline__ void route_row(const float *__restrict__ row, int E, int k,
                                           const RouteRule &rule, const float (&b)[RS_Q], int lane,
-                                          uint32_t *status, int &my_idx, float &my_w) {
+                                          uint32_t *status, uint64_t *scratch, int &my_idx,
+                                          float &my_w) {
     float l[RS_Q];
     bool bad = false;
 #pragma unroll
     for (int q = 0; q < RS_Q; ++q) {
         const int e = lane + 32 * q;
         l[q] = e < E ? row[e] : 0.f;
-        if (!isfinite(l[q])) {  // reported; any finite value keeps the outputs in range
-            bad = true;
-            l[q] = 0.f;
-        }
+        bad |= !isfinite(l[q]);
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) set_dev_error(status, RVQ_DEV_ERR_NONFINITE);
-    if (choose<float>(l, b, E, k, rule, lane, my_idx)) my_idx = choose_64(l, b, E, k, rule, lane);
-    // the chosen logit: register my_idx / 32 of lane my_idx % 32
-    float mine = 0.f;
+    if (__any_sync(0xffffffffu, bad)) {  // reported; finite values keep the outputs in range
+        if (lane == 0) set_dev_error(status, RVQ_DEV_ERR_NONFINITE);
 #pragma unroll
-    for (int q = 0; q < RS_Q; ++q) {
-        const float v = __shfl_sync(0xffffffffu, l[q], my_idx & 31);
-        if (q == my_idx >> 5) mine = v;
+        for (int q = 0; q < RS_Q; ++q) l[q] = finite_or_0(l[q]);
     }
+    my_idx = choose(l, b, row, E, k, rule, lane, scratch);
     const bool on = lane < k;
+    const float mine = finite_or_0(row[on ? my_idx : 0]);
     const float top = from_key(warp_max(on ? to_key(mine) : 0u));
     float e;
     if (rule.score == MOE_SCORE_SIGMOID) {
-        if (rule.renorm) {
-            // sigmoids over e^m, m the largest logit up to 0: sums of very negative
-            // logits stay away from 0
-            const float m = fminf(top, 0.f);
-            e = mine <= 0.f ? expf(mine - m) / (1.f + expf(mine)) : 1.f / (1.f + expf(-mine));
-        } else {
-            e = 1.f / (1.f + expf(-mine));
-        }
+        // renormalised: sigmoids over e^m, m the largest logit up to 0, so that sums of
+        // very negative logits stay away from 0
+        const float m = rule.renorm ? fminf(top, 0.f) : 0.f;
+        const float t = expf(-fabsf(mine));
+        e = mine <= 0.f ? expf(mine - m) / (1.f + t) : 1.f / (1.f + t);
     } else if (rule.renorm) {
         e = expf(mine - top);
     } else {
@@ -310,6 +411,7 @@ template <int NT>
 __global__ void __launch_bounds__(NT) route_scored_one_kernel(const RouteScoredJob j) {
     __shared__ uint32_t mask[256][2];
     __shared__ int cnt[256];
+    extern __shared__ uint64_t scratch[];  // [warps][E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < 512; i += NT) mask[i >> 1][i & 1] = 0u;
     dependency_wait();
@@ -320,7 +422,8 @@ __global__ void __launch_bounds__(NT) route_scored_one_kernel(const RouteScoredJ
     for (int t = warp; t < j.n; t += NT / 32) {
         int idx;
         float w;
-        route_row(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status, idx, w);
+        route_row(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status,
+                  scratch + warp * j.E, idx, w);
         if (lane < j.k) {
             j.idx[t * j.k + lane] = idx;
             j.w[t * j.k + lane] = w;
@@ -347,20 +450,22 @@ __global__ void __launch_bounds__(NT) route_scored_one_kernel(const RouteScoredJ
 
 // Many tokens, first launch: block b chooses for tokens run * b .. and counts its
 // experts into hist[b][E].
-__global__ void __launch_bounds__(RS_NT) route_scored_choose_kernel(const RouteScoredJob j) {
+__global__ void __launch_bounds__(1024) route_scored_choose_kernel(const RouteScoredJob j) {
     __shared__ int cnt[256];
+    extern __shared__ uint64_t scratch[];  // [warps][E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    cnt[threadIdx.x] = 0;
+    for (int e = threadIdx.x; e < 256; e += blockDim.x) cnt[e] = 0;
     dependency_wait();
     dependents_may_start();
     __syncthreads();
     float b[RS_Q];
     load_bias(j.rule, j.E, lane, j.status, b);
     const int t0 = blockIdx.x * j.run, t1 = min(j.n, t0 + j.run);
-    for (int t = t0 + warp; t < t1; t += RS_NT / 32) {
+    for (int t = t0 + warp; t < t1; t += (int)blockDim.x / 32) {
         int idx;
         float w;
-        route_row(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status, idx, w);
+        route_row(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status,
+                  scratch + warp * j.E, idx, w);
         if (lane < j.k) {
             j.idx[(int64_t)t * j.k + lane] = idx;
             j.w[(int64_t)t * j.k + lane] = w;
@@ -368,53 +473,60 @@ __global__ void __launch_bounds__(RS_NT) route_scored_choose_kernel(const RouteS
         }
     }
     __syncthreads();
-    if (threadIdx.x < j.E) j.hist[blockIdx.x * j.E + threadIdx.x] = cnt[threadIdx.x];
+    for (int e = threadIdx.x; e < j.E; e += blockDim.x) j.hist[blockIdx.x * j.E + e] = cnt[e];
 }
 
 // Second launch: block b places its run's pairs.
-__global__ void __launch_bounds__(RS_NT) route_scored_place_kernel(const RouteScoredJob j) {
+__global__ void __launch_bounds__(RS_PLACE) route_scored_place_kernel(const RouteScoredJob j) {
     extern __shared__ uint32_t mask[];  // [E][words], then [E][words] of 16-bit ranks
     __shared__ int cnt[256], before[256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int words = (j.run + 31) / 32;
     uint16_t *pre = reinterpret_cast<uint16_t *>(mask + j.E * words);
-    for (int i = threadIdx.x; i < j.E * words; i += RS_NT) mask[i] = 0u;
+    for (int i = threadIdx.x; i < j.E * words; i += RS_PLACE) mask[i] = 0u;
+    if (threadIdx.x < 256) cnt[threadIdx.x] = before[threadIdx.x] = 0;
     dependency_wait();
     dependents_may_start();
     __syncthreads();
     const int t0 = blockIdx.x * j.run, t1 = min(j.n, t0 + j.run);
     const int64_t p0 = (int64_t)t0 * j.k;
     const int np = (t1 - t0) * j.k;
-    for (int i = threadIdx.x; i < np; i += RS_NT) {
+    for (int i = threadIdx.x; i < np; i += RS_PLACE) {
         const int t = i / j.k;
         atomicOr(&mask[j.idx[p0 + i] * words + (t >> 5)], 1u << (t & 31));
     }
-    if (threadIdx.x < j.E) {
+    {
+        // counts of all runs and of those before this one: a thread per expert and share
+        // of the runs, all its loads in flight at once
+        const int shares = RS_PLACE / j.E, e = threadIdx.x % j.E, share = threadIdx.x / j.E;
         int all = 0, mine = 0;
-#pragma unroll 8
-        for (int r = 0; r < (int)gridDim.x; ++r) {
-            const int c = j.hist[r * j.E + threadIdx.x];
-            all += c;
-            if (r < (int)blockIdx.x) mine += c;
+        if (share < shares) {
+#pragma unroll 16
+            for (int r = share; r < (int)gridDim.x; r += shares) {
+                const int c = j.hist[r * j.E + e];
+                all += c;
+                mine += r < (int)blockIdx.x ? c : 0;
+            }
+            atomicAdd(&cnt[e], all);
+            atomicAdd(&before[e], mine);
         }
-        cnt[threadIdx.x] = all;
-        before[threadIdx.x] = mine;
     }
     __syncthreads();
     if (warp == 0) {
         const int end = scan_counts(cnt, j.E, lane);
         if (blockIdx.x == 0 && lane == 0) j.offsets[j.E] = end;
-    }
-    for (int e = threadIdx.x; e < j.E; e += RS_NT) {
-        int run = 0;
-        for (int w = 0; w < words; ++w) {
-            pre[e * words + w] = (uint16_t)run;
-            run += __popc(mask[e * words + w]);
+    } else {
+        for (int e = threadIdx.x - 32; e < j.E; e += RS_PLACE - 32) {
+            int run = 0;
+            for (int w = 0; w < words; ++w) {
+                pre[e * words + w] = (uint16_t)run;
+                run += __popc(mask[e * words + w]);
+            }
         }
     }
     __syncthreads();
     if (blockIdx.x == 0 && threadIdx.x < j.E) j.offsets[threadIdx.x] = cnt[threadIdx.x];
-    for (int i = threadIdx.x; i < np; i += RS_NT) {
+    for (int i = threadIdx.x; i < np; i += RS_PLACE) {
         const int t = i / j.k, e = j.idx[p0 + i], at = e * words + (t >> 5);
         j.pairs[cnt[e] + before[e] + pre[at] + __popc(mask[at] & ((1u << (t & 31)) - 1u))] =
             (int32_t)(p0 + i);
@@ -501,27 +613,34 @@ int route_scored_run(int n) {
 }
 
 rvq_status launch_route_scored(const RouteScoredJob &job, cudaStream_t stream) {
-    if (job.n <= kRouteOneBlock) {
-        if (job.n <= 8)
-            RVQ_CUDA(launch_after(route_scored_one_kernel<256>, 1, 256, 0, stream, job));
-        else
-            RVQ_CUDA(launch_after(route_scored_one_kernel<1024>, 1, 1024, 0, stream, job));
-        return RVQ_OK;
-    }
-    RouteScoredJob j = job;
-    j.run = route_scored_run(j.n);
-    const unsigned blocks = (unsigned)((j.n + j.run - 1) / j.run);
-    const size_t smem = (size_t)j.E * ((j.run + 31) / 32) * 6;
     static std::atomic<int> attr_done[64];  // per device; setting twice is harmless
     int dev = 0;
     RVQ_CUDA(cudaGetDevice(&dev));
     if (dev < 64 && !attr_done[dev]) {
         RVQ_CUDA(cudaFuncSetAttribute(route_scored_place_kernel,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10));
+        RVQ_CUDA(cudaFuncSetAttribute(route_scored_choose_kernel,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10));
+        RVQ_CUDA(cudaFuncSetAttribute(route_scored_one_kernel<1024>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10));
         attr_done[dev] = 1;
     }
-    RVQ_CUDA(launch_after(route_scored_choose_kernel, blocks, RS_NT, 0, stream, j));
-    RVQ_CUDA(launch_after(route_scored_place_kernel, blocks, RS_NT, smem, stream, j));
+    if (job.n <= kRouteOneBlock) {
+        if (job.n <= 8)
+            RVQ_CUDA(launch_after(route_scored_one_kernel<256>, 1, 256, 8 * job.E * 8, stream, job));
+        else
+            RVQ_CUDA(launch_after(route_scored_one_kernel<1024>, 1, 1024, 32 * job.E * 8, stream, job));
+        return RVQ_OK;
+    }
+    RouteScoredJob j = job;
+    j.run = route_scored_run(j.n);
+    const unsigned blocks = (unsigned)((j.n + j.run - 1) / j.run);
+    const size_t smem = (size_t)j.E * ((j.run + 31) / 32) * 6;
+    // a warp per token of a run, up to 32
+    const int warps = j.run < 32 ? j.run : 32;
+    RVQ_CUDA(launch_after(route_scored_choose_kernel, blocks, 32 * warps, (size_t)warps * j.E * 8,
+                          stream, j));
+    RVQ_CUDA(launch_after(route_scored_place_kernel, blocks, RS_PLACE, smem, stream, j));
     return RVQ_OK;
 }
 
