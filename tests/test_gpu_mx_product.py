@@ -270,3 +270,22 @@ def test_together():
     vh = X.dequantize(hc, hs, n, f, F8)
     R.check(out, want_linear(vh, vd, None, "none", 1.0, ho, F32), "out")
     assert rvq.rvq_ws_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+@pytest.mark.parametrize("n,rows,cols", [(257, 8, 8), (512, 256, 256), (1025, 520, 2056),
+                                         (4100, 1304, 264)])
+def test_many_tokens(n, rows, cols, xf, wf):
+    """Tiles of CTA pairs: one, several per pair (102 of the last), ragged in every way."""
+    run_linear(n, rows, cols, xf, wf)
+    run_gated(n, rows, cols, xf, wf)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(513, 264, 520), (4100, 712, 136)])
+def test_many_tokens_epilogue(n, rows, cols):
+    run_linear(n, rows, cols, F8, F4, act="gelu", alpha=0.5, bias=True, res=F32, out=BF)
+    run_linear(n, rows, cols, F4, F4, act="silu", res=BF, out=F32)
+    run_linear(n, rows, cols, F4, F4, bias=True, out=HF)
+    for ofmt in (F8, F4):
+        run_gated(n, rows, cols, F8, F4, bias=True, ofmt=ofmt)
+        run_gated(n, rows, cols, F4, F4, act="gelu_tanh", ofmt=ofmt)
