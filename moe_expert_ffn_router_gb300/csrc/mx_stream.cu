@@ -104,6 +104,84 @@ __device__ __forceinline__ void put_block(const StreamArgs &g, int t, int c, con
         g.scales[mx_scale_at(t, c / kMxTile, g.otiles) + (c / kMxBlock & 3)] = (uint8_t)byte;
 }
 
+// Outputs of units first, first + step, .. of `units`: sums of the cluster's parts in rank
+// order, finished and written.
+template <bool GATED, int SPLIT>
+__device__ __forceinline__ void join(const StreamArgs &g, const float *part, int units, int first,
+                                     int step, int r0, int t0) {
+    constexpr int MATS = GATED ? 2 : 1, AT_ONCE = 8 / SPLIT / MATS < 1 ? 1 : 8 / SPLIT / MATS;
+    constexpr int PITCH = MATS * MS_ROWS + 4;
+    for (int base = first & ~1; base < units; base += AT_ONCE * step) {
+        float2 x[AT_ONCE][SPLIT], y[AT_ONCE][SPLIT];
+        float b[AT_ONCE][2];
+        int r[AT_ONCE], tok[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int u = base + (first & 1) + i * step;
+            const bool in = u < units;
+            const int t = in ? u >> 2 : 0, qr = (u & 3) * 32 + (int)(threadIdx.x & 15) * 2;
+            r[i] = r0 + qr;
+            tok[i] = in ? t0 + t : g.n;
+            const uint32_t at = smem_u32(part + t * PITCH + qr);
+#pragma unroll
+            for (int p = 0; p < SPLIT; ++p) {
+                const uint32_t a = cluster_addr(at, (uint32_t)p);
+                x[i][p] = ld_cluster2(a);
+                if (GATED) y[i][p] = ld_cluster2(a + MS_ROWS * 4);
+            }
+            b[i][0] = b[i][1] = 0.f;
+            if (!GATED && g.residual && in && r[i] < g.rows)
+                ld2(g.residual, g.rdt, (int64_t)tok[i] * g.ldr + r[i], b[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            float v[2] = {}, w[2] = {};
+#pragma unroll
+            for (int p = 0; p < SPLIT; ++p) {
+                v[0] += x[i][p].x;
+                v[1] += x[i][p].y;
+                if (GATED) {
+                    w[0] += y[i][p].x;
+                    w[1] += y[i][p].y;
+                }
+            }
+            const bool real = tok[i] < g.n && r[i] < g.rows;
+            if (g.bias[0] && real) {
+                v[0] += g.bias[0][r[i]];
+                v[1] += g.bias[0][r[i] + 1];
+            }
+            act_group(g.act, v);
+            if (GATED) {
+                if (g.bias[1] && real) {
+                    w[0] += g.bias[1][r[i]];
+                    w[1] += g.bias[1][r[i] + 1];
+                }
+                v[0] *= w[0];
+                v[1] *= w[1];
+            } else {
+                v[0] = g.alpha * v[0] + b[i][0];
+                v[1] = g.alpha * v[1] + b[i][1];
+            }
+            if (GATED && g.codes) {
+                if (!real) v[0] = v[1] = 0.f;  // padded columns
+                if (g.ofmt == MOE_MX_F8)
+                    put_block<MOE_MX_F8>(g, tok[i], r[i], v);
+                else
+                    put_block<MOE_MX_F4>(g, tok[i], r[i], v);
+                continue;
+            }
+            if (!real) continue;
+            const int64_t o = (int64_t)tok[i] * g.ldo + r[i];
+            if (g.odt == RVQ_F32)
+                *reinterpret_cast<float2 *>(reinterpret_cast<float *>(g.out) + o) =
+                    make_float2(v[0], v[1]);
+            else
+                *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(g.out) + o) =
+                    pack16(g.odt, v[0], v[1]);
+        }
+    }
+}
+
 template <bool GATED, bool F4>
 __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
     const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
@@ -154,11 +232,9 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
         // (whatever that kernel writes is read coherently after the wait).
         for (int k = k0; k < k1 && k < k0 + g.stages; ++k) {
             tma_prefetch(&mw0, k * 128, r0);
+            if (GATED) tma_prefetch(&mw1, k * 128, r0);
             tma_prefetch(&sw0, k * KT * 128, row_tile);
-            if (GATED) {
-                tma_prefetch(&mw1, k * 128, r0);
-                tma_prefetch(&sw1, k * KT * 128, row_tile);
-            }
+            if (GATED) tma_prefetch(&sw1, k * KT * 128, row_tile);
         }
     }
     dependency_wait();
@@ -216,6 +292,19 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
         }
         if (elect_one()) mma_commit(accfull);
         __syncwarp();
+    } else if (!GATED && g.residual) {
+        // the residual of this CTA's outputs into L2 meanwhile: a row's 128 columns are
+        // four (16-bit: two) lines of 128 bytes
+        const int e = g.rdt == RVQ_F32 ? 4 : 2, lines = e;
+        const int tokens = min(g.n - t0, g.npad);
+        for (int i = (int)threadIdx.x - 64 + rank * (MS_THREADS - 64); i < tokens * lines;
+             i += g.split * (MS_THREADS - 64)) {
+            const int c = r0 + i % lines * (128 / e);
+            if (c < g.rows)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                    reinterpret_cast<const char *>(g.residual) +
+                    ((int64_t)(t0 + i / lines) * g.ldr + c) * e));
+        }
     }
     // the partial tile, [token][row], over the ring (its last slice is consumed)
     warp_wait(accfull, 0, abort_flag, g.status);
@@ -248,75 +337,19 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
     cluster_sync();  // every partial tile of the cluster is in place
     if (ok) {
         // blocks of 32 outputs of a token, dealt over the cluster's half warps; two
-        // outputs per lane, every peer's values requested before the first is added.
-        // Whole warps go through the loop together (the shuffles of put_block).
+        // outputs per lane, and as many blocks at once as make eight loads from the
+        // peers (a block at a time cost a round trip each: 64 tokens 6 us more than
+        // one).  Whole warps go through the loop together (the shuffles of put_block).
         const int units = nt * 4, step = g.split * (MS_THREADS / 16);
         const int first = rank * (MS_THREADS / 16) + (int)(threadIdx.x >> 4);
-        for (int base = 0; base < units; base += step) {
-            const int u = base + first;
-            const bool in = u < units;
-            const int t = in ? u >> 2 : 0, qr = (u & 3) * 32 + (int)(threadIdx.x & 15) * 2;
-            const int r = r0 + qr, tok = t0 + t;
-            const uint32_t at = smem_u32(part + t * PITCH + qr);
-            float2 x[8], y[8];
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                if (p >= g.split) continue;
-                const uint32_t a = cluster_addr(at, (uint32_t)p);
-                x[p] = ld_cluster2(a);
-                if (GATED) y[p] = ld_cluster2(a + MS_ROWS * 4);
-            }
-            float v[2] = {}, w[2] = {};
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                if (p >= g.split) continue;
-                v[0] += x[p].x;
-                v[1] += x[p].y;
-                if (GATED) {
-                    w[0] += y[p].x;
-                    w[1] += y[p].y;
-                }
-            }
-            const bool real = in && r < g.rows;
-            if (g.bias[0] && real) {
-                v[0] += g.bias[0][r];
-                v[1] += g.bias[0][r + 1];
-            }
-            act_group(g.act, v);
-            if (GATED) {
-                if (g.bias[1] && real) {
-                    w[0] += g.bias[1][r];
-                    w[1] += g.bias[1][r + 1];
-                }
-                v[0] *= w[0];
-                v[1] *= w[1];
-            } else {
-                v[0] *= g.alpha;
-                v[1] *= g.alpha;
-                if (g.residual && real) {
-                    float b[2];
-                    ld2(g.residual, g.rdt, (int64_t)tok * g.ldr + r, b);
-                    v[0] += b[0];
-                    v[1] += b[1];
-                }
-            }
-            if (GATED && g.codes) {
-                if (!real) v[0] = v[1] = 0.f;  // padded columns
-                if (g.ofmt == MOE_MX_F8)
-                    put_block<MOE_MX_F8>(g, in ? tok : g.n, r, v);
-                else
-                    put_block<MOE_MX_F4>(g, in ? tok : g.n, r, v);
-                continue;
-            }
-            if (!real) continue;
-            const int64_t o = (int64_t)tok * g.ldo + r;
-            if (g.odt == RVQ_F32)
-                *reinterpret_cast<float2 *>(reinterpret_cast<float *>(g.out) + o) =
-                    make_float2(v[0], v[1]);
-            else
-                *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(g.out) + o) =
-                    pack16(g.odt, v[0], v[1]);
-        }
+        if (g.split == 8)
+            join<GATED, 8>(g, part, units, first, step, r0, t0);
+        else if (g.split == 4)
+            join<GATED, 4>(g, part, units, first, step, r0, t0);
+        else if (g.split == 2)
+            join<GATED, 2>(g, part, units, first, step, r0, t0);
+        else
+            join<GATED, 1>(g, part, units, first, step, r0, t0);
     }
     cluster_sync();  // the peers' tiles stay in place until read
     if (warp == 2) {
@@ -325,7 +358,37 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
     }
 }
 
-constexpr int kRingSmall = 96 << 10, kRingLarge = 200 << 10;
+// of one CTA where two share an SM, and of one alone
+constexpr int kRingSmall = 111 << 10, kRingLarge = 200 << 10;
+
+// Clusters of `split` CTAs that the device holds at once with one CTA per SM (the query
+// does not count a second one per SM; it gives 15 clusters of eight, 36 of four).
+template <bool GATED, bool F4>
+int resident_clusters(int split) {
+    static std::atomic<int> cached[64][4];  // per device and split, plus one
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+    std::atomic<int> &known = cached[dev][split == 8 ? 3 : split == 4 ? 2 : split - 1];
+    if (known) return known - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms() / split * split));
+    cfg.blockDim = dim3(MS_THREADS);
+    cfg.dynamicSmemBytes = kRingLarge;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, mx_stream_kernel<GATED, F4>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();  // not the caller's error: the depth stays whole
+        n = 0;
+    }
+    known = n + 1;
+    return n;
+}
 
 template <bool GATED, bool F4>
 rvq_status launch(const MxJob &job, cudaStream_t stream) {
@@ -350,17 +413,24 @@ rvq_status launch(const MxJob &job, cudaStream_t stream) {
         set_error("microscaled product: %lld tiles", tiles);
         return RVQ_ENOTIMPL;
     }
-    // Depth split: as many CTAs as are resident at once, each with two slices or more.
-    const int sms = num_sms();
-    g.split = 1;
-    while (g.split < 8 && tiles * g.split * 2 <= sms && g.slices >= g.split * 4) g.split *= 2;
-    const int ring = kRingLarge;
+    g.cols = 32;
+    while ((int)g.cols < MATS * g.npad + (MATS + 1) * KT * 4) g.cols *= 2;
     g.stage = (MATS * MS_ABYTES + g.npad * 128 + (MATS + 1) * KT * kMxTileBytes + 1023) / 1024 * 1024;
+    // Two CTAs per SM where both fit (a ring of two stages or more and 256 columns of
+    // tensor memory each), and the depth split among as many CTAs, up to eight, as leaves
+    // every cluster resident at once, with two slices or more each.  One token, gated
+    // 7168 -> 2048, 16 tiles of 4-bit weights: eight CTAs each 7.7 us, four 9.7; with the
+    // large ring, where a sixteenth cluster of eight waits for the others, 13.7; 2048 ->
+    // 7168, 56 tiles: four 5.5, eight 9.5, two 6.5.
+    const bool two = g.cols <= 256 && 2 * g.stage <= kRingSmall;
+    const int ring = two ? kRingSmall : kRingLarge;
+    g.split = 8;
+    while (g.split > 1 &&
+           (g.slices < 2 * g.split || tiles > (two ? 2 : 1) * resident_clusters<GATED, F4>(g.split)))
+        g.split /= 2;
     g.stages = ring / g.stage < MS_MAX_ST ? ring / g.stage : MS_MAX_ST;
     g.expect = MATS * slice_bytes(F4, job.wfmt, MS_ROWS) + slice_bytes(F4, job.xfmt, g.npad) +
                (MATS + 1) * KT * kMxTileBytes;
-    g.cols = 32;
-    while ((int)g.cols < MATS * g.npad + (MATS + 1) * KT * 4) g.cols *= 2;
     g.idesc = mx_idesc(F4, job.wfmt, job.xfmt, MS_ROWS, g.npad);
     g.act = job.act;
     g.rdt = job.rdt;
