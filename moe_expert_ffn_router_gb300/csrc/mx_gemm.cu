@@ -65,9 +65,26 @@ struct MxGemmParams {
     MxGemmArgs g;
 };
 
+// Relaxed: what the barrier guards is tensor memory, whose loads have been waited for
+// (a release would wait for the warp's stores to global memory too).
 __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
                  : "memory");
+}
+
+// Registers move from the warps that only issue to those of the epilogue: the shares
+// add up to what the block was launched with.
+constexpr int MG_REGS = 168, MG_REGS_ISSUE = 56, MG_REGS_EPI = 224;
+static_assert(MG_THREADS * MG_REGS <= 65536 &&
+                  128 * MG_REGS_ISSUE + 32 * MG_EPI_WARPS * MG_REGS_EPI <= MG_THREADS * MG_REGS,
+              "registers of a block");
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // box at (col, row) into this CTA's shared memory, counted on the leader's barrier
@@ -200,87 +217,91 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(
     const uint32_t tmem = *tslot;
     dependency_wait();
 
-    if (warp == 0) {
-        // producer: this CTA's rows of both operands for every slice, and the scales
-        int s = 0;
-        uint32_t lap = 0;  // trips around the ring
-        bool ok = true;
-        for (int t = pair; ok && t < tiles; t += pairs) {
-            int m, n;
-            tile_at(g, t, m, n);
-            const int a0 = m * 2 + (int)rank;                          // groups of 128 rows
-            const int b0 = GATED ? n : n * 2 + (int)rank;
-            const CUtensorMap *mb = &p.b[GATED ? rank : 0];
-            for (int k = 0; k < g.slices; ++k) {
-                if (lap > 0 && !warp_wait(empty0 + 8 * s, (lap - 1) & 1, abort_flag, g.status)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t st = smem_u32(smem + s * S::BYTES);
-                const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
-                const int kx = k * 128, ks = k * S::KT * 128;
-                if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, g.expect);
-                    tma_pair(st, &p.a, kx, a0 * MG_ROWS, bar);
-                    tma_pair(st + S::B, mb, kx, b0 * MG_ROWS, bar);
-                    tma_pair(st + S::SA, &p.sa, ks, a0, bar);
-                    if (GATED) {
-                        tma_pair(st + S::SB, &p.sb[0], ks, n, bar);
-                        tma_pair(st + S::SB + S::KT * kMxTileBytes, &p.sb[1], ks, n, bar);
-                    } else {
-                        tma_pair(st + S::SB, &p.sb[0], ks, 2 * n, bar);
+    if (warp < 4) {
+        fewer_registers<MG_REGS_ISSUE>();
+        if (warp == 0) {
+            // producer: this CTA's rows of both operands for every slice, and the scales
+            int s = 0;
+            uint32_t lap = 0;  // trips around the ring
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                int m, n;
+                tile_at(g, t, m, n);
+                const int a0 = m * 2 + (int)rank;                          // groups of 128 rows
+                const int b0 = GATED ? n : n * 2 + (int)rank;
+                const CUtensorMap *mb = &p.b[GATED ? rank : 0];
+                for (int k = 0; k < g.slices; ++k) {
+                    if (lap > 0 && !warp_wait(empty0 + 8 * s, (lap - 1) & 1, abort_flag, g.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(smem + s * S::BYTES);
+                    const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
+                    const int kx = k * 128, ks = k * S::KT * 128;
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, g.expect);
+                        tma_pair(st, &p.a, kx, a0 * MG_ROWS, bar);
+                        tma_pair(st + S::B, mb, kx, b0 * MG_ROWS, bar);
+                        tma_pair(st + S::SA, &p.sa, ks, a0, bar);
+                        if (GATED) {
+                            tma_pair(st + S::SB, &p.sb[0], ks, n, bar);
+                            tma_pair(st + S::SB + S::KT * kMxTileBytes, &p.sb[1], ks, n, bar);
+                        } else {
+                            tma_pair(st + S::SB, &p.sb[0], ks, 2 * n, bar);
+                        }
+                    }
+                    __syncwarp();
+                    if (++s == MG_STAGES) {
+                        s = 0;
+                        ++lap;
                     }
                 }
-                __syncwarp();
-                if (++s == MG_STAGES) {
-                    s = 0;
-                    ++lap;
-                }
             }
-        }
-    } else if (warp == 1 && rank == 0) {
-        // issuer: the slice's scales, then four MMAs
-        int s = 0, done = 0;
-        uint32_t lap = 0;
-        bool ok = true;
-        const uint32_t tsa = tmem + MG_SCALES, tsb = tsa + 4 * S::KT;
-        for (int t = pair; ok && t < tiles; t += pairs, ++done) {
-            if (done >= 1 && !warp_wait(accempty, (done - 1) & 1, abort_flag, g.status)) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            for (int k = 0; k < g.slices; ++k) {
-                if (!warp_wait(full0 + 8 * s, lap & 1, abort_flag, g.status)) {
-                    ok = false;
-                    break;
-                }
+        } else if (warp == 1 && rank == 0) {
+            // issuer: the slice's scales, then four MMAs
+            int s = 0, done = 0;
+            uint32_t lap = 0;
+            bool ok = true;
+            const uint32_t tsa = tmem + MG_SCALES, tsb = tsa + 4 * S::KT;
+            for (int t = pair; ok && t < tiles; t += pairs, ++done) {
+                if (done >= 1 && !warp_wait(accempty, (done - 1) & 1, abort_flag, g.status)) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t st = smem_u32(smem + s * S::BYTES);
-                const uint64_t a = smem_desc(st), b = smem_desc(st + S::B);
-                if (elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < S::KT; ++i) {
-                        copy_scales<2>(tsa + 4 * i, st + S::SA + i * kMxTileBytes);
-                        copy_scales<2>(tsb + 8 * i, st + S::SB + i * kMxTileBytes);
-                        copy_scales<2>(tsb + 8 * i + 4, st + S::SB + (S::KT + i) * kMxTileBytes);
+                for (int k = 0; k < g.slices; ++k) {
+                    if (!warp_wait(full0 + 8 * s, lap & 1, abort_flag, g.status)) {
+                        ok = false;
+                        break;
                     }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t st = smem_u32(smem + s * S::BYTES);
+                    const uint64_t a = smem_desc(st), b = smem_desc(st + S::B);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int kt = F4 ? q >> 1 : 0;
-                        mx_mma<2, F4>(tmem, a + 2 * q, b + 2 * q,
-                                      g.idesc | scale_places(F4 ? 2 * (q & 1) : q), tsa + 4 * kt,
-                                      tsb + 8 * kt, (k > 0 || q > 0) ? 1u : 0u);
+                        for (int i = 0; i < S::KT; ++i) {
+                            copy_scales<2>(tsa + 4 * i, st + S::SA + i * kMxTileBytes);
+                            copy_scales<2>(tsb + 8 * i, st + S::SB + i * kMxTileBytes);
+                            copy_scales<2>(tsb + 8 * i + 4, st + S::SB + (S::KT + i) * kMxTileBytes);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int kt = F4 ? q >> 1 : 0;
+                            mx_mma<2, F4>(tmem, a + 2 * q, b + 2 * q,
+                                          g.idesc | scale_places(F4 ? 2 * (q & 1) : q), tsa + 4 * kt,
+                                          tsb + 8 * kt, (k > 0 || q > 0) ? 1u : 0u);
+                        }
+                        commit_pair(empty0 + 8 * s);
                     }
-                    commit_pair(empty0 + 8 * s);
+                    __syncwarp();
+                    if (++s == MG_STAGES) {
+                        s = 0;
+                        ++lap;
+                    }
                 }
+                if (elect_one()) commit_pair(accfull);
                 __syncwarp();
-                if (++s == MG_STAGES) {
-                    s = 0;
-                    ++lap;
-                }
             }
-            if (elect_one()) commit_pair(accfull);
-            __syncwarp();
         }
-    } else if (warp >= 4) {
+    } else {
+        more_registers<MG_REGS_EPI>();
         // epilogue: lanes 32 q .. 32 q + 31 of the accumulator, one half of its columns
         const int q = warp & 3, par = (warp - 4) >> 2;
         const uint32_t turn = smem_u32(smem + S::TURN) + (uint32_t)(warp - 4) * MG_TURN;
@@ -318,6 +339,9 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(
                 float x[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
+                Residual res;
+                if (!GATED && g.residual && width > 0 && row < g.M)
+                    res.load(g.residual, g.rdt, g.ldr, lane, row, g.M, col, width);
                 if (width > 0 && row < g.M) {
                     if (g.bias[0]) add_bias(g.bias[0], col, width, x);
                     if (g.act != MOE_ACT_NONE) act_group(g.act, x);
@@ -350,9 +374,6 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(
                         rows_16_plain(turn, lane, g.out, g.odt, g.ldo, row, g.M, col, width, x);
                     } else {
                         turn_in(turn, lane, x);
-                        Residual res;
-                        if (!GATED && g.residual)
-                            res.load(g.residual, g.rdt, g.ldr, lane, row, g.M, col, width);
                         turn_rows(turn, lane, g.out, g.odt, g.ldo, row, g.M, col, width,
                                   !GATED && g.residual ? &res : nullptr, g.rdt);
                     }
