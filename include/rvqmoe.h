@@ -846,6 +846,11 @@ typedef enum moe_way {
 rvq_status rvq_selftest_dense_plan(int32_t gated, int32_t backward, int32_t n, int32_t rows,
                                    int32_t cols, int32_t out[7]);
 
+/* The same of moe_mx_linear or (gated) moe_mx_gated_linear: out[0] is MOE_WAY_STREAM or
+ * MOE_WAY_TILES, out[1] the CTAs that the depth of a streamed product is split among. */
+rvq_status rvq_selftest_mx_plan(int32_t gated, moe_mx xfmt, moe_mx wfmt, int32_t n, int32_t rows,
+                                int32_t cols, int32_t out[2]);
+
 /* Self-test of the failure path of the tensor-core kernel (no counterpart in
  * the pages): launches the prefill GEMM on one zero token routed to expert 0
  * with its MMA role first waiting for an mbarrier arrival that nothing makes.

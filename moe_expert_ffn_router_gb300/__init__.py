@@ -160,6 +160,7 @@ _SIGS = {
     "moe_norm_join_mx": (_i32, [_vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _i32, _i32, _i32, _vp,
                                 _vp, _i32, _f32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp]),
     "rvq_selftest_dense_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
+    "rvq_selftest_mx_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
     "rvq_selftest_prefill_timeout": (_i32, [_BANKP, _vp, _sz, _vp]),
     "rvq_ws_clear": (_i32, [_vp, _vp]),
     "rvq_ws_status": (_i32, [_vp, ctypes.POINTER(_u32), _vp]),
@@ -874,6 +875,15 @@ def moe_mx_gated_linear(x, x_scales, wg, wg_scales, wu, wu_scales, n, rows, cols
                                   ldo, pc, ps, ofmt, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
     if rc:
         _check("moe_mx_gated_linear", rc)
+
+
+def rvq_selftest_mx_plan(gated, xfmt, wfmt, n, rows, cols) -> tuple[str, int]:
+    """How moe_mx_linear or (gated) moe_mx_gated_linear computes its product: "stream" or
+    "tiles", and the CTAs that the depth of a streamed one is split among."""
+    out = (_i32 * 2)()
+    _check("rvq_selftest_mx_plan",
+           _lib.rvq_selftest_mx_plan(int(gated), xfmt, wfmt, n, rows, cols, out))
+    return MOE_WAYS[out[0]], out[1]
 
 
 def moe_norm_join_mx(y, n, d, h_out, codes, scales, fmt=MOE_MX_F8, xn=None, h=None, alpha=1.0,

@@ -218,6 +218,20 @@ rvq_status moe_mx_gated_linear(const uint8_t *x_dev, const uint8_t *x_scales_dev
     return launch_mx_product(j, (cudaStream_t)stream);
 }
 
+rvq_status rvq_selftest_mx_plan(int32_t gated, moe_mx xfmt, moe_mx wfmt, int32_t n, int32_t rows,
+                                int32_t cols, int32_t out[2]) {
+    const char *who = "rvq_selftest_mx_plan";
+    CHECK_ARG(mx_product_shape(n, rows, cols) && mx_format((int)xfmt) && mx_format((int)wfmt) && out,
+              "%s: n %d, rows %d, cols %d, formats %d and %d, out %p", who, n, rows, cols, (int)xfmt,
+              (int)wfmt, (void *)out);
+    const MxJob j = mx_job(gated ? 2 : 1, n, rows, cols, nullptr, nullptr, (int)xfmt, (int)wfmt, 0,
+                           nullptr);
+    const bool tiles = mx_by_tiles(j);
+    out[0] = tiles ? MOE_WAY_TILES : MOE_WAY_STREAM;
+    out[1] = tiles ? 1 : plan_mx_stream(j).split;
+    return RVQ_OK;
+}
+
 rvq_status moe_norm_join_mx(const void *h_dev, rvq_dtype hdt, const void *y_dev, rvq_dtype ydt,
                             int32_t n, int32_t d, float alpha, const void *gate_dev,
                             moe_gate gate_kind, rvq_dtype gdt, int32_t post_norm,

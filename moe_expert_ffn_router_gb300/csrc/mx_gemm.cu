@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1) mx_gemm_kernel(
                     bytes |= byte << (8 * i);
                     if (i == STEPS - 1 && on)
                         *reinterpret_cast<uint16_t *>(
-                            g.scales + mx_scale_at(row + lane, n, g.otiles) + 2 * par) = (uint16_t)bytes;
+                            g.scales + mx_scale_at(row + lane, n, g.otiles) + 2 * par) =
+                            (uint16_t)bytes;
                 } else if (width > 0 && row < g.M) {
                     if (g.odt != RVQ_F32 && g.residual == nullptr) {
                         rows_16_plain(turn, lane, g.out, g.odt, g.ldo, row, g.M, col, width, x);
@@ -467,9 +468,6 @@ rvq_status launch_tiles(const MxJob &job, cudaStream_t stream) {
     return RVQ_OK;
 }
 
-// Tokens from which tiles beat the stream of weights.
-bool tiles_fit(const MxJob &job) { return job.n > 256; }
-
 }  // namespace
 
 static rvq_status encode(CUtensorMap *map, CUtensorMapDataType type, const void *p, uint64_t inner,
@@ -511,11 +509,35 @@ rvq_status encode_scales(CUtensorMap *map, const uint8_t *scales, int rows, int 
                   words * 4, f4 ? 256 : 128, (uint32_t)box_tiles, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Past 128 tokens the faster by a model of both (measured, us, stream / tiles; 8-bit
+// tokens and 4-bit weights: gated 7168 -> 2048, 256 tokens 15.6 / 22.8, 512 22.9 / 21.7;
+// plain 7168 -> 2048, 512 13.4 / 21.6, 1024 18.6 / 21.7; 2048 -> 7168 with a residual, 256
+// 13.3 / 16.2, 384 19.4 / 16.3; 1736 -> 4104, 256 9.7 / 11.6, 777 15.8 / 10.7; two 4-bit
+// operands: gated 256 12.7 / 15.4, 384 15.8 / 13.8).  A slice takes a CTA of the stream
+// 0.42 us (0.66 with two matrices) and a pair of CTAs 0.31 (0.33 of two 4-bit operands,
+// bound by their fill); launch and outputs take both 6 us.
+bool mx_by_tiles(const MxJob &job) {
+    if (job.n <= 128) return false;
+    const MxStreamPlan s = plan_mx_stream(job);
+    const int pairs = num_sms() / 2;
+    const long long slots = (long long)num_sms() * (s.two ? 2 : 1);
+    const long long rounds = s.split > 1 ? 1 : (s.tiles + slots - 1) / slots;
+    const long long per = (s.slices + s.split - 1) / s.split;
+    const double stream = 6.3 + rounds * per * (job.mats == 2 ? 0.66 : 0.42);
+    const long long tiles = (long long)((job.n + 255) / 256) *
+                            (job.mats == 2 ? mx_tiles(job.rows) : (job.rows + 255) / 256);
+    const double tiled =
+        6.2 + (double)((tiles + pairs - 1) / pairs) * s.slices * (job.f4() ? 0.33 : 0.31);
+    return tiled < stream;
+}
+
 rvq_status launch_mx_product(const MxJob &job, cudaStream_t stream) {
-    if (!tiles_fit(job)) return launch_mx_stream(job, stream);
+    if (!mx_by_tiles(job)) return launch_mx_stream(job, stream);
     if (job.mats == 2)
-        return job.f4() ? launch_tiles<true, true>(job, stream) : launch_tiles<true, false>(job, stream);
-    return job.f4() ? launch_tiles<false, true>(job, stream) : launch_tiles<false, false>(job, stream);
+        return job.f4() ? launch_tiles<true, true>(job, stream)
+                        : launch_tiles<true, false>(job, stream);
+    return job.f4() ? launch_tiles<false, true>(job, stream)
+                    : launch_tiles<false, false>(job, stream);
 }
 
 }  // namespace rvq

@@ -382,12 +382,49 @@ int resident_clusters(int split) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mx_stream_kernel<GATED, F4>, &cfg) != cudaSuccess) {
+    if (cudaFuncSetAttribute(mx_stream_kernel<GATED, F4>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kRingLarge) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, mx_stream_kernel<GATED, F4>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();  // not the caller's error: the depth stays whole
         n = 0;
     }
     known = n + 1;
     return n;
+}
+
+// Tokens of a tile, padded to a multiple of 16; bytes of a stage; TMEM columns.
+struct Shape {
+    int npad, stage;
+    uint32_t cols;
+};
+template <bool GATED, bool F4>
+Shape shape_of(const MxJob &job) {
+    constexpr int MATS = GATED ? 2 : 1, KT = F4 ? 2 : 1;
+    Shape s;
+    s.npad = ((job.n < MS_TOKENS ? job.n : MS_TOKENS) + 15) / 16 * 16;
+    s.stage = (MATS * MS_ABYTES + s.npad * 128 + (MATS + 1) * KT * kMxTileBytes + 1023) / 1024 * 1024;
+    s.cols = 32;
+    while ((int)s.cols < MATS * s.npad + (MATS + 1) * KT * 4) s.cols *= 2;
+    return s;
+}
+
+// Two CTAs per SM where both fit (a ring of two stages or more and 256 columns of
+// tensor memory each), and the depth split among as many CTAs, up to eight, as leaves
+// every cluster resident at once, with two slices or more each.  One token, gated
+// 7168 -> 2048, 16 tiles of 4-bit weights: eight CTAs each 7.7 us, four 9.7; with the
+// large ring, where a sixteenth cluster of eight waits for the others, 13.7; 2048 ->
+// 7168, 56 tiles: four 5.5, eight 9.5, two 6.5.
+template <bool GATED, bool F4>
+MxStreamPlan plan_of(const MxJob &job, const Shape &s) {
+    MxStreamPlan p;
+    p.slices = F4 ? (mx_tiles(job.cols) + 1) / 2 : mx_tiles(job.cols);
+    p.tiles = (long long)mx_tiles(job.rows) * ((job.n + MS_TOKENS - 1) / MS_TOKENS);
+    p.two = s.cols <= 256 && 2 * s.stage <= kRingSmall;
+    p.split = 8;
+    while (p.split > 1 && (p.slices < 2 * p.split ||
+                           p.tiles > (p.two ? 2 : 1) * resident_clusters<GATED, F4>(p.split)))
+        p.split /= 2;
+    return p;
 }
 
 template <bool GATED, bool F4>
@@ -401,33 +438,22 @@ rvq_status launch(const MxJob &job, cudaStream_t stream) {
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kRingLarge));
         attr_done[dev] = 1;
     }
+    const Shape s = shape_of<GATED, F4>(job);
+    const MxStreamPlan plan = plan_of<GATED, F4>(job, s);
+    if (plan.tiles > 0x7fffffff / 8) {
+        set_error("microscaled product: %lld tiles", plan.tiles);
+        return RVQ_ENOTIMPL;
+    }
     StreamArgs g = {};
     g.n = job.n;
     g.rows = job.rows;
-    g.slices = (mx_tiles(job.cols) + KT - 1) / KT;
-    const int most = job.n < MS_TOKENS ? job.n : MS_TOKENS;  // tokens of a tile
-    g.npad = (most + 15) / 16 * 16;
+    g.slices = plan.slices;
+    g.npad = s.npad;
     g.tiles = mx_tiles(job.rows);
-    const long long tiles = (long long)g.tiles * ((job.n + MS_TOKENS - 1) / MS_TOKENS);
-    if (tiles > 0x7fffffff / 8) {
-        set_error("microscaled product: %lld tiles", tiles);
-        return RVQ_ENOTIMPL;
-    }
-    g.cols = 32;
-    while ((int)g.cols < MATS * g.npad + (MATS + 1) * KT * 4) g.cols *= 2;
-    g.stage = (MATS * MS_ABYTES + g.npad * 128 + (MATS + 1) * KT * kMxTileBytes + 1023) / 1024 * 1024;
-    // Two CTAs per SM where both fit (a ring of two stages or more and 256 columns of
-    // tensor memory each), and the depth split among as many CTAs, up to eight, as leaves
-    // every cluster resident at once, with two slices or more each.  One token, gated
-    // 7168 -> 2048, 16 tiles of 4-bit weights: eight CTAs each 7.7 us, four 9.7; with the
-    // large ring, where a sixteenth cluster of eight waits for the others, 13.7; 2048 ->
-    // 7168, 56 tiles: four 5.5, eight 9.5, two 6.5.
-    const bool two = g.cols <= 256 && 2 * g.stage <= kRingSmall;
-    const int ring = two ? kRingSmall : kRingLarge;
-    g.split = 8;
-    while (g.split > 1 &&
-           (g.slices < 2 * g.split || tiles > (two ? 2 : 1) * resident_clusters<GATED, F4>(g.split)))
-        g.split /= 2;
+    g.cols = s.cols;
+    g.stage = s.stage;
+    g.split = plan.split;
+    const int ring = plan.two ? kRingSmall : kRingLarge;
     g.stages = ring / g.stage < MS_MAX_ST ? ring / g.stage : MS_MAX_ST;
     g.expect = MATS * slice_bytes(F4, job.wfmt, MS_ROWS) + slice_bytes(F4, job.xfmt, g.npad) +
                (MATS + 1) * KT * kMxTileBytes;
@@ -459,10 +485,10 @@ rvq_status launch(const MxJob &job, cudaStream_t stream) {
     RVQ_TRY(encode_codes(&mx, job.x, job.n, job.cols, job.xfmt, F4, g.npad));
     RVQ_TRY(encode_scales(&sx, job.xs, job.n, job.cols, F4, 1));
     // the ring, or the partial tile that takes its place
-    const int part = most * (MATS * MS_ROWS + 4) * 4;
+    const int part = (job.n < MS_TOKENS ? job.n : MS_TOKENS) * (MATS * MS_ROWS + 4) * 4;
     const int dyn = g.stages * g.stage > part ? g.stages * g.stage : part;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * g.split));
+    cfg.gridDim = dim3((unsigned)(plan.tiles * g.split));
     cfg.blockDim = dim3(MS_THREADS);
     cfg.dynamicSmemBytes = (size_t)dyn;
     cfg.stream = stream;
@@ -482,6 +508,14 @@ rvq_status launch(const MxJob &job, cudaStream_t stream) {
 }
 
 }  // namespace
+
+MxStreamPlan plan_mx_stream(const MxJob &job) {
+    if (job.mats == 2)
+        return job.f4() ? plan_of<true, true>(job, shape_of<true, true>(job))
+                        : plan_of<true, false>(job, shape_of<true, false>(job));
+    return job.f4() ? plan_of<false, true>(job, shape_of<false, true>(job))
+                    : plan_of<false, false>(job, shape_of<false, false>(job));
+}
 
 rvq_status launch_mx_stream(const MxJob &job, cudaStream_t stream) {
     if (job.mats == 2)

@@ -101,6 +101,18 @@ struct MxJob {
     bool f4() const { return xfmt == MOE_MX_F4 && wfmt == MOE_MX_F4; }
 };
 rvq_status launch_mx_product(const MxJob &job, cudaStream_t stream);
+
+// How a product's weights are streamed: CTAs that share a tile's depth, tiles (of 128
+// weight rows, up to 128 tokens), slices of the whole depth, and whether two CTAs fit an
+// SM.
+struct MxStreamPlan {
+    int split, slices;
+    long long tiles;
+    bool two;
+};
+MxStreamPlan plan_mx_stream(const MxJob &job);
 rvq_status launch_mx_stream(const MxJob &job, cudaStream_t stream);
+// Whether tiles of CTA pairs take the product (n, rows, cols, mats and formats of job).
+bool mx_by_tiles(const MxJob &job);
 
 }  // namespace rvq

@@ -289,3 +289,26 @@ def test_many_tokens_epilogue(n, rows, cols):
     for ofmt in (F8, F4):
         run_gated(n, rows, cols, F8, F4, bias=True, ofmt=ofmt)
         run_gated(n, rows, cols, F4, F4, act="gelu_tanh", ofmt=ofmt)
+
+
+# one shape for every way of a product: (gated, formats, n, rows, cols)
+WAYS = {("stream", 1): (False, F8, F4, 5, 136, 264), ("stream", 2): (False, F8, F4, 9, 264, 520),
+        ("stream", 4): (True, F8, F4, 40, 136, 1040), ("stream", 8): (True, F4, F4, 3, 264, 4360),
+        ("tiles", 1): (False, F8, F4, 2040, 2040, 1032)}
+MORE_WAYS = [(("stream", 1), (True, F4, F4, 20, 136, 520)),
+             (("stream", 4), (True, F8, F4, 200, 1032, 2056)),
+             (("stream", 8), (False, F8, F8, 128, 1000, 2056)),
+             (("tiles", 1), (True, F4, F4, 1100, 1032, 520))]
+
+
+@pytest.mark.parametrize("way,case", list(WAYS.items()) + MORE_WAYS)
+def test_ways(way, case):
+    """Streams whole and split among two, four and eight CTAs, and tiles: the shapes take
+    the way they are meant for."""
+    gated, xf, wf, n, rows, cols = case
+    assert rvq.rvq_selftest_mx_plan(gated, xf, wf, n, rows, cols) == way
+    if gated:
+        run_gated(n, rows, cols, xf, wf, bias=True)
+        run_gated(n, rows, cols, xf, wf, ofmt=F8)
+    else:
+        run_linear(n, rows, cols, xf, wf, bias=True, act="silu", res=F32)
