@@ -15,7 +15,8 @@
 //    the next, the worst group kept and the best dropped) are within the error of the
 //    32-bit ones (under 1 % of rows of 256 experts).  Without a bias c grows with l, and
 //    the logits themselves are the keys.
-//  * Up to 64 tokens one block chooses and groups.  More: blocks of equal runs of tokens
+//  * Up to 8 tokens one block chooses and groups (64 would take it 29 us, two launches
+//    11).  More: blocks of equal runs of tokens
 //    choose and count their experts, and a second launch places every pair from the
 //    counts of the runs before its own and a bitmap of tokens per expert in its run.
 //    No atomics on order: pairs are sorted by (expert, token).
@@ -27,12 +28,12 @@ namespace {
 
 constexpr int RS_NT = 256;
 constexpr int RS_PLACE = 1024;  // threads of a placing block
-constexpr int RS_Q = 8;  // experts per lane
+constexpr int RS_Q = 8;          // experts per lane, at most
 
 // Order-preserving keys (after -0 -> +0): larger value, larger key, never 0.
 __device__ __forceinline__ uint32_t to_key(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t to_key(double f) {
     const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
@@ -60,8 +61,8 @@ __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
-// 1 / (1 + e^-l): expf's two units, half a step of the sum, two of the quotient's
-__device__ __forceinline__ float sigmoid32(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
+// 1 / (1 + e^-l), from the fast exponential (2 + 1.2 |l| units of its last place)
+__device__ __forceinline__ float sigmoid32(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
 
 // Groups of a row that stay, as bits: lane g holds the value of group g.
@@ -143,46 +144,49 @@ __device__ __noinline__ int choose_64(const float *row, const float *bias, int E
 // The k experts of a row: lane s < k gets the s-th.  l, b: logits and biases of the
 // lane's experts, finite.
 //
-// Error of a 32-bit score: sigmoid p (1 - p) 2.4e-7 and p 3e-7, at most 4e-7; softmax
-// p (6 + |l - m|) 2^-23 with p |l - m| <= 0.37, and 14 half steps of the sum, at most
-// 1.7e-6.  Two values c are told apart by more than twice that and a step of the larger
+// Error of a 32-bit score: sigmoid p (1 - p) (2 + 1.2 |l|) 2^-23, where p (1 - p) |l| is at
+// most 0.23 (the exponential), and p 3e-7 (the sum's half step, two units of the
+// quotient), at most 4e-7; softmax p (6 + 2.2 |l - m|) 2^-23 with p |l - m| <= 0.37, and 14
+// half steps of the sum, at most 1.7e-6.  Two values c are told apart by more than twice that and a step of the larger
 // |c|; sums of two by twice as much.
-__device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[RS_Q],
+template <int Q>
+__device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
                                       const float *row, int E, int k, const RouteRule &rule,
                                       int lane, uint64_t *scratch) {
     const bool biased = rule.bias != nullptr, grouped = rule.top_groups < rule.groups;
     const int size = E / rule.groups;
-    uint32_t key[RS_Q];
+    uint32_t key[Q];
     float apart = 0.f;
     if (biased || grouped) {
-        float p[RS_Q];
+        float p[Q];
         if (rule.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-            for (int q = 0; q < RS_Q; ++q) p[q] = sigmoid32(l[q]);
+            for (int q = 0; q < Q; ++q) p[q] = sigmoid32(l[q]);
         } else {
             uint32_t top = 0;
 #pragma unroll
-            for (int q = 0; q < RS_Q; ++q)
+            for (int q = 0; q < Q; ++q)
                 if (lane + 32 * q < E) top = max(top, to_key(l[q]));
             const float m = from_key(warp_max(top));
             float z = 0.f;
 #pragma unroll
-            for (int q = 0; q < RS_Q; ++q) {
-                p[q] = lane + 32 * q < E ? expf(l[q] - m) : 0.f;
+            for (int q = 0; q < Q; ++q) {
+                p[q] = lane + 32 * q < E ? __expf(l[q] - m) : 0.f;
                 z += p[q];
             }
             const float inv = 1.f / warp_sum(z);
 #pragma unroll
-            for (int q = 0; q < RS_Q; ++q) p[q] *= inv;
+            for (int q = 0; q < Q; ++q) p[q] *= inv;
         }
         uint32_t big = 0;
 #pragma unroll
-        for (int q = 0; q < RS_Q; ++q) {
+        for (int q = 0; q < Q; ++q) {
             const float c = p[q] + b[q];
             key[q] = lane + 32 * q < E ? to_key(c) : 0u;
             big = max(big, __float_as_uint(c) & 0x7FFFFFFFu);
         }
-        apart = 3.6e-6f + 2.4e-7f * __uint_as_float(warp_max(big));
+        apart = (rule.score == MOE_SCORE_SIGMOID ? 8.4e-7f : 3.6e-6f) +
+                2.4e-7f * __uint_as_float(warp_max(big));
     }
     const bool whole = size % 32 == 0;  // register q is of group 32 q / size
     uint32_t stays = 0xffu;             // bit q: expert lane + 32 q is of a group that stays
@@ -192,7 +196,7 @@ __device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[R
             uint32_t a1 = 0, a2 = 0;
             int next = size / 32, g = 0;
 #pragma unroll
-            for (int q = 0; q < RS_Q; ++q) {
+            for (int q = 0; q < Q; ++q) {
                 a2 = max(a2, min(a1, key[q]));
                 a1 = max(a1, key[q]);
                 if (q + 1 == next) {
@@ -211,7 +215,7 @@ __device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[R
                 const int lo = g * size - lane;  // 32 q of its members: lo .. lo + size - 1
                 uint32_t a1 = 0, a2 = 0;
 #pragma unroll
-                for (int q = 0; q < RS_Q; ++q) {
+                for (int q = 0; q < Q; ++q) {
                     const uint32_t c = (uint32_t)(32 * q - lo) < (uint32_t)size ? key[q] : 0u;
                     a2 = max(a2, min(a1, c));
                     a1 = max(a1, c);
@@ -231,14 +235,14 @@ __device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[R
         stays = 0;
         int g = whole ? 0 : lane / size, left = whole ? size : size - lane % size;
 #pragma unroll
-        for (int q = 0; q < RS_Q; ++q) {
+        for (int q = 0; q < Q; ++q) {
             stays |= ((kept >> (g & 31)) & 1u) << q;
             for (left -= 32; left <= 0; left += size) ++g;
         }
     }
-    uint32_t id[RS_Q];
+    uint32_t id[Q];
 #pragma unroll
-    for (int q = 0; q < RS_Q; ++q) {
+    for (int q = 0; q < Q; ++q) {
         const int e = lane + 32 * q;
         if (!biased) key[q] = to_key(l[q]);
         if (e >= E || !((stays >> q) & 1u)) key[q] = 0;
@@ -254,12 +258,18 @@ __device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[R
         key[j] = s ? x : key[j];                                         \
         id[j] = s ? y : id[j];                                           \
     }
-    RVQ_CE(0, 1) RVQ_CE(2, 3) RVQ_CE(4, 5) RVQ_CE(6, 7)
-    RVQ_CE(0, 2) RVQ_CE(1, 3) RVQ_CE(4, 6) RVQ_CE(5, 7)
-    RVQ_CE(1, 2) RVQ_CE(5, 6)
-    RVQ_CE(0, 4) RVQ_CE(1, 5) RVQ_CE(2, 6) RVQ_CE(3, 7)
-    RVQ_CE(2, 4) RVQ_CE(3, 5)
-    RVQ_CE(1, 2) RVQ_CE(3, 4) RVQ_CE(5, 6)
+    if constexpr (Q == 2) {
+        RVQ_CE(0, 1)
+    } else if constexpr (Q == 4) {
+        RVQ_CE(0, 1) RVQ_CE(2, 3) RVQ_CE(0, 2) RVQ_CE(1, 3) RVQ_CE(1, 2)
+    } else {
+        RVQ_CE(0, 1) RVQ_CE(2, 3) RVQ_CE(4, 5) RVQ_CE(6, 7)
+        RVQ_CE(0, 2) RVQ_CE(1, 3) RVQ_CE(4, 6) RVQ_CE(5, 7)
+        RVQ_CE(1, 2) RVQ_CE(5, 6)
+        RVQ_CE(0, 4) RVQ_CE(1, 5) RVQ_CE(2, 6) RVQ_CE(3, 7)
+        RVQ_CE(2, 4) RVQ_CE(3, 5)
+        RVQ_CE(1, 2) RVQ_CE(3, 4) RVQ_CE(5, 6)
+    }
 #undef RVQ_CE
     // lane s takes the s-th pick and its key; with a bias one more than k (up to 32)
     uint32_t my_id = 0, my_key = 0;
@@ -273,11 +283,11 @@ __device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[R
         }
         if (id[0] == e) {
 #pragma unroll
-            for (int q = 0; q + 1 < RS_Q; ++q) {
+            for (int q = 0; q + 1 < Q; ++q) {
                 key[q] = key[q + 1];
                 id[q] = id[q + 1];
             }
-            key[RS_Q - 1] = 0;
+            key[Q - 1] = 0;
         }
     };
 #pragma unroll 1
@@ -293,13 +303,19 @@ __device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[R
         return __ballot_sync(0xffffffffu, lane < picked && lane <= 31 && next != 0 &&
                                               !(from_key(my_key) - from_key(next) > apart));
     };
-    if ((open_after(most) & (0xffffffffu >> (32 - k))) == 0) return (int)my_id;
+    int have = most, cut = k;
+    uint32_t open = open_after(have);
+    if ((open & (0xffffffffu >> (32 - k))) == 0) return (int)my_id;
     if (rule.score != MOE_SCORE_SIGMOID) return choose_64(row, rule.bias, E, k, rule, lane, scratch);
     // on until a pick is told apart from the next: the first `cut` are the candidates
-    for (int s = most; s < 32; ++s) pick(s);
-    const uint32_t after = ~open_after(32) >> (k - 1);
-    if (after == 0) return choose_64(row, rule.bias, E, k, rule, lane, scratch);
-    const int cut = k - 1 + __ffs(after);
+#pragma unroll 1
+    while ((open >> (cut - 1)) & 1u) {
+        if (cut == 32) return choose_64(row, rule.bias, E, k, rule, lane, scratch);
+        if (++cut == have) {
+            if (have < 32) pick(have++);
+            open = open_after(have);
+        }
+    }
     // the first `cut` values again in 64 bits, one per lane, and their order
     const double c = lane < cut ? sigmoid64(finite_or_0(row[my_id])) +
                                       (double)finite_or_0(rule.bias[my_id])
@@ -322,22 +338,23 @@ __device__ __forceinline__ int choose(const float (&l)[RS_Q], const float (&b)[R
 }
 
 // Chosen expert and weight of lane s < k.
+template <int Q>
 __device__ __forceinline__ void route_row(const float *__restrict__ row, int E, int k,
-                                          const RouteRule &rule, const float (&b)[RS_Q], int lane,
+                                          const RouteRule &rule, const float (&b)[Q], int lane,
                                           uint32_t *status, uint64_t *scratch, int &my_idx,
                                           float &my_w) {
-    float l[RS_Q];
-    bool bad = false;
+    float l[Q];
+    uint32_t big = 0;
 #pragma unroll
-    for (int q = 0; q < RS_Q; ++q) {
+    for (int q = 0; q < Q; ++q) {
         const int e = lane + 32 * q;
         l[q] = e < E ? row[e] : 0.f;
-        bad |= !isfinite(l[q]);
+        big = max(big, __float_as_uint(l[q]) & 0x7FFFFFFFu);
     }
-    if (__any_sync(0xffffffffu, bad)) {  // reported; finite values keep the outputs in range
+    if (__any_sync(0xffffffffu, big >= 0x7F800000u)) {  // reported; finite values keep the outputs in range
         if (lane == 0) set_dev_error(status, RVQ_DEV_ERR_NONFINITE);
 #pragma unroll
-        for (int q = 0; q < RS_Q; ++q) l[q] = finite_or_0(l[q]);
+        for (int q = 0; q < Q; ++q) l[q] = finite_or_0(l[q]);
     }
     my_idx = choose(l, b, row, E, k, rule, lane, scratch);
     const bool on = lane < k;
@@ -356,21 +373,22 @@ __device__ __forceinline__ void route_row(const float *__restrict__ row, int E, 
         uint32_t all = 0;
         float z = 0.f;
 #pragma unroll
-        for (int q = 0; q < RS_Q; ++q)
+        for (int q = 0; q < Q; ++q)
             if (lane + 32 * q < E) all = max(all, to_key(l[q]));
         const float m = from_key(warp_max(all));
 #pragma unroll
-        for (int q = 0; q < RS_Q; ++q)
+        for (int q = 0; q < Q; ++q)
             if (lane + 32 * q < E) z += expf(l[q] - m);
         e = expf(mine - m) / warp_sum(z);
     }
     my_w = rule.scale * (rule.renorm ? e / warp_sum(on ? e : 0.f) : e);
 }
 
+template <int Q>
 __device__ __forceinline__ void load_bias(const RouteRule &rule, int E, int lane, uint32_t *status,
-                                          float (&b)[RS_Q]) {
+                                          float (&b)[Q]) {
 #pragma unroll
-    for (int q = 0; q < RS_Q; ++q) {
+    for (int q = 0; q < Q; ++q) {
         const int e = lane + 32 * q;
         b[q] = rule.bias && e < E ? rule.bias[e] : 0.f;
         if (!isfinite(b[q])) {
@@ -406,50 +424,45 @@ __device__ __forceinline__ int scan_counts(int *cnt, int E, int lane) {
     return __shfl_sync(0xffffffffu, run, 31);
 }
 
-// One block, up to 64 tokens: choice and grouping.
-template <int NT>
-__global__ void __launch_bounds__(NT) route_scored_one_kernel(const RouteScoredJob j) {
-    __shared__ uint32_t mask[256][2];
+// One block, a warp per token: choice and grouping.
+template <int Q>
+__global__ void __launch_bounds__(RS_NT) route_scored_one_kernel(const RouteScoredJob j) {
+    __shared__ uint32_t mask[256];  // tokens of an expert
     __shared__ int cnt[256];
     extern __shared__ uint64_t scratch[];  // [warps][E]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < 512; i += NT) mask[i >> 1][i & 1] = 0u;
+    const int lane = threadIdx.x & 31, t = threadIdx.x >> 5;
+    mask[threadIdx.x] = 0u;
     dependency_wait();
     dependents_may_start();
     __syncthreads();
-    float b[RS_Q];
-    load_bias(j.rule, j.E, lane, j.status, b);
-    for (int t = warp; t < j.n; t += NT / 32) {
-        int idx;
-        float w;
-        route_row(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status,
-                  scratch + warp * j.E, idx, w);
+    int idx = 0;
+    if (t < j.n) {
+        float b[Q], w;
+        load_bias<Q>(j.rule, j.E, lane, j.status, b);
+        route_row<Q>(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status,
+                     scratch + t * j.E, idx, w);
         if (lane < j.k) {
             j.idx[t * j.k + lane] = idx;
             j.w[t * j.k + lane] = w;
-            atomicOr(&mask[idx][t >> 5], 1u << (t & 31));
+            atomicOr(&mask[idx], 1u << t);
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < j.E; e += NT) cnt[e] = __popc(mask[e][0]) + __popc(mask[e][1]);
+    cnt[threadIdx.x] = __popc(mask[threadIdx.x]);
     __syncthreads();
-    if (warp == 0) {
+    if (t == 0) {
         const int end = scan_counts(cnt, j.E, lane);
         if (lane == 0) j.offsets[j.E] = end;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < j.E; e += NT) j.offsets[e] = cnt[e];
-    for (int t = warp; t < j.n && lane < j.k; t += NT / 32) {
-        const uint32_t below = (1u << (t & 31)) - 1u;
-        const int e = j.idx[t * j.k + lane];  // this thread's own
-        const int before = t < 32 ? __popc(mask[e][0] & below)
-                                  : __popc(mask[e][0]) + __popc(mask[e][1] & below);
-        j.pairs[cnt[e] + before] = t * j.k + lane;
-    }
+    if (threadIdx.x < j.E) j.offsets[threadIdx.x] = cnt[threadIdx.x];
+    if (t < j.n && lane < j.k)
+        j.pairs[cnt[idx] + __popc(mask[idx] & ((1u << t) - 1u))] = t * j.k + lane;
 }
 
 // Many tokens, first launch: block b chooses for tokens run * b .. and counts its
 // experts into hist[b][E].
+template <int Q>
 __global__ void __launch_bounds__(1024) route_scored_choose_kernel(const RouteScoredJob j) {
     __shared__ int cnt[256];
     extern __shared__ uint64_t scratch[];  // [warps][E]
@@ -458,13 +471,13 @@ __global__ void __launch_bounds__(1024) route_scored_choose_kernel(const RouteSc
     dependency_wait();
     dependents_may_start();
     __syncthreads();
-    float b[RS_Q];
-    load_bias(j.rule, j.E, lane, j.status, b);
+    float b[Q];
+    load_bias<Q>(j.rule, j.E, lane, j.status, b);
     const int t0 = blockIdx.x * j.run, t1 = min(j.n, t0 + j.run);
     for (int t = t0 + warp; t < t1; t += (int)blockDim.x / 32) {
         int idx;
         float w;
-        route_row(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status,
+        route_row<Q>(j.logits + (int64_t)t * j.E, j.E, j.k, j.rule, b, lane, j.status,
                   scratch + warp * j.E, idx, w);
         if (lane < j.k) {
             j.idx[(int64_t)t * j.k + lane] = idx;
@@ -612,36 +625,41 @@ int route_scored_run(int n) {
     return (run + RS_NT / 32 - 1) / (RS_NT / 32) * (RS_NT / 32);
 }
 
-rvq_status launch_route_scored(const RouteScoredJob &job, cudaStream_t stream) {
+// Q: experts per lane that the kernels are made for (64 experts or fewer: half the
+// instructions of 256).
+template <int Q>
+static rvq_status launch_choice(const RouteScoredJob &job, cudaStream_t stream) {
     static std::atomic<int> attr_done[64];  // per device; setting twice is harmless
     int dev = 0;
     RVQ_CUDA(cudaGetDevice(&dev));
     if (dev < 64 && !attr_done[dev]) {
         RVQ_CUDA(cudaFuncSetAttribute(route_scored_place_kernel,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10));
-        RVQ_CUDA(cudaFuncSetAttribute(route_scored_choose_kernel,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10));
-        RVQ_CUDA(cudaFuncSetAttribute(route_scored_one_kernel<1024>,
+        RVQ_CUDA(cudaFuncSetAttribute(route_scored_choose_kernel<Q>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10));
         attr_done[dev] = 1;
     }
     if (job.n <= kRouteOneBlock) {
-        if (job.n <= 8)
-            RVQ_CUDA(launch_after(route_scored_one_kernel<256>, 1, 256, 8 * job.E * 8, stream, job));
-        else
-            RVQ_CUDA(launch_after(route_scored_one_kernel<1024>, 1, 1024, 32 * job.E * 8, stream, job));
+        RVQ_CUDA(launch_after(route_scored_one_kernel<Q>, 1, RS_NT,
+                              (size_t)kRouteOneBlock * job.E * 8, stream, job));
         return RVQ_OK;
     }
     RouteScoredJob j = job;
     j.run = route_scored_run(j.n);
     const unsigned blocks = (unsigned)((j.n + j.run - 1) / j.run);
-    const size_t smem = (size_t)j.E * ((j.run + 31) / 32) * 6;
     // a warp per token of a run, up to 32
     const int warps = j.run < 32 ? j.run : 32;
-    RVQ_CUDA(launch_after(route_scored_choose_kernel, blocks, 32 * warps, (size_t)warps * j.E * 8,
+    RVQ_CUDA(launch_after(route_scored_choose_kernel<Q>, blocks, 32 * warps, (size_t)warps * j.E * 8,
                           stream, j));
+    const size_t smem = (size_t)j.E * ((j.run + 31) / 32) * 6;
     RVQ_CUDA(launch_after(route_scored_place_kernel, blocks, RS_PLACE, smem, stream, j));
     return RVQ_OK;
+}
+
+rvq_status launch_route_scored(const RouteScoredJob &job, cudaStream_t stream) {
+    if (job.E <= 64) return launch_choice<2>(job, stream);
+    if (job.E <= 128) return launch_choice<4>(job, stream);
+    return launch_choice<8>(job, stream);
 }
 
 rvq_status launch_route_scored_backward(const RouteScoredJob &job, cudaStream_t stream) {

@@ -29,7 +29,7 @@ struct RouteScoredJob {
     float *dlogits;
 };
 
-constexpr int kRouteOneBlock = 64;         // tokens that one block chooses and groups
+constexpr int kRouteOneBlock = 8;          // tokens that one block chooses and groups
 constexpr int kRouteRuns = 148;            // blocks of the two launches past that
 constexpr int kRouteMaxTokens = 1 << 18;   // a run's bitmaps fit shared memory
 int route_scored_run(int n);

@@ -92,7 +92,7 @@ def test_groups(n, E, k, groups, top, score):
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("groups,top", [(1, 1), (8, 3)])
-@pytest.mark.parametrize("n", [20, 200])
+@pytest.mark.parametrize("n", [6, 20, 200])
 def test_ties_and_near_ties(n, groups, top, score):
     """Logits from few values, all equal, and an ulp apart, with biases that cancel what
     32 bits tell apart: the choice is the 64-bit one."""
@@ -188,7 +188,7 @@ def test_many_tokens():
 
 def test_streams_and_graph():
     """Two calls at once on two streams, and a captured call replayed on new logits."""
-    for n in (20, 500):
+    for n in (7, 20, 500):
         ls = [torch.randn((n, 64), device=DEV, generator=gen(20 + i)) for i in range(3)]
         bs = [buffers(n, 64, 8) for _ in range(3)]
         streams = [torch.cuda.Stream() for _ in range(2)]
