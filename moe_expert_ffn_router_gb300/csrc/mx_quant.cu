@@ -4,49 +4,74 @@
 // Memory-bound: 2 or 4 bytes read and 1.03 or 0.53 written per value.  A lane holds
 // eight values (16 or 32 bytes), a half warp the 128 columns that share a word of
 // scales, so the largest magnitude of a block is two shuffles away and every store is
-// whole words.  Blocks of 256 threads take kUnits runs of 16 half warps, all of
+// whole words.  Blocks of 256 threads take up to four runs of 16 half warps, all of
 // whose loads are in flight before the first is used.
 #include "mx.cuh"
 
 namespace rvq {
 namespace {
 
-constexpr int kUnits = 4;
+constexpr int kMost = 4;  // units of a thread
 
-// 128 columns of a row
+// 128 columns of a row: unit u is of row u / tiles.  One division per thread: its next
+// unit is 16 further, `down` rows and `right` tiles.
+struct Units {
+    int tiles, down, right;
+    uint32_t count;
+};
 struct Unit {
-    int row, tile, c;
-    bool in;  // this lane's eight columns are the matrix's
+    int row, tile;
+    __device__ __forceinline__ Unit(uint32_t u, const Units &k)
+        : row((int)(u / (uint32_t)k.tiles)), tile((int)(u - (uint32_t)row * (uint32_t)k.tiles)) {}
+    __device__ __forceinline__ void next(const Units &k) {
+        row += k.down;
+        tile += k.right;
+        if (tile >= k.tiles) {
+            tile -= k.tiles;
+            ++row;
+        }
+    }
+    // this lane's first column
+    __device__ __forceinline__ int c() const {
+        return tile * kMxTile + (int)(threadIdx.x & 15) * 8;
+    }
 };
 
-__device__ __forceinline__ Unit unit_at(uint32_t u, uint32_t units, int tiles, int cols) {
-    Unit r;
-    const uint32_t row = u / (uint32_t)tiles;
-    r.row = (int)row;
-    r.tile = (int)(u - row * (uint32_t)tiles);
-    r.c = r.tile * kMxTile + (int)(threadIdx.x & 15) * 8;
-    r.in = u < units && r.c < cols;
-    return r;
-}
-
-template <int FMT, int XDT>
-__global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantJob j, int tiles,
-                                                          uint32_t units) {
+template <int FMT, int XDT, int kUnits>
+__global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantJob j,
+                                                          const Units k) {
     dependency_wait();
     dependents_may_start();
     const uint32_t first = blockIdx.x * (16 * kUnits) + (threadIdx.x >> 4);
-    float v[kUnits][8];
+    // as they lie in memory: widening a unit at once would wait for its load before the
+    // next one's
+    constexpr int W = XDT == RVQ_F32 ? 2 : 1;
+    uint4 raw[kUnits][W];
+    Unit u(first, k);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const Unit u = unit_at(first + 16 * i, units, tiles, j.cols);
+    for (int i = 0; i < kUnits; ++i, u.next(k)) {
+        const bool in = first + 16 * i < k.count && u.c() < j.cols;
+        const char *p = reinterpret_cast<const char *>(j.x) +
+                        ((int64_t)u.row * j.ldx + u.c()) * (XDT == RVQ_F32 ? 4 : 2);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-        if (u.in) ld8(j.x, XDT, (int64_t)u.row * j.ldx + u.c, v[i]);
+        for (int w = 0; w < W; ++w) {
+            raw[i][w] = make_uint4(0u, 0u, 0u, 0u);
+            if (in) raw[i][w] = reinterpret_cast<const uint4 *>(p)[w];
+        }
     }
+    u = Unit(first, k);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const Unit u = unit_at(first + 16 * i, units, tiles, j.cols);
-        mx_put8<FMT>(v[i], j.codes, j.scales, u.row, u.c, tiles, first + 16 * i < units);
+    for (int i = 0; i < kUnits; ++i, u.next(k)) {
+        float v[8];
+        const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                               raw[i][W - 1].x, raw[i][W - 1].y, raw[i][W - 1].z, raw[i][W - 1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (XDT == RVQ_F32)
+                v[e] = __uint_as_float(w[e]);
+            else if (e % 2 == 0)
+                unpack16(XDT, w[e / 2], v[e], v[e + 1]);
+        mx_put8<FMT>(v, j.codes, j.scales, u.row, u.c(), k.tiles, first + 16 * i < k.count);
     }
 }
 
@@ -74,72 +99,96 @@ __device__ __forceinline__ void widen8(uint2 q, float (&v)[8]) {
     for (int i = 0; i < 4; ++i) unpack16(RVQ_F16, h[i], v[2 * i], v[2 * i + 1]);
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantJob j, int tiles,
-                                                            uint32_t units) {
+template <int FMT, int kUnits>
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantJob j,
+                                                            const Units k) {
     dependency_wait();
     dependents_may_start();
     const uint32_t first = blockIdx.x * (16 * kUnits) + (threadIdx.x >> 4);
     uint2 q[kUnits];
     uint32_t s[kUnits];
+    Unit u(first, k);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const Unit u = unit_at(first + 16 * i, units, tiles, j.cols);
+    for (int i = 0; i < kUnits; ++i, u.next(k)) {
         q[i] = make_uint2(0u, 0u);
         s[i] = 0u;
-        if (!u.in) continue;
-        const int64_t at = (int64_t)u.row * tiles * kMxTile + u.c;
+        if (first + 16 * i >= k.count || u.c() >= j.cols) continue;
+        const int64_t at = (int64_t)u.row * k.tiles * kMxTile + u.c();
         if (FMT == MOE_MX_F8)
             q[i] = *reinterpret_cast<const uint2 *>(j.codes + at);
         else
             q[i].x = *reinterpret_cast<const uint32_t *>(j.codes + at / 2);
-        s[i] = j.scales[mx_scale_at(u.row, u.tile, tiles) + (u.c / kMxBlock & 3)];
+        s[i] = j.scales[mx_scale_at(u.row, u.tile, k.tiles) + (u.c() / kMxBlock & 3)];
     }
+    u = Unit(first, k);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const Unit u = unit_at(first + 16 * i, units, tiles, j.cols);
-        if (!u.in) continue;
+    for (int i = 0; i < kUnits; ++i, u.next(k)) {
+        if (first + 16 * i >= k.count || u.c() >= j.cols) continue;
         float v[8];
         widen8<FMT>(q[i], v);
         const float scale = mx_scale(s[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= scale;
-        st8(j.out, j.odt, (int64_t)u.row * j.ldo + u.c, v);
+        st8(j.out, j.odt, (int64_t)u.row * j.ldo + u.c(), v);
     }
 }
 
-unsigned blocks_of(uint32_t units) { return (units + 16 * kUnits - 1) / (16 * kUnits); }
+Units units_of(int rows, int cols) {
+    Units k;
+    k.tiles = mx_tiles(cols);
+    k.down = 16 / k.tiles;
+    k.right = 16 % k.tiles;
+    k.count = (uint32_t)rows * (uint32_t)k.tiles;
+    return k;
+}
+
+unsigned blocks_of(uint32_t units, int each) { return (units + 16 * each - 1) / (16 * each); }
+
+// One unit per thread where more would leave SMs idle (one row of 7168: 2.5 us with four,
+// 1.7 with one).
+bool few(const Units &k) { return k.count <= (uint32_t)num_sms() * 16 * kMost; }
+
+template <int FMT, int XDT>
+rvq_status quantize_as(const MxQuantJob &job, cudaStream_t stream) {
+    const Units k = units_of(job.rows, job.cols);
+    if (few(k))
+        RVQ_CUDA(launch_after(mx_quantize_kernel<FMT, XDT, 1>, blocks_of(k.count, 1), 256, 0, stream,
+                              job, k));
+    else
+        RVQ_CUDA(launch_after(mx_quantize_kernel<FMT, XDT, kMost>, blocks_of(k.count, kMost), 256, 0,
+                              stream, job, k));
+    return RVQ_OK;
+}
 
 template <int FMT>
-rvq_status quantize(const MxQuantJob &job, int tiles, uint32_t units, cudaStream_t stream) {
-    const dim3 grid(blocks_of(units));
-    if (job.xdt == RVQ_F32)
-        RVQ_CUDA(launch_after(mx_quantize_kernel<FMT, RVQ_F32>, grid, 256, 0, stream, job, tiles, units));
-    else if (job.xdt == RVQ_BF16)
-        RVQ_CUDA(launch_after(mx_quantize_kernel<FMT, RVQ_BF16>, grid, 256, 0, stream, job, tiles, units));
+rvq_status quantize(const MxQuantJob &job, cudaStream_t stream) {
+    if (job.xdt == RVQ_F32) return quantize_as<FMT, RVQ_F32>(job, stream);
+    if (job.xdt == RVQ_BF16) return quantize_as<FMT, RVQ_BF16>(job, stream);
+    return quantize_as<FMT, RVQ_F16>(job, stream);
+}
+
+template <int FMT>
+rvq_status dequantize(const MxDequantJob &job, cudaStream_t stream) {
+    const Units k = units_of(job.rows, job.cols);
+    if (few(k))
+        RVQ_CUDA(launch_after(mx_dequantize_kernel<FMT, 1>, blocks_of(k.count, 1), 256, 0, stream,
+                              job, k));
     else
-        RVQ_CUDA(launch_after(mx_quantize_kernel<FMT, RVQ_F16>, grid, 256, 0, stream, job, tiles, units));
+        RVQ_CUDA(launch_after(mx_dequantize_kernel<FMT, kMost>, blocks_of(k.count, kMost), 256, 0,
+                              stream, job, k));
     return RVQ_OK;
 }
 
 }  // namespace
 
 rvq_status launch_mx_quantize(const MxQuantJob &job, cudaStream_t stream) {
-    const int tiles = mx_tiles(job.cols);
-    const uint32_t units = (uint32_t)job.rows * (uint32_t)tiles;
-    return job.fmt == MOE_MX_F8 ? quantize<MOE_MX_F8>(job, tiles, units, stream)
-                                : quantize<MOE_MX_F4>(job, tiles, units, stream);
+    return job.fmt == MOE_MX_F8 ? quantize<MOE_MX_F8>(job, stream)
+                                : quantize<MOE_MX_F4>(job, stream);
 }
 
 rvq_status launch_mx_dequantize(const MxDequantJob &job, cudaStream_t stream) {
-    const int tiles = mx_tiles(job.cols);
-    const uint32_t units = (uint32_t)job.rows * (uint32_t)tiles;
-    const dim3 grid(blocks_of(units));
-    if (job.fmt == MOE_MX_F8)
-        RVQ_CUDA(launch_after(mx_dequantize_kernel<MOE_MX_F8>, grid, 256, 0, stream, job, tiles, units));
-    else
-        RVQ_CUDA(launch_after(mx_dequantize_kernel<MOE_MX_F4>, grid, 256, 0, stream, job, tiles, units));
-    return RVQ_OK;
+    return job.fmt == MOE_MX_F8 ? dequantize<MOE_MX_F8>(job, stream)
+                                : dequantize<MOE_MX_F4>(job, stream);
 }
 
 }  // namespace rvq
