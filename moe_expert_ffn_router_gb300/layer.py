@@ -5,13 +5,16 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (MOE_ACT_SILU, MOE_SCORE_SIGMOID, RVQ_WS_STATUS_BYTES, moe_bank_init, moe_bank_record_bytes,
+from . import (MOE_ACT_SILU, MOE_MX_F4, MOE_MX_F8, MOE_SCORE_SIGMOID, RVQ_WS_STATUS_BYTES, moe_bank_init, moe_bank_record_bytes,
                moe_bank_validate, moe_bank_write_expert, moe_cache_bank, moe_cache_create,
                moe_cache_destroy, moe_cache_stats, moe_combine, moe_expert_ffn,
                moe_gated_linear, moe_gated_linear_backward, moe_gated_linear_workspace_bytes,
                moe_layer_forward, moe_layer_forward_host, moe_layer_forward_prenorm,
                moe_layer_forward_streamed, moe_layer_graph_create, moe_linear,
-               moe_linear_backward, moe_linear_workspace_bytes, moe_norm_join, moe_rms_norm,
+               moe_linear_backward, moe_linear_workspace_bytes, moe_mx_code_bytes,
+               moe_mx_gated_linear, moe_mx_gated_linear_workspace_bytes, moe_mx_linear,
+               moe_mx_linear_workspace_bytes, moe_mx_quantize, moe_mx_scale_bytes,
+               moe_norm_join, moe_norm_join_mx, moe_rms_norm,
                moe_route, moe_route_rule, moe_route_scored,
                moe_router_logits,
                moe_workspace_bytes, rvq_ws_clear, rvq_ws_status)
@@ -375,20 +378,82 @@ class SharedExpert:
         return rvq_ws_status(self.buffers(n, train)["ws"])
 
 
+class MxSharedExpert:
+    """A shared expert in microscaled formats, for serving: out = residual +
+    (act(x Wg^T) * (x Wu^T)) Wd^T.  The weights (gate and up [f][d], down [d][f]; fp32,
+    bf16 or fp16) are quantised once to wfmt; tokens and hidden values are xfmt."""
+
+    def __init__(self, wg, wu, wd, act: int = MOE_ACT_SILU, wfmt: int = MOE_MX_F4,
+                 xfmt: int = MOE_MX_F8, device: str | torch.device = "cuda"):
+        self.device = torch.device(device)
+        self.act, self.wfmt, self.xfmt = act, wfmt, xfmt
+        self.f, self.d = wg.shape
+        assert wu.shape == (self.f, self.d) and wd.shape == (self.d, self.f)
+        self.wg, self.wu, self.wd = (self._quantized(w, wfmt) for w in (wg, wu, wd))
+        self._bufs = {}
+
+    def _empty(self, rows: int, cols: int, fmt: int):
+        """Codes and scales of a matrix (bytes of rows behind the last hold no scale)."""
+        return (torch.empty(moe_mx_code_bytes(fmt, rows, cols), dtype=torch.uint8,
+                            device=self.device),
+                torch.zeros(moe_mx_scale_bytes(rows, cols), dtype=torch.uint8, device=self.device))
+
+    def _quantized(self, w, fmt: int):
+        w = _dev(w, self.device)
+        q = self._empty(*w.shape, fmt)
+        moe_mx_quantize(w, *w.shape, *q, fmt)
+        return q
+
+    def buffers(self, n: int) -> dict:
+        """Microscaled tokens and hidden values (codes and scales each), the output and
+        the workspace for n tokens, kept."""
+        b = self._bufs.get(n)
+        if b is None:
+            nbytes = max(moe_mx_gated_linear_workspace_bytes(n, self.f, self.d),
+                         moe_mx_linear_workspace_bytes(n, self.d, self.f))
+            b = dict(x=self._empty(n, self.d, self.xfmt), hidden=self._empty(n, self.f, self.xfmt),
+                     out=torch.empty((n, self.d), dtype=torch.float32, device=self.device),
+                     ws=torch.empty(nbytes, dtype=torch.uint8, device=self.device))
+            rvq_ws_clear(b["ws"])
+            self._bufs[n] = b
+        return b
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> dict:
+        """out (fp32) = residual + the block of x [n][d] (fp32, bf16 or fp16)."""
+        n = x.shape[0]
+        moe_mx_quantize(x, n, self.d, *self.buffers(n)["x"], self.xfmt)
+        return self.forward_quantized(n, residual)
+
+    def forward_quantized(self, n: int, residual: torch.Tensor | None = None) -> dict:
+        """The block of the n tokens that buffers(n)["x"] holds (moe_norm_join_mx writes
+        them there)."""
+        b = self.buffers(n)
+        moe_mx_gated_linear(*b["x"], *self.wg, *self.wu, n, self.f, self.d, b["hidden"][0],
+                            b["ws"], xfmt=self.xfmt, wfmt=self.wfmt, act=self.act,
+                            out_scales=b["hidden"][1], ofmt=self.xfmt)
+        moe_mx_linear(*b["hidden"], *self.wd, n, self.d, self.f, b["out"], b["ws"],
+                      xfmt=self.xfmt, wfmt=self.wfmt, residual=residual)
+        return b
+
+    def status(self, n: int) -> tuple[int, int]:
+        return rvq_ws_status(self.buffers(n)["ws"])
+
+
 class SharedExpertStack:
     """Blocks of routed experts with a shared expert, normed before and after:
         xn = norm(h) * w_pre;  y = shared(xn) + sum_slot w * expert(xn)
         h  = alpha * h + gate * norm(y) * w_post
-    for each block (MoeLayer, SharedExpert, dict of w_pre, w_post, gate: tensors
-    or None).  The norm after a block, its gate, the residual's scale and the
+    for each block (MoeLayer, SharedExpert or MxSharedExpert, dict of w_pre, w_post,
+    gate: tensors or None).  The norm after a block, its gate, the residual's scale and the
     norm before the next block are one launch (moe_norm_join), and the shared
     expert's output enters the routed layer as its residual.  h is fp32, xn bf16 (the
-    routed layers take no fp16), so the shared experts are bf16 (TypeError)."""
+    routed layers take no fp16), so dense shared experts are bf16 (TypeError).  For a
+    microscaled one the join before its block writes the normed rows in its format too."""
 
     def __init__(self, blocks, alpha: float = 1.0, eps: float = 1e-6):
         assert blocks and all(L.d == S.d == blocks[0][0].d for L, S, _ in blocks)
         for i, (_, S, _) in enumerate(blocks):
-            if S.wg.dtype != torch.bfloat16:
+            if not isinstance(S, MxSharedExpert) and S.wg.dtype != torch.bfloat16:
                 raise TypeError(f"block {i}: shared expert of {S.wg.dtype}, and the normed stream "
                                 "that the routed experts read too is bf16")
         self.blocks, self.alpha, self.eps = list(blocks), alpha, eps
@@ -412,22 +477,31 @@ class SharedExpertStack:
         "out" y, "h" the stream after the block)."""
         n = x.shape[0]
         bufs = self.buffers(n)
-        first = self.blocks[0]
-        moe_norm_join(x, n, first[0].d, None, bufs[0]["xn"], post_norm=False,
-                      w_pre=first[2].get("w_pre"), eps=self.eps)
+
+        def join(y, h_out, i, **kw):
+            """The norm after a block joined with the one before block i, whose shared
+            expert's format the normed rows are written in too."""
+            nxt = self.blocks[i] if i < len(self.blocks) else None
+            xn = bufs[i]["xn"] if nxt else None
+            kw.update(w_pre=nxt[2].get("w_pre") if nxt else None, eps=self.eps)
+            if nxt and isinstance(nxt[1], MxSharedExpert):
+                moe_norm_join_mx(y, n, nxt[1].d, h_out, *nxt[1].buffers(n)["x"], fmt=nxt[1].xfmt,
+                                 xn=xn, **kw)
+            else:
+                moe_norm_join(y, n, self.blocks[0][0].d, h_out, xn, **kw)
+
+        join(x, None, 0, post_norm=False)
         h = x
         for i, (L, S, p) in enumerate(self.blocks):
             b = bufs[i]
-            shared = S.forward(b["xn"])["out"]
-            L.forward(b["xn"], b, tc_min_tokens=tc_min_tokens, residual=shared)
-            last = i + 1 == len(self.blocks)
-            moe_norm_join(b["out"], n, L.d, b["h"], None if last else bufs[i + 1]["xn"], h=h,
-                          alpha=self.alpha, gate=p.get("gate"), w_post=p.get("w_post"),
-                          w_pre=None if last else self.blocks[i + 1][2].get("w_pre"),
-                          eps=self.eps)
+            shared = S.forward_quantized(n) if isinstance(S, MxSharedExpert) else S.forward(b["xn"])
+            L.forward(b["xn"], b, tc_min_tokens=tc_min_tokens, residual=shared["out"])
+            join(b["out"], b["h"], i + 1, h=h, alpha=self.alpha, gate=p.get("gate"),
+                 w_post=p.get("w_post"))
             h = b["h"]
         return bufs
 
 
-__all__ = ["MoeLayer", "MoeStack", "MoeStreamedStack", "SharedExpert", "SharedExpertStack",
+__all__ = ["MoeLayer", "MoeStack", "MoeStreamedStack", "MxSharedExpert", "SharedExpert",
+           "SharedExpertStack",
            "RVQ_WS_STATUS_BYTES"]
