@@ -388,7 +388,8 @@ size_t moe_route_scored_workspace_bytes(int32_t n, int32_t E);
 /* topk_idx int32 [n][k], topk_w fp32 [n][k], offsets int32 [E+1], pairs int32 [n*k] as
  * moe_route writes them; logits fp32 [n][E] (all dev).  1 <= k <= min(32, experts of
  * top_groups groups), E <= 256, n <= 262144.  The outputs overlap nothing (EINVAL); ws
- * 256-byte aligned, moe_route_scored_workspace_bytes long.  A logit or bias that is not
+ * 256-byte aligned, moe_route_scored_workspace_bytes long, its status block cleared once;
+ * calls that share it run one after another.  A logit or bias that is not
  * finite sets RVQ_DEV_ERR_NONFINITE and counts as 0. */
 rvq_status moe_route_scored(const float *logits_dev, int32_t n, int32_t E, int32_t k,
                             const moe_route_rule *rule, int32_t *topk_idx_dev, float *topk_w_dev,
@@ -784,7 +785,9 @@ rvq_status moe_mx_dequantize(const uint8_t *codes_dev, const uint8_t *scales_dev
                              int32_t rows, int32_t cols, void *out_dev, rvq_dtype odt, int64_t ldo,
                              rvq_stream_t stream);
 
-/* Workspaces of the products below, for up to n tokens.  0 for a shape they refuse. */
+/* Workspaces of the products below, for up to n tokens (256-byte aligned; rvq_ws_clear()
+ * once, then any number of calls on one stream; a bounded device wait that expires sets
+ * RVQ_DEV_ERR_TIMEOUT, and the outputs are undefined).  0 for a shape they refuse. */
 size_t moe_mx_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols);
 size_t moe_mx_gated_linear_workspace_bytes(int32_t n, int32_t rows, int32_t cols);
 

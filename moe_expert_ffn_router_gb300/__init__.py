@@ -431,7 +431,8 @@ def moe_route_scored(logits, n, E, k, topk_idx, topk_w, offsets, pairs, ws,
                                _vec(topk_w, n * k, "topk_w", f32),
                                _vec(offsets, E + 1, "offsets", i32),
                                _vec(pairs, n * k, "pairs", i32), ws.data_ptr(), ws.nbytes,
-                               _raw_stream(stream))
+                               _stream_of(stream, logits, bias, topk_idx, topk_w, offsets, pairs,
+                                          ws))
     if rc:
         _check("moe_route_scored", rc)
 
@@ -445,7 +446,7 @@ def moe_route_scored_backward(dtopk_w, logits, topk_idx, n, E, k, dlogits,
                                         _vec(logits, n * E, "logits", f32),
                                         _vec(topk_idx, n * k, "topk_idx", torch.int32), n, E, k,
                                         rule, _vec(dlogits, n * E, "dlogits", f32),
-                                        _raw_stream(stream))
+                                        _stream_of(stream, dtopk_w, logits, topk_idx, dlogits))
     if rc:
         _check("moe_route_scored_backward", rc)
 
@@ -583,6 +584,15 @@ def _raw_stream(stream) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
+
+
+def _stream_of(stream, *tensors) -> int:
+    """_raw_stream, once every tensor (or None) is on the stream's device."""
+    device = torch._C._cuda_getDevice() if stream is None else stream.device_index
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor is on {t.device}, the call on cuda:{device}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _mat(t, rows, cols, what, dtype=None):
@@ -815,7 +825,8 @@ def moe_mx_quantize(x, rows, cols, codes, scales, fmt=MOE_MX_F8, stream=None):
     in a microscaled format."""
     px, ldx = _mat(x, rows, cols, "x")
     pc, ps = _mx(codes, scales, rows, cols, fmt, "codes")
-    rc = _lib.moe_mx_quantize(px, ldx, _dt_any(x), rows, cols, fmt, pc, ps, _raw_stream(stream))
+    rc = _lib.moe_mx_quantize(px, ldx, _dt_any(x), rows, cols, fmt, pc, ps,
+                              _stream_of(stream, x, codes, scales))
     if rc:
         _check("moe_mx_quantize", rc)
 
@@ -825,7 +836,7 @@ def moe_mx_dequantize(codes, scales, rows, cols, out, fmt=MOE_MX_F8, stream=None
     pc, ps = _mx(codes, scales, rows, cols, fmt, "codes")
     po, ldo = _mat(out, rows, cols, "out")
     rc = _lib.moe_mx_dequantize(pc, ps, fmt, rows, cols, po, _dt_any(out), ldo,
-                                _raw_stream(stream))
+                                _stream_of(stream, codes, scales, out))
     if rc:
         _check("moe_mx_dequantize", rc)
 
@@ -850,7 +861,8 @@ def moe_mx_linear(x, x_scales, w, w_scales, n, rows, cols, out, ws, xfmt=MOE_MX_
     pr, ldr = _mat(residual, n, rows, "residual")
     rc = _lib.moe_mx_linear(px, pxs, xfmt, pw, pws, wfmt, _vec(bias, rows, "bias", torch.float32),
                             n, rows, cols, act, alpha, pr, _dt_any(residual), ldr, po,
-                            _dt_any(out), ldo, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+                            _dt_any(out), ldo, ws.data_ptr(), ws.nbytes,
+                            _stream_of(stream, x, x_scales, w, w_scales, bias, residual, out, ws))
     if rc:
         _check("moe_mx_linear", rc)
 
@@ -872,7 +884,9 @@ def moe_mx_gated_linear(x, x_scales, wg, wg_scales, wu, wu_scales, n, rows, cols
     rc = _lib.moe_mx_gated_linear(px, pxs, xfmt, pg, pgs, pu, pus, wfmt,
                                   _vec(bg, rows, "bg", torch.float32),
                                   _vec(bu, rows, "bu", torch.float32), n, rows, cols, act, po, odt,
-                                  ldo, pc, ps, ofmt, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+                                  ldo, pc, ps, ofmt, ws.data_ptr(), ws.nbytes,
+                                  _stream_of(stream, x, x_scales, wg, wg_scales, wu, wu_scales, bg,
+                                             bu, out, out_scales, ws))
     if rc:
         _check("moe_mx_gated_linear", rc)
 
@@ -901,7 +915,8 @@ def moe_norm_join_mx(y, n, d, h_out, codes, scales, fmt=MOE_MX_F8, xn=None, h=No
         int(post_norm), _vec(w_post, d, "w_post"),
         _vec(w_pre, d, "w_pre", None if wdt is w_pre else wdt.dtype), _dt_any(wdt), eps,
         _vec(h_out, nd, "h_out", None if ho is h_out else ho.dtype), _vec(xn, nd, "xn"),
-        _dt_any(xn), fmt, pc, ps, _vec(rstd, 2 * n, "rstd", torch.float32), _raw_stream(stream))
+        _dt_any(xn), fmt, pc, ps, _vec(rstd, 2 * n, "rstd", torch.float32),
+        _stream_of(stream, y, h, gate, w_post, w_pre, h_out, codes, scales, xn, rstd))
     if rc:
         _check("moe_norm_join_mx", rc)
 

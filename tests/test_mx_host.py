@@ -202,3 +202,27 @@ def test_product_binding_refusals():
         rvq.moe_mx_gated_linear(x, xs, w, ws_, w, ws_[:256], 4, 8, 64, out, ws)
     with pytest.raises(ValueError, match="out scales"):
         rvq.moe_mx_gated_linear(x, xs, w, ws_, w, ws_, 4, 8, 64, x, ws, out_scales=ws)
+
+
+def test_tensors_of_another_device():
+    """Tensors that are not on the call's device are refused before the library is
+    called (here: all are on the CPU, the call would be on cuda:0)."""
+    class Fake:
+        device_index, cuda_stream = 0, 0
+
+    u8 = torch.uint8
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    c, s = torch.zeros(512, dtype=u8), torch.zeros(512, dtype=u8)
+    w, ws = torch.zeros(8 * 64, dtype=u8), torch.zeros(256, dtype=u8)
+    out, i32 = torch.zeros((4, 8)), torch.zeros(8, dtype=torch.int32)
+    st = dict(stream=Fake())
+    for call in (lambda: rvq.moe_mx_quantize(x, 4, 64, c, s, **st),
+                 lambda: rvq.moe_mx_dequantize(c, s, 4, 64, x, **st),
+                 lambda: rvq.moe_norm_join_mx(x, 4, 64, None, c, s, **st),
+                 lambda: rvq.moe_mx_linear(c, s, w, s, 4, 8, 64, out, ws, **st),
+                 lambda: rvq.moe_mx_gated_linear(c, s, w, s, w, s, 4, 8, 64, out, ws, **st),
+                 lambda: rvq.moe_route_scored(out, 4, 8, 2, i32, out[:1], i32.new_zeros(9), i32,
+                                              ws, **st),
+                 lambda: rvq.moe_route_scored_backward(out[:1], out, i32, 4, 8, 2, out, **st)):
+        with pytest.raises(ValueError, match="on cpu, the call on cuda:0"):
+            call()
