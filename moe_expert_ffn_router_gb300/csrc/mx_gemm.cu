@@ -18,6 +18,13 @@
 //    each), let the next tile begin, and finish and write it from there.
 // Rows, columns and depth past the ends are zero-filled by TMA (scales and codes) and not
 // stored.  Each output is rounded once, from fp32.  Every wait is bounded (1 s).
+//
+// Measured (GB300; two 4-bit operands, 8-bit tokens and 4-bit weights): 8192^3 143 and
+// 261 us (7.7 and 4.2 PFLOP/s), 2048 tokens through the gated projection 7168 -> 2048 23.8
+// and 38.7 (128 tiles for 76 pairs: 1.68 waves), 4096 tokens 40.5 and 69.8; 2048 x 2048 ->
+// 7168 with an fp32 residual 33.7 and 36.5 (its 117 MB of rows, 17 us at the copy rate, in
+// epilogues of three tiles a pair).  A slice takes about 640 cycles of two 4-bit
+// operands, whose MMAs take 512: the fill (35 KB a CTA, 55 bytes per cycle and SM).
 #include "dense_epilogue.cuh"
 #include "mx_tc.cuh"
 

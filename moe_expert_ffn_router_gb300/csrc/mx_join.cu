@@ -9,9 +9,13 @@
 // blocks walk over them; a row is copied into shared memory (cp.async) while the one
 // before is worked on in registers, so one place is enough and two blocks or more share
 // an SM, whose sums and round trips overlap (a ring of two or three rows, one block of
-// fp32 7168 per SM, took 44 and 53 us for 2048 rows where this takes 34).  A thread's groups are of four
-// columns, eight adjacent lanes hold a block of 32 and a warp the 128 columns of a word
-// of scales.
+// fp32 7168 per SM, took 44 and 53 us for 2048 rows where this takes 34).  A thread's
+// groups are of four columns, eight adjacent lanes hold a block of 32 and a warp the 128
+// columns of a word of scales.
+//
+// Measured (GB300, 8 bits out): 2048 x 7168 fp32 with a post norm and a channel gate 34 us
+// (191 MB, 5.6 TB/s), fp32 stream and bf16 block 28.7 (5.6), all bf16 28.7 (3.6: issue, 45
+// instructions per value and lane); 1531 x 2040 bf16 7.7; 64 x 7168 3.6.
 #include "join_common.cuh"
 #include "mx.cuh"
 

@@ -6,6 +6,9 @@
 // scales, so the largest magnitude of a block is two shuffles away and every store is
 // whole words.  Blocks of 256 threads take up to four runs of 16 half warps, all of
 // whose loads are in flight before the first is used.
+//
+// Measured (GB300): 8192 x 7168 fp32 to 8 bits 42.8 us (6.9 TB/s, the copy rate), bf16 35
+// (5.0; bound by issue), back to bf16 27 (6.5); one row of 7168 1.3.
 #include "mx.cuh"
 
 namespace rvq {

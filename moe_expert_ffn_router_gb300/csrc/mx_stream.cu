@@ -16,6 +16,13 @@
 //  * Launched programmatically: while the kernel before it ends, a CTA brings its first
 //    slices of weights into L2.
 // Every wait is bounded (1 s).
+//
+// Measured (GB300, weights rotated through more than L2, launches back to back; 8-bit
+// tokens and 4-bit weights, two 4-bit operands): one token through the gated projection
+// 7168 -> 2048 7.8 and 6.1 us (15.6 MB: 2.3 us at the copy rate), 64 tokens 13.0 and 11.3;
+// 2048 -> 7168 with a residual 5.5 and 5.0, 64 tokens 7.8 and 7.1; 512 -> 256 3.2-4.1.
+// About 3 us of it are launch, first load and joining; an MMA takes some 130 cycles however
+// few the tokens, which is what 8-bit tokens, of twice as many MMAs, cost more.
 #include "mx_tc.cuh"
 
 namespace rvq {

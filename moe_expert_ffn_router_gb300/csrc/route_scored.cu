@@ -8,18 +8,23 @@
 //   w_j = scale p_j, or scale p_j / sum of the chosen p
 //
 // The bytes are few (a logit row in, 12 bytes per choice out), so what counts is the
-// chain of a row: one warp per token, expert lane + 32 q in register q, and a choice is
-// two warp-wide reductions of order-preserving integer keys.
-//  * The choice is that of 64-bit arithmetic.  A row is worked out in 32 bits, and again
-//    in 64 where two values that decide (neighbours among the picks, the last pick and
-//    the next, the worst group kept and the best dropped) are within the error of the
-//    32-bit ones (under 1 % of rows of 256 experts).  Without a bias c grows with l, and
-//    the logits themselves are the keys.
+// chain of a row: one warp per token, expert lane + 32 q in register q, a lane's experts
+// sorted, and a pick is two warp-wide reductions of order-preserving integer keys.
+//  * The choice is that of 64-bit arithmetic.  A row is worked out in 32 bits; where two
+//    values that decide are within the error of the 32-bit ones (neighbours among the
+//    picks, the last pick and the next: some rows in a thousand of 256 experts), those
+//    picks alone are compared in 64 bits, and where groups are (one in ten thousand), the
+//    whole row is.  Without a bias c grows with l, and the logits are the keys.
 //  * Up to 8 tokens one block chooses and groups (64 would take it 29 us, two launches
-//    11).  More: blocks of equal runs of tokens
-//    choose and count their experts, and a second launch places every pair from the
-//    counts of the runs before its own and a bitmap of tokens per expert in its run.
-//    No atomics on order: pairs are sorted by (expert, token).
+//    10).  More: blocks of equal runs of tokens choose and count their experts, and a
+//    second launch places every pair from the counts of the runs before its own and a
+//    bitmap of tokens per expert in its run.  No atomics decide an order: pairs are sorted
+//    by (expert, token).
+//
+// Measured (GB300; bias, 4 of 8 groups, 16 of 256 experts): one token 6.7 us, 64 10.3, 2048
+// 20 (11 without bias and groups), 8 of 64 experts, 4096 tokens 10.3, with the softmax and
+// its gradient 13.9.  Latency: some 2500 instructions a token, 1200 of 64 experts, and in
+// nearly every launch of 2048 tokens a row that is decided in 64 bits.
 #include "dense.cuh"
 #include "route_scored.cuh"
 

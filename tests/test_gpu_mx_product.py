@@ -131,6 +131,7 @@ def test_linear_epilogue(n, act):
 @pytest.mark.parametrize("n,rows,cols", [(3, 72, 264), (130, 200, 520), (517, 384, 256)])
 def test_gated_epilogue(n, rows, cols, act):
     run_gated(n, rows, cols, F8, F4, act=act, bias=True, out=HF)
+    run_gated(n, rows, cols, F4, F4, act=act, out=F32)
     for ofmt in (F8, F4):
         run_gated(n, rows, cols, F4, F4, act=act, bias=True, ofmt=ofmt)
         run_gated(n, rows, cols, F8, F4, act=act, ofmt=ofmt)
@@ -286,6 +287,7 @@ def test_many_tokens_epilogue(n, rows, cols):
     run_linear(n, rows, cols, F8, F4, act="gelu", alpha=0.5, bias=True, res=F32, out=BF)
     run_linear(n, rows, cols, F4, F4, act="silu", res=BF, out=F32)
     run_linear(n, rows, cols, F4, F4, bias=True, out=HF)
+    run_gated(n, rows, cols, F8, F4, bias=True, out=F32)
     for ofmt in (F8, F4):
         run_gated(n, rows, cols, F8, F4, bias=True, ofmt=ofmt)
         run_gated(n, rows, cols, F4, F4, act="gelu_tanh", ofmt=ofmt)
