@@ -414,6 +414,15 @@ rvq_status launch_tiles(const MxJob &job, cudaStream_t stream) {
     int dev = 0;
     RVQ_CUDA(cudaGetDevice(&dev));
     if (dev < 64 && !attr_done[dev]) {
+        // the epilogue's share of registers comes out of what the block is launched with:
+        // with fewer it would wait for them forever
+        cudaFuncAttributes attr;
+        RVQ_CUDA(cudaFuncGetAttributes(&attr, mx_gemm_kernel<GATED, F4>));
+        if (attr.numRegs < MG_REGS) {
+            set_error("microscaled product: built with %d registers a thread, %d needed",
+                      attr.numRegs, MG_REGS);
+            return RVQ_ENOTIMPL;
+        }
         RVQ_CUDA(cudaFuncSetAttribute(mx_gemm_kernel<GATED, F4>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM));
         attr_done[dev] = 1;

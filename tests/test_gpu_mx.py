@@ -264,3 +264,42 @@ def test_join_gradient_straight_through():
     for a, b in zip(*got):
         rel = (a.double() - b.double()).norm() / b.double().norm()
         assert rel <= 260 * U + (R.half_step(BF) if a.dtype is BF else 0), rel
+
+
+def test_past_two_gigabytes():
+    """Matrices of more than 2^31 values: offsets of the last rows, of a tile boundary past
+    2^31 and of the first, in every call."""
+    n, d = 270000, 8192
+    x = torch.empty((n, d), dtype=BF, device=DEV).normal_(generator=gen(1))
+    codes, scales = new_mx(n, d, F8)
+    rvq.moe_mx_quantize(x, n, d, codes, scales)
+    places = (0, 262144 - 64, n - 100)
+
+    def part(c, s, r):
+        return (c.view(n, -1)[r:r + 100].reshape(-1),
+                X.to_tiles(X.from_tiles(s, n, d)[r:r + 100]))
+
+    for r in places:
+        q, byte = X.quantize(x[r:r + 100], F8)
+        c, s = part(codes, scales, r)
+        assert torch.equal(X.values(F8, DEV)[X.unpack(c, 100, d, F8)], q)
+        assert torch.equal(X.from_tiles(s, 100, d), byte)
+    w, ws_, vw = X.random_mx(136, d, F4, gen(2), std=d ** -0.5)
+    out = torch.zeros((n, 136), dtype=BF, device=DEV)
+    ws = torch.zeros(rvq.moe_mx_linear_workspace_bytes(n, 136, d), dtype=torch.uint8, device=DEV)
+    rvq.moe_mx_linear(codes, scales, w, ws_, n, 136, d, out, ws)
+    assert rvq.rvq_ws_status(ws) == (0, 0)
+    for r in places:
+        v = X.dequantize(*part(codes, scales, r), 100, d, F8)
+        y, e = R.product(v, vw)
+        R.check(out[r:r + 100], (y, e + R.half_step(BF) * 1.001 * y.abs() + R.tiny(BF)), f"row {r}")
+    rvq.moe_mx_dequantize(codes, scales, n, d, x)
+    for r in places:
+        assert torch.equal(x[r:r + 100].double(), X.dequantize(*part(codes, scales, r), 100, d, F8))
+    h = torch.zeros((n, d), dtype=BF, device=DEV)
+    rvq.moe_norm_join_mx(x, n, d, h, codes, scales, post_norm=False, eps=EPS)
+    for r in places:
+        y = x[r:r + 100].double()
+        xn = y / torch.sqrt(y.square().mean(1, keepdim=True) + EPS)
+        X.check_quantized(*part(codes, scales, r), 100, d, F8, xn, 72 * U * xn.abs(), f"row {r}")
+        assert torch.equal(h[r:r + 100], x[r:r + 100])
