@@ -8,7 +8,8 @@
 //  * A CTA multiplies 128 rows of the weights (128 gate rows and the 128 up rows
 //    beside them for a gated product, two accumulators) with the tokens over one part
 //    of the depth; a cluster of up to 8 CTAs splits the depth.
-//  * Codes and scales arrive by TMA, one slice a stage; the issuing thread copies the
+//  * Codes arrive by TMA, one slice a stage, and their scales as plain bulk copies (a
+//    tensor map costs the host half a microsecond a call); the issuing thread copies the
 //    scales into tensor memory ahead of the slice's MMAs, in order with them.
 //  * The partial tiles (fp32) go to shared memory, and the CTAs of the cluster share
 //    the outputs, 32 of a token at a time (a block of a microscaled output), adding the
@@ -42,6 +43,8 @@ struct StreamArgs {
     int stages, split;    // ring depth; CTAs of a cluster
     int stage;            // bytes of a stage
     uint32_t expect;      // bytes that TMA counts per stage
+    const uint8_t *sw[2], *sx;  // scales of the weights, of the tokens
+    int ktiles;           // tiles of scales of a row
     uint32_t cols;        // TMEM columns
     uint32_t idesc;
     int act, rdt, odt;
@@ -62,6 +65,35 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *tm, in
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(col), "r"(row), "r"(mbar)
         : "memory");
+}
+
+// contiguous bytes (16-byte aligned, a multiple of 16)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            dst),
+        "l"(src), "r"(bytes), "r"(mbar)
+        : "memory");
+}
+
+__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// A slice's KT tiles of scales (tile k KT .. of the row at `row`).  Where a row has an odd
+// number of tiles, the last slice's second one, whose codes are zero padding, takes the
+// first's scales: finite, or NaN of a row that is NaN already.
+template <int KT>
+__device__ __forceinline__ void load_scales(uint32_t dst, const uint8_t *row, int k, int ktiles,
+                                            uint32_t mbar) {
+    const uint8_t *src = row + (int64_t)k * KT * kMxTileBytes;
+    if (KT == 1 || k * KT + 1 < ktiles) {
+        bulk_load(dst, src, KT * kMxTileBytes, mbar);
+    } else {
+        bulk_load(dst, src, kMxTileBytes, mbar);
+        bulk_load(dst + kMxTileBytes, src, kMxTileBytes, mbar);
+    }
 }
 
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap *tm, int col, int row) {
@@ -192,9 +224,7 @@ __device__ __forceinline__ void join(const StreamArgs &g, const float *part, int
 template <bool GATED, bool F4>
 __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
     const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
-    const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap sw0,
-    const __grid_constant__ CUtensorMap sw1, const __grid_constant__ CUtensorMap sx,
-    const __grid_constant__ StreamArgs g) {
+    const __grid_constant__ CUtensorMap mx, const __grid_constant__ StreamArgs g) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int MATS = GATED ? 2 : 1;
     constexpr int KT = F4 ? 2 : 1;                     // tiles of scales a slice is deep
@@ -208,6 +238,9 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
     const int k1 = (int)((int64_t)g.slices * (rank + 1) / g.split);
     // a stage: codes of the weights, of the tokens, scales of the weights, of the tokens
     const int b_at = MATS * MS_ABYTES, sw_at = b_at + g.npad * 128, sx_at = sw_at + MATS * KT * kMxTileBytes;
+    const int64_t srow = (int64_t)g.ktiles * kMxTileBytes;  // scales of 128 rows
+    const uint8_t *sw0 = g.sw[0] + row_tile * srow, *sw1 = GATED ? g.sw[1] + row_tile * srow : nullptr;
+    const uint8_t *sx = g.sx + tok_tile * srow;
     __shared__ __align__(8) uint64_t bars[2 * MS_MAX_ST + 1];
     __shared__ uint32_t tslot;
     __shared__ int abort_word;
@@ -240,9 +273,11 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
         for (int k = k0; k < k1 && k < k0 + g.stages; ++k) {
             tma_prefetch(&mw0, k * 128, r0);
             if (GATED) tma_prefetch(&mw1, k * 128, r0);
-            tma_prefetch(&sw0, k * KT * 128, row_tile);
-            if (GATED) tma_prefetch(&sw1, k * KT * 128, row_tile);
         }
+        const int first = k0 * KT, last = min(min(k1, k0 + g.stages) * KT, g.ktiles);
+        const uint32_t bytes = (uint32_t)(last - first) * kMxTileBytes;
+        bulk_prefetch(sw0 + (int64_t)first * kMxTileBytes, bytes);
+        if (GATED) bulk_prefetch(sw1 + (int64_t)first * kMxTileBytes, bytes);
     }
     dependency_wait();
     dependents_may_start();
@@ -257,13 +292,13 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar, g.expect);
                 tma_load(st, &mw0, k * 128, r0, bar);
-                tma_load(st + sw_at, &sw0, k * KT * 128, row_tile, bar);
+                load_scales<KT>(st + sw_at, sw0, k, g.ktiles, bar);
                 if (GATED) {
                     tma_load(st + MS_ABYTES, &mw1, k * 128, r0, bar);
-                    tma_load(st + sw_at + KT * kMxTileBytes, &sw1, k * KT * 128, row_tile, bar);
+                    load_scales<KT>(st + sw_at + KT * kMxTileBytes, sw1, k, g.ktiles, bar);
                 }
                 tma_load(st + b_at, &mx, k * 128, t0, bar);
-                tma_load(st + sx_at, &sx, k * KT * 128, tok_tile, bar);
+                load_scales<KT>(st + sx_at, sx, k, g.ktiles, bar);
             }
             __syncwarp();
         }
@@ -480,17 +515,15 @@ rvq_status launch(const MxJob &job, cudaStream_t stream) {
     g.ofmt = job.ofmt;
     g.otiles = mx_tiles(job.rows);
     g.status = job.status;
-    CUtensorMap mw[2], sw[2], mx, sx;
+    CUtensorMap mw[2], mx;
     for (int i = 0; i < MATS; ++i) {
         RVQ_TRY(encode_codes(&mw[i], job.w[i], job.rows, job.cols, job.wfmt, F4, MS_ROWS));
-        RVQ_TRY(encode_scales(&sw[i], job.ws[i], job.rows, job.cols, F4, 1));
+        g.sw[i] = job.ws[i];
     }
-    if (!GATED) {
-        mw[1] = mw[0];
-        sw[1] = sw[0];
-    }
+    if (!GATED) mw[1] = mw[0];
     RVQ_TRY(encode_codes(&mx, job.x, job.n, job.cols, job.xfmt, F4, g.npad));
-    RVQ_TRY(encode_scales(&sx, job.xs, job.n, job.cols, F4, 1));
+    g.sx = job.xs;
+    g.ktiles = mx_tiles(job.cols);
     // the ring, or the partial tile that takes its place
     const int part = (job.n < MS_TOKENS ? job.n : MS_TOKENS) * (MATS * MS_ROWS + 4) * 4;
     const int dyn = g.stages * g.stage > part ? g.stages * g.stage : part;
@@ -508,8 +541,7 @@ rvq_status launch(const MxJob &job, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    RVQ_CUDA(cudaLaunchKernelEx(&cfg, mx_stream_kernel<GATED, F4>, mw[0], mw[1], mx, sw[0], sw[1],
-                                sx, g));
+    RVQ_CUDA(cudaLaunchKernelEx(&cfg, mx_stream_kernel<GATED, F4>, mw[0], mw[1], mx, g));
     RVQ_LAUNCHED("mx_stream");
     return RVQ_OK;
 }
