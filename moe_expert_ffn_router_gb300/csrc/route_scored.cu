@@ -12,9 +12,8 @@
 // sorted, and a pick is two warp-wide reductions of order-preserving integer keys.
 //  * The choice is that of 64-bit arithmetic.  A row is worked out in 32 bits; where two
 //    values that decide are within the error of the 32-bit ones (neighbours among the
-//    picks, the last pick and the next: some rows in a thousand of 256 experts), those
-//    picks alone are compared in 64 bits, and where groups are (one in ten thousand), the
-//    whole row is.  Without a bias c grows with l, and the logits are the keys.
+//    picks, the last pick and the next: a few rows in ten thousand of 256 experts), those
+//    picks alone are compared in 64 bits, and where groups are, the whole row is.  Without a bias c grows with l, and the logits are the keys.
 //  * Up to 8 tokens one block chooses and groups (64 would take it 29 us, two launches
 //    10).  More: blocks of equal runs of tokens choose and count their experts, and a
 //    second launch places every pair from the counts of the runs before its own and a
@@ -66,8 +65,9 @@ __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
-// 1 / (1 + e^-l), from the fast exponential (2 + 1.2 |l| units of its last place)
-__device__ __forceinline__ float sigmoid32(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+// 1 - sigmoid(l) = 1 / (1 + e^l): two units of the exponential, half a step of the sum and
+// two units of the quotient, 5.4e-7 of its value
+__device__ __forceinline__ float rest32(float l) { return __fdividef(1.f, 1.f + expf(l)); }
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
 
 // Groups of a row that stay, as bits: lane g holds the value of group g.
@@ -146,14 +146,23 @@ __device__ __noinline__ int choose_64(const float *row, const float *bias, int E
     return my_idx;
 }
 
+// The two largest of a pair and another.
+__device__ __forceinline__ void top_two(uint32_t &o1, uint32_t &o2, uint32_t a1, uint32_t a2,
+                                        uint32_t b1, uint32_t b2) {
+    o2 = max(min(a1, b1), max(a2, b2));
+    o1 = max(a1, b1);
+}
+
 // The k experts of a row: lane s < k gets the s-th.  l, b: logits and biases of the
 // lane's experts, finite.
 //
-// Error of a 32-bit score: sigmoid p (1 - p) (2 + 1.2 |l|) 2^-23, where p (1 - p) |l| is at
-// most 0.23 (the exponential), and p 3e-7 (the sum's half step, two units of the
-// quotient), at most 4e-7; softmax p (6 + 2.2 |l - m|) 2^-23 with p |l - m| <= 0.37, and 14
-// half steps of the sum, at most 1.7e-6.  Two values c are told apart by more than twice that and a step of the larger
-// |c|; sums of two by twice as much.
+// In 32 bits a sigmoid's c is held as c - 1 = b - (1 - p), which is exact to 5.4e-7 of 1 - p
+// and half a step of itself: scores near 1, where the picks are, keep their differences.
+// With |c - 1| and the largest |b| no smaller than 1 - p together, two values are told
+// apart by more than 6.5e-7 (|x| + |y| + 2 max |b|), and by 2e-15, what 64 bits tell apart.
+// Softmax: p is off by p (6 + 2.2 |l - m|) 2^-23, p |l - m| <= 0.37, and 14 half steps of the
+// sum, at most 1.7e-6, and c by half a step.  Sums of two: four times and twice that
+// (one of them may be positive, up to max |b|, and the other as far below).
 template <int Q>
 __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
                                       const float *row, int E, int k, const RouteRule &rule,
@@ -161,12 +170,12 @@ __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
     const bool biased = rule.bias != nullptr, grouped = rule.top_groups < rule.groups;
     const int size = E / rule.groups;
     uint32_t key[Q];
-    float apart = 0.f;
+    float base = 0.f, part = 0.f;
     if (biased || grouped) {
         float p[Q];
         if (rule.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) p[q] = sigmoid32(l[q]);
+            for (int q = 0; q < Q; ++q) p[q] = -rest32(l[q]);
         } else {
             uint32_t top = 0;
 #pragma unroll
@@ -186,34 +195,65 @@ __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
         uint32_t big = 0;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const float c = p[q] + b[q];
-            key[q] = lane + 32 * q < E ? to_key(c) : 0u;
-            big = max(big, __float_as_uint(c) & 0x7FFFFFFFu);
+            key[q] = lane + 32 * q < E ? to_key(p[q] + b[q]) : 0u;
+            big = max(big, __float_as_uint(b[q]) & 0x7FFFFFFFu);
         }
-        apart = (rule.score == MOE_SCORE_SIGMOID ? 8.4e-7f : 3.6e-6f) +
-                2.4e-7f * __uint_as_float(warp_max(big));
+        if (rule.score == MOE_SCORE_SIGMOID) {
+            part = 6.5e-7f;
+            base = 1.3e-6f * (biased ? __uint_as_float(warp_max(big)) : 0.f) + 2e-15f;
+        } else {
+            part = 2.4e-7f;
+            base = 3.6e-6f;
+        }
     }
     const bool whole = size % 32 == 0;  // register q is of group 32 q / size
     uint32_t stays = 0xffu;             // bit q: expert lane + 32 q is of a group that stays
     if (grouped) {
         uint32_t v1 = 0, v2 = 0;  // of group `lane`
-        if (whole) {
-            uint32_t a1 = 0, a2 = 0;
-            int next = size / 32, g = 0;
+        if (size == 32 || size == 64 || size == 128) {
+            // registers of one group merged, then all groups' two largest at once: a lane
+            // keeps half of them a step (a reduction per group and value took more than
+            // the picks)
+            uint32_t a1[Q], a2[Q];
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                a2 = max(a2, min(a1, key[q]));
-                a1 = max(a1, key[q]);
-                if (q + 1 == next) {
-                    const uint32_t t1 = warp_max(a1);
-                    const int winner = __ffs(__ballot_sync(0xffffffffu, a1 == t1)) - 1;
-                    const uint32_t t2 = warp_max(lane == winner ? a2 : a1);
-                    if (lane == g) { v1 = t1; v2 = t2; }
-                    a1 = a2 = 0;
-                    ++g;
-                    next += size / 32;
+                a1[q] = key[q];
+                a2[q] = 0;
+            }
+#pragma unroll
+            for (int span = 64; span <= 128; span *= 2) {
+                if (size < span) continue;
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    if (i < Q / 2)
+                        top_two(a1[i], a2[i], a1[2 * i], a2[2 * i], a1[2 * i + 1], a2[2 * i + 1]);
+                    else
+                        a1[i] = a2[i] = 0;
                 }
             }
+            int off = 16;
+#pragma unroll
+            for (int n = Q / 2; n >= 1; n /= 2, off /= 2) {
+                const bool upper = lane & off;
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t g1 = __shfl_xor_sync(0xffffffffu, upper ? a1[i] : a1[i + n], off);
+                    const uint32_t g2 = __shfl_xor_sync(0xffffffffu, upper ? a2[i] : a2[i + n], off);
+                    const uint32_t k1 = upper ? a1[i + n] : a1[i], k2 = upper ? a2[i + n] : a2[i];
+                    top_two(a1[i], a2[i], k1, k2, g1, g2);
+                }
+            }
+            for (; off >= 1; off /= 2) {
+                const uint32_t g1 = __shfl_xor_sync(0xffffffffu, a1[0], off);
+                const uint32_t g2 = __shfl_xor_sync(0xffffffffu, a2[0], off);
+                top_two(a1[0], a2[0], a1[0], a2[0], g1, g2);
+            }
+            // group g is where the bits of g chose the halves
+            int src = 0;
+#pragma unroll
+            for (int n = Q / 2, bit = 16; n >= 1; n /= 2, bit /= 2) src |= lane & n ? bit : 0;
+            v1 = __shfl_sync(0xffffffffu, a1[0], src);
+            v2 = __shfl_sync(0xffffffffu, a2[0], src);
         } else {
 #pragma unroll 1
             for (int g = 0; g < rule.groups; ++g) {
@@ -236,7 +276,8 @@ __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
         const bool in = (kept >> lane) & 1u;
         const float worst = from_key(__reduce_min_sync(0xffffffffu, in ? to_key(mine) : 0xffffffffu));
         const float best = from_key(warp_max(!in && lane < rule.groups ? to_key(mine) : 0u));
-        if (!(worst - best > 2.f * apart)) return choose_64(row, rule.bias, E, k, rule, lane, scratch);
+        if (!(worst - best > 4.f * base + 2.f * part * (fabsf(worst) + fabsf(best))))
+            return choose_64(row, rule.bias, E, k, rule, lane, scratch);
         stays = 0;
         int g = whole ? 0 : lane / size, left = whole ? size : size - lane % size;
 #pragma unroll
@@ -276,7 +317,9 @@ __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
         RVQ_CE(1, 2) RVQ_CE(3, 4) RVQ_CE(5, 6)
     }
 #undef RVQ_CE
-    // lane s takes the s-th pick and its key; with a bias one more than k (up to 32)
+    // lane s takes the s-th pick and its key; with a bias one more than k (up to 32).  (Rows
+    // of the lists sorted across the warp and merged instead: 11.4 -> 14 us for 2048 tokens
+    // without bias and groups.)
     uint32_t my_id = 0, my_key = 0;
     const int most = biased ? min(k + 1, 32) : k;
     const auto pick = [&](int s) {
@@ -305,8 +348,9 @@ __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
             const uint32_t top = warp_max(key[0]);
             if (lane == 31) next = top;
         }
-        return __ballot_sync(0xffffffffu, lane < picked && lane <= 31 && next != 0 &&
-                                              !(from_key(my_key) - from_key(next) > apart));
+        const float x = from_key(my_key), y = from_key(next);
+        return __ballot_sync(0xffffffffu, lane < picked && next != 0 &&
+                                              !(x - y > base + part * (fabsf(x) + fabsf(y))));
     };
     int have = most, cut = k;
     uint32_t open = open_after(have);

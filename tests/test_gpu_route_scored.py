@@ -124,6 +124,22 @@ def test_extreme_logits(score):
     check(l, 4, score, None, 1, 1, False, 1.0)
 
 
+@pytest.mark.parametrize("biased", [False, True])
+def test_saturated_scores(biased):
+    """Logits whose sigmoids are 1 (or 0) in 64 bits, and nearly so, among groups: ties go
+    to the lower group, and scores a 2^-53 apart keep their order."""
+    g = gen(12)
+    for scale, shift in ((3.0, 34.0), (1.0, 17.0), (0.5, 60.0), (4.0, -40.0), (20.0, 0.0)):
+        l = torch.randn((90, 64), device=DEV, generator=g) * scale + shift
+        bias = torch.randint(-2, 3, (64,), device=DEV, generator=g).float() * 2.0 ** -50 if biased \
+            else None
+        idx = S.choice(l, 6, "sigmoid", bias, 8, 3)
+        b = buffers(90, 64, 6)
+        rvq.moe_route_scored(l, 90, 64, 6, **b, bias=bias, groups=8, top_groups=3)
+        assert torch.equal(b["topk_idx"].long(), idx), (scale, shift)
+        assert torch.equal(b["pairs"].long(), S.grouping(idx, 64)[1])
+
+
 @pytest.mark.parametrize("n", [5, 130])
 def test_non_finite_is_reported(n):
     """A logit or bias that is not finite counts as 0, and everything stays in range."""
