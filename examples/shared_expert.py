@@ -1,5 +1,6 @@
 """A two-block stack of routed RVQ experts with shared experts: a prefill chunk,
-decode steps, and a training step of one shared expert.
+decode steps, a training step of one shared expert, and decode with the shared experts
+in microscaled formats.
 
     python examples/shared_expert.py [--tokens 512] [--steps 8]
 
@@ -41,6 +42,18 @@ def build(torch, n_blocks=2, d=2048, f=1024, n_experts=16, k=4):
     return SharedExpertStack(blocks)
 
 
+def microscaled(torch, stack):
+    """The stack for serving: shared experts in 4-bit weights and 8-bit tokens, experts
+    chosen by sigmoid scores with a balance bias from two of four groups."""
+    from moe_expert_ffn_router_gb300.layer import MxSharedExpert, SharedExpertStack
+
+    blocks = []
+    for L, S, p in stack.blocks:
+        L.set_scoring(bias=torch.zeros(L.E, device="cuda"), groups=4, top_groups=2)
+        blocks.append((L, MxSharedExpert(S.wg, S.wu, S.wd), p))
+    return SharedExpertStack(blocks)
+
+
 def train_step(torch, shared, x, target, lr):
     """One SGD step of a shared expert towards target (mean squared error);
     returns the loss before the step."""
@@ -63,7 +76,7 @@ def main():
     stack = build(torch)
     g = torch.Generator(device="cuda").manual_seed(1)
 
-    def timed(name, x, reps, **kw):
+    def timed(name, x, reps, stack=stack, **kw):
         stack.forward(x, **kw)
         s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         s.record()
@@ -84,6 +97,11 @@ def main():
     target = torch.randn((a.tokens, d), device="cuda", generator=g) * 0.1
     losses = [train_step(torch, shared, x, target, lr=1.0) for _ in range(a.steps)]
     print("training loss:", " ".join(f"{v:.5f}" for v in losses))
+    mx = microscaled(torch, stack)
+    timed("microscaled decode", torch.randn((1, d), device="cuda", generator=g), 20, stack=mx)
+    for _, S, _ in mx.blocks:
+        for n in S._bufs:
+            assert S.status(n) == (0, 0)
     for L, S, _ in stack.blocks:
         for n, train in S._bufs:
             assert S.status(n, train) == (0, 0)

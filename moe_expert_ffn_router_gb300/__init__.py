@@ -816,8 +816,13 @@ def _mx(codes, scales, rows, cols, fmt, what):
     if codes is None and scales is None:
         return None, None
     tiles = -(-cols // 128)
-    return (_vec(codes, rows * tiles * (64 if fmt == MOE_MX_F4 else 128), what, torch.uint8),
-            _vec(scales, -(-rows // 128) * tiles * 512, what + " scales", torch.uint8))
+    n, m = rows * tiles * (64 if fmt == MOE_MX_F4 else 128), -(-rows // 128) * tiles * 512
+    if codes is not None and scales is not None and codes.dtype is scales.dtype is torch.uint8 and \
+            codes.numel() == n and scales.numel() == m and codes.is_contiguous() and \
+            scales.is_contiguous():
+        return codes.data_ptr(), scales.data_ptr()
+    # one of them is refused, or left to the library (None)
+    return _vec(codes, n, what, torch.uint8), _vec(scales, m, what + " scales", torch.uint8)
 
 
 def moe_mx_quantize(x, rows, cols, codes, scales, fmt=MOE_MX_F8, stream=None):

@@ -266,6 +266,41 @@ def test_join_gradient_straight_through():
         assert rel <= 260 * U + (R.half_step(BF) if a.dtype is BF else 0), rel
 
 
+@pytest.mark.parametrize("n", [3, 400])
+def test_join_streams_and_graph(n):
+    """Two calls at once on two streams, and a captured call replayed on new rows, few
+    and walked: the bits of a call alone."""
+    d = 1032
+    ins = [make(n, d, F32, BF, F32, "channel", True, seed=40 + i) for i in range(3)]
+
+    def call(s, q, **kw):
+        rvq.moe_norm_join_mx(s["y"], n, d, None, *q, h=s["h"], gate=s["gate"], w_post=s["w_post"],
+                             w_pre=s["w_pre"], eps=EPS, **kw)
+
+    alone = [new_mx(n, d, F8) for _ in ins]
+    for s, q in zip(ins, alone):
+        call(s, q)
+    together = [new_mx(n, d, F8) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, q, st in zip(ins, together, streams):
+            call(s, q, stream=st)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, together):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    s, q = {k: None if v is None else v.clone() for k, v in ins[2].items()}, new_mx(n, d, F8)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(s, q)
+    for i in range(3):
+        for k, v in ins[i].items():
+            s[k].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(q[0], alone[i][0]) and torch.equal(q[1], alone[i][1])
+
+
 def test_past_two_gigabytes():
     """Matrices of more than 2^31 values: offsets of the last rows, of a tile boundary past
     2^31 and of the first, in every call."""
