@@ -81,7 +81,9 @@ def test_plain(n, E, k, score, renorm, scale, biased):
 @pytest.mark.parametrize("n,E,k,groups,top", [(1, 256, 16, 8, 4), (70, 256, 8, 8, 1),
                                               (33, 60, 5, 5, 2), (200, 64, 4, 32, 3),
                                               (17, 16, 3, 16, 4), (500, 96, 12, 3, 2),
-                                              (40, 256, 32, 2, 1), (5, 32, 8, 32, 31)])
+                                              (40, 256, 32, 2, 1), (5, 32, 8, 32, 31),
+                                              (30, 192, 8, 2, 1), (21, 256, 8, 4, 2),
+                                              (25, 128, 6, 4, 1), (12, 64, 5, 2, 1)])
 def test_groups(n, E, k, groups, top, score):
     g = gen(n + E + groups)
     l = torch.randn((n, E), device=DEV, generator=g) * 1.5
