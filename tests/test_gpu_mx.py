@@ -183,7 +183,8 @@ def check_join(s, n, d, alpha, post, hdt, xdt, fmt, outs=("h_out", "xn", "rstd")
 
 JOINS = [(1, 8, F32, BF), (1, 7168, F32, F32), (5, 40, BF, BF), (200, 136, F32, BF),
          (130, 2040, BF, BF), (3, 8200, F32, F32), (2, 16384, BF, HF), (333, 1000, HF, F32),
-         (400, 7168, F32, BF), (161, 8192, BF, BF)]
+         (350, 1096, BF, F32), (610, 2056, BF, BF), (4100, 72, F32, BF), (400, 7168, F32, BF),
+         (161, 8192, BF, BF)]
 
 
 @pytest.mark.parametrize("fmt", [F8, F4])
@@ -213,9 +214,9 @@ def test_join_agrees_with_quantize():
         assert torch.equal(codes, c2) and torch.equal(scales, s2)
 
 
-def test_join_in_place_and_zero_rows():
+@pytest.mark.parametrize("n,d", [(300, 520), (700, 1032)])
+def test_join_in_place_and_zero_rows(n, d):
     """h_out over h, xn over y; a row of zeros (eps > 0) is a row of zeros."""
-    n, d = 300, 520
     s = make(n, d, F32, F32, F32, "none", False, seed=9)
     s["h"][7], s["y"][7] = 0, 0
     want = {k: None if v is None else v.clone() for k, v in s.items()}
@@ -228,15 +229,18 @@ def test_join_in_place_and_zero_rows():
     assert (X.from_tiles(scales, n, d)[7] == 0).all()
 
 
-def test_join_non_finite_row():
-    """A NaN makes its own row NaN and no other."""
-    s = make(4, 256, F32, F32, F32, "none", False, seed=2)
+@pytest.mark.parametrize("n,d", [(4, 264), (500, 1096)])
+def test_join_non_finite_row(n, d):
+    """A NaN makes its own row NaN and no other, and no padding."""
+    s = make(n, d, F32, F32, F32, "none", False, seed=2)
     s["y"][2, 100] = float("nan")
-    codes, scales = new_mx(4, 256, F8)
-    rvq.moe_norm_join_mx(s["y"], 4, 256, None, codes, scales, h=s["h"], post_norm=False, eps=EPS)
-    byte = X.from_tiles(scales, 4, 256)
-    assert (byte[2] == 255).all() and (byte[[0, 1, 3]] < 255).all()
-    assert (X.unpack(codes, 4, 256, F8)[2] == 0).all()
+    codes, scales = new_mx(n, d, F8)
+    rvq.moe_norm_join_mx(s["y"], n, d, None, codes, scales, h=s["h"], post_norm=False, eps=EPS)
+    byte, blocks = X.from_tiles(scales, n, d), -(-d // 32)
+    assert (byte[2, :blocks] == 255).all() and (byte[:, blocks:] == 0).all()
+    byte[2] = 0
+    assert (byte < 255).all()
+    assert (X.unpack(codes, n, d, F8)[2] == 0).all()
 
 
 def test_join_gradient_straight_through():
