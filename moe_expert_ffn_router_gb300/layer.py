@@ -5,8 +5,8 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (MOE_ACT_SILU, MOE_MX_F4, MOE_MX_F8, MOE_SCORE_SIGMOID, RVQ_WS_STATUS_BYTES, moe_bank_init, moe_bank_record_bytes,
-               moe_bank_validate, moe_bank_write_expert, moe_cache_bank, moe_cache_create,
+from . import (MOE_ACT_SILU, MOE_MX_F4, MOE_MX_F8, MOE_SCORE_SIGMOID, RVQ_WS_STATUS_BYTES,
+               moe_bank_init, moe_bank_record_bytes, moe_bank_validate, moe_bank_write_expert, moe_cache_bank, moe_cache_create,
                moe_cache_destroy, moe_cache_stats, moe_combine, moe_expert_ffn,
                moe_gated_linear, moe_gated_linear_backward, moe_gated_linear_workspace_bytes,
                moe_layer_forward, moe_layer_forward_host, moe_layer_forward_prenorm,
@@ -14,10 +14,8 @@ from . import (MOE_ACT_SILU, MOE_MX_F4, MOE_MX_F8, MOE_SCORE_SIGMOID, RVQ_WS_STA
                moe_linear_backward, moe_linear_workspace_bytes, moe_mx_code_bytes,
                moe_mx_gated_linear, moe_mx_gated_linear_workspace_bytes, moe_mx_linear,
                moe_mx_linear_workspace_bytes, moe_mx_quantize, moe_mx_scale_bytes,
-               moe_norm_join, moe_norm_join_mx, moe_rms_norm,
-               moe_route, moe_route_rule, moe_route_scored,
-               moe_router_logits,
-               moe_workspace_bytes, rvq_ws_clear, rvq_ws_status)
+               moe_norm_join, moe_norm_join_mx, moe_rms_norm, moe_route, moe_route_rule,
+               moe_route_scored, moe_router_logits, moe_workspace_bytes, rvq_ws_clear, rvq_ws_status)
 
 
 def _dev(a, device, dtype=None):
@@ -503,5 +501,4 @@ class SharedExpertStack:
 
 
 __all__ = ["MoeLayer", "MoeStack", "MoeStreamedStack", "MxSharedExpert", "SharedExpert",
-           "SharedExpertStack",
-           "RVQ_WS_STATUS_BYTES"]
+           "SharedExpertStack", "RVQ_WS_STATUS_BYTES"]
