@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(512, 2) mx_join_walk_kernel(const MxJoinJob jo
         }
         cp_commit();
     };
-    if (threadIdx.x < 64) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
+    // places of absent warps are added too; a block may have fewer threads than places
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i >> 4][i & 15] = 0.f;
     int t = blockIdx.x;
     dependency_wait();
     fetch(t);
