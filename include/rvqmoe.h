@@ -400,6 +400,7 @@ rvq_status moe_route_scored(const float *logits_dev, int32_t n, int32_t E, int32
  * the choice topk_idx (which has no gradient; indices outside 0 .. E-1 take no part):
  *   dp_j = scale dw_j, or with renorm scale (dw_j - sum_i dw_i p_i / P) / P, P = sum_i p_i
  *   sigmoid: dl_j = dp_j p_j (1 - p_j);  softmax: dl_e = p_e (dp_e - sum_j dp_j p_j)
+ * A logit that is not finite counts as 0 here too (the choice reported it).
  * dlogits may take the place of logits and overlaps nothing else (EINVAL). */
 rvq_status moe_route_scored_backward(const float *dtopk_w_dev, const float *logits_dev,
                                      const int32_t *topk_idx_dev, int32_t n, int32_t E, int32_t k,

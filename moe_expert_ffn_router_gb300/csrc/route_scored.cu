@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(RS_PLACE) route_scored_place_kernel(const Rout
 //   sigmoid        dl_j = dp_j p_j (1 - p_j), 0 elsewhere
 //   softmax        dl_e = p_e (dp_e - sum_j dp_j p_j) over all experts; renormalised it
 //                  is scale w'_j (dw_j - sum_i dw_i w'_i) of the chosen alone, w' = w / scale
+// A logit that is not finite is 0, as it was for the weights.
 __global__ void __launch_bounds__(RS_NT) route_scored_backward_kernel(const RouteScoredJob j) {
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * (RS_NT / 32) + (int)(threadIdx.x >> 5);
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(RS_NT) route_scored_backward_kernel(const Rout
     const bool on = lane < j.k;
     const int idx = on ? j.idx[(int64_t)t * j.k + lane] : -1;
     const bool in = idx >= 0 && idx < j.E;  // others take no part
-    const float l = in ? row[idx] : 0.f, dw = in ? j.dw[(int64_t)t * j.k + lane] : 0.f;
+    const float l = in ? finite_or_0(row[idx]) : 0.f, dw = in ? j.dw[(int64_t)t * j.k + lane] : 0.f;
     const RouteRule &rule = j.rule;
     float g = 0.f, rest = 0.f, m = 0.f, z = 1.f;
     const bool dense = rule.score == MOE_SCORE_SOFTMAX && !rule.renorm;
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(RS_NT) route_scored_backward_kernel(const Rout
         float s = 0.f;
 #pragma unroll
         for (int q = 0; q < RS_Q; ++q) {
-            all[q] = lane + 32 * q < j.E ? row[lane + 32 * q] : 0.f;
+            all[q] = lane + 32 * q < j.E ? finite_or_0(row[lane + 32 * q]) : 0.f;
             if (lane + 32 * q < j.E) top = max(top, to_key(all[q]));
         }
         m = from_key(warp_max(top));

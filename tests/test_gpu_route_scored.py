@@ -261,3 +261,39 @@ def test_layer(n, tc):
     if tc == 0:
         h = MoeStack([L]).forward(x.float())[0]
         assert torch.equal(h["idx"].long(), S.choice(h["logits"], 4, "sigmoid", bias, 4, 2))
+
+
+@pytest.mark.parametrize("n", [5, 130])
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False),
+                                          ("softmax", True), ("softmax", False)])
+def test_gradient_of_non_finite_logits(score, renorm, n):
+    """NaN and infinities, chosen and not: the gradient of the weights that the forward
+    call returned, which took such a logit as 0."""
+    E, k = 64, 8
+    l = torch.randn((n, E), device=DEV, generator=gen(31))
+    dw = torch.randn((n, k), device=DEV, generator=gen(32))
+    bad = l.clone()
+    bad[0, 3], bad[1, 7], bad[2, 9] = float("nan"), float("inf"), -float("inf")
+    bad[3, :40] = float("nan")
+    bad[4] = float("inf")
+    fixed = bad.nan_to_num(0, 0, 0)
+    idx = S.choice(fixed, k, score, None, 1, 1)
+    idx[0, k - 1], idx[1, k - 1], idx[2, k - 1] = 3, 7, 9       # chosen all the same
+    # and choices that are not the largest
+    idx[:, 0] = torch.where(torch.arange(n, device=DEV) % 2 == 0, idx[:, 0], idx[:, 1])
+    idx[:, 1] = torch.where(idx[:, 0] == idx[:, 1], 63 - idx[:, 1], idx[:, 1])
+    kw = dict(score=rvq.MOE_SCORES[score], renorm=renorm, scale=2.5)
+    got = {}
+    for name, rows in (("bad", bad), ("fixed", fixed)):
+        got[name] = torch.full((n, E), 99.0, device=DEV)
+        rvq.moe_route_scored_backward(dw, rows, idx.int(), n, E, k, got[name], **kw)
+    assert torch.equal(got["bad"], got["fixed"])
+    want = S.gradient(fixed, idx, dw, score, renorm, 2.5)
+    # terms of at most the sum of the magnitudes of scale dw, each after two exponentials
+    # (two units of the last place and |l| 2^-24, |l| < 8), sums of up to 64 terms and a
+    # few products and quotients
+    bound = 256 * U * 2.5 * dw.double().abs().sum(1, keepdim=True)
+    assert ((got["bad"].double() - want).abs() <= bound).all()
+    place = bad.clone()
+    rvq.moe_route_scored_backward(dw, place, idx.int(), n, E, k, place, **kw)
+    assert torch.equal(place, got["bad"])
