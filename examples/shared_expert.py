@@ -7,6 +7,7 @@ in microscaled formats.
 Weights and tokens are seeded and synthetic (d = 2048, f = 1024, 16 routed
 experts, 4 per token)."""
 import argparse
+import copy
 import os
 import sys
 
@@ -44,11 +45,14 @@ def build(torch, n_blocks=2, d=2048, f=1024, n_experts=16, k=4):
 
 def microscaled(torch, stack):
     """The stack for serving: shared experts in 4-bit weights and 8-bit tokens, experts
-    chosen by sigmoid scores with a balance bias from two of four groups."""
+    chosen by sigmoid scores with a balance bias from two of four groups.  Its layers are
+    others on the same expert records and workspaces, so the given stack goes on choosing
+    by logits."""
     from moe_expert_ffn_router_gb300.layer import MxSharedExpert, SharedExpertStack
 
     blocks = []
     for L, S, p in stack.blocks:
+        L = copy.copy(L)
         L.set_scoring(bias=torch.zeros(L.E, device="cuda"), groups=4, top_groups=2)
         blocks.append((L, MxSharedExpert(S.wg, S.wu, S.wd), p))
     return SharedExpertStack(blocks)

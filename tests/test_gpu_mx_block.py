@@ -138,3 +138,26 @@ def test_shared_expert_alone():
         torch.cuda.synchronize()
         got = sh.buffers(7)["out"].clone()
         assert torch.equal(got, sh.forward(x)["out"])
+
+
+def test_example_leaves_the_given_stack():
+    """The example's microscaled stack scores its experts; the stack that it was made from
+    still chooses by logits, and gives the same bits."""
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                      "shared_expert.py")
+    spec = importlib.util.spec_from_file_location("shared_expert_example", at)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    stack = example.build(torch, n_blocks=2, d=512, f=512, n_experts=8, k=2)
+    x = torch.randn((5, 512), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    keys = ("logits", "idx", "w", "out", "h")
+    before = [{k: b[k].clone() for k in keys} for b in stack.forward(x)]
+    mx = example.microscaled(torch, stack)
+    for b in mx.forward(x):
+        assert torch.equal(b["idx"].long(), S.choice(b["logits"], 2, "sigmoid", None, 4, 2))
+    for L, _, _ in stack.blocks:
+        assert L.rule is None
+    for b, want in zip(stack.forward(x), before):
+        assert all(torch.equal(b[k], want[k]) for k in keys)
