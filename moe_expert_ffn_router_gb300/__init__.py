@@ -55,6 +55,7 @@ class MoeRouteRule(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("bias", ctypes.c_void_p),
                 ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+    keep = None  # the tensor that `bias` points into (moe_route_rule)
 
 
 class RvqCacheStats(ctypes.Structure):
@@ -453,19 +454,21 @@ def moe_route_scored_backward(dtopk_w, logits, topk_idx, n, E, k, dlogits,
 
 def moe_layer_forward(bank, wr, bias, x, n, k, logits, topk_idx, topk_w, offsets, pairs, out,
                       ws, events=None, stream=None, tc_min_tokens=0, residual=None, rule=None):
-    """rule (moe_route_rule): experts chosen by moe_route_scored instead of moe_route."""
+    """rule (moe_route_rule, for as many experts as the bank has): experts chosen by
+    moe_route_scored instead of moe_route."""
     ev = None
     if events is not None:
         assert len(events) == MOE_LAYER_EVENTS
         ev = (ctypes.c_void_p * MOE_LAYER_EVENTS)(*[e.cuda_event for e in events])
     rdt = _dt(residual) if residual is not None else _dt(x)
     if rule is not None:
+        _vec(rule.keep, bank.n_experts, "bias")
+        raw = _stream_of(stream, rule.keep)
         _check("moe_layer_forward_scored",
                _lib.moe_layer_forward_scored(ctypes.byref(bank), _p(wr), _p(bias), rule, _p(x),
                                              _dt(x), n, k, _p(logits), _p(topk_idx), _p(topk_w),
                                              _p(offsets), _p(pairs), _p(out), _p(ws), _nbytes(ws),
-                                             _p(residual), rdt, int(tc_min_tokens), ev,
-                                             _stream(stream)))
+                                             _p(residual), rdt, int(tc_min_tokens), ev, raw))
         return
     _check("moe_layer_forward",
            _lib.moe_layer_forward_ex(ctypes.byref(bank), _p(wr), _p(bias), _p(x), _dt(x), n, k,

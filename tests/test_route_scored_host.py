@@ -128,3 +128,27 @@ def test_definition_choice():
     assert S.choice(l, 2, "sigmoid", b, 4, 1).tolist() == [[0, 1]]
     off, pairs = S.grouping(torch.tensor([[1, 0], [1, 2]]), 4)
     assert off.tolist() == [0, 1, 3, 4, 4] and pairs.tolist() == [1, 0, 2, 3]
+
+
+def test_layer_refuses_a_rule_of_other_experts():
+    """A rule's bias is as long as the bank has experts and on the call's device: the
+    layer call would read behind it, or where the GPU cannot."""
+    class Fake:
+        device_index, cuda_stream = 0, 0
+
+    bank = rvq.RvqMoeBank()
+    rb = rvq.moe_bank_record_bytes(512, 512)
+    assert lib.moe_bank_init(ctypes.byref(bank), A, rb * 32, 32, 512, 512, 0) == OK
+    x = torch.zeros((4, 512))
+    i32, f32 = torch.zeros(128, dtype=torch.int32), torch.zeros((4, 32))
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+
+    def forward(rule):
+        rvq.moe_layer_forward(bank, x, None, x, 4, 4, f32, i32, f32, i32, i32, x, ws, rule=rule,
+                              stream=Fake())
+
+    for n in (16, 64):
+        with pytest.raises(ValueError, match="bias"):
+            forward(rvq.moe_route_rule(n, bias=torch.zeros(n)))
+    with pytest.raises(ValueError, match="on cpu, the call on cuda:0"):
+        forward(rvq.moe_route_rule(32, bias=torch.zeros(32)))
