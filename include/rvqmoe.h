@@ -490,7 +490,9 @@ rvq_status moe_layer_forward_ex(const rvq_moe_bank *bank, const float *wr_dev,
                                 void **events, rvq_stream_t stream);
 
 /* moe_layer_forward_ex with the experts chosen by `rule` (moe_route_scored) in the
- * place of moe_route; bias_dev is the router's own bias, added to the logits. */
+ * place of moe_route; bias_dev is the router's own bias, added to the logits.  Sizes
+ * are those of the layer calls, n <= moe_route_max_tokens(E) (4224 for 256 experts) among
+ * them, though moe_route_scored by itself takes more; more are refused (EINVAL). */
 rvq_status moe_layer_forward_scored(const rvq_moe_bank *bank, const float *wr_dev,
                                     const float *bias_dev, const moe_route_rule *rule,
                                     const void *x_dev, rvq_dtype xdt, int32_t n, int32_t k,

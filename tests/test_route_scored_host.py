@@ -12,6 +12,7 @@ lib = rvq._lib
 A = 0x10000000       # fake, aligned "device" addresses far apart (never dereferenced)
 B, C, D, E_, F = (A + i * 0x10000000 for i in range(1, 6))
 OK, EINVAL, EALIGN, ENOMEM = 0, 1, 2, 3
+F32 = 0
 
 
 def rule(score=1, bias=None, groups=1, top=1, renorm=1, scale=1.0):
@@ -152,3 +153,22 @@ def test_layer_refuses_a_rule_of_other_experts():
             forward(rvq.moe_route_rule(n, bias=torch.zeros(n)))
     with pytest.raises(ValueError, match="on cpu, the call on cuda:0"):
         forward(rvq.moe_route_rule(32, bias=torch.zeros(32)))
+
+
+@pytest.mark.parametrize("E,most", [(256, 4224), (64, 17024)])
+def test_layer_token_limit(E, most):
+    """The layer call takes as many tokens as the layer calls by logits; more are refused
+    before any launch, as the header says."""
+    assert rvq.moe_route_max_tokens(E) == most
+    bank = rvq.RvqMoeBank()
+    rb = rvq.moe_bank_record_bytes(512, 512)
+    assert lib.moe_bank_init(ctypes.byref(bank), A, rb * E, E, 512, 512, 0) == OK
+
+    def layer(n, ws):
+        return lib.moe_layer_forward_scored(ctypes.byref(bank), A, None, rule(), A, F32, n, 4, B, C,
+                                            D, E_, E_ + 0x1000000, F, F + 0x8000000, ws, None, F32,
+                                            0, None, None)
+
+    assert layer(most + 1, 1 << 60) == EINVAL
+    assert f"max {most}".encode() in lib.rvq_last_error()
+    assert layer(most, 0) == ENOMEM
