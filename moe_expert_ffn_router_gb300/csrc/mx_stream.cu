@@ -402,6 +402,10 @@ __global__ void __launch_bounds__(MS_THREADS, 2) mx_stream_kernel(
 
 // of one CTA where two share an SM, and of one alone
 constexpr int kRingSmall = 111 << 10, kRingLarge = 200 << 10;
+// the most that two CTAs of an SM have each: half its 228 KB, less 1 KB that every block
+// takes and 1 KB for the barriers
+constexpr int kHalfSm = 112 << 10;
+static_assert(kRingSmall <= kHalfSm, "two rings on an SM");
 
 // Clusters of `split` CTAs that the device holds at once with one CTA per SM (the query
 // does not count a second one per SM; it gives 15 clusters of eight, 36 of four).
@@ -434,34 +438,38 @@ int resident_clusters(int split) {
     return n;
 }
 
-// Tokens of a tile, padded to a multiple of 16; bytes of a stage; TMEM columns.
+// Tokens of a tile, padded to a multiple of 16; bytes of a stage; of the partial tile that
+// takes the ring's place; TMEM columns.
 struct Shape {
-    int npad, stage;
+    int npad, stage, part;
     uint32_t cols;
 };
 template <bool GATED, bool F4>
 Shape shape_of(const MxJob &job) {
     constexpr int MATS = GATED ? 2 : 1, KT = F4 ? 2 : 1;
     Shape s;
-    s.npad = ((job.n < MS_TOKENS ? job.n : MS_TOKENS) + 15) / 16 * 16;
+    const int tokens = job.n < MS_TOKENS ? job.n : MS_TOKENS;
+    s.npad = (tokens + 15) / 16 * 16;
+    s.part = tokens * (MATS * MS_ROWS + 4) * 4;
     s.stage = (MATS * MS_ABYTES + s.npad * 128 + (MATS + 1) * KT * kMxTileBytes + 1023) / 1024 * 1024;
     s.cols = 32;
     while ((int)s.cols < MATS * s.npad + (MATS + 1) * KT * 4) s.cols *= 2;
     return s;
 }
 
-// Two CTAs per SM where both fit (a ring of two stages or more and 256 columns of
-// tensor memory each), and the depth split among as many CTAs, up to eight, as leaves
-// every cluster resident at once, with two slices or more each.  One token, gated
+// Two CTAs per SM where both fit (a ring of two stages or more, the partial tile and 256
+// columns of tensor memory each), and the depth split among as many CTAs, up to eight, as
+// leaves every cluster resident at once, with two slices or more each.  One token, gated
 // 7168 -> 2048, 16 tiles of 4-bit weights: eight CTAs each 7.7 us, four 9.7; with the
 // large ring, where a sixteenth cluster of eight waits for the others, 13.7; 2048 ->
-// 7168, 56 tiles: four 5.5, eight 9.5, two 6.5.
+// 7168, 56 tiles: four 5.5, eight 9.5, two 6.5.  112 tokens, whose partial tiles do not fit
+// an SM twice: planned as if they did 24.7, alone 13.9 (110, two to an SM, 16.9).
 template <bool GATED, bool F4>
 MxStreamPlan plan_of(const MxJob &job, const Shape &s) {
     MxStreamPlan p;
     p.slices = F4 ? (mx_tiles(job.cols) + 1) / 2 : mx_tiles(job.cols);
     p.tiles = (long long)mx_tiles(job.rows) * ((job.n + MS_TOKENS - 1) / MS_TOKENS);
-    p.two = s.cols <= 256 && 2 * s.stage <= kRingSmall;
+    p.two = s.cols <= 256 && 2 * s.stage <= kRingSmall && s.part <= kHalfSm;
     p.split = 8;
     while (p.split > 1 && (p.slices < 2 * p.split ||
                            p.tiles > (p.two ? 2 : 1) * resident_clusters<GATED, F4>(p.split)))
@@ -525,8 +533,7 @@ rvq_status launch(const MxJob &job, cudaStream_t stream) {
     g.sx = job.xs;
     g.ktiles = mx_tiles(job.cols);
     // the ring, or the partial tile that takes its place
-    const int part = (job.n < MS_TOKENS ? job.n : MS_TOKENS) * (MATS * MS_ROWS + 4) * 4;
-    const int dyn = g.stages * g.stage > part ? g.stages * g.stage : part;
+    const int dyn = g.stages * g.stage > s.part ? g.stages * g.stage : s.part;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(plan.tiles * g.split));
     cfg.blockDim = dim3(MS_THREADS);

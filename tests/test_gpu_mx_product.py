@@ -314,3 +314,17 @@ def test_ways(way, case):
         run_gated(n, rows, cols, xf, wf, ofmt=F8)
     else:
         run_linear(n, rows, cols, xf, wf, bias=True, act="silu", res=F32)
+
+
+@pytest.mark.parametrize("xf,wf", [(F8, F4), (F4, F4)])
+def test_partial_tiles_that_fit_an_sm_once(xf, wf):
+    """Gated products of 111 and 112 tokens: their partial tile is longer than the ring and
+    does not fit an SM twice, so the depth is split as for 113 to 128 tokens, which take an
+    SM alone too; and the outputs around that border."""
+    alone = rvq.rvq_selftest_mx_plan(True, xf, wf, 128, 2048, 7168)
+    for n in (111, 112, 113):
+        assert rvq.rvq_selftest_mx_plan(True, xf, wf, n, 2048, 7168) == alone
+    for n in (110, 111, 112, 113):
+        run_gated(n, 264, 1024, xf, wf, out=F32)
+        run_gated(n, 264, 1024, xf, wf, ofmt=F8)
+    run_gated(112, 2048, 1024, xf, wf)
