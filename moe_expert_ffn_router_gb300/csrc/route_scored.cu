@@ -164,7 +164,8 @@ __device__ __forceinline__ void top_two(uint32_t &o1, uint32_t &o2, uint32_t a1,
 // apart by more than 6.5e-7 (|x| + |y| + 2 max |b|), and by 2e-15, what 64 bits tell apart.
 // Softmax: p is off by p (6 + 2.2 |l - m|) 2^-23, p |l - m| <= 0.37, and 14 half steps of the
 // sum, at most 1.7e-6, and c by half a step.  Sums of two: four times and twice that
-// (one of them may be positive, up to max |b|, and the other as far below).
+// (one of them may be positive, up to max |b|, and the other as far below, so the half
+// steps of a softmax's two c are up to 2^-23 max |b|, of two sums twice that).
 template <int Q>
 __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
                                       const float *row, int E, int k, const RouteRule &rule,
@@ -205,7 +206,7 @@ __device__ __forceinline__ int choose(const float (&l)[Q], const float (&b)[Q],
             base = 1.3e-6f * (biased ? __uint_as_float(warp_max(big)) : 0.f) + 2e-15f;
         } else {
             part = 2.4e-7f;
-            base = 3.6e-6f;
+            base = 1.2e-7f * (biased ? __uint_as_float(warp_max(big)) : 0.f) + 3.6e-6f;
         }
     }
     const bool whole = size % 32 == 0;  // register q is of group 32 q / size

@@ -297,3 +297,24 @@ def test_gradient_of_non_finite_logits(score, renorm, n):
     place = bad.clone()
     rvq.moe_route_scored_backward(dw, place, idx.int(), n, E, k, place, **kw)
     assert torch.equal(place, got["bad"])
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("big", [1.0, 40.0, 1000.0, 1e5])
+@pytest.mark.parametrize("E,groups,top,k", [(64, 8, 3, 4), (256, 8, 4, 8), (60, 5, 2, 3)])
+def test_groups_of_large_biases_of_both_signs(E, groups, top, k, big, score):
+    """A group's two largest c are about +big and -big: their sum is the scores', which 32
+    bits of c do not hold."""
+    n = 3000
+    g = gen(51)
+    l = torch.randn((n, E), device=DEV, generator=g)
+    bias = torch.full((groups, E // groups), -big, device=DEV)
+    bias[:, 1] = big
+    bias = bias.view(-1) + torch.randint(0, 2, (E,), device=DEV, generator=g) * (big / 1024)
+    b = buffers(n, E, k)
+    for biases in (bias, bias.view(groups, -1).roll(1, 0).reshape(-1).contiguous()):
+        rvq.moe_route_scored(l, n, E, k, **b, score=rvq.MOE_SCORES[score], bias=biases,
+                             groups=groups, top_groups=top)
+        assert rvq.rvq_ws_status(b["ws"]) == (0, 0)
+        idx = S.choice(l, k, score, biases, groups, top)
+        assert torch.equal(b["topk_idx"].long(), idx)
