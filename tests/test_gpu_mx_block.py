@@ -161,3 +161,39 @@ def test_example_leaves_the_given_stack():
         assert L.rule is None
     for b, want in zip(stack.forward(x), before):
         assert all(torch.equal(b[k], want[k]) for k in keys)
+
+
+@pytest.mark.parametrize("n", [1, 9, 130])
+def test_stack_in_a_graph_and_on_a_stream(n):
+    """A whole pass captured and replayed on new tokens, and one on a side stream, between
+    passes of another batch size: the bits of a pass alone."""
+    stack, _ = build([(F8, F4), (F4, F4)])
+    g = torch.Generator(device=DEV).manual_seed(n)
+    xs = [torch.randn((n, D), device=DEV, generator=g) for _ in range(3)]
+    keys = ("logits", "idx", "w", "offsets", "pairs", "out", "h")
+
+    def outputs(bufs):
+        torch.cuda.synchronize()
+        return [{k: b[k].clone() for k in keys} for b in bufs]
+
+    def same(a, b):
+        return all(torch.equal(p[k], q[k]) for p, q in zip(a, b) for k in keys)
+
+    alone = [outputs(stack.forward(x)) for x in xs]
+    x = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bufs = stack.forward(x)
+    other = torch.randn((5, D), device=DEV, generator=g)
+    for i in (2, 0, 1):
+        x.copy_(xs[i])
+        stack.forward(other)
+        graph.replay()
+        assert same(outputs(bufs), alone[i]), i
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        bufs = stack.forward(xs[2])
+    assert same(outputs(bufs), alone[2])
+    for L, sh, _ in stack.blocks:
+        assert L.status(n) == (0, 0) and sh.status(n) == (0, 0)
