@@ -304,10 +304,11 @@ rvq_status walk(const MxJoinJob &job, cudaStream_t stream) {
 }
 
 // Whether blocks walk over the rows: more rows than the row kernel holds at once, long or
-// many enough to pay for the setup (2048 x 512 fp32 and bf16, walked and a block per row,
-// 4.4 and 3.5 us; 2048 x 1536 8.7 and 8.9; 8192 x 512 10.9 and 11.5; 2048 x 7168 28.9 and
-// 36.7); one fits with its gains, and the types have an instance (fp32 or bf16 rows and
-// gains, a full gate of h's type).
+// many enough to pay for the setup (walked and a block per row, fp32 stream, bf16 block, post
+// norm, past L2: 2048 x 512 4.9 and 5.1 us; 2048 x 1536 9.1 and 11.5; 4200 x 512 7.8 and
+// 7.1, 8192 x 512 10.8 and 12.8; 20000 x 72 18.1 and 20.8; 2048 x 7168 32.9 and 45.4; rows
+// that L2 holds, 2048 x 512 4.4 and 3.5); one fits with its gains, and the types have an
+// instance (fp32 or bf16 rows and gains, a full gate of h's type).
 bool walks(const JoinJob &j) {
     return j.n > 2 * num_sms() && (j.d > 1024 || j.n > 4096) && j.d <= 8192 && j.hdt != RVQ_F16 &&
            j.ydt != RVQ_F16 && j.wdt != RVQ_F16 &&

@@ -21,11 +21,11 @@
 //    bitmap of tokens per expert in its run.  No atomics decide an order: pairs are sorted
 //    by (expert, token).
 //
-// Measured (GB300; bias, 4 of 8 groups, 16 of 256 experts): one token 6.5 us, 64 10.2, 2048
-// 16 to 20 (11.4 without bias and groups); 8 of 64 experts, 4096 tokens 10.4, with the
-// softmax and its gradient 13.9.  Latency: some 2400 instructions a token, 1200 of 64
-// experts; a row that is decided in 64 bits adds microseconds to its launch, most of them
-// to fetch that code.
+// Measured (GB300; bias, 4 of 8 groups, 16 of 256 experts): one token 6.5 to 6.9 us, 64 10.8,
+// 2048 15 to 17 (11.4 without bias and groups), with the softmax, more of whose rows are
+// decided in 64 bits, 37; 8 of 64 experts, 4096 tokens 9.0, with the softmax and its gradient
+// 13.9.  Latency: some 2400 instructions a token, 1200 of 64 experts; a row that is decided
+// in 64 bits adds microseconds to its launch, most of them to fetch that code.
 #include "dense.cuh"
 #include "route_scored.cuh"
 
